@@ -62,6 +62,8 @@ typedef enum pa_status {
 #define PA_DEVERR_SLOT 2      /* a slot_mapping entry >= num_blocks * block_size */
 #define PA_DEVERR_TIMEOUT 4   /* a kernel gave up a bounded wait; its outputs are invalid */
 #define PA_DEVERR_LENGTH 8    /* a request's lengths break a call's stated precondition */
+#define PA_DEVERR_POSITION 16 /* a position outside the cos/sin table */
+#define PA_DEVERR_NO_BLOCKS 32 /* a step plan ran out of free blocks */
 
 /* Shape of a standard-layout paged batch. */
 typedef struct pa_shape {
@@ -389,6 +391,137 @@ pa_status pa_mla_prefill(const void* q, const void* kv_cache, const void* w_kv_b
                          int num_heads, int block_size, int num_blocks, int max_blocks_per_seq,
                          int max_seq_len, float scale, int causal, void* workspace, void* out,
                          float* lse, void* stream);
+
+/*
+ * The step plan: the index tensors that a serving step needs, built on the
+ * GPU from the requests' lengths (the page has the scheduler hand them over:
+ * "Attention Backends", section "What 'paged attention' requires of a
+ * kernel", block_table and slot_mapping).  Request i has context_lens[i]
+ * tokens in the cache and gets query_lens[i] new ones.  With
+ *   seq_i  = context_lens[i] + query_lens[i],
+ *   have_i = ceil(context_lens[i] / bs),  need_i = ceil(seq_i / bs),
+ *   base_i = free_start + sum_{j < i} (need_j - have_j)
+ * the call writes
+ *   seq_lens[i] = seq_i;
+ *   query_start_loc[0..N]: exclusive prefix sums of query_lens, then the sum T;
+ *   block_table[i, have_i + k] = free_blocks[base_i + k], k < need_i - have_i
+ *     (other entries stay as they are);
+ *   for token t = query_start_loc[i] + j, j < query_lens[i]:
+ *     positions[t] = p = context_lens[i] + j,
+ *     slot_mapping[t] = block_table[i, p / bs] * bs + p % bs;
+ *   for the padding tokens t in [T, max_tokens): positions[t] = 0,
+ *     slot_mapping[t] = -1 (the cache writes skip them);
+ *   totals[0] = T, totals[1] = free_start + the number of blocks taken (the
+ *     next step's free_start).
+ * free_start is a device int32, NULL for 0; totals must not overlap it.
+ * Nothing else of the outputs may overlap an input.
+ * Refused on the device, without a write out of range:
+ *   - a new block when free_blocks (num_free entries) is used up: its table
+ *     entry becomes -1, its tokens get slot -1, PA_DEVERR_NO_BLOCKS;
+ *   - a block id outside [0, num_blocks), in free_blocks or in the table's
+ *     entry for a part-filled last block: -1 as above, PA_DEVERR_BLOCK_ID;
+ *   - a block past the table's columns: not written, slot -1; a negative
+ *     length (read as 0), a negative free_start (its blocks read as used up),
+ *     seq_i beyond INT_MAX (new tokens cut there) or T > max_tokens (tokens
+ *     past max_tokens are not written, the blocks they would open stay
+ *     unwritten in the table; sums saturate at INT_MAX): PA_DEVERR_LENGTH.
+ * max_tokens >= 0 is the length of positions and slot_mapping.  num_seqs == 0
+ * writes query_start_loc[0] = 0, the padding and totals.
+ */
+pa_status pa_plan_step(const int32_t* context_lens, const int32_t* query_lens,
+                       const int32_t* free_blocks, const int32_t* free_start, int num_free,
+                       int num_seqs, int max_blocks_per_seq, int block_size, int num_blocks,
+                       int max_tokens, int32_t* block_table, int32_t* query_start_loc,
+                       int32_t* seq_lens, int32_t* positions, int64_t* slot_mapping,
+                       int32_t* totals, void* stream);
+
+/*
+ * Norms of queries and keys for each head, the position rotation and the
+ * cache write in one pass: what stands between a layer's projection and
+ * attention over the pool.  For every token t and head h, with x the row of d
+ * values and everything in fp32:
+ *   y = x * w / sqrt(mean(x^2) + eps)   (w: q_weight for queries, k_weight for
+ *                                        keys, [d] bf16; NULL: y = x)
+ *   rotation of the first rotary_dim = r entries by the angles of the token's
+ *   position p (cos_sin[p, 0:r/2] cosines, cos_sin[p, r/2:r] sines), over the
+ *   pairs (y_k, y_{k + r/2}), or (y_{2k}, y_{2k+1}) with interleaved != 0:
+ *     (a, b) -> (a cos_k - b sin_k, b cos_k + a sin_k)
+ *   queries: q_out[t, h, :] = the result, rounded once to bf16;
+ *   keys and values: as pa_reshape_and_cache writes them at slot_mapping[t]
+ *   (keys the result rounded once to bf16, values bit copies).  slot < 0
+ *   writes no key and value (the query is still computed); a slot >=
+ *   num_blocks * bs likewise, and sets PA_DEVERR_SLOT.
+ * A position outside [0, max_position) sets PA_DEVERR_POSITION and leaves all
+ * of the token's outputs as they were.
+ * q: [num_tokens, Hq, d] bf16 with q_stride elements from token to token (the
+ * heads of a token are dense), key and value likewise with Hkv heads: views of
+ * one packed projection need no copy.  Strides: multiples of 8, at least H * d.
+ * q_out: [num_tokens, Hq, d] bf16, dense; it may be q itself when q is dense,
+ * and overlaps no other argument.  cos_sin: [max_position, r] fp32;
+ * positions: [num_tokens] int32; with r == 0 both are unused and may be NULL.
+ * Supported: head_size in {64, 128}, r a multiple of 16, at most head_size.
+ * Data pointers 16-byte aligned.  eps >= 0.  Uses shape->num_q_heads,
+ * num_kv_heads, head_size, block_size, num_blocks.  num_tokens == 0 is a no-op.
+ */
+pa_status pa_qk_norm_rope_cache(const void* q, const void* key, const void* value,
+                                int64_t q_stride, int64_t key_stride, int64_t value_stride,
+                                const void* q_weight, const void* k_weight, float eps,
+                                const float* cos_sin, int max_position, int rotary_dim,
+                                int interleaved, const int32_t* positions, void* kv_cache,
+                                const int64_t* slot_mapping, int num_tokens,
+                                const pa_shape* shape, void* q_out, void* stream);
+
+/*
+ * The same with an fp8 pool: keys are written as E(result / k_scale) (the
+ * fp32 result is not rounded to bf16 before) and values as E(value /
+ * v_scale), E and the scales as for pa_reshape_and_cache_fp8.
+ */
+pa_status pa_qk_norm_rope_cache_fp8(const void* q, const void* key, const void* value,
+                                    int64_t q_stride, int64_t key_stride, int64_t value_stride,
+                                    const void* q_weight, const void* k_weight, float eps,
+                                    const float* cos_sin, int max_position, int rotary_dim,
+                                    int interleaved, const int32_t* positions, void* kv_cache,
+                                    const int64_t* slot_mapping, int num_tokens,
+                                    const pa_shape* shape, float k_scale, float v_scale,
+                                    void* q_out, void* stream);
+
+/*
+ * Varlen paged attention with a sliding window and a few first tokens that
+ * stay visible: pa_varlen_fwd_window in which row j at position p_j sees
+ *   p <= p_j and (p > p_j - sliding_window or p < num_sinks).
+ * num_sinks >= 0; 0 is pa_varlen_fwd_window's mask.  Blocks that no row of a
+ * request sees (between the first tokens and the oldest window) are not
+ * read: their table entries and contents may be anything.  A position that
+ * one row of a request sees must hold finite values, as for pa_varlen_fwd.
+ */
+pa_status pa_varlen_fwd_sinks(const void* q, const void* kv_cache, const int32_t* block_table,
+                              const int32_t* query_start_loc, const int32_t* seq_lens,
+                              int total_q, int max_query_len, const pa_shape* shape, float scale,
+                              int sliding_window, int num_sinks, void* out, float* lse,
+                              void* stream);
+
+/*
+ * Decode (one query per request, at position seq_lens[i] - 1) with the same
+ * mask: positions p in [seq_lens[i] - sliding_window, seq_lens[i]) and p <
+ * num_sinks, each read once and nothing between them (the table entries and
+ * contents there may be anything).  One launch and no workspace: a request's
+ * visible tokens are cut over the CTAs of a thread-block cluster, which merge
+ * their partial results in shared memory.
+ * q, out: [N, Hq, d] bf16; lse: [N, Hq] fp32, nullable.  seq_lens[i] <= 0:
+ * out = 0, lse = -inf.  sliding_window >= 1, num_sinks >= 0.
+ * Supported: head_size in {64, 128}, Hq / Hkv <= 16.  q 4-byte, kv_cache
+ * 16-byte, out 2-byte aligned.
+ */
+pa_status pa_decode_window(const void* q, const void* kv_cache, const int32_t* block_table,
+                           const int32_t* seq_lens, const pa_shape* shape, float scale,
+                           int sliding_window, int num_sinks, void* out, float* lse, void* stream);
+
+/* The same over an fp8 pool (entries and operand types as for
+ * pa_decode_splitkv_fp8). */
+pa_status pa_decode_window_fp8(const void* q, const void* kv_cache, const int32_t* block_table,
+                               const int32_t* seq_lens, const pa_shape* shape, float scale,
+                               float k_scale, float v_scale, int sliding_window, int num_sinks,
+                               void* out, float* lse, void* stream);
 
 /* Size of the fixed device array pa_decode_noalloc keeps its split partials in. */
 #define PA_NOALLOC_WORKSPACE_BYTES (16u * 1024u * 1024u)

@@ -269,6 +269,27 @@ pa_status pa_varlen_fwd_window(const void* q, const void* kv_cache, const int32_
       static_cast<cudaStream_t>(stream)));
 }
 
+pa_status pa_varlen_fwd_sinks(const void* q, const void* kv_cache, const int32_t* block_table,
+                              const int32_t* query_start_loc, const int32_t* seq_lens,
+                              int total_q, int max_query_len, const pa_shape* shape, float scale,
+                              int sliding_window, int num_sinks, void* out, float* lse,
+                              void* stream) {
+  if (!shape_ok(shape) || total_q < 0 || max_query_len < 0 || sliding_window < 1 || num_sinks < 0)
+    return PA_ERR_INVALID;
+  if (shape->head_size != 64 && shape->head_size != 128) return PA_ERR_UNSUPPORTED;
+  if (total_q == 0 || shape->num_seqs == 0 || max_query_len == 0) return PA_OK;
+  if (q == nullptr || kv_cache == nullptr || block_table == nullptr ||
+      query_start_loc == nullptr || seq_lens == nullptr || out == nullptr)
+    return PA_ERR_INVALID;
+  if (!aligned(q, 16) || !aligned(kv_cache, 16) || !aligned(out, 16) || !aligned(lse, 4) ||
+      !aligned(block_table, 4) || !aligned(query_start_loc, 4) || !aligned(seq_lens, 4))
+    return PA_ERR_INVALID;
+  pa::VarlenLaunch L = varlen_launch(q, kv_cache, block_table, query_start_loc, seq_lens,
+                                     max_query_len, shape, scale, 1, sliding_window, out, lse);
+  L.sinks = num_sinks;
+  return from_cuda(pa::launch_varlen_tc(L, static_cast<cudaStream_t>(stream)));
+}
+
 int pa_cascade_prefix_splits(int total_q, int num_q_heads, int num_kv_heads,
                              int prefix_tokens, int sm_count) {
   if (total_q <= 0 || num_q_heads <= 0 || num_kv_heads <= 0 || prefix_tokens <= 0) return 1;
@@ -486,6 +507,179 @@ pa_status pa_decode_splitkv_fp8(const void* q, const void* kv_cache, const int32
       shape->max_blocks_per_seq, scale, k_scale, v_scale, num_splits,
       static_cast<int>(pa::split_chunk(max_seq_len, num_splits, shape->block_size)), workspace,
       device_error_ptr(), static_cast<cudaStream_t>(stream)));
+}
+
+static pa_status decode_window(const void* q, const void* kv_cache, const int32_t* block_table,
+                               const int32_t* seq_lens, const pa_shape* shape, float scale,
+                               bool fp8, float k_scale, float v_scale, int sliding_window,
+                               int num_sinks, void* out, float* lse, void* stream) {
+  if (!shape_ok(shape) || sliding_window < 1 || num_sinks < 0) return PA_ERR_INVALID;
+  if (!scale_ok(k_scale) || !scale_ok(v_scale)) return PA_ERR_INVALID;
+  if (shape->head_size != 64 && shape->head_size != 128) return PA_ERR_UNSUPPORTED;
+  if (shape->num_q_heads / shape->num_kv_heads > 16) return PA_ERR_UNSUPPORTED;
+  if (shape->num_seqs == 0) return PA_OK;
+  if (q == nullptr || kv_cache == nullptr || block_table == nullptr || seq_lens == nullptr ||
+      out == nullptr)
+    return PA_ERR_INVALID;
+  if (!aligned(q, 4) || !aligned(kv_cache, 16) || !aligned(out, 2) || !aligned(lse, 4) ||
+      !aligned(block_table, 4) || !aligned(seq_lens, 4))
+    return PA_ERR_INVALID;
+  pa::DecodeWindowLaunch n{};
+  n.q = q;
+  n.cache = kv_cache;
+  n.block_table = block_table;
+  n.seq_lens = seq_lens;
+  n.N = shape->num_seqs;
+  n.Hq = shape->num_q_heads;
+  n.Hkv = shape->num_kv_heads;
+  n.d = shape->head_size;
+  n.bs = shape->block_size;
+  n.num_blocks = shape->num_blocks;
+  n.max_blocks = shape->max_blocks_per_seq;
+  n.window = sliding_window;
+  n.sinks = num_sinks;
+  n.scale = scale;
+  n.k_scale = k_scale;
+  n.v_scale = v_scale;
+  n.fp8 = fp8;
+  n.out = out;
+  n.lse = lse;
+  n.err = device_error_ptr();
+  n.sm_count = pa_device_sm_count();
+  if (n.sm_count <= 0) return PA_ERR_CUDA;
+  return from_cuda(pa::launch_decode_window(n, static_cast<cudaStream_t>(stream)));
+}
+
+pa_status pa_decode_window(const void* q, const void* kv_cache, const int32_t* block_table,
+                           const int32_t* seq_lens, const pa_shape* shape, float scale,
+                           int sliding_window, int num_sinks, void* out, float* lse,
+                           void* stream) {
+  return decode_window(q, kv_cache, block_table, seq_lens, shape, scale, false, 1.f, 1.f,
+                       sliding_window, num_sinks, out, lse, stream);
+}
+
+pa_status pa_decode_window_fp8(const void* q, const void* kv_cache, const int32_t* block_table,
+                               const int32_t* seq_lens, const pa_shape* shape, float scale,
+                               float k_scale, float v_scale, int sliding_window, int num_sinks,
+                               void* out, float* lse, void* stream) {
+  return decode_window(q, kv_cache, block_table, seq_lens, shape, scale, true, k_scale, v_scale,
+                       sliding_window, num_sinks, out, lse, stream);
+}
+
+pa_status pa_plan_step(const int32_t* context_lens, const int32_t* query_lens,
+                       const int32_t* free_blocks, const int32_t* free_start, int num_free,
+                       int num_seqs, int max_blocks_per_seq, int block_size, int num_blocks,
+                       int max_tokens, int32_t* block_table, int32_t* query_start_loc,
+                       int32_t* seq_lens, int32_t* positions, int64_t* slot_mapping,
+                       int32_t* totals, void* stream) {
+  if (num_free < 0 || num_seqs < 0 || num_seqs > kMaxGridYZ || max_blocks_per_seq <= 0 ||
+      block_size <= 0 || block_size % 16 != 0 || num_blocks <= 0 || max_tokens < 0)
+    return PA_ERR_INVALID;
+  if (query_start_loc == nullptr || totals == nullptr ||
+      (num_seqs > 0 && (context_lens == nullptr || query_lens == nullptr ||
+                        block_table == nullptr || seq_lens == nullptr)) ||
+      (num_free > 0 && free_blocks == nullptr) ||
+      (max_tokens > 0 && (positions == nullptr || slot_mapping == nullptr)))
+    return PA_ERR_INVALID;
+  if (!aligned(context_lens, 4) || !aligned(query_lens, 4) || !aligned(free_blocks, 4) ||
+      !aligned(free_start, 4) || !aligned(block_table, 4) || !aligned(query_start_loc, 4) ||
+      !aligned(seq_lens, 4) || !aligned(positions, 4) || !aligned(slot_mapping, 8) ||
+      !aligned(totals, 4))
+    return PA_ERR_INVALID;
+  return from_cuda(pa::launch_plan_step(
+      context_lens, query_lens, free_blocks, free_start, num_free, num_seqs, max_blocks_per_seq,
+      block_size, num_blocks, max_tokens, block_table, query_start_loc, seq_lens, positions,
+      slot_mapping, totals, device_error_ptr(), static_cast<cudaStream_t>(stream)));
+}
+
+static pa_status norm_rope(const void* q, const void* key, const void* value, int64_t q_stride,
+                           int64_t key_stride, int64_t value_stride, const void* q_weight,
+                           const void* k_weight, float eps, const float* cos_sin,
+                           int max_position, int rotary_dim, int interleaved,
+                           const int32_t* positions, void* kv_cache, const int64_t* slot_mapping,
+                           int num_tokens, const pa_shape* shape, bool fp8, float k_scale,
+                           float v_scale, void* q_out, void* stream) {
+  if (shape == nullptr || num_tokens < 0 || shape->num_q_heads <= 0 || shape->num_kv_heads <= 0 ||
+      shape->num_q_heads > kMaxGridYZ || shape->num_kv_heads > kMaxGridYZ ||
+      shape->head_size <= 0 || shape->block_size <= 0 || shape->block_size % 16 != 0 ||
+      shape->num_blocks <= 0 || rotary_dim < 0 || rotary_dim > shape->head_size ||
+      !(eps >= 0.f && eps <= 3.4028234663852886e38f))
+    return PA_ERR_INVALID;
+  if (!scale_ok(k_scale) || !scale_ok(v_scale)) return PA_ERR_INVALID;
+  if ((shape->head_size != 64 && shape->head_size != 128) || rotary_dim % 16 != 0)
+    return PA_ERR_UNSUPPORTED;
+  const int64_t qw = static_cast<int64_t>(shape->num_q_heads) * shape->head_size;
+  const int64_t kw = static_cast<int64_t>(shape->num_kv_heads) * shape->head_size;
+  if (q_stride < qw || key_stride < kw || value_stride < kw || q_stride % 8 != 0 ||
+      key_stride % 8 != 0 || value_stride % 8 != 0)
+    return PA_ERR_INVALID;
+  if (rotary_dim > 0 && max_position <= 0) return PA_ERR_INVALID;
+  if (num_tokens == 0) return PA_OK;
+  if (q == nullptr || key == nullptr || value == nullptr || kv_cache == nullptr ||
+      slot_mapping == nullptr || q_out == nullptr || (q_weight == nullptr) != (k_weight == nullptr) ||
+      (rotary_dim > 0 && (cos_sin == nullptr || positions == nullptr)))
+    return PA_ERR_INVALID;
+  if (!aligned(q, 16) || !aligned(key, 16) || !aligned(value, 16) || !aligned(q_weight, 16) ||
+      !aligned(k_weight, 16) || !aligned(cos_sin, 16) || !aligned(kv_cache, 16) ||
+      !aligned(q_out, 16) || !aligned(positions, 4) || !aligned(slot_mapping, 8))
+    return PA_ERR_INVALID;
+  if (q_out == q && q_stride != qw) return PA_ERR_INVALID;
+  pa::NormRopeLaunch n{};
+  n.q = q;
+  n.key = key;
+  n.value = value;
+  n.q_stride = q_stride;
+  n.key_stride = key_stride;
+  n.value_stride = value_stride;
+  n.q_weight = q_weight;
+  n.k_weight = k_weight;
+  n.eps = eps;
+  n.cos_sin = cos_sin;
+  n.max_position = max_position;
+  n.rotary_dim = rotary_dim;
+  n.interleaved = interleaved ? 1 : 0;
+  n.positions = positions;
+  n.cache = kv_cache;
+  n.slot_mapping = slot_mapping;
+  n.num_tokens = num_tokens;
+  n.Hq = shape->num_q_heads;
+  n.Hkv = shape->num_kv_heads;
+  n.d = shape->head_size;
+  n.bs = shape->block_size;
+  n.num_blocks = shape->num_blocks;
+  n.fp8 = fp8;
+  n.k_scale = k_scale;
+  n.v_scale = v_scale;
+  n.q_out = q_out;
+  n.err = device_error_ptr();
+  n.sm_count = pa_device_sm_count();
+  if (n.sm_count <= 0) return PA_ERR_CUDA;
+  return from_cuda(pa::launch_norm_rope(n, static_cast<cudaStream_t>(stream)));
+}
+
+pa_status pa_qk_norm_rope_cache(const void* q, const void* key, const void* value,
+                                int64_t q_stride, int64_t key_stride, int64_t value_stride,
+                                const void* q_weight, const void* k_weight, float eps,
+                                const float* cos_sin, int max_position, int rotary_dim,
+                                int interleaved, const int32_t* positions, void* kv_cache,
+                                const int64_t* slot_mapping, int num_tokens,
+                                const pa_shape* shape, void* q_out, void* stream) {
+  return norm_rope(q, key, value, q_stride, key_stride, value_stride, q_weight, k_weight, eps,
+                   cos_sin, max_position, rotary_dim, interleaved, positions, kv_cache,
+                   slot_mapping, num_tokens, shape, false, 1.f, 1.f, q_out, stream);
+}
+
+pa_status pa_qk_norm_rope_cache_fp8(const void* q, const void* key, const void* value,
+                                    int64_t q_stride, int64_t key_stride, int64_t value_stride,
+                                    const void* q_weight, const void* k_weight, float eps,
+                                    const float* cos_sin, int max_position, int rotary_dim,
+                                    int interleaved, const int32_t* positions, void* kv_cache,
+                                    const int64_t* slot_mapping, int num_tokens,
+                                    const pa_shape* shape, float k_scale, float v_scale,
+                                    void* q_out, void* stream) {
+  return norm_rope(q, key, value, q_stride, key_stride, value_stride, q_weight, k_weight, eps,
+                   cos_sin, max_position, rotary_dim, interleaved, positions, kv_cache,
+                   slot_mapping, num_tokens, shape, true, k_scale, v_scale, q_out, stream);
 }
 
 pa_status pa_lse_merge(const float* workspace, int num_seqs, int num_q_heads, int num_splits,

@@ -96,8 +96,60 @@ struct VarlenLaunch {
   const void* mla_k = nullptr;
   const void* mla_v = nullptr;
   int mla_s_max = 0;
+  // >= 0: a sliding window (`window`, causal) whose first `sinks` positions
+  // stay visible, and none of the split, offset or partial-output fields.
+  int sinks = -1;
 };
 cudaError_t launch_varlen_tc(const VarlenLaunch& L, cudaStream_t stream);
+
+// Decode with a sliding window and first tokens that stay visible, bf16 or
+// e4m3 pool, in one launch.
+struct DecodeWindowLaunch {
+  const void* q;
+  const void* cache;
+  const int32_t* block_table;
+  const int32_t* seq_lens;
+  int N, Hq, Hkv, d, bs, num_blocks, max_blocks, window, sinks;
+  float scale, k_scale, v_scale;   // k_scale, v_scale 1 for bf16
+  bool fp8;
+  void* out;
+  float* lse;
+  int* err;
+  int sm_count;
+};
+cudaError_t launch_decode_window(const DecodeWindowLaunch& n, cudaStream_t stream);
+
+// Step plan: query_start_loc, seq_lens, positions, slot_mapping and new table
+// entries from the requests' lengths.
+cudaError_t launch_plan_step(const int32_t* context_lens, const int32_t* query_lens,
+                             const int32_t* free_blocks, const int32_t* free_start, int num_free,
+                             int num_seqs, int max_blocks, int bs, int num_blocks, int max_tokens,
+                             int32_t* block_table, int32_t* query_start_loc, int32_t* seq_lens,
+                             int32_t* positions, int64_t* slot_mapping, int32_t* totals, int* err,
+                             cudaStream_t stream);
+
+// Head norms, rotation and cache write in one pass (bf16 or e4m3 pool).
+struct NormRopeLaunch {
+  const void* q;
+  const void* key;
+  const void* value;
+  int64_t q_stride, key_stride, value_stride;   // elements from token to token
+  const void* q_weight;                         // both or neither
+  const void* k_weight;
+  float eps;
+  const float* cos_sin;
+  int max_position, rotary_dim, interleaved;
+  const int32_t* positions;
+  void* cache;
+  const int64_t* slot_mapping;
+  int num_tokens, Hq, Hkv, d, bs, num_blocks;
+  bool fp8;
+  float k_scale, v_scale;
+  void* q_out;
+  int* err;
+  int sm_count;
+};
+cudaError_t launch_norm_rope(const NormRopeLaunch& n, cudaStream_t stream);
 
 // MLA stage 1 on tcgen05 tensor cores + merge.
 cudaError_t launch_mla_tc(const void* q, const void* cache, const int32_t* block_table,
