@@ -10,14 +10,19 @@
 // off by 2^-25 * 131072 radians at far positions.
 //
 // Bound by HBM: every input is read once and every output written once.  A
-// group of d/8 lanes holds one head row, 16 bytes a lane, so that a row is one
-// coalesced load and one store; the sum of squares is a shuffle reduction
-// inside the group.  The halves of a pair k, k + r/2 sit r/16 lanes apart:
-// the raw bf16 words are exchanged (4 shuffles instead of 8 for the fp32
-// values) and both lanes scale them alike.  A lane's place in its row is the
-// same for every row it takes, so weights, cosines and sines stay in
-// registers over a token's rows, and the loads of up to kRows rows are in
-// flight together with the position -> table chain.
+// warp takes a token: its rows pass in steps of 32 / (d / 8) rows, d/8 lanes to
+// a row, eight values to a lane.  A lane holds both halves of its pairs (values
+// 4l.. and r/2 + 4l.., two 8-byte loads), so the rotation needs no exchange
+// between lanes and the sum of squares is the only reduction; weight times
+// cosine and sine is formed once per token and kept in registers over its
+// rows; arithmetic is on packed pairs of fp32.  18432 tokens of 32 / 8 heads,
+// d 128 (457 MB): 72.5 us, 6.3 TB/s, 0.93 of the copy rate.  Before: a CTA per
+// token, 16-byte loads and the other half by shuffles 207 us, a warp per token
+// 131 us (instructions); one loop over all kinds of rows with loads a round
+// ahead 98 us (spilled registers).  An e4m3 pool adds an IEEE division per
+// value: 8191 tokens of 64 / 8 heads, d 64 (160 MB): 35.0 us.
+#include <type_traits>
+
 #include "pa_common.cuh"
 #include "pa_launch.h"
 
@@ -41,184 +46,244 @@ struct NormRopeArgs {
   int64_t num_slots;
   float eps, k_scale, v_scale;
   int max_position, rot, interleaved, Hq, Hkv, bs, bs_log2;
+  unsigned num_tokens, shares;
+  int per;   // warps per token above, steps per warp here
 };
 
-__device__ __forceinline__ void unpack8(uint4 v, float (&f)[8]) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    f[2 * k] = __uint_as_float(w[k] << 16);
-    f[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
-  }
+// Pairs of fp32 in one 64-bit register (fma.rn.f32x2 and the like: each half
+// rounded as its scalar counterpart).
+struct F2 {
+  uint64_t v;
+};
+__device__ __forceinline__ F2 f2(float lo, float hi) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 split(F2 a) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
+  return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+__device__ __forceinline__ F2 swap2(F2 a) {
+  const float2 f = split(a);
+  return f2(f.y, f.x);
+}
+// Two bf16 (low half first) as fp32.
+__device__ __forceinline__ F2 widen(uint32_t w) {
+  return f2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+__device__ __forceinline__ uint32_t narrow(F2 a) {
+  const float2 f = split(a);
+  return pack_bf16(f.x, f.y);
 }
 
-__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
-  return make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]),
-                    pack_bf16(f[6], f[7]));
+// Four values as e4m3 codes of value / scale (IEEE quotient, saturating).
+__device__ __forceinline__ uint32_t quant4(F2 a, F2 b, float scale) {
+  const float2 x = split(a), y = split(b);
+  const __nv_fp8x2_storage_t lo = __nv_cvt_float2_to_fp8x2(
+      make_float2(__fdiv_rn(x.x, scale), __fdiv_rn(x.y, scale)), __NV_SATFINITE, __NV_E4M3);
+  const __nv_fp8x2_storage_t hi = __nv_cvt_float2_to_fp8x2(
+      make_float2(__fdiv_rn(y.x, scale), __fdiv_rn(y.y, scale)), __NV_SATFINITE, __NV_E4M3);
+  return static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
 }
 
-// Eight values as e4m3 codes of value / scale (IEEE quotient, saturating).
-__device__ __forceinline__ uint2 quant8(const float (&f)[8], float scale) {
-  uint32_t r[2] = {0, 0};
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const float2 x = make_float2(__fdiv_rn(f[2 * k], scale), __fdiv_rn(f[2 * k + 1], scale));
-    const __nv_fp8x2_storage_t c = __nv_cvt_float2_to_fp8x2(x, __NV_SATFINITE, __NV_E4M3);
-    r[k >> 1] |= static_cast<uint32_t>(c) << (16 * (k & 1));
-  }
-  return make_uint2(r[0], r[1]);
-}
+constexpr int kWarps = 4;    // units per CTA
+constexpr int kFlight = 4;   // steps whose loads are in flight per warp
 
-constexpr int kThreads = 256;
-constexpr int kRows = 3;   // rows of a token in flight per group
+enum Kind { kQuery, kKey, kValue };
 
 template <int D, bool FP8>
-__global__ void __launch_bounds__(kThreads) norm_rope_kernel(const NormRopeArgs a) {
+__global__ void __launch_bounds__(kWarps * 32, 8) norm_rope_kernel(const NormRopeArgs a) {
   constexpr int L = D / 8;              // lanes per row
-  constexpr int G = kThreads / L;       // rows in flight per CTA and step
+  constexpr int G = 32 / L;             // rows per step
   pdl_wait();
   pdl_trigger();
-  const int64_t t = blockIdx.x;
-  const int l = threadIdx.x % L, g = threadIdx.x / L;
-  const int rows = a.Hq + 2 * a.Hkv;
-  const int step = G * gridDim.y;
-  const int first = blockIdx.y * G + g;
-
-  const uint4* qsrc = reinterpret_cast<const uint4*>(a.q + t * a.q_stride) + l;
-  const uint4* ksrc = reinterpret_cast<const uint4*>(a.k + t * a.k_stride) + l;
-  const uint4* vsrc = reinterpret_cast<const uint4*>(a.v + t * a.v_stride) + l;
-  auto load = [&](int r) -> uint4 {
-    if (r < a.Hq) return __ldcs(qsrc + r * L);
-    if (r < a.Hq + a.Hkv) return __ldcs(ksrc + (r - a.Hq) * L);
-    if (r < rows) return __ldcs(vsrc + (r - a.Hq - a.Hkv) * L);
-    return make_uint4(0, 0, 0, 0);
-  };
-  uint4 raw[kRows];
-#pragma unroll
-  for (int u = 0; u < kRows; ++u) raw[u] = load(first + u * step);
-
-  // Where this token's keys and values go (< 0: nowhere).
-  int64_t slot = a.slots[t];
-  if (slot >= a.num_slots) {
-    if (threadIdx.x == 0 && blockIdx.y == 0) record_error(a.err, PA_DEVERR_SLOT);
-    slot = -1;
-  }
-  // This lane's weights, its rotation and its pair's lane.  c, s: cos and
-  // signed sin for the eight values, y_own c + y_pair s.
-  const bool norm = a.q_weight != nullptr;
-  uint4 wq = make_uint4(0, 0, 0, 0), wk = wq, wqp = wq, wkp = wq;
-  float c[8], s[8];
+  const int lane = threadIdx.x & 31, l = lane % L, g = lane / L;
+  // Unit = (token, share of its steps); steps run over the queries, then the
+  // keys, then the values, G rows each (the last of a kind may be partial).
+  const unsigned unit = blockIdx.x * kWarps + (threadIdx.x >> 5);
+  const unsigned t = unit / a.shares;
+  if (t >= a.num_tokens) return;   // whole warps
+  const int share = static_cast<int>(unit - t * a.shares);
+  // The lane's two chunks of four values: the halves of four pairs where they
+  // are rotated, neighbours otherwise.
   const int half = a.rot / 2;
   const bool turned = 8 * l < a.rot;
-  int pair = l;
+  const bool apart = !a.interleaved && turned;
+  const int c0 = apart ? l : 2 * l, c1 = apart ? l + half / 4 : 2 * l + 1;
+
+  // Where this token's keys and values go (null: nowhere), and its angles.
+  const int64_t slot = a.slots[t];
+  const float* angles = nullptr;
   if (a.rot > 0) {
     const int pos = a.positions[t];
     if (pos < 0 || pos >= a.max_position) {
-      if (threadIdx.x == 0 && blockIdx.y == 0) record_error(a.err, PA_DEVERR_POSITION);
+      if (lane == 0 && share == 0) record_error(a.err, PA_DEVERR_POSITION);
       return;
     }
-    if (turned) {
-      const float* row = a.cos_sin + static_cast<int64_t>(pos) * a.rot;
-      if (a.interleaved) {
-        // Pairs 4l .. 4l + 3 inside the lane: (c, -s), (c, s).
-        const float4 cc = __ldg(reinterpret_cast<const float4*>(row + 4 * l));
-        const float4 ss = __ldg(reinterpret_cast<const float4*>(row + half + 4 * l));
-        const float c4[4] = {cc.x, cc.y, cc.z, cc.w}, s4[4] = {ss.x, ss.y, ss.z, ss.w};
+    angles = a.cos_sin + static_cast<int64_t>(pos) * a.rot;
+  }
+  const bool keep = slot >= 0 && slot < a.num_slots;
+  if (slot >= a.num_slots && lane == 0 && share == 0) record_error(a.err, PA_DEVERR_SLOT);
+  constexpr int kEl = FP8 ? 1 : 2;
+  uint8_t* cell = static_cast<uint8_t*>(a.cache);   // the token's keys in its block
+  if (keep) {
+    const int64_t blk = a.bs_log2 >= 0 ? slot >> a.bs_log2 : slot / a.bs;
+    const int off = static_cast<int>(slot - blk * a.bs);
+    cell += (blk * 2 * a.bs + off) * a.Hkv * (D * kEl);
+  }
+  const bool norm = a.q_weight != nullptr;
+
+  // All rows of one kind that lie in this unit's share.
+  int s0 = share * a.per, s1 = s0 + a.per;   // steps left, counted from the kind's first
+  auto rows = [&](auto kind_tag, const __nv_bfloat16* src, int H, const __nv_bfloat16* weight) {
+    constexpr Kind kind = decltype(kind_tag)::value;
+    const int steps = (H + G - 1) / G;
+    const int end = min(s1, steps);
+    // y = rstd (A own + B other): A = w cos, B = -+ w_other sin; [chunk][pair].
+    F2 A[2][2], B[2][2];
+    if (kind != kValue && s0 < end) {
+      F2 w[2][2];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          c[2 * k] = c[2 * k + 1] = c4[k];
-          s[2 * k] = -s4[k];
-          s[2 * k + 1] = s4[k];
+      for (int k = 0; k < 2; ++k) {
+        w[k][0] = w[k][1] = f2(1.f, 1.f);
+        if (norm) {
+          const uint2 x = __ldg(reinterpret_cast<const uint2*>(weight + 4 * (k ? c1 : c0)));
+          w[k][0] = widen(x.x);
+          w[k][1] = widen(x.y);
         }
-      } else {
-        const bool low = 8 * l < half;
-        pair = low ? l + half / 8 : l - half / 8;
-        const int k0 = low ? 8 * l : 8 * l - half;
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const float4 cc = __ldg(reinterpret_cast<const float4*>(row + k0) + k);
-          const float4 ss = __ldg(reinterpret_cast<const float4*>(row + half + k0) + k);
-          c[4 * k] = cc.x, c[4 * k + 1] = cc.y, c[4 * k + 2] = cc.z, c[4 * k + 3] = cc.w;
-          s[4 * k] = ss.x, s[4 * k + 1] = ss.y, s[4 * k + 2] = ss.z, s[4 * k + 3] = ss.w;
-        }
-        if (low) {
+        for (int e = 0; e < 2; ++e) A[k][e] = w[k][e];
+      }
+      if (turned) {
+        const float4 c = __ldg(reinterpret_cast<const float4*>(angles + 4 * l));
+        const float4 s = __ldg(reinterpret_cast<const float4*>(angles + half + 4 * l));
+        if (apart) {
+          const F2 cc[2] = {f2(c.x, c.y), f2(c.z, c.w)};
+          const F2 sp[2] = {f2(s.x, s.y), f2(s.z, s.w)};
+          const F2 sn[2] = {f2(-s.x, -s.y), f2(-s.z, -s.w)};
 #pragma unroll
-          for (int k = 0; k < 8; ++k) s[k] = -s[k];
+          for (int e = 0; e < 2; ++e) {
+            B[0][e] = mul2(w[1][e], sn[e]);
+            B[1][e] = mul2(w[0][e], sp[e]);
+            A[0][e] = mul2(w[0][e], cc[e]);
+            A[1][e] = mul2(w[1][e], cc[e]);
+          }
+        } else {   // pairs 4l .. 4l + 3, inside the lane
+          const float c4[4] = {c.x, c.y, c.z, c.w}, s4[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              B[k][e] = mul2(swap2(w[k][e]), f2(-s4[2 * k + e], s4[2 * k + e]));
+              A[k][e] = mul2(w[k][e], f2(c4[2 * k + e], c4[2 * k + e]));
+            }
         }
       }
     }
-  }
-  if (norm) {
-    wq = __ldg(reinterpret_cast<const uint4*>(a.q_weight) + l);
-    wk = __ldg(reinterpret_cast<const uint4*>(a.k_weight) + l);
-    wqp = __ldg(reinterpret_cast<const uint4*>(a.q_weight) + pair);
-    wkp = __ldg(reinterpret_cast<const uint4*>(a.k_weight) + pair);
-  }
-  const int lane = threadIdx.x & 31;
-  const int src_lane = (lane & ~(L - 1)) | pair;
-  const int64_t blk = slot < 0 ? 0 : (a.bs_log2 >= 0 ? slot >> a.bs_log2 : slot / a.bs);
-  const int off = slot < 0 ? 0 : static_cast<int>(slot - blk * a.bs);
-
-  // Whole warps only: the groups of a warp differ in r by less than a warp's
-  // rows, and rows past the end take part in the shuffles with zeros.
-  for (int base = first; base - g < rows; base += kRows * step) {
+    uint8_t* dst = kind == kQuery
+                       ? reinterpret_cast<uint8_t*>(a.q_out + static_cast<int64_t>(t) * a.Hq * D)
+                       : cell + (kind == kValue ? static_cast<int64_t>(a.bs) * a.Hkv * (D * kEl) : 0);
+    for (int base = s0; base < end; base += kFlight) {
+      uint2 raw[kFlight][2];
 #pragma unroll
-    for (int u = 0; u < kRows; ++u) {
-      const int r = base + u * step;
-      if (r - g >= rows) break;   // uniform over the CTA
-      const uint4 x = raw[u];
-      raw[u] = load(r + kRows * step);
-      const bool is_q = r < a.Hq, is_v = r >= a.Hq + a.Hkv;
-      float y[8];
-      unpack8(x, y);
-      float ss = 0.f;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) ss = fmaf(y[k], y[k], ss);
-#pragma unroll
-      for (int o = L / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-      uint4 xp;
-      xp.x = __shfl_sync(0xffffffffu, x.x, src_lane);
-      xp.y = __shfl_sync(0xffffffffu, x.y, src_lane);
-      xp.z = __shfl_sync(0xffffffffu, x.z, src_lane);
-      xp.w = __shfl_sync(0xffffffffu, x.w, src_lane);
-      if (!is_v) {
-        const float rstd = norm ? rsqrtf(ss * (1.f / D) + a.eps) : 1.f;
-        if (norm) {
-          float w[8];
-          unpack8(is_q ? wq : wk, w);
-#pragma unroll
-          for (int k = 0; k < 8; ++k) y[k] = y[k] * rstd * w[k];
+      for (int u = 0; u < kFlight; ++u) {
+        const int r = (base + u) * G + g;
+        raw[u][0] = raw[u][1] = make_uint2(0, 0);
+        if (base + u < end && r < H) {
+          const uint2* p = reinterpret_cast<const uint2*>(src + r * D);
+          raw[u][0] = __ldcs(p + c0);
+          raw[u][1] = __ldcs(p + c1);
         }
-        if (turned) {
-          float z[8];
-          if (a.interleaved) {
+      }
 #pragma unroll
-            for (int k = 0; k < 8; ++k) z[k] = y[k ^ 1];
-          } else {
-            unpack8(xp, z);
-            if (norm) {
-              float w[8];
-              unpack8(is_q ? wqp : wkp, w);
+      for (int u = 0; u < kFlight; ++u) {
+        if (base + u >= end) break;
+        const int r = (base + u) * G + g;
+        const bool store = r < H && (kind == kQuery || keep);
+        const uint2 x0 = raw[u][0], x1 = raw[u][1];
+        if (kind == kValue && !FP8) {   // a bit copy
+          if (store) {
+            uint2* p = reinterpret_cast<uint2*>(dst + r * (D * 2));
+            p[c0] = x0;
+            p[c1] = x1;
+          }
+          continue;
+        }
+        F2 y[2][2] = {{widen(x0.x), widen(x0.y)}, {widen(x1.x), widen(x1.y)}};
+        if (kind != kValue) {
+          float rstd = 1.f;
+          if (norm) {
+            F2 s2 = mul2(y[0][0], y[0][0]);
+            s2 = fma2(y[0][1], y[0][1], s2);
+            s2 = fma2(y[1][0], y[1][0], s2);
+            s2 = fma2(y[1][1], y[1][1], s2);
+            const float2 f = split(s2);
+            float ss = f.x + f.y;
 #pragma unroll
-              for (int k = 0; k < 8; ++k) z[k] = z[k] * rstd * w[k];
+            for (int o = L / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+            rstd = rsqrtf(ss * (1.f / D) + a.eps);
+          }
+          F2 z[2][2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            z[0][e] = y[0][e];
+            z[1][e] = y[1][e];
+            y[0][e] = mul2(y[0][e], A[0][e]);
+            y[1][e] = mul2(y[1][e], A[1][e]);
+          }
+          if (apart) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              y[0][e] = fma2(z[1][e], B[0][e], y[0][e]);
+              y[1][e] = fma2(z[0][e], B[1][e], y[1][e]);
+            }
+          } else if (turned) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              y[0][e] = fma2(swap2(z[0][e]), B[0][e], y[0][e]);
+              y[1][e] = fma2(swap2(z[1][e]), B[1][e], y[1][e]);
             }
           }
+          if (norm) {
+            const F2 r2 = f2(rstd, rstd);
 #pragma unroll
-          for (int k = 0; k < 8; ++k) y[k] = fmaf(y[k], c[k], z[k] * s[k]);
+            for (int e = 0; e < 2; ++e) {
+              y[0][e] = mul2(y[0][e], r2);
+              y[1][e] = mul2(y[1][e], r2);
+            }
+          }
+        }
+        if (!store) continue;
+        if (kind != kQuery && FP8) {
+          const float scale = kind == kValue ? a.v_scale : a.k_scale;
+          uint32_t* p = reinterpret_cast<uint32_t*>(dst + r * D);
+          p[c0] = quant4(y[0][0], y[0][1], scale);
+          p[c1] = quant4(y[1][0], y[1][1], scale);
+        } else {
+          uint2* p = reinterpret_cast<uint2*>(dst + r * (D * 2));
+          p[c0] = make_uint2(narrow(y[0][0]), narrow(y[0][1]));
+          p[c1] = make_uint2(narrow(y[1][0]), narrow(y[1][1]));
         }
       }
-      if (is_q) {
-        reinterpret_cast<uint4*>(a.q_out)[(t * a.Hq + r) * L + l] = pack8(y);
-      } else if (slot >= 0 && r < rows) {
-        const int h = is_v ? r - a.Hq - a.Hkv : r - a.Hq;
-        const int64_t row = ((blk * 2 + (is_v ? 1 : 0)) * a.bs + off) * a.Hkv + h;
-        if (FP8)
-          static_cast<uint2*>(a.cache)[row * L + l] = quant8(y, is_v ? a.v_scale : a.k_scale);
-        else
-          static_cast<uint4*>(a.cache)[row * L + l] = is_v ? x : pack8(y);
-      }
     }
-  }
+    s0 = max(s0 - steps, 0);
+    s1 = max(s1 - steps, 0);
+  };
+  rows(std::integral_constant<Kind, kQuery>(), a.q + t * a.q_stride, a.Hq, a.q_weight);
+  rows(std::integral_constant<Kind, kKey>(), a.k + t * a.k_stride, a.Hkv, a.k_weight);
+  rows(std::integral_constant<Kind, kValue>(), a.v + t * a.v_stride, a.Hkv, nullptr);
 }
 
 }  // namespace
@@ -250,18 +315,23 @@ cudaError_t launch_norm_rope(const NormRopeLaunch& n, cudaStream_t stream) {
   a.Hkv = n.Hkv;
   a.bs = n.bs;
   a.bs_log2 = block_size_log2(n.bs);
-  // One CTA per token; a batch of few tokens spreads each token's rows over
-  // several, up to two CTAs per SM.
-  const int groups = kThreads / (n.d / 8);
-  const int by_rows = (n.Hq + 2 * n.Hkv + groups - 1) / groups;
-  int split = (2 * n.sm_count + n.num_tokens - 1) / n.num_tokens;
-  if (split > by_rows) split = by_rows;
-  const dim3 grid(n.num_tokens, split);
+  // One warp per token; a batch of few tokens deals each token's steps out
+  // over several warps, until about 16 warps per SM have work.
+  const int rows = 32 / (n.d / 8);
+  const int steps = (n.Hq + rows - 1) / rows + 2 * ((n.Hkv + rows - 1) / rows);
+  long long shares = (16LL * n.sm_count + n.num_tokens - 1) / n.num_tokens;
+  if (shares > steps) shares = steps;
+  a.per = static_cast<int>((steps + shares - 1) / shares);
+  a.shares = (steps + a.per - 1) / a.per;
+  a.num_tokens = n.num_tokens;
+  // shares > 1 only below 16 tokens per SM: the units fit 32 bits.
+  const unsigned units = static_cast<unsigned>(n.num_tokens) * a.shares;
+  const dim3 grid((units + kWarps - 1) / kWarps), block(kWarps * 32);
   if (n.d == 128)
-    return n.fp8 ? launch_pdl(norm_rope_kernel<128, true>, grid, dim3(kThreads), 0, stream, a)
-                 : launch_pdl(norm_rope_kernel<128, false>, grid, dim3(kThreads), 0, stream, a);
-  return n.fp8 ? launch_pdl(norm_rope_kernel<64, true>, grid, dim3(kThreads), 0, stream, a)
-               : launch_pdl(norm_rope_kernel<64, false>, grid, dim3(kThreads), 0, stream, a);
+    return n.fp8 ? launch_pdl(norm_rope_kernel<128, true>, grid, block, 0, stream, a)
+                 : launch_pdl(norm_rope_kernel<128, false>, grid, block, 0, stream, a);
+  return n.fp8 ? launch_pdl(norm_rope_kernel<64, true>, grid, block, 0, stream, a)
+               : launch_pdl(norm_rope_kernel<64, false>, grid, block, 0, stream, a);
 }
 
 }  // namespace pa
