@@ -41,15 +41,16 @@ __device__ __forceinline__ void e4m3x4_to_f16(uint32_t w, uint32_t& lo, uint32_t
 // to bf16 for the PV product, and the output's divisor sums the rounded ones.
 template <int D>
 struct KvBf16 {
-  static constexpr int kElBytes = 2;
-  static constexpr int kRowBytes = D * 2;
-  static constexpr int kChunks = kRowBytes / 16;   // 16-byte chunks per token row
-  static constexpr int kTileBytes = 16 * kRowBytes;
+  static constexpr int kChunks = D / 8;          // 16-byte chunks per token row
+  static constexpr int kTileBytes = 16 * D * 2;  // 16 tokens of K or V
+  static constexpr int kGroups = D / 64;         // 128-byte column groups of a row
   static constexpr bool kRoundedSums = true;
   // Combine buffer row: = 4 mod 32 floats apart, no bank conflict.
   static constexpr int kOStride = D + 4;
+  // Byte offset of chunk c of token row r: [d / 64][16 tokens][128 B],
+  // 128-byte swizzled, as the TMA box of a tile lays it out.
   __device__ static __forceinline__ uint32_t at(int r, int c) {
-    return static_cast<uint32_t>(r * kRowBytes + ((c ^ (r & 7)) << 4));
+    return static_cast<uint32_t>((c >> 3) * 2048 + r * 128 + (((c ^ r) & 7) << 4));
   }
   __device__ static __forceinline__ void load_q(const __nv_bfloat16* row, int tid4, int kk,
                                                 uint32_t (&f)[2]) {
@@ -97,12 +98,12 @@ struct KvBf16 {
 // rows so that a lane's codes are d/8 contiguous ones.
 template <int D>
 struct KvE4m3 {
-  static constexpr int kElBytes = 1;
-  static constexpr int kRowBytes = D;
-  static constexpr int kChunks = kRowBytes / 16;
-  static constexpr int kTileBytes = 16 * kRowBytes;
+  static constexpr int kChunks = D / 16;
+  static constexpr int kTileBytes = 16 * D;
+  static constexpr int kGroups = 1;
   static constexpr bool kRoundedSums = false;
   static constexpr int kOStride = D == 128 ? 164 : 68;
+  // [16 tokens][d B], swizzled over 128 (d = 128) or 64 bytes.
   __device__ static __forceinline__ uint32_t at(int r, int c) {
     if constexpr (D == 128)
       return static_cast<uint32_t>(r * 128 + ((c ^ (r & 7)) << 4));
@@ -204,13 +205,14 @@ struct State {
   }
 };
 
-// Adds the sub-block whose K and V tiles lie at kb and vb in shared memory;
+// The softmax weights of a sub-block (as the PV product's operand pb) from its
+// K tile at kb in shared memory, with the state's maxima and sums moved on;
 // v0, v1: whether this lane's tokens gid and gid + 8 are visible (rows that
-// are not hold zeros).
+// are not hold zeros).  KV::values adds the sub-block's V tile afterwards.
 template <class KV, int D, int NT>
-__device__ __forceinline__ void add_sub_block(State<D, NT>& st, uint32_t kb, uint32_t vb, int lane,
-                                              bool v0, bool v1, float scale_log2,
-                                              const uint32_t (&qf)[NT][D / 16][2]) {
+__device__ __forceinline__ void weights(State<D, NT>& st, uint32_t kb, int lane, bool v0, bool v1,
+                                        float scale_log2, const uint32_t (&qf)[NT][D / 16][2],
+                                        uint32_t (&pb)[NT][2]) {
   constexpr float kRescale = 8.f;
   const int gid = lane >> 2, tid4 = lane & 3;
   // Even and odd k-steps in two chains of half the length.
@@ -224,7 +226,6 @@ __device__ __forceinline__ void add_sub_block(State<D, NT>& st, uint32_t kb, uin
   // head gid are in the lane of tid4' = gid / 2, half gid % 2.
   const int src_a = 8 * tid4 + (gid >> 1), src_b = src_a + 4;
   const uint32_t sel = (gid & 1) ? 0x7632u : 0x5410u;
-  uint32_t pb[NT][2];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     float p[4];
@@ -265,7 +266,6 @@ __device__ __forceinline__ void add_sub_block(State<D, NT>& st, uint32_t kb, uin
     pb[nt][0] = __byte_perm(xa, xb, sel);
     pb[nt][1] = __byte_perm(ya, yb, sel);
   }
-  KV::template values<NT>(vb, lane, pb, st.o);
 }
 
 }  // namespace dec

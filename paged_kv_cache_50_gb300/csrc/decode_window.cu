@@ -10,15 +10,23 @@
 // first ones, then those from lo rounded down to 16 (one run from position 0
 // where the two meet).  Nothing else is read.  One cluster of S CTAs serves
 // one (request, kv head): CTA r takes the r-th share of the list, its four
-// warps sub-blocks in turn, each warp with its own cp.async ring; the warps'
-// states are merged in shared memory and the CTAs' in distributed shared
-// memory, every CTA writing a share of the outputs.  A window bounds a
-// request's work, so unlike split-KV decode over a whole context S <= 16
-// shares are enough, and the second launch and its fp32 workspace (written
-// and read once) go.
+// warps sub-blocks in turn, each warp with its own ring of K and V tiles,
+// filled by TMA boxes of 16 token rows of a head (a box is one instruction of
+// one lane; the same ring filled by cp.async took 49.7 us instead of 42.5 on
+// the batch below, its address and mask arithmetic being what a warp spent its
+// time on).  The warps' states are merged in shared memory, the CTAs' in
+// distributed shared memory, every CTA writing a share of the outputs.  A
+// window bounds a request's work, so unlike split-KV decode over a whole
+// context S <= 16 shares are enough, and the second launch and its fp32
+// workspace (written and read once) go.
 //
 // Bound by HBM where the batch fills the GPU, else by latency (lengths ->
-// block ids -> K/V -> merge, one after the other).
+// block ids -> K/V -> merge, one after the other).  Measured (32 / 8 heads,
+// d 128): 64 requests, window 1024 over U[128, 4096] tokens, 242 MB: 42.5 us,
+// 5.7 TB/s; window 4096 over U[1024, 8192], 899 MB: 140.6 us, 6.4 TB/s; an e4m3
+// pool, 128 requests, window 4096, 911 MB: 163 us, 5.6 TB/s (instruction-bound:
+// 372 warp instructions per 16 tokens, 64 of them conversions); one request of
+// 64 / 8 heads, window 4096: 11.4 us.
 #include <algorithm>
 #include <climits>
 
@@ -32,7 +40,6 @@ namespace {
 
 struct WindowArgs {
   const __nv_bfloat16* q;
-  const uint8_t* cache;
   const int32_t* block_table;
   const int32_t* seq_lens;
   int max_blocks, Hq, Hkv, bs, bs_log2, num_blocks;
@@ -44,18 +51,26 @@ struct WindowArgs {
   int* err;
 };
 
-template <class KV, int D, int STAGES, int NT>
+// A warp's ring has R places; while one is worked on, the next R - 1 are on
+// their way.  Where a row is one column group, a place takes the K and V tiles
+// of a sub-block, by one 4 KB TMA box (2 KB boxes, one for K and one for V, took
+// twice as long on 64-wide bf16 rows: 87 us against 42 for 64 requests, window
+// 2048); else K and V take a place and a box each.
+template <class KV, int D, int R, int NT>
 struct WindowCfg {
   static constexpr int kWarps = 4;
   static constexpr int kThreads = kWarps * 32;
-  static constexpr int kStageBytes = 2 * KV::kTileBytes;   // K + V
-  static constexpr int kWarpBytes = STAGES * kStageBytes;
+  static constexpr bool kPair = KV::kGroups == 1;
+  static constexpr int kPlaceBytes = (kPair ? 2 : 1) * KV::kTileBytes;
+  static constexpr int kWarpBytes = R * kPlaceBytes;   // a multiple of the swizzle atom
   static constexpr int kPipeBytes = kWarps * kWarpBytes;
   static constexpr int kHeads = 8 * NT;
   // Combine buffer: O rows per warp, then max, sum and divisor per (warp,
   // head), then the CTA's max, sum and divisor per head.
   static constexpr int kCombineBytes = (kWarps * kHeads * (KV::kOStride + 3) + 3 * kHeads) * 4;
-  static constexpr int kSmemBytes = kPipeBytes > kCombineBytes ? kPipeBytes : kCombineBytes;
+  static constexpr int kDataBytes = kPipeBytes > kCombineBytes ? kPipeBytes : kCombineBytes;
+  static constexpr int kOffBar = (kDataBytes + 7) / 8 * 8;   // [warp][R] barriers
+  static constexpr int kSmemBytes = kOffBar + kWarps * R * 8 + 1024;   // + alignment slack
 };
 
 __device__ __forceinline__ float ld_remote(uint32_t addr) {
@@ -64,16 +79,29 @@ __device__ __forceinline__ float ld_remote(uint32_t addr) {
   return v;
 }
 
-template <class KV, int D, int STAGES, int NT>
-__global__ void __launch_bounds__(128) decode_window_kernel(const WindowArgs a) {
-  using C = WindowCfg<KV, D, STAGES, NT>;
+template <class KV, int D, int R, int NT, int MINB>
+__global__ void __launch_bounds__(128, MINB) decode_window_kernel(
+    const __grid_constant__ CUtensorMap map, const __grid_constant__ WindowArgs a) {
+  using C = WindowCfg<KV, D, R, NT>;
+  constexpr int kAhead = C::kPair ? R - 1 : (R + 1) / 2;   // block ids in hand
+
   constexpr int kK = D / 16;
-  extern __shared__ __align__(128) uint8_t smem[];
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* const smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const int S = gridDim.x, s = blockIdx.x, kvh = blockIdx.y, i = blockIdx.z;   // cluster = grid.x
   const int grp = a.Hq / a.Hkv;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int gid = lane >> 2, tid4 = lane & 3;
 
+  const uint32_t wbase = smem_u32(smem) + warp * C::kWarpBytes;
+  const uint32_t bars = smem_u32(smem) + C::kOffBar + warp * R * 8;
+  if (lane == 0) {
+    tc::tma_prefetch_desc(&map);
+#pragma unroll
+    for (int k = 0; k < R; ++k) tc::mbar_init(bars + 8 * k, 1);
+    tc::fence_barrier_init();
+  }
+  __syncwarp();   // each warp uses its own barriers only
   pdl_wait();
   const int seq = min(max(0, a.seq_lens[i]), INT_MAX - 64);   // sums below stay in range
   const int32_t* table = a.block_table + static_cast<int64_t>(i) * a.max_blocks;
@@ -95,9 +123,11 @@ __global__ void __launch_bounds__(128) decode_window_kernel(const WindowArgs a) 
   auto lookup = [&](int n) {
     return block_at(table, div_bs(token(n), a.bs, a.bs_log2), a.max_blocks);
   };
-  int first_blk[STAGES];
+  // Block ids of sub-blocks n .. n + kAhead (the copies of the last one go
+  // out while sub-block n is worked on).
+  int ids[kAhead + 1];
 #pragma unroll
-  for (int n = 0; n < STAGES; ++n) first_blk[n] = n < my_n ? lookup(n) : -1;
+  for (int n = 0; n <= kAhead; ++n) ids[n] = n < my_n ? lookup(n) : -1;
 
   uint32_t qf[NT][kK][2];
   {
@@ -114,56 +144,91 @@ __global__ void __launch_bounds__(128) decode_window_kernel(const WindowArgs a) 
     }
   }
 
-  const uint32_t wbase = smem_u32(smem) + warp * C::kWarpBytes;
-  const int64_t row_bytes = static_cast<int64_t>(a.Hkv) * KV::kRowBytes;
-  // Bit n % 32: the n-th sub-block's block id was valid.
-  uint32_t okbits = 0;
-  auto issue = [&](int n, int blk) {
-    const int tb = token(n);
-    const bool ok = blk >= 0 && blk < a.num_blocks;
-    if (!ok && lane == 0) record_error(a.err, PA_DEVERR_BLOCK_ID);
-    okbits = (okbits & ~(1u << (n & 31))) | (static_cast<uint32_t>(ok) << (n & 31));
-    const int off = mod_bs(tb, a.bs, a.bs_log2);
-    const uint8_t* kbase = a.cache +
-                           (static_cast<int64_t>(ok ? blk : 0) * 2 * a.bs + off) * row_bytes +
-                           static_cast<int64_t>(kvh) * KV::kRowBytes;
-    const uint8_t* vbase = kbase + a.bs * row_bytes;
-    const uint32_t kdst = wbase + (n % STAGES) * C::kStageBytes;
-    const uint32_t vdst = kdst + KV::kTileBytes;
-#pragma unroll
-    for (int k = 0; k < 16 * KV::kChunks / 32; ++k) {
-      const int c = lane + 32 * k;
-      const int r = c / KV::kChunks, cc = c % KV::kChunks;
-      const int bytes = ok && visible(tb + r) ? 16 : 0;   // others: zeros, nothing read
-      const uint32_t so = KV::at(r, cc);
-      cp_async_16(kdst + so, kbase + r * row_bytes + cc * 16, bytes);
-      cp_async_16(vdst + so, vbase + r * row_bytes + cc * 16, bytes);
+  // Box h into ring place `place`: sub-block h, or the K or V of sub-block
+  // h / 2, in block blk.  A box that is not loaded (no such block) completes
+  // its barrier all the same.
+  auto issue = [&](int h, int blk, int place) {
+    const int n = C::kPair ? h : h >> 1;
+    if (lane != 0 || n >= my_n) return;
+    const uint32_t bar = bars + 8 * place;
+    if (blk >= 0 && blk < a.num_blocks) {
+      const int off = mod_bs(token(n), a.bs, a.bs_log2);
+      tc::mbar_arrive_expect_tx(bar, C::kPlaceBytes);
+      if (C::kPair)
+        tc::tma_load_5d(wbase + place * C::kPlaceBytes, &map, bar, 0, off, kvh, 0, blk);
+      else
+        tc::tma_load_5d(wbase + place * C::kPlaceBytes, &map, bar, 0, off, 0, kvh,
+                        2 * blk + (h & 1));
+    } else {
+      record_error(a.err, PA_DEVERR_BLOCK_ID);
+      tc::mbar_arrive(bar);
     }
+  };
+  bool alive = true;   // no wait has run out
+  int at = 0, parity = 0;   // place and barrier parity of the tile worked on
+  auto arrived = [&]() {
+    if (!__all_sync(0xffffffffu, tc::mbar_wait(bars + 8 * at, parity))) alive = false;
+  };
+  auto next_tile = [&]() {
+    if (++at == R) at = 0, parity ^= 1;
   };
 
   dec::State<D, NT> st;
   st.clear();
 #pragma unroll
-  for (int n = 0; n < STAGES - 1; ++n) {
-    if (n < my_n) issue(n, first_blk[n]);
-    cp_async_commit();
-  }
-  int next_blk = STAGES - 1 < my_n ? first_blk[STAGES - 1] : -1;
-  for (int n = 0; n < my_n; ++n) {
-    cp_async_wait<STAGES - 2>();
-    __syncwarp();
-    if (n + STAGES - 1 < my_n) {
-      issue(n + STAGES - 1, next_blk);
-      if (n + STAGES < my_n) next_blk = lookup(n + STAGES);
-    }
-    cp_async_commit();
+  for (int h = 0; h < R - 1; ++h) issue(h, ids[C::kPair ? h : h >> 1], h);
+  for (int n = 0; n < my_n && alive; ++n) {
+    const int blk = ids[0];
+    const int after = n + kAhead + 1;   // the next block id, a sub-block ahead of its copies
+    const int fetched = after < my_n ? lookup(after) : -1;
     const int tb = token(n);
-    const bool ok = (okbits >> (n & 31)) & 1u;
-    const uint32_t kb = wbase + (n % STAGES) * C::kStageBytes;
-    dec::add_sub_block<KV, D, NT>(st, kb, kb + KV::kTileBytes, lane, ok && visible(tb + gid),
-                                  ok && visible(tb + gid + 8), a.scale_log2, qf);
+    const bool ok = blk >= 0 && blk < a.num_blocks;
+    const bool v0 = ok && visible(tb + gid), v1 = ok && visible(tb + gid + 8);
+    // The next box goes to the place of the one before this.
+    const int before = at == 0 ? R - 1 : at - 1;
+    if (C::kPair)
+      issue(n + R - 1, ids[R - 1], before);
+    else
+      issue(2 * n + R - 1, ids[(R - 1) >> 1], before);
+    arrived();
+    uint32_t pb[NT][2];
+    dec::weights<KV, D, NT>(st, wbase + at * C::kPlaceBytes, lane, v0, v1, a.scale_log2, qf, pb);
+    uint32_t vb = wbase + at * C::kPlaceBytes + KV::kTileBytes;
+    if (!C::kPair) {
+      __syncwarp();   // every lane is done with K(n): its place is free
+      issue(2 * n + R, ids[R >> 1], at);
+      next_tile();
+      arrived();
+      vb = wbase + at * C::kPlaceBytes;
+    }
+    if (!__all_sync(0xffffffffu, v0 && v1)) {
+      // Weights of unseen tokens are 0, but 0 * NaN is not: clear their rows.
+      for (int c = lane; c < 16 * KV::kChunks; c += 32) {
+        const int r = c / KV::kChunks;
+        if (!(ok && visible(tb + r)))
+          asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(vb + KV::at(r, c % KV::kChunks)),
+                       "r"(0u)
+                       : "memory");
+      }
+      tc::fence_proxy_async_smem();   // before a later TMA box lands here
+      __syncwarp();
+    }
+    KV::template values<NT>(vb, lane, pb, st.o);
+    __syncwarp();
+    next_tile();
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) ids[k] = ids[k + 1];
+    ids[kAhead] = fetched;
   }
-  cp_async_wait<0>();
+  if (!alive && lane == 0) {
+    // Given up: the outputs are invalid.  No copy may still be landing when
+    // the CTA goes on, so each place's barrier gets one more bounded wait.
+    record_error(a.err, PA_DEVERR_TIMEOUT);
+    for (int k = 0; k < R; ++k) {
+      tc::mbar_wait(bars + 8 * at, parity);
+      next_tile();
+    }
+  }
   pdl_trigger();
 
   // Sums over the 8 token lanes.
@@ -268,10 +333,36 @@ __global__ void __launch_bounds__(128) decode_window_kernel(const WindowArgs a) 
   tc::cluster_sync();   // no CTA leaves while another reads its shared memory
 }
 
-template <class KV, int D, int STAGES, int NT>
+// The pool viewed 5-D, innermost first.  Rows of one column group (128 bytes,
+// or 64 codes): row, tokens of a block, heads, K or V, blocks; a box is the
+// 16-token K and V tiles of one head.  Rows of two: column group, tokens,
+// groups, heads, 2 * block + (K or V); a box is one of the two tiles.
+bool make_tile_map(CUtensorMap* map, const DecodeWindowLaunch& n) {
+  auto fn = tensor_map_encoder();
+  if (fn == nullptr || 2LL * n.num_blocks > INT_MAX) return false;   // 32-bit coordinates
+  const cuuint64_t el = n.fp8 ? 1 : 2, row = n.d * el, group = row < 128 ? row : 128;
+  const cuuint64_t bs = n.bs, heads = n.Hkv, blocks = n.num_blocks, tok = row * heads;
+  const cuuint64_t dims1[5] = {group / el, bs, heads, 2, blocks};
+  const cuuint64_t strides1[4] = {tok, row, tok * bs, 2 * tok * bs};
+  const cuuint64_t dims2[5] = {group / el, bs, row / group, heads, 2 * blocks};
+  const cuuint64_t strides2[4] = {tok, group, row, tok * bs};
+  const cuuint32_t width = static_cast<cuuint32_t>(group / el);
+  const cuuint32_t box1[5] = {width, 16, 1, 2, 1}, box2[5] = {width, 16, 2, 1, 1};
+  const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+  const bool one = row == group;
+  return fn(map, n.fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5,
+            const_cast<void*>(n.cache), one ? dims1 : dims2, one ? strides1 : strides2,
+            one ? box1 : box2, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            group == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <class KV, int D, int R, int NT, int MINB>
 cudaError_t launch_t(const DecodeWindowLaunch& n, const WindowArgs& a, int S, cudaStream_t stream) {
-  using C = WindowCfg<KV, D, STAGES, NT>;
-  auto kern = decode_window_kernel<KV, D, STAGES, NT>;
+  using C = WindowCfg<KV, D, R, NT>;
+  auto kern = decode_window_kernel<KV, D, R, NT, MINB>;
+  CUtensorMap map;
+  if (!make_tile_map(&map, n)) return cudaErrorInvalidValue;
   static DeviceFlags smem_set, cluster_set;
   cudaError_t e = set_smem_once(kern, C::kSmemBytes, smem_set);
   if (e != cudaSuccess) return e;
@@ -299,27 +390,26 @@ cudaError_t launch_t(const DecodeWindowLaunch& n, const WindowArgs& a, int S, cu
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = S > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kern, a);
+  return cudaLaunchKernelEx(&cfg, kern, map, a);
 }
 
 }  // namespace
 
-// CTAs per (request, kv head): enough for about 12 CTAs per SM, as the
-// split-KV planner, at least 16 sub-blocks (4 per warp) each, a power of two
-// up to 16.
+// CTAs per (request, kv head): as many as leave at most two per SM, up to 16,
+// and at least 64 tokens to each.  More CTAs cost more than they bring, since
+// each pays for its start, its merge and its cluster: 64 requests x 8 heads
+// (window 1024) take 42.5 us on one CTA each, 49.4 on two, 54.5 on four; 8 x 8
+// (window 4096) 62.1 on one, 36.3 on two, 26.7 on four, 27.1 on eight; 1 x 8
+// 61.6 on one, 13.5 on eight, 11.4 on sixteen.
 int decode_window_shares(int N, int Hkv, long long visible, int sm_count) {
   const long long units = static_cast<long long>(N) * Hkv;
-  const long long want = (12LL * sm_count + units - 1) / units;
-  const long long most = visible / 256;
-  int S = 1;
-  while (S < 16 && S < want && 2 * S <= most) S *= 2;
-  return S;
+  const long long s = std::min({16LL, 2LL * sm_count / units, visible / 64});
+  return s < 1 ? 1 : static_cast<int>(s);
 }
 
 cudaError_t launch_decode_window(const DecodeWindowLaunch& n, cudaStream_t stream) {
   WindowArgs a{};
   a.q = static_cast<const __nv_bfloat16*>(n.q);
-  a.cache = static_cast<const uint8_t*>(n.cache);
   a.block_table = n.block_table;
   a.seq_lens = n.seq_lens;
   a.max_blocks = n.max_blocks;
@@ -335,24 +425,26 @@ cudaError_t launch_decode_window(const DecodeWindowLaunch& n, cudaStream_t strea
   a.out = static_cast<__nv_bfloat16*>(n.out);
   a.lse = n.lse;
   a.err = n.err;
-  const long long table = static_cast<long long>(n.max_blocks) * n.bs;
-  const long long visible = std::min(static_cast<long long>(n.window) + n.sinks, table);
+  const long long positions = static_cast<long long>(n.max_blocks) * n.bs;
+  const long long visible = std::min(static_cast<long long>(n.window) + n.sinks, positions);
   const int S = decode_window_shares(n.N, n.Hkv, visible, n.sm_count);
   const bool wide = n.Hq / n.Hkv > 8;   // groups of 9..16 heads take two n-tiles
   using dec::KvBf16;
   using dec::KvE4m3;
+  // Ring places and CTAs per SM (48 KB of ring each, 4 warps; the two-n-tile
+  // forms are held to fewer by their registers).
   if (n.fp8) {
     if (n.d == 128)
-      return wide ? launch_t<KvE4m3<128>, 128, 4, 2>(n, a, S, stream)
-                  : launch_t<KvE4m3<128>, 128, 3, 1>(n, a, S, stream);
-    return wide ? launch_t<KvE4m3<64>, 64, 8, 2>(n, a, S, stream)
-                : launch_t<KvE4m3<64>, 64, 8, 1>(n, a, S, stream);
+      return wide ? launch_t<KvE4m3<128>, 128, 3, 2, 3>(n, a, S, stream)
+                  : launch_t<KvE4m3<128>, 128, 3, 1, 4>(n, a, S, stream);
+    return wide ? launch_t<KvE4m3<64>, 64, 6, 2, 4>(n, a, S, stream)
+                : launch_t<KvE4m3<64>, 64, 6, 1, 4>(n, a, S, stream);
   }
   if (n.d == 128)
-    return wide ? launch_t<KvBf16<128>, 128, 2, 2>(n, a, S, stream)
-                : launch_t<KvBf16<128>, 128, 2, 1>(n, a, S, stream);
-  return wide ? launch_t<KvBf16<64>, 64, 4, 2>(n, a, S, stream)
-              : launch_t<KvBf16<64>, 64, 4, 1>(n, a, S, stream);
+    return wide ? launch_t<KvBf16<128>, 128, 3, 2, 2>(n, a, S, stream)
+                : launch_t<KvBf16<128>, 128, 3, 1, 4>(n, a, S, stream);
+  return wide ? launch_t<KvBf16<64>, 64, 3, 2, 3>(n, a, S, stream)
+              : launch_t<KvBf16<64>, 64, 3, 1, 4>(n, a, S, stream);
 }
 
 }  // namespace pa
