@@ -17,6 +17,8 @@ around attention is ``pa_plan_step``, ``pa_qk_norm_rope_cache`` (and ``_fp8``),
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 import threading
 
@@ -24,6 +26,7 @@ import torch
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "_build", "libpa.so")
+BINDING_PATH = os.path.join(_PKG, "_build", "_binding.so")
 
 PA_OK, PA_ERR_INVALID, PA_ERR_UNSUPPORTED, PA_ERR_CUDA = 0, 1, 2, 3
 PA_DEVERR_BLOCK_ID, PA_DEVERR_SLOT, PA_DEVERR_TIMEOUT, PA_DEVERR_LENGTH = 1, 2, 4, 8
@@ -31,6 +34,7 @@ PA_DEVERR_POSITION, PA_DEVERR_NO_BLOCKS = 16, 32
 
 _lock = threading.Lock()
 _lib = None
+_steps = None   # the compiled checks of the serving-step calls, bound to _lib
 
 
 class PaError(RuntimeError):
@@ -49,6 +53,8 @@ class PaShape(ctypes.Structure):
 def lib() -> ctypes.CDLL:
     """Loads libpa.so (once).  Raises if it has not been built."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -110,6 +116,26 @@ def lib() -> ctypes.CDLL:
             getattr(L, name).restype = st
         _lib = L
         return L
+
+
+def _binding():
+    """The compiled argument checks (csrc/binding.cpp), bound to libpa.so."""
+    global _steps
+    if _steps is None:
+        L = lib()
+        with _lock:
+            if not os.path.exists(BINDING_PATH):
+                raise RuntimeError(f"{BINDING_PATH} is missing: build it with "
+                                   "`python -m paged_kv_cache_50_gb300.build`")
+            loader = importlib.machinery.ExtensionFileLoader("_binding", BINDING_PATH)
+            m = importlib.util.module_from_spec(
+                importlib.util.spec_from_loader("_binding", loader))
+            loader.exec_module(m)
+            m.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
+                L.pa_plan_step, L.pa_qk_norm_rope_cache, L.pa_qk_norm_rope_cache_fp8,
+                L.pa_varlen_fwd_sinks, L.pa_decode_window, L.pa_decode_window_fp8)))
+            _steps = m
+    return _steps
 
 
 def status_string(status: int) -> str:
@@ -501,7 +527,8 @@ def pa_mla_decode(q, kv_cache, block_table, seq_lens, scale, workspace, out=None
 
 # ---------------------------------------------------------------------------
 # The serving step: plan, norm + rotation + cache write, windowed attention.
-# These calls take every tensor on one device, which must be the current one.
+# These calls take every tensor on one device, which must be the current one;
+# their checks are compiled (csrc/binding.cpp).
 # ---------------------------------------------------------------------------
 
 def _call_device(t, name: str) -> int:
@@ -514,19 +541,6 @@ def _call_device(t, name: str) -> int:
         raise ValueError(f"{name} is on cuda:{dev}, the current device is "
                          f"cuda:{torch.cuda.current_device()}")
     return dev
-
-
-def _at(t, name: str, dtype: torch.dtype, dev: int) -> int:
-    """Data pointer of a dense tensor of ``dtype`` on device ``dev``."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.get_device() != dev:
-        raise ValueError(f"{name} must be on cuda:{dev}, is on {t.device}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
 
 
 def _raw_stream(stream, dev: int) -> int:
@@ -558,15 +572,12 @@ def pa_plan_step(context_lens, query_lens, block_table, free_blocks, block_size,
     and slot -1.  ``max_tokens`` defaults to the length of ``slot_mapping`` or
     ``positions``; with neither it must be given."""
     dev = _call_device(block_table, "block_table")
-    if block_table.dim() != 2:
-        raise ValueError("block_table must be [num_seqs, max_blocks]")
-    n, width = block_table.shape
     if max_tokens is None:
         given = slot_mapping if slot_mapping is not None else positions
         if given is None:
             raise ValueError("max_tokens, slot_mapping or positions must be given")
         max_tokens = given.shape[0]
-    max_tokens = int(max_tokens)
+    n = block_table.shape[0]
     if query_start_loc is None:
         query_start_loc = _new(stream, n + 1, torch.int32, dev)
     if seq_lens is None:
@@ -577,24 +588,9 @@ def pa_plan_step(context_lens, query_lens, block_table, free_blocks, block_size,
         slot_mapping = _new(stream, max_tokens, torch.int64, dev)
     if totals is None:
         totals = _new(stream, 2, torch.int32, dev)
-    if context_lens.shape != (n,) or query_lens.shape != (n,) or seq_lens.shape != (n,):
-        raise ValueError("context_lens, query_lens and seq_lens must be [num_seqs]")
-    if query_start_loc.shape != (n + 1,) or totals.shape != (2,):
-        raise ValueError("query_start_loc must be [num_seqs + 1] and totals [2]")
-    if positions.shape != (max_tokens,) or slot_mapping.shape != (max_tokens,):
-        raise ValueError("positions and slot_mapping must be [max_tokens]")
-    if free_blocks.dim() != 1 or (free_start is not None and free_start.numel() != 1):
-        raise ValueError("free_blocks must be [num_free] and free_start [1]")
-    i32 = torch.int32
-    _check(lib().pa_plan_step(
-        _at(context_lens, "context_lens", i32, dev), _at(query_lens, "query_lens", i32, dev),
-        _at(free_blocks, "free_blocks", i32, dev),
-        None if free_start is None else _at(free_start, "free_start", i32, dev),
-        free_blocks.shape[0], n, width, int(block_size), int(num_blocks), max_tokens,
-        _at(block_table, "block_table", i32, dev),
-        _at(query_start_loc, "query_start_loc", i32, dev), _at(seq_lens, "seq_lens", i32, dev),
-        _at(positions, "positions", i32, dev),
-        _at(slot_mapping, "slot_mapping", torch.int64, dev), _at(totals, "totals", i32, dev),
+    _check(_binding().plan_step(
+        dev, context_lens, query_lens, free_blocks, free_start, block_table, block_size,
+        num_blocks, max_tokens, query_start_loc, seq_lens, positions, slot_mapping, totals,
         _raw_stream(stream, dev)), "pa_plan_step")
     return query_start_loc, seq_lens, positions, slot_mapping, totals
 
@@ -609,73 +605,6 @@ def rope_table(max_position, rotary_dim, theta=10000.0, device="cuda"):
     return torch.cat([ang.cos(), ang.sin()], 1).float()
 
 
-def _token_rows(t, name, heads, d, tokens, dev):
-    """(pointer, token stride) of a [tokens, heads, d] view with dense heads."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != torch.bfloat16:
-        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
-    if t.get_device() != dev:
-        raise ValueError(f"{name} must be on cuda:{dev}, is on {t.device}")
-    if t.shape != (tokens, heads, d):
-        raise ValueError(f"{name} must be [{tokens}, {heads}, {d}], is {list(t.shape)}")
-    st, sh, se = t.stride()
-    if se != 1 or (sh != d and heads > 1):
-        raise ValueError(f"the heads of {name} must be dense")
-    return t.data_ptr(), st if tokens > 1 else heads * d
-
-
-def _norm_rope(q, key, value, kv_cache, slot_mapping, scales, q_weight, k_weight, eps, cos_sin,
-               positions, interleaved, q_out, stream):
-    dev = _call_device(q, "q")
-    codes = kv_cache if scales is None else _codes(kv_cache)
-    if q.dim() != 3:
-        raise ValueError("q must be [num_tokens, num_q_heads, head_size]")
-    T, hq, d = q.shape
-    shape = _pool_shape(codes, 0, hq, 1)
-    hkv = shape.num_kv_heads
-    if d != shape.head_size:
-        raise ValueError("q head_size does not match kv_cache")
-    q_ptr, q_stride = _token_rows(q, "q", hq, d, T, dev)
-    k_ptr, k_stride = _token_rows(key, "key", hkv, d, T, dev)
-    v_ptr, v_stride = _token_rows(value, "value", hkv, d, T, dev)
-    if slot_mapping.shape != (T,):
-        raise ValueError("slot_mapping must be [num_tokens]")
-    if (q_weight is None) != (k_weight is None):
-        raise ValueError("q_weight and k_weight must be given together")
-    qw = kw = cs = pos = None
-    if q_weight is not None:
-        if q_weight.shape != (d,) or k_weight.shape != (d,):
-            raise ValueError("q_weight and k_weight must be [head_size]")
-        qw = _at(q_weight, "q_weight", torch.bfloat16, dev)
-        kw = _at(k_weight, "k_weight", torch.bfloat16, dev)
-    rows = rot = 0
-    if cos_sin is not None:
-        if cos_sin.dim() != 2 or positions is None or positions.shape != (T,):
-            raise ValueError("cos_sin [max_position, rotary_dim] needs positions [num_tokens]")
-        rows, rot = cos_sin.shape
-        cs = _at(cos_sin, "cos_sin", torch.float32, dev)
-        pos = _at(positions, "positions", torch.int32, dev)
-    if q_out is None:
-        q_out = _new(stream, (T, hq, d), torch.bfloat16, dev)
-    elif q_out.shape != q.shape:
-        raise ValueError("q_out must have the shape of q")
-    out = _at(q_out, "q_out", torch.bfloat16, dev)
-    head = (q_ptr, k_ptr, v_ptr, q_stride, k_stride, v_stride, qw, kw, float(eps), cs, rows, rot,
-            int(bool(interleaved)), pos)
-    slots = _at(slot_mapping, "slot_mapping", torch.int64, dev)
-    if scales is None:
-        _check(lib().pa_qk_norm_rope_cache(
-            *head, _at(codes, "kv_cache", torch.bfloat16, dev), slots, T, ctypes.byref(shape), out,
-            _raw_stream(stream, dev)), "pa_qk_norm_rope_cache")
-    else:
-        _check(lib().pa_qk_norm_rope_cache_fp8(
-            *head, _at(codes, "kv_cache", torch.uint8, dev), slots, T, ctypes.byref(shape),
-            float(scales[0]), float(scales[1]), out, _raw_stream(stream, dev)),
-            "pa_qk_norm_rope_cache_fp8")
-    return q_out
-
-
 def pa_qk_norm_rope_cache(q, key, value, kv_cache, slot_mapping, q_weight=None, k_weight=None,
                           eps=1e-6, cos_sin=None, positions=None, interleaved=False, q_out=None,
                           stream=None):
@@ -688,8 +617,13 @@ def pa_qk_norm_rope_cache(q, key, value, kv_cache, slot_mapping, q_weight=None, 
     ``q_weight`` and ``k_weight`` [d] bf16 (neither: no norm), ``cos_sin``
     [max_position, rotary_dim] fp32 (see rope_table; none: no rotation) with
     ``positions`` [T] int32, ``slot_mapping`` [T] int64 (< 0: no cache write)."""
-    return _norm_rope(q, key, value, kv_cache, slot_mapping, None, q_weight, k_weight, eps,
-                      cos_sin, positions, interleaved, q_out, stream)
+    dev = _call_device(q, "q")
+    if q_out is None:
+        q_out = _new(stream, q.shape, torch.bfloat16, dev)
+    _check(_binding().norm_rope(
+        dev, q, key, value, kv_cache, slot_mapping, None, q_weight, k_weight, eps, cos_sin,
+        positions, interleaved, q_out, _raw_stream(stream, dev)), "pa_qk_norm_rope_cache")
+    return q_out
 
 
 def pa_qk_norm_rope_cache_fp8(q, key, value, kv_cache, slot_mapping, k_scale, v_scale,
@@ -697,35 +631,14 @@ def pa_qk_norm_rope_cache_fp8(q, key, value, kv_cache, slot_mapping, k_scale, v_
                               positions=None, interleaved=False, q_out=None, stream=None):
     """pa_qk_norm_rope_cache into an fp8 pool: e4m3 codes of key / k_scale and
     value / v_scale (uint8 or float8_e4m3fn)."""
-    return _norm_rope(q, key, value, kv_cache, slot_mapping, (k_scale, v_scale), q_weight,
-                      k_weight, eps, cos_sin, positions, interleaved, q_out, stream)
-
-
-def _window_call(q, kv_cache, block_table, seq_lens, out, lse, return_lse, stream, dtype):
-    """Checks and pointers that the windowed attention calls share."""
     dev = _call_device(q, "q")
-    if q.dim() != 3:
-        raise ValueError("q must be [tokens, num_q_heads, head_size]")
-    T, hq, d = q.shape
-    if seq_lens.dim() != 1 or block_table.dim() != 2 or block_table.shape[0] != seq_lens.shape[0]:
-        raise ValueError("seq_lens must be [num_seqs] and block_table [num_seqs, max_blocks]")
-    shape = _pool_shape(kv_cache, seq_lens.shape[0], hq, block_table.shape[1])
-    if d != shape.head_size:
-        raise ValueError("q head_size does not match kv_cache")
-    if out is None:
-        out = _new(stream, (T, hq, d), torch.bfloat16, dev)
-    elif out.shape != q.shape:
-        raise ValueError("out must have the shape of q")
-    if lse is None:
-        if return_lse:
-            lse = _new(stream, (T, hq), torch.float32, dev)
-    elif lse.shape != (T, hq):
-        raise ValueError("lse must be [tokens, num_q_heads]")
-    return (dev, shape, out, lse, _at(q, "q", torch.bfloat16, dev),
-            _at(kv_cache, "kv_cache", dtype, dev),
-            _at(block_table, "block_table", torch.int32, dev),
-            _at(seq_lens, "seq_lens", torch.int32, dev), _at(out, "out", torch.bfloat16, dev),
-            None if lse is None else _at(lse, "lse", torch.float32, dev))
+    if q_out is None:
+        q_out = _new(stream, q.shape, torch.bfloat16, dev)
+    _check(_binding().norm_rope(
+        dev, q, key, value, kv_cache, slot_mapping, (k_scale, v_scale), q_weight, k_weight, eps,
+        cos_sin, positions, interleaved, q_out, _raw_stream(stream, dev)),
+        "pa_qk_norm_rope_cache_fp8")
+    return q_out
 
 
 def pa_varlen_fwd_sinks(q, kv_cache, block_table, query_start_loc, seq_lens, max_query_len, scale,
@@ -734,14 +647,14 @@ def pa_varlen_fwd_sinks(q, kv_cache, block_table, query_start_loc, seq_lens, max
     """Causal varlen paged attention in which a row at position p sees
     p - sliding_window < p' <= p and p' < num_sinks.  Blocks that no row sees
     are not read.  Returns (out, lse) like pa_varlen_fwd_window."""
-    dev, shape, out, lse, qp, kv, table, seq, op, lp = _window_call(
-        q, kv_cache, block_table, seq_lens, out, lse, return_lse, stream, torch.bfloat16)
-    if query_start_loc.shape != (shape.num_seqs + 1,):
-        raise ValueError("query_start_loc must be [num_seqs + 1]")
-    _check(lib().pa_varlen_fwd_sinks(
-        qp, kv, table, _at(query_start_loc, "query_start_loc", torch.int32, dev), seq, q.shape[0],
-        int(max_query_len), ctypes.byref(shape), float(scale), int(sliding_window),
-        int(num_sinks), op, lp, _raw_stream(stream, dev)), "pa_varlen_fwd_sinks")
+    dev = _call_device(q, "q")
+    if out is None:
+        out = _new(stream, q.shape, torch.bfloat16, dev)
+    if lse is None and return_lse:
+        lse = _new(stream, q.shape[:2], torch.float32, dev)
+    _check(_binding().varlen_sinks(
+        dev, q, kv_cache, block_table, seq_lens, out, lse, query_start_loc, max_query_len, scale,
+        sliding_window, num_sinks, _raw_stream(stream, dev)), "pa_varlen_fwd_sinks")
     return out, lse
 
 
@@ -750,28 +663,30 @@ def pa_decode_window(q, kv_cache, block_table, seq_lens, scale, sliding_window, 
     """Decode (q [N, Hq, d], one query per request at its last position) over
     the last ``sliding_window`` and the first ``num_sinks`` cached tokens, in
     one launch without a workspace.  Returns (out [N, Hq, d] bf16, lse [N, Hq])."""
-    dev, shape, out, lse, qp, kv, table, seq, op, lp = _window_call(
-        q, kv_cache, block_table, seq_lens, out, lse, return_lse, stream, torch.bfloat16)
-    if q.shape[0] != shape.num_seqs:
-        raise ValueError("q must hold one row per request")
-    _check(lib().pa_decode_window(
-        qp, kv, table, seq, ctypes.byref(shape), float(scale), int(sliding_window),
-        int(num_sinks), op, lp, _raw_stream(stream, dev)), "pa_decode_window")
+    dev = _call_device(q, "q")
+    if out is None:
+        out = _new(stream, q.shape, torch.bfloat16, dev)
+    if lse is None and return_lse:
+        lse = _new(stream, q.shape[:2], torch.float32, dev)
+    _check(_binding().decode_window(
+        dev, q, kv_cache, block_table, seq_lens, out, lse, None, scale, sliding_window, num_sinks,
+        _raw_stream(stream, dev)), "pa_decode_window")
     return out, lse
 
 
 def pa_decode_window_fp8(q, kv_cache, block_table, seq_lens, scale, k_scale, v_scale,
                          sliding_window, num_sinks=0, out=None, lse=None, return_lse=True,
                          stream=None):
-    """pa_decode_window over an fp8 pool (entries = e4m3 value x k_scale or v_scale)."""
-    dev, shape, out, lse, qp, kv, table, seq, op, lp = _window_call(
-        q, _codes(kv_cache), block_table, seq_lens, out, lse, return_lse, stream, torch.uint8)
-    if q.shape[0] != shape.num_seqs:
-        raise ValueError("q must hold one row per request")
-    _check(lib().pa_decode_window_fp8(
-        qp, kv, table, seq, ctypes.byref(shape), float(scale), float(k_scale), float(v_scale),
-        int(sliding_window), int(num_sinks), op, lp, _raw_stream(stream, dev)),
-        "pa_decode_window_fp8")
+    """pa_decode_window over an fp8 pool (entries = e4m3 value x k_scale or
+    v_scale; uint8 or float8_e4m3fn)."""
+    dev = _call_device(q, "q")
+    if out is None:
+        out = _new(stream, q.shape, torch.bfloat16, dev)
+    if lse is None and return_lse:
+        lse = _new(stream, q.shape[:2], torch.float32, dev)
+    _check(_binding().decode_window(
+        dev, q, kv_cache, block_table, seq_lens, out, lse, (k_scale, v_scale), scale,
+        sliding_window, num_sinks, _raw_stream(stream, dev)), "pa_decode_window_fp8")
     return out, lse
 
 

@@ -1,7 +1,8 @@
 """Builds ``libpa.so`` (the C-ABI paged-attention library) in-tree with nvcc.
 
 Every ``csrc/*.cu`` translation unit is compiled in parallel for sm_103a only
-and linked into ``paged_kv_cache_50_gb300/_build/libpa.so``.  Run as
+and linked into ``paged_kv_cache_50_gb300/_build/libpa.so``; the compiled
+argument checks (``csrc/binding.cpp``) become ``_build/_binding.so``.  Run as
 ``python -m paged_kv_cache_50_gb300.build`` or call :func:`build`.
 """
 
@@ -13,6 +14,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -20,6 +22,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OUT_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(OUT_DIR, "libpa.so")
+
+BINDING = os.path.join(OUT_DIR, "_binding.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "--expt-relaxed-constexpr",
@@ -49,16 +53,56 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(p) <= t for p in _deps())
 
 
+def build_binding(force: bool = False, verbose: bool = False) -> str:
+    """Compile csrc/binding.cpp (a CPython extension over torch's headers) with
+    the host compiler; returns its path."""
+    src = os.path.join(CSRC, "binding.cpp")
+    deps = [src, os.path.join(INCLUDE, "pa.h"), os.path.abspath(__file__)]
+    if not force and os.path.exists(BINDING) and all(
+            os.path.getmtime(p) <= os.path.getmtime(BINDING) for p in deps):
+        return BINDING
+    import torch
+    os.makedirs(OUT_DIR, exist_ok=True)
+    root = os.path.dirname(torch.__file__)
+    inc, lib = os.path.join(root, "include"), os.path.join(root, "lib")
+    tmp = BINDING + f".{os.getpid()}.tmp"
+    cmd = [os.environ.get("CXX") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+           "-I", INCLUDE, "-isystem", inc, "-isystem",
+           os.path.join(inc, "torch", "csrc", "api", "include"),
+           "-isystem", sysconfig.get_paths()["include"], src, "-o", tmp, "-L", lib,
+           "-ltorch_python", "-ltorch_cpu", "-lc10", f"-Wl,-rpath,{lib}"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
+    return BINDING
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags=None, out_dir=None,
           lib_name="libpa.so") -> str:
     """Compile and link libpa.so; returns its path.  ``out_dir`` / ``lib_name``
     build a variant elsewhere (the tests' timeout variant, with its own
     defines in ``extra_flags``); the default build never includes one."""
+    binding = out_dir is None
     out_dir = out_dir or OUT_DIR
     lib = os.path.join(out_dir, lib_name)
+    if binding:
+        with cf.ThreadPoolExecutor(max_workers=1) as side:   # beside the nvcc runs
+            made = side.submit(build_binding, force, verbose)
+            _build_lib(lib, force, verbose, extra_flags, out_dir)
+            made.result()
+    else:
+        _build_lib(lib, force, verbose, extra_flags, out_dir)
+    return lib
+
+
+def _build_lib(lib, force, verbose, extra_flags, out_dir) -> None:
     if not force and os.path.exists(lib) and all(
             os.path.getmtime(p) <= os.path.getmtime(lib) for p in _deps()):
-        return lib
+        return
     os.makedirs(out_dir, exist_ok=True)
     cc = nvcc()
     flags = NVCC_FLAGS + list(extra_flags or [])
@@ -83,7 +127,6 @@ def build(force: bool = False, verbose: bool = False, extra_flags=None, out_dir=
     tmp = lib + f".{os.getpid()}.tmp"
     run([cc, *ARCH, "-shared", "--cudart", "static", "-o", tmp, *objs])
     os.replace(tmp, lib)
-    return lib
 
 
 if __name__ == "__main__":
