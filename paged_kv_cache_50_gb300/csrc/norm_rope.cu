@@ -19,8 +19,8 @@
 // d 128 (457 MB): 72.5 us, 6.3 TB/s, 0.93 of the copy rate.  Before: a CTA per
 // token, 16-byte loads and the other half by shuffles 207 us, a warp per token
 // 131 us (instructions); one loop over all kinds of rows with loads a round
-// ahead 98 us (spilled registers).  An e4m3 pool adds an IEEE division per
-// value: 8191 tokens of 64 / 8 heads, d 64 (160 MB): 35.0 us.
+// ahead 98 us (spilled registers).  An e4m3 pool adds a division per
+// value: 8191 tokens of 64 / 8 heads, d 64 (160 MB): 34.4 us.
 #include <type_traits>
 
 #include "pa_common.cuh"
@@ -88,13 +88,30 @@ __device__ __forceinline__ uint32_t narrow(F2 a) {
   return pack_bf16(f.x, f.y);
 }
 
+// x / scale, correctly rounded, by a multiplication and one correction
+// (Markstein, "Computation of elementary functions on the IBM RISC System/6000
+// processor", 1990: with r the rounded reciprocal and q near x / s, q + r (x -
+// q s), the remainder exact by fma, rounds to the quotient).  Magnitudes from
+// 480 on saturate and those below 2^-20 become a zero of their sign, whatever
+// their last bits (infinities, NaN and -0 among them); scales outside [2^-100,
+// 2^100], whose reciprocal could leave the normal range, take the division.
+__device__ __forceinline__ float quotient(float x, float scale, float r, bool plain) {
+  if (!plain) return __fdiv_rn(x, scale);
+  const float q = x * r;
+  const uint32_t above = (__float_as_uint(q) & 0x7fffffffu) - __float_as_uint(0x1p-20f);
+  return above < __float_as_uint(480.f) - __float_as_uint(0x1p-20f)
+             ? fmaf(fmaf(-q, scale, x), r, q) : q;
+}
+
 // Four values as e4m3 codes of value / scale (IEEE quotient, saturating).
-__device__ __forceinline__ uint32_t quant4(F2 a, F2 b, float scale) {
+__device__ __forceinline__ uint32_t quant4(F2 a, F2 b, float scale, float r, bool plain) {
   const float2 x = split(a), y = split(b);
   const __nv_fp8x2_storage_t lo = __nv_cvt_float2_to_fp8x2(
-      make_float2(__fdiv_rn(x.x, scale), __fdiv_rn(x.y, scale)), __NV_SATFINITE, __NV_E4M3);
+      make_float2(quotient(x.x, scale, r, plain), quotient(x.y, scale, r, plain)), __NV_SATFINITE,
+      __NV_E4M3);
   const __nv_fp8x2_storage_t hi = __nv_cvt_float2_to_fp8x2(
-      make_float2(__fdiv_rn(y.x, scale), __fdiv_rn(y.y, scale)), __NV_SATFINITE, __NV_E4M3);
+      make_float2(quotient(y.x, scale, r, plain), quotient(y.y, scale, r, plain)), __NV_SATFINITE,
+      __NV_E4M3);
   return static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
 }
 
@@ -192,9 +209,11 @@ __global__ void __launch_bounds__(kWarps * 32, 8) norm_rope_kernel(const NormRop
         }
       }
     }
+    const float scale = kind == kValue ? a.v_scale : a.k_scale, inv = __frcp_rn(scale);
+    const bool plain = scale >= 0x1p-100f && scale <= 0x1p100f;
     uint8_t* dst = kind == kQuery
                        ? reinterpret_cast<uint8_t*>(a.q_out + static_cast<int64_t>(t) * a.Hq * D)
-                       : cell + (kind == kValue ? static_cast<int64_t>(a.bs) * a.Hkv * (D * kEl) : 0);
+                       : cell + (kind == kValue ? static_cast<int64_t>(a.bs) * a.Hkv : 0) * (D * kEl);
     for (int base = s0; base < end; base += kFlight) {
       uint2 raw[kFlight][2];
 #pragma unroll
@@ -267,10 +286,9 @@ __global__ void __launch_bounds__(kWarps * 32, 8) norm_rope_kernel(const NormRop
         }
         if (!store) continue;
         if (kind != kQuery && FP8) {
-          const float scale = kind == kValue ? a.v_scale : a.k_scale;
           uint32_t* p = reinterpret_cast<uint32_t*>(dst + r * D);
-          p[c0] = quant4(y[0][0], y[0][1], scale);
-          p[c1] = quant4(y[1][0], y[1][1], scale);
+          p[c0] = quant4(y[0][0], y[0][1], scale, inv, plain);
+          p[c1] = quant4(y[1][0], y[1][1], scale, inv, plain);
         } else {
           uint2* p = reinterpret_cast<uint2*>(dst + r * (D * 2));
           p[c0] = make_uint2(narrow(y[0][0]), narrow(y[0][1]));

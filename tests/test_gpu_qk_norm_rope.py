@@ -204,6 +204,26 @@ def test_equals_the_plain_cache_write(pa):
     assert torch.equal(got, q) and torch.equal(p1.view(torch.int16), p2.view(torch.int16))
 
 
+def test_fp8_codes_are_those_of_the_division(pa):
+    """Every bf16 pattern (infinities, NaN, zeros of both signs among them) at
+    scales that are powers of two, far out, or anything: the same codes as
+    pa_reshape_and_cache_fp8, which divides."""
+    v = torch.arange(65536, dtype=torch.int32, device="cuda").to(torch.int16).view(torch.bfloat16)
+    v = v.view(512, 2, 64)
+    q = torch.zeros((512, 2, 64), dtype=torch.bfloat16, device="cuda")
+    slots = torch.arange(512, device="cuda")
+    rng = np.random.default_rng(12)
+    scales = [2.0 ** e for e in (-126, -101, -100, -99, -20, -3, 0, 1, 7, 40, 99, 100, 101, 127)]
+    scales += list(np.exp2(rng.uniform(-12, 12, 150))) + list(np.exp2(rng.uniform(-126, 127, 60)))
+    scales += [1.5, 3.0, 1 / 3, 0.1, 1 + 2.0 ** -23, 2 - 2.0 ** -23, 448.0, 1 / 448, 1e-45, 3e38]
+    for s in scales:
+        s = float(np.float32(s))
+        a, b = (torch.zeros((32, 2, 16, 2, 64), dtype=torch.uint8, device="cuda") for _ in range(2))
+        pa.pa_qk_norm_rope_cache_fp8(q, v, v, a, slots, s, s)
+        pa.pa_reshape_and_cache_fp8(v, v, b, slots, s, s)
+        assert torch.equal(a, b), s
+
+
 def test_argument_checks(pa):
     c = Case(8, 6, 4, 2, 64, 16, False)
     slots = torch.from_numpy(c.slots).cuda()
