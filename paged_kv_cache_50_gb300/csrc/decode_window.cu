@@ -9,24 +9,24 @@
 // The visible tokens form a list of 16-token sub-blocks: ceil(sinks / 16)
 // first ones, then those from lo rounded down to 16 (one run from position 0
 // where the two meet).  Nothing else is read.  One cluster of S CTAs serves
-// one (request, kv head): CTA r takes the r-th share of the list, its four
-// warps sub-blocks in turn, each warp with its own ring of K and V tiles,
+// one (request, kv head): CTA r takes the r-th share of the list, its four or
+// eight warps sub-blocks in turn, each warp with its own ring of K and V tiles,
 // filled by TMA boxes of 16 token rows of a head (a box is one instruction of
 // one lane; the same ring filled by cp.async took 49.7 us instead of 42.5 on
 // the batch below, its address and mask arithmetic being what a warp spent its
 // time on).  The warps' states are merged in shared memory, the CTAs' in
 // distributed shared memory, every CTA writing a share of the outputs.  A
 // window bounds a request's work, so unlike split-KV decode over a whole
-// context S <= 16 shares are enough, and the second launch and its fp32
+// context S <= 8 shares are enough, and the second launch and its fp32
 // workspace (written and read once) go.
 //
 // Bound by HBM where the batch fills the GPU, else by latency (lengths ->
 // block ids -> K/V -> merge, one after the other).  Measured (32 / 8 heads,
-// d 128): 64 requests, window 1024 over U[128, 4096] tokens, 242 MB: 42.5 us,
-// 5.7 TB/s; window 4096 over U[1024, 8192], 899 MB: 140.6 us, 6.4 TB/s; an e4m3
-// pool, 128 requests, window 4096, 911 MB: 163 us, 5.6 TB/s (instruction-bound:
-// 372 warp instructions per 16 tokens, 64 of them conversions); one request of
-// 64 / 8 heads, window 4096: 11.4 us.
+// d 128): 64 requests, window 1024 over U[128, 4096] tokens, 242 MB: 41.7 us,
+// 5.8 TB/s; window 4096 over U[1024, 8192], 899 MB: 135.2 us, 6.6 TB/s; an e4m3
+// pool, 128 requests, window 4096, 911 MB: 149 us, 6.1 TB/s (372 warp
+// instructions per 16 tokens, 64 of them conversions); one request of 64 / 8
+// heads, window 4096: 10.1 us.
 #include <algorithm>
 #include <climits>
 
@@ -51,14 +51,16 @@ struct WindowArgs {
   int* err;
 };
 
+constexpr int kMaxShares = 8;   // the largest portable cluster
+
 // A warp's ring has R places; while one is worked on, the next R - 1 are on
 // their way.  Where a row is one column group, a place takes the K and V tiles
 // of a sub-block, by one 4 KB TMA box (2 KB boxes, one for K and one for V, took
 // twice as long on 64-wide bf16 rows: 87 us against 42 for 64 requests, window
 // 2048); else K and V take a place and a box each.
-template <class KV, int D, int R, int NT>
+template <class KV, int D, int R, int NT, int W>
 struct WindowCfg {
-  static constexpr int kWarps = 4;
+  static constexpr int kWarps = W;
   static constexpr int kThreads = kWarps * 32;
   static constexpr bool kPair = KV::kGroups == 1;
   static constexpr int kPlaceBytes = (kPair ? 2 : 1) * KV::kTileBytes;
@@ -79,10 +81,10 @@ __device__ __forceinline__ float ld_remote(uint32_t addr) {
   return v;
 }
 
-template <class KV, int D, int R, int NT, int MINB>
-__global__ void __launch_bounds__(128, MINB) decode_window_kernel(
+template <class KV, int D, int R, int NT, int W, int MINB>
+__global__ void __launch_bounds__(32 * W, MINB) decode_window_kernel(
     const __grid_constant__ CUtensorMap map, const __grid_constant__ WindowArgs a) {
-  using C = WindowCfg<KV, D, R, NT>;
+  using C = WindowCfg<KV, D, R, NT, W>;
   constexpr int kAhead = C::kPair ? R - 1 : (R + 1) / 2;   // block ids in hand
 
   constexpr int kK = D / 16;
@@ -113,7 +115,8 @@ __global__ void __launch_bounds__(128, MINB) decode_window_kernel(
   const int nsb = n_first + static_cast<int>((static_cast<unsigned>(seq - wb) + 15u) >> 4);
   const int per = (nsb + S - 1) / S;
   const int v_begin = min(nsb, s * per), v_end = min(nsb, v_begin + per);
-  const int my_n = v_end - v_begin > warp ? (v_end - v_begin - warp + C::kWarps - 1) / C::kWarps : 0;
+  const int left = v_end - v_begin - warp;
+  const int my_n = left > 0 ? (left + C::kWarps - 1) / C::kWarps : 0;
   // First position of the warp's n-th sub-block.
   auto token = [&](int n) {
     const int v = v_begin + warp + n * C::kWarps;
@@ -205,10 +208,9 @@ __global__ void __launch_bounds__(128, MINB) decode_window_kernel(
       // Weights of unseen tokens are 0, but 0 * NaN is not: clear their rows.
       for (int c = lane; c < 16 * KV::kChunks; c += 32) {
         const int r = c / KV::kChunks;
+        const uint32_t dst = vb + KV::at(r, c % KV::kChunks);
         if (!(ok && visible(tb + r)))
-          asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(vb + KV::at(r, c % KV::kChunks)),
-                       "r"(0u)
-                       : "memory");
+          asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(dst), "r"(0u) : "memory");
       }
       tc::fence_proxy_async_smem();   // before a later TMA box lands here
       __syncwarp();
@@ -307,16 +309,16 @@ __global__ void __launch_bounds__(128, MINB) decode_window_kernel(
   for (int idx = s * C::kThreads + threadIdx.x; idx < grp * D; idx += S * C::kThreads) {
     const int r = idx / D, e = idx % D;
     const uint32_t oa = o_at + (r * KV::kOStride + KV::place(e)) * 4, ca = c_at + r * 4;
-    float m[16], M = -CUDART_INF_F;
+    float m[kMaxShares], M = -CUDART_INF_F;
 #pragma unroll
-    for (int k = 0; k < 16; ++k) {
+    for (int k = 0; k < kMaxShares; ++k) {
       m[k] = k < S ? ld_remote(tc::map_to_rank(ca, k)) : -CUDART_INF_F;
       M = fmaxf(M, m[k]);
     }
     float L = 0.f, LR = 0.f, acc = 0.f;
     if (M != -CUDART_INF_F) {
 #pragma unroll
-      for (int k = 0; k < 16; ++k) {
+      for (int k = 0; k < kMaxShares; ++k) {
         if (k < S) {
           const float f = fast_exp2(m[k] - M);
           L += f * ld_remote(tc::map_to_rank(ca + C::kHeads * 4, k));
@@ -357,25 +359,15 @@ bool make_tile_map(CUtensorMap* map, const DecodeWindowLaunch& n) {
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <class KV, int D, int R, int NT, int MINB>
+template <class KV, int D, int R, int NT, int W, int MINB>
 cudaError_t launch_t(const DecodeWindowLaunch& n, const WindowArgs& a, int S, cudaStream_t stream) {
-  using C = WindowCfg<KV, D, R, NT>;
-  auto kern = decode_window_kernel<KV, D, R, NT, MINB>;
+  using C = WindowCfg<KV, D, R, NT, W>;
+  auto kern = decode_window_kernel<KV, D, R, NT, W, MINB>;
   CUtensorMap map;
   if (!make_tile_map(&map, n)) return cudaErrorInvalidValue;
-  static DeviceFlags smem_set, cluster_set;
+  static DeviceFlags smem_set;
   cudaError_t e = set_smem_once(kern, C::kSmemBytes, smem_set);
   if (e != cudaSuccess) return e;
-  if (S > 8) {
-    // Clusters of more than 8 CTAs are opt-in.
-    int dev = 0;
-    if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
-    if (dev >= 64 || !cluster_set.done[dev]) {
-      e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-      if (e != cudaSuccess) return e;
-      if (dev < 64) cluster_set.done[dev] = true;
-    }
-  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(S, n.Hkv, n.N);
   cfg.blockDim = dim3(C::kThreads);
@@ -393,18 +385,36 @@ cudaError_t launch_t(const DecodeWindowLaunch& n, const WindowArgs& a, int S, cu
   return cudaLaunchKernelEx(&cfg, kern, map, a);
 }
 
+template <class KV, int D, int R, int NT, int MINB>
+cudaError_t launch_warps(const DecodeWindowLaunch& n, const WindowArgs& a, int S, int warps,
+                         cudaStream_t stream) {
+  return warps == 8 ? launch_t<KV, D, R, NT, 8, 3 - NT>(n, a, S, stream)
+                    : launch_t<KV, D, R, NT, 4, MINB>(n, a, S, stream);
+}
+
 }  // namespace
 
-// CTAs per (request, kv head): as many as leave at most two per SM, up to 16,
+// CTAs per (request, kv head): as many as leave at most two per SM, up to 8,
 // and at least 64 tokens to each.  More CTAs cost more than they bring, since
-// each pays for its start, its merge and its cluster: 64 requests x 8 heads
-// (window 1024) take 42.5 us on one CTA each, 49.4 on two, 54.5 on four; 8 x 8
-// (window 4096) 62.1 on one, 36.3 on two, 26.7 on four, 27.1 on eight; 1 x 8
-// 61.6 on one, 13.5 on eight, 11.4 on sixteen.
+// each pays for its start, its merge and its cluster (an empty call takes 2.6
+// us without a cluster, 4.7 with one of 8, 5.6 with one of 16): 64 requests x 8
+// heads (window 1024) take 42.5 us on one CTA each, 49.4 on two, 54.5 on four;
+// 8 x 8 (window 4096) 62.1 on one, 36.3 on two, 26.7 on four, 27.1 on eight; 1
+// x 8 61.7 on one, 21.2 on four, 13.5 on eight.
 int decode_window_shares(int N, int Hkv, long long visible, int sm_count) {
   const long long units = static_cast<long long>(N) * Hkv;
-  const long long s = std::min({16LL, 2LL * sm_count / units, visible / 64});
+  const long long s =
+      std::min({static_cast<long long>(kMaxShares), 2LL * sm_count / units, visible / 64});
   return s < 1 ? 1 : static_cast<int>(s);
+}
+
+// Warps per CTA: 8 where no SM gets a second CTA, or where a share is long
+// (and registers leave room for two such CTAs); else 4, so that twice as many
+// CTAs are resident.  8 against 4: one request x 8 heads 10.7 us (13.5), 64 x 8
+// at 4100 tokens each 137.5 (140), 128 x 8 over an e4m3 pool 152 (164); but 64
+// x 8 at 1028 tokens 43.2 (42.5), over an e4m3 pool 31.8 (26.8).
+int decode_window_warps(long long ctas, long long share, bool wide, int sm_count) {
+  return ctas <= sm_count || (share >= 4096 && !wide) ? 8 : 4;
 }
 
 cudaError_t launch_decode_window(const DecodeWindowLaunch& n, cudaStream_t stream) {
@@ -431,20 +441,22 @@ cudaError_t launch_decode_window(const DecodeWindowLaunch& n, cudaStream_t strea
   const bool wide = n.Hq / n.Hkv > 8;   // groups of 9..16 heads take two n-tiles
   using dec::KvBf16;
   using dec::KvE4m3;
-  // Ring places and CTAs per SM (48 KB of ring each, 4 warps; the two-n-tile
-  // forms are held to fewer by their registers).
+  const int warps = decode_window_warps(static_cast<long long>(S) * n.Hkv * n.N, visible / S,
+                                        wide, n.sm_count);
+  // Ring places, n-tiles and, with four warps, CTAs per SM (48 KB of ring each;
+  // the two-n-tile forms are held to fewer by their registers).
   if (n.fp8) {
     if (n.d == 128)
-      return wide ? launch_t<KvE4m3<128>, 128, 3, 2, 3>(n, a, S, stream)
-                  : launch_t<KvE4m3<128>, 128, 3, 1, 4>(n, a, S, stream);
-    return wide ? launch_t<KvE4m3<64>, 64, 6, 2, 4>(n, a, S, stream)
-                : launch_t<KvE4m3<64>, 64, 6, 1, 4>(n, a, S, stream);
+      return wide ? launch_warps<KvE4m3<128>, 128, 3, 2, 3>(n, a, S, warps, stream)
+                  : launch_warps<KvE4m3<128>, 128, 3, 1, 4>(n, a, S, warps, stream);
+    return wide ? launch_warps<KvE4m3<64>, 64, 6, 2, 4>(n, a, S, warps, stream)
+                : launch_warps<KvE4m3<64>, 64, 6, 1, 4>(n, a, S, warps, stream);
   }
   if (n.d == 128)
-    return wide ? launch_t<KvBf16<128>, 128, 3, 2, 2>(n, a, S, stream)
-                : launch_t<KvBf16<128>, 128, 3, 1, 4>(n, a, S, stream);
-  return wide ? launch_t<KvBf16<64>, 64, 3, 2, 3>(n, a, S, stream)
-              : launch_t<KvBf16<64>, 64, 3, 1, 4>(n, a, S, stream);
+    return wide ? launch_warps<KvBf16<128>, 128, 3, 2, 2>(n, a, S, warps, stream)
+                : launch_warps<KvBf16<128>, 128, 3, 1, 4>(n, a, S, warps, stream);
+  return wide ? launch_warps<KvBf16<64>, 64, 3, 2, 3>(n, a, S, warps, stream)
+              : launch_warps<KvBf16<64>, 64, 3, 1, 4>(n, a, S, warps, stream);
 }
 
 }  // namespace pa
