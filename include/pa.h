@@ -493,6 +493,7 @@ pa_status pa_qk_norm_rope_cache_fp8(const void* q, const void* key, const void* 
  * request sees (between the first tokens and the oldest window) are not
  * read: their table entries and contents may be anything.  A position that
  * one row of a request sees must hold finite values, as for pa_varlen_fwd.
+ * Supported: head_size in {64, 128}, Hq / Hkv <= 128.
  */
 pa_status pa_varlen_fwd_sinks(const void* q, const void* kv_cache, const int32_t* block_table,
                               const int32_t* query_start_loc, const int32_t* seq_lens,

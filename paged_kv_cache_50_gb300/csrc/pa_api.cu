@@ -277,6 +277,7 @@ pa_status pa_varlen_fwd_sinks(const void* q, const void* kv_cache, const int32_t
   if (!shape_ok(shape) || total_q < 0 || max_query_len < 0 || sliding_window < 1 || num_sinks < 0)
     return PA_ERR_INVALID;
   if (shape->head_size != 64 && shape->head_size != 128) return PA_ERR_UNSUPPORTED;
+  if (shape->num_q_heads / shape->num_kv_heads > 128) return PA_ERR_UNSUPPORTED;
   if (total_q == 0 || shape->num_seqs == 0 || max_query_len == 0) return PA_OK;
   if (q == nullptr || kv_cache == nullptr || block_table == nullptr ||
       query_start_loc == nullptr || seq_lens == nullptr || out == nullptr)
@@ -284,10 +285,28 @@ pa_status pa_varlen_fwd_sinks(const void* q, const void* kv_cache, const int32_t
   if (!aligned(q, 16) || !aligned(kv_cache, 16) || !aligned(out, 16) || !aligned(lse, 4) ||
       !aligned(block_table, 4) || !aligned(query_start_loc, 4) || !aligned(seq_lens, 4))
     return PA_ERR_INVALID;
-  pa::VarlenLaunch L = varlen_launch(q, kv_cache, block_table, query_start_loc, seq_lens,
-                                     max_query_len, shape, scale, 1, sliding_window, out, lse);
-  L.sinks = num_sinks;
-  return from_cuda(pa::launch_varlen_tc(L, static_cast<cudaStream_t>(stream)));
+  pa::WindowPrefillLaunch n{};
+  n.q = q;
+  n.cache = kv_cache;
+  n.block_table = block_table;
+  n.qsl = query_start_loc;
+  n.seq_lens = seq_lens;
+  n.N = shape->num_seqs;
+  n.Hq = shape->num_q_heads;
+  n.Hkv = shape->num_kv_heads;
+  n.d = shape->head_size;
+  n.bs = shape->block_size;
+  n.num_blocks = shape->num_blocks;
+  n.max_blocks = shape->max_blocks_per_seq;
+  n.total_q = total_q;
+  n.max_query_len = max_query_len;
+  n.scale = scale;
+  n.window = sliding_window;
+  n.sinks = num_sinks;
+  n.out = out;
+  n.lse = lse;
+  n.err = device_error_ptr();
+  return from_cuda(pa::launch_window_prefill(n, static_cast<cudaStream_t>(stream)));
 }
 
 int pa_cascade_prefix_splits(int total_q, int num_q_heads, int num_kv_heads,

@@ -96,11 +96,25 @@ struct VarlenLaunch {
   const void* mla_k = nullptr;
   const void* mla_v = nullptr;
   int mla_s_max = 0;
-  // >= 0: a sliding window (`window`, causal) whose first `sinks` positions
-  // stay visible, and none of the split, offset or partial-output fields.
-  int sinks = -1;
 };
 cudaError_t launch_varlen_tc(const VarlenLaunch& L, cudaStream_t stream);
+
+// Varlen attention with a causal sliding window and first tokens that stay
+// visible (Hq / Hkv <= 128).
+struct WindowPrefillLaunch {
+  const void* q;
+  const void* cache;
+  const int32_t* block_table;
+  const int32_t* qsl;
+  const int32_t* seq_lens;
+  int N, Hq, Hkv, d, bs, num_blocks, max_blocks, total_q, max_query_len;
+  float scale;
+  int window, sinks;
+  void* out;    // bf16 [T, Hq, d]
+  float* lse;   // [T, Hq], nullable
+  int* err;
+};
+cudaError_t launch_window_prefill(const WindowPrefillLaunch& n, cudaStream_t stream);
 
 // Decode with a sliding window and first tokens that stay visible, bf16 or
 // e4m3 pool, in one launch.

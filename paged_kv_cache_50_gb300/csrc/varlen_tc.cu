@@ -49,7 +49,7 @@
 
 #include "pa_common.cuh"
 #include "pa_launch.h"
-#include "tc_common.cuh"
+#include "tc_tiles.cuh"
 
 namespace pa {
 
@@ -83,29 +83,6 @@ struct TcCfg {
   __host__ __device__ static constexpr uint32_t col_o(int x) { return 256u + 128u * x; }
 };
 
-// Byte offset of 16-byte chunk `c` (0..7) of row `r` in a 128-byte swizzled
-// [rows][128 B] region.
-__device__ __forceinline__ uint32_t sw128(int r, int c) {
-  return static_cast<uint32_t>((r >> 3) * 1024 + (r & 7) * 128 + ((c ^ (r & 7)) << 4));
-}
-
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float y;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
-  return y;
-}
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-// The lowest n bits (none for n <= 0, all for n >= 32).
-__device__ __forceinline__ uint32_t bits_below(int n) {
-  return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
-}
-
 // Barriers; pairs are indexed by stage (j & 1) or by Q tile x.
 enum TcBar {
   kQFull = 0,
@@ -132,7 +109,6 @@ struct VarlenArgs {
   float scale_log2;
   int causal;
   int window;       // > 0: sliding window (causal), row at p sees p - window < p' <= p
-  int sinks;        // FIRST kernels: ... or p' < sinks
   __nv_bfloat16* out;
   float* lse;
   int* err;
@@ -164,13 +140,7 @@ __device__ int2 g_test_skip = {-1, -1};
 // MLA = true: keys and values come from the contiguous expanded workspaces
 // of the MLA prefill (k_map over [N * s_max][H][DK], v_map over
 // [N * s_max][H][DV]) instead of the paged pool; no block table.
-// FIRST = true: causal sliding window whose first `sinks` positions stay
-// visible, and nothing else of EXT.  The context becomes a list of 16-token
-// pieces -- those of the first tokens, then those from the CTA's oldest
-// visible position rounded down to 16 -- and a K/V tile is eight pieces of the
-// list, so a handful of first tokens costs one piece (1/8 of a tile) and the
-// window starts at a piece instead of a tile.
-template <int DK, int DV, int BN, int VST, bool EXT, bool MLA, bool FIRST = false>
+template <int DK, int DV, int BN, int VST, bool EXT, bool MLA>
 __global__ void __launch_bounds__(384, 1)
 varlen_tc_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant__ CUtensorMap v_map,
                  const __grid_constant__ VarlenArgs a) {
@@ -188,7 +158,7 @@ varlen_tc_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_consta
   const __nv_bfloat16* __restrict__ q = a.q;
   const int32_t* __restrict__ block_table = a.block_table;
   const int Hq = a.Hq, Hkv = a.Hkv, bs = a.bs, num_blocks = a.num_blocks;
-  const int causal = FIRST ? 1 : a.causal, window = EXT || FIRST ? a.window : 0;
+  const int causal = a.causal, window = EXT ? a.window : 0;
   const int table_col0 = EXT ? a.table_col0 : 0, seq_off = EXT ? a.seq_off : 0;
   const int kv_splits = EXT ? a.kv_splits : 1;
   float* const ws = EXT ? a.ws : nullptr;
@@ -231,17 +201,7 @@ varlen_tc_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_consta
   // before ctx + q_first + 1 - window, so the tiles start at that position
   // rounded down to a tile; later rows mask their own lower bound.
   int tbase = 0;
-  // FIRST: the CTA's oldest visible position, the pieces of the first tokens
-  // (0 where they meet the window: one run from position 0) and of the list.
-  int lo_cta = 0, n_first = 0, npieces = 0;
-  if (FIRST) {
-    const int q_first = min(qt * C::kRows, rows_total - 1) / grp;
-    lo_cta = max(0, ctx + q_first + 1 - window);
-    n_first = (min(a.sinks, kv_end) + 15) >> 4;
-    tbase = lo_cta & ~15;
-    if (tbase <= 16 * n_first) tbase = n_first = 0;
-    npieces = n_first + ((max(0, kv_end - tbase) + 15) >> 4);
-  } else if (window > 0) {
+  if (window > 0) {
     const int q_first = min(qt * C::kRows, rows_total - 1) / grp;
     tbase = max(0, ctx + q_first + 1 - window) / C::kBN * C::kBN;
   }
@@ -252,15 +212,8 @@ varlen_tc_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_consta
     tbase = static_cast<int>(max(static_cast<long long>(tbase), s0));
     if (split < kv_splits - 1) kv_end = static_cast<int>(min(static_cast<long long>(kv_end), s0 + a.kv_chunk));
   }
-  if (!FIRST) tbase = min(tbase, kv_end);
-  const int ntiles = FIRST ? (npieces + C::kBN / 16 - 1) / (C::kBN / 16)
-                           : (kv_end - tbase + C::kBN - 1) / C::kBN;
-  // First position of piece pc of tile j.
-  auto piece_tok = [&](int j, int pc) -> int {
-    if (!FIRST) return tbase + j * C::kBN + 16 * pc;
-    const int v = j * (C::kBN / 16) + pc;
-    return v < n_first ? 16 * v : tbase + 16 * (v - n_first);
-  };
+  tbase = min(tbase, kv_end);
+  const int ntiles = (kv_end - tbase + C::kBN - 1) / C::kBN;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int32_t* table =
@@ -360,8 +313,7 @@ varlen_tc_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_consta
     float m_used = -CUDART_INF_F, l = 0.f, lr = 0.f;
     for (int j = 0; j < ntiles; ++j) {
       if (__any_sync(0xffffffffu, *abort_flag != 0)) break;
-      // Position of column 0; FIRST: as if the tile held no first tokens.
-      const int tok0 = tbase + j * C::kBN - (FIRST ? 16 * n_first : 0);
+      const int tok0 = tbase + j * C::kBN;
       if (!wait_warp(BAR(kSFull + x), j & 1)) break;
       tc::tc_fence_after();
       // Loaded pieces of this tile, from the producer's ring (written before
@@ -390,29 +342,7 @@ varlen_tc_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_consta
       }
       // Mask only where some column is not visible (the diagonal tile, the
       // end of the sequence, the window's start, an unloaded piece).
-      if (FIRST) {
-        if (!(tok0 + C::kBN <= lim && tok0 >= lo && tok0 >= tbase &&
-              vm == (1u << (C::kBN / 16)) - 1u)) {
-          // Visible columns as bits: the window's range [wa, wb), past the
-          // columns of the first tokens' pieces, and the first tokens [0, fe).
-          const int cf = max(0, min(16 * n_first - j * C::kBN, C::kBN));
-          const int wa = max(lo - tok0, cf), wb = lim - tok0;
-          const int fe = cf > 0 ? min(cf, min(a.sinks, lim) - j * C::kBN)
-                                : min(a.sinks, lim) - tok0;
-#pragma unroll
-          for (int w = 0; w < C::kBN / 32; ++w) {
-            const uint32_t loaded = ((vm >> (2 * w)) & 1u ? 0xffffu : 0u) |
-                                    ((vm >> (2 * w + 1)) & 1u ? 0xffff0000u : 0u);
-            const uint32_t bits = ((bits_below(wb - 32 * w) & ~bits_below(wa - 32 * w)) |
-                                   bits_below(fe - 32 * w)) & loaded;
-            if (bits != 0xffffffffu) {
-#pragma unroll
-              for (int c = 0; c < 32; ++c)
-                s[32 * w + c] = (bits >> c) & 1u ? s[32 * w + c] : -CUDART_INF_F;
-            }
-          }
-        }
-      } else if (!(tok0 + C::kBN <= lim && tok0 >= lo && vm == (1u << (C::kBN / 16)) - 1u)) {
+      if (!(tok0 + C::kBN <= lim && tok0 >= lo && vm == (1u << (C::kBN / 16)) - 1u)) {
 #pragma unroll
         for (int col = 0; col < C::kBN; ++col) {
           const bool vis = (tok0 + col < lim) && (tok0 + col >= lo) && ((vm >> (col >> 4)) & 1u);
@@ -455,11 +385,9 @@ varlen_tc_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_consta
       // before it publishes its own P: PV_0(j) and PV_1(j) go out in either
       // order.  Both write zeros, so the overlap is harmless.
       {
-        // FIRST: rows that no query of the CTA sees may hold anything.
-        const int tok = FIRST ? piece_tok(j, t >> 4) + (t & 15) : tok0 + t;
-        const bool seen = FIRST ? tok < kv_end && (tok >= lo_cta || tok < a.sinks) : tok < seq;
+        const int tok = tok0 + t;
         // Threads past the tile's kBN rows own no V row.
-        const bool row_ok = t >= C::kBN || (seen && ((vm >> (t >> 4)) & 1u));
+        const bool row_ok = t >= C::kBN || (tok < seq && ((vm >> (t >> 4)) & 1u));
         if (!row_ok) {
           if (!tc::mbar_wait(BAR(kVFull + j % C::kVStages), (j / C::kVStages) & 1)) fail();
           const uint32_t vbase = sbase + C::kOffV + (j % C::kVStages) * C::kVBytes;
@@ -698,13 +626,12 @@ varlen_tc_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_consta
     const bool box_lane = lane < C::kBN / 16;
     const bool my_piece = box_lane;
     auto in_range = [&](int j) -> bool {
-      if (FIRST) return box_lane && j * (C::kBN / 16) + pc < npieces;
       return box_lane && j < ntiles && tbase + j * C::kBN + 16 * pc < kv_end;
     };
     auto raw_of = [&](int j) -> int {
       if (!in_range(j)) return -1;
       if (MLA) return 0;   // contiguous workspace: every in-range piece is loaded
-      const int idx = piece_tok(j, pc) / bs;
+      const int idx = (tbase + j * C::kBN + 16 * pc) / bs;
       return idx < max_blocks ? __ldg(table + idx) : -1;
     };
     // The piece's block id, -1 (not visible) or -2 (invalid id).
@@ -712,7 +639,7 @@ varlen_tc_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_consta
       return !in_range(j) ? -1 : (raw >= 0 && raw < num_blocks) ? raw : -2;
     };
     auto issue = [&](int j, int blk, int which, uint32_t dst, uint32_t full) {
-      const int ptok = piece_tok(j, pc);
+      const int tok0 = tbase + j * C::kBN;
       const unsigned loaded = __ballot_sync(0xffffffffu, blk >= 0);
       const unsigned bad = __ballot_sync(0xffffffffu, blk == -2);
       if (lane == 0) {
@@ -725,7 +652,7 @@ varlen_tc_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_consta
       __syncwarp();
       if (MLA && my_piece && blk >= 0) {
         // Token row (request i, position tok0 + 16 pc) of the workspace.
-        const int row = static_cast<int>(static_cast<long long>(i) * a.mla_s_max + ptok);
+        const int row = static_cast<int>(static_cast<long long>(i) * a.mla_s_max + tok0 + 16 * pc);
         const int halves = which == 0 ? C::kHalvesK : C::kHalvesV;
         for (int h = 0; h < halves; ++h)
           tc::tma_load_3d(dst + h * (C::kBN * 128) + pc * C::kPieceBytes,
@@ -733,13 +660,13 @@ varlen_tc_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_consta
       } else if (!MLA && my_piece && blk >= 0 && which == 1) {
         // V: both halves of the piece in one box (tensor map coordinates:
         // column 0, token, half 0, head, 2 * block + 1).
-        tc::tma_load_5d(dst + pc * kVPiece, &v_map, full, 0, ptok % bs, 0, kvh,
+        tc::tma_load_5d(dst + pc * kVPiece, &v_map, full, 0, (tok0 + 16 * pc) % bs, 0, kvh,
                         2 * blk + 1);
       } else if (!MLA && my_piece && blk >= 0) {
 #pragma unroll
         for (int h = 0; h < C::kHalvesK; ++h) {
           tc::tma_load_5d(dst + h * (C::kBN * 128) + pc * C::kPieceBytes, &kv_map, full, h * 64, kvh,
-                          ptok % bs, which, blk);
+                          (tok0 + 16 * pc) % bs, which, blk);
         }
       }
     };
@@ -808,46 +735,6 @@ varlen_tc_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_consta
 
 // ---------------------------------------------------------------- host side
 
-namespace {
-
-// 5-D view of the standard pool [nb][2][bs][Hkv][d] (innermost first) with a
-// 64-element x 1 head x 16 token box and 128-byte swizzle.
-bool make_kv_map(CUtensorMap* map, const void* cache, int nb, int bs, int Hkv, int d) {
-  auto fn = tensor_map_encoder();
-  if (fn == nullptr) return false;
-  const cuuint64_t dims[5] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(Hkv),
-                              static_cast<cuuint64_t>(bs), 2, static_cast<cuuint64_t>(nb)};
-  const cuuint64_t row = static_cast<cuuint64_t>(d) * 2;
-  const cuuint64_t strides[4] = {row, row * Hkv, row * Hkv * bs, row * Hkv * bs * 2};
-  const cuuint32_t box[5] = {64, 1, 16, 1, 1};
-  const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
-  CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(cache), dims,
-                  strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS;
-}
-
-// The V half of the same pool viewed 5-D so that one box holds a 16-token
-// piece's 64-column halves as consecutive 128-byte-swizzled [16][128 B]
-// tiles: dims (innermost first) 64 columns, bs tokens, d/64 halves, Hkv
-// heads, 2 nb (kv index + 2 * block); box 64 x 16 x d/64 x 1 x 1.
-bool make_v_map(CUtensorMap* map, const void* cache, int nb, int bs, int Hkv, int d) {
-  auto fn = tensor_map_encoder();
-  if (fn == nullptr) return false;
-  const cuuint64_t dims[5] = {64, static_cast<cuuint64_t>(bs), static_cast<cuuint64_t>(d / 64),
-                              static_cast<cuuint64_t>(Hkv), 2 * static_cast<cuuint64_t>(nb)};
-  const cuuint64_t row = static_cast<cuuint64_t>(d) * 2;
-  const cuuint64_t strides[4] = {row * Hkv, 128, row, row * Hkv * bs};
-  const cuuint32_t box[5] = {64, 16, static_cast<cuuint32_t>(d / 64), 1, 1};
-  const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
-  CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(cache), dims,
-                  strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS;
-}
-
-}  // namespace
-
 // MLA prefill workspaces [rows][H][width] viewed 3-D (innermost first):
 // 64-column x 1-head x 16-token boxes, 128-byte swizzle.
 bool make_ws_map(CUtensorMap* map, const void* ws, long long rows, int H, int width) {
@@ -864,7 +751,7 @@ bool make_ws_map(CUtensorMap* map, const void* ws, long long rows, int H, int wi
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int DK, int DV, int BN, int VST, bool EXT, bool MLA, bool FIRST = false>
+template <int DK, int DV, int BN, int VST, bool EXT, bool MLA>
 static cudaError_t launch_varlen_tc_t(const VarlenLaunch& L, cudaStream_t stream) {
   using C = TcCfg<DK, DV, BN, VST>;
   CUtensorMap map, vmap;
@@ -879,7 +766,7 @@ static cudaError_t launch_varlen_tc_t(const VarlenLaunch& L, cudaStream_t stream
         !make_v_map(&vmap, L.cache, L.num_blocks, L.bs, L.Hkv, DV))
       return cudaErrorInvalidValue;
   }
-  auto kern = varlen_tc_kernel<DK, DV, BN, VST, EXT, MLA, FIRST>;
+  auto kern = varlen_tc_kernel<DK, DV, BN, VST, EXT, MLA>;
   static DeviceFlags attr_set;
   cudaError_t e = set_smem_once(kern, C::kSmemBytes, attr_set);
   if (e != cudaSuccess) return e;
@@ -913,7 +800,6 @@ static cudaError_t launch_varlen_tc_t(const VarlenLaunch& L, cudaStream_t stream
   a.scale_log2 = L.scale * kLog2e;
   a.causal = L.causal;
   a.window = L.window;
-  a.sinks = L.sinks;
   a.out = static_cast<__nv_bfloat16*>(L.out);
   a.lse = L.lse;
   a.err = L.err;
@@ -956,9 +842,6 @@ extern "C" int pa_test_skip_tile_loads(int cta, int tile) {
 cudaError_t launch_varlen_tc(const VarlenLaunch& L, cudaStream_t stream) {
   if (L.mla_k != nullptr)   // MLA prefill attention: [nope | rope] keys, 128-wide values
     return launch_varlen_tc_t<192, 128, 128, 1, false, true>(L, stream);
-  if (L.sinks >= 0)
-    return L.d == 128 ? launch_varlen_tc_t<128, 128, 128, 2, false, false, true>(L, stream)
-                      : launch_varlen_tc_t<64, 64, 128, 2, false, false, true>(L, stream);
   const bool ext = L.window > 0 || L.kv_splits > 1 || L.ws != nullptr || L.virt_total_q > 0 ||
                    L.table_col0 != 0 || L.seq_off != 0;
   if (L.d == 128)

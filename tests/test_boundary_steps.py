@@ -110,6 +110,7 @@ def test_windowed_attention_refusals(pa):
         assert f(shape=_shape(pa, num_seqs=0), ptrs=(NULL,) * n) == pa.PA_OK
     assert varlen(total=-1) == pa.PA_ERR_INVALID
     assert varlen(total=0, ptrs=(NULL,) * 5) == pa.PA_OK
+    assert varlen(shape=_shape(pa, num_q_heads=258)) == pa.PA_ERR_UNSUPPORTED
     wide = _shape(pa, num_q_heads=34)
     assert decode(shape=wide) == decode8(shape=wide) == pa.PA_ERR_UNSUPPORTED
     for bad in (0.0, -1.0, float("inf"), float("nan")):

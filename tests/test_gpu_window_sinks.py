@@ -103,6 +103,9 @@ PREFILL = {
     "g5_bs48": ([400, 290], [150, 257], 10, 2, 64, 48),
     "g1_bs256": ([513, 1030], [513, 400], 3, 3, 128, 256),
     "late_chunk": ([2100], [70], 12, 4, 128, 16),
+    "g128_d64": ([40, 300], [7, 33], 128, 1, 64, 16),
+    "g100": ([70, 140], [12, 5], 100, 1, 128, 32),
+    "many_empty": ([1, 400, 2, 3, 1, 30], [1, 400, 1, 2, 1, 1], 8, 4, 64, 16),
 }
 MASKS = [(1, 0), (1, 1), (7, 2), (16, 16), (100, 4), (128, 0), (129, 17), (64, 15), (250, 130),
          (300, 256), (33, 400), (BIG, 0), (5, BIG)]
