@@ -26,6 +26,27 @@
 //  * A piece's keys come in one TMA box (as its values do), both 64-column
 //    halves interleaved by 8-row groups.
 //
+//  * Code is kept short.  Unrolled over a tile's 128 columns, with masks,
+//    rescaling and output inline, the hot loops did not fit the SM's
+//    instruction cache and the GPC's second level ran at 86 % of its rate (364
+//    us on the batch below).  So each row's maximum comes with the TMEM load
+//    itself (tcgen05.ld.red), weights are made 32 columns at a time in a loop
+//    that reads S again, and masks are written back into S beforehand.
+//  * The MMA thread's instructions bound the tile rate next: descriptors are
+//    formed by one addition each, and the thread is chosen by elect.sync, so
+//    that they live in uniform registers.
+//
+// Bound by the chain S -> softmax -> PV -> S of a Q tile (~3200 of a 128-token
+// tile pair's ~3300 cycles; its MMAs take 2290) and, at a unit's ends, by mask
+// and output code that is not in the instruction cache.  Measured (d 128, 16
+// requests of U[256, 2048] new tokens, 32 / 8 heads, window 1024, 4 first
+// tokens): 285 us, 1035 TFLOP/s; 8192 tokens of 64 / 8 heads, window 4096: 769
+// us, 1430 TFLOP/s; varlen_tc.cu's kernel with the same mask, one unit per CTA
+// and 128-token steps, took 419 and 1016.  Steps: persistent CTAs 365 / 953;
+// the short loops 318 / 880; descriptors 301 / 818; elect.sync 286 / 778.  Two
+// MMA threads (368 / 1008), the next unit's first S between the last PVs (328 /
+// 915) and one loop for all S (354 / 1012) were slower.
+//
 // Warp roles (384 threads): warp 0 MMA issue; warp 1 K/V producer (lane p:
 // piece p); warp 2 units and queries; warp 3 idle; warps 4-7 / 8-11 softmax and
 // output of Q tile 0 / 1.  Every wait is bounded; a CTA whose wait runs out sets
@@ -35,6 +56,7 @@
 #include <math_constants.h>
 
 #include <algorithm>
+#include <type_traits>
 #include <climits>
 
 #include "pa_common.cuh"
@@ -60,8 +82,6 @@ struct WinCfg {
   static constexpr int kSmemBytes = kOffBar + 512 + 1024;   // control block + alignment slack
   static constexpr uint32_t kTmemCols = 512;
   static constexpr int kThreads = 384;
-  static constexpr uint32_t kRegSoftmax = 216;
-  static constexpr uint32_t kRegOther = 56;
   __host__ __device__ static constexpr uint32_t col_s(int x) { return 128u * x; }
   __host__ __device__ static constexpr uint32_t col_o(int x) { return 256u + 128u * x; }
 };
@@ -75,8 +95,8 @@ enum WinBar {
   kVFull = 8,
   kVEmpty = 10,
   kSFull = 12,    // [x]
-  kPLo = 14,      // [x] P of tokens 0-63 written
-  kPHi = 16,      // [x] P of tokens 64-127 written
+  kPLo = 14,      // [x] P of tokens 0-95 written
+  kPHi = 16,      // [x] P of tokens 96-127 written
   kODone = 18,    // [x] the unit's last PV_x has been computed
   kUnitFull = 20, // [unit & 1] unit descriptor written
   kUnitEmpty = 22,// [unit & 1] ... read by everyone
@@ -98,17 +118,21 @@ constexpr int kPieceRing = 4;
 // What a unit is (in shared memory, 64 bytes each).
 struct Unit {
   int live;       // 0: no more units
-  int request, kvh, q0, rows, tile;   // rows: packed rows of the request; tile: which 2 x RT of them
+  int request, kvh, q0;
+  int rows, tile;   // packed rows of the request, and which two Q tiles of them
   int seq, ctx;
-  int first, oldest, base, end, pieces, tiles;   // list of pieces, see unit_of
+  // The unit sees [oldest, end) and the first tokens: `first` pieces from
+  // position 0, then pieces from `base`.
+  int first, oldest, base, end, pieces, tiles;
 };
-static_assert(sizeof(Unit) <= 64 && kOffUnits + 2 * 64 <= 512 && kOffAbort + 4 <= kOffClc, "layout");
+static_assert(sizeof(Unit) <= 64 && kOffUnits + 2 * 64 <= 512 && kOffAbort + 4 <= kOffClc,
+              "layout");
 
 struct WinArgs {
   const int32_t* block_table;
   const int32_t* qsl;
   const int32_t* seq_lens;
-  int max_blocks, Hq, Hkv, grp, bs, num_blocks;
+  int max_blocks, Hq, Hkv, grp, bs, bs_log2, num_blocks;
   int row_tokens;   // query rows of a Q tile: 128 / grp
   int total_q;
   float scale_log2;
@@ -121,6 +145,66 @@ struct WinArgs {
 // The lowest n bits (none for n <= 0, all for n >= 32).
 __device__ __forceinline__ uint32_t bits_below(int n) {
   return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
+}
+
+// 32 consecutive fp32 columns of this thread's TMEM lane and their maximum
+// (warp-collective).
+__device__ __forceinline__ void tmem_ld32_max(uint32_t taddr, uint32_t (&r)[32], float& mx) {
+  asm volatile(
+      "tcgen05.ld.red.sync.aligned.32x32b.x32.max.f32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, %32, [%33];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]),
+        "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+        "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
+        "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]),
+        "=r"(r[30]), "=r"(r[31]), "=f"(mx)
+      : "r"(taddr));
+}
+
+// Whether a phase has completed, without waiting (try_wait may suspend).
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n.reg .pred p;\nmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+      "selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(done)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return done != 0;
+}
+
+// D[tmem] (+)= A B with descriptors given as their low words and a common high
+// word each (bits 32-63: stride offset, version, swizzle).
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo,
+                                       uint32_t b_hi, uint32_t idesc, bool acc) {
+  asm volatile(
+      "{\n.reg .pred p;\n.reg .b64 da, db;\nsetp.ne.b32 p, %6, 0;\n"
+      "mov.b64 da, {%1, %2};\nmov.b64 db, {%3, %4};\n"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %5, p;\n}\n" ::"r"(d),
+      "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(static_cast<uint32_t>(acc))
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a_tmem, uint32_t b_lo, uint32_t b_hi,
+                                       uint32_t idesc, bool acc) {
+  asm volatile(
+      "{\n.reg .pred p;\n.reg .b64 db;\nsetp.ne.b32 p, %5, 0;\nmov.b64 db, {%2, %3};\n"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %4, p;\n}\n" ::"r"(d),
+      "r"(a_tmem), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(static_cast<uint32_t>(acc))
+      : "memory");
+}
+template <int K>
+using Step = std::integral_constant<int, K>;   // a 16-token step of a tile
+constexpr uint32_t desc_hi(uint32_t sbo) { return (sbo >> 4) | (1u << 14) | (2u << 29); }
+
+// True in one thread of the (converged) warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}\n"
+               : "=r"(p));
+  return p != 0;
 }
 
 // Asks for the launch of one more CTA to be cancelled in favour of this one;
@@ -153,7 +237,8 @@ __device__ __forceinline__ bool clc_answer(uint32_t resp, int& x, int& y, int& z
 
 template <int D>
 __global__ void __launch_bounds__(384, 1)
-window_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
+window_tc_kernel(const __grid_constant__ CUtensorMap q_map,
+                 const __grid_constant__ CUtensorMap k_map,
                  const __grid_constant__ CUtensorMap v_map, const __grid_constant__ WinArgs a) {
   using C = WinCfg<D>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -166,9 +251,8 @@ window_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
   // Ring of loaded-piece masks: (tile << 8) | mask in slot tile % kPieceRing,
   // written by the producer before the tile's K is issued.
   volatile uint32_t* piece_ring = reinterpret_cast<volatile uint32_t*>(ctl + kOffRing);
-  volatile Unit* units = reinterpret_cast<volatile Unit*>(ctl + kOffUnits);   // 64 bytes apart
   auto unit_slot = [&](int u) {
-    return reinterpret_cast<volatile Unit*>(reinterpret_cast<volatile uint8_t*>(units) + 64 * (u & 1));
+    return reinterpret_cast<volatile Unit*>(ctl + kOffUnits + 64 * (u & 1));
   };
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -209,11 +293,6 @@ window_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
   };
   // Inputs and the output buffer may belong to the previous kernel until here.
   pdl_wait();
-
-  if (warp >= 4)
-    tc::reg_alloc<C::kRegSoftmax>();
-  else
-    tc::reg_dealloc<C::kRegOther>();
 
   if (warp >= 4) {
     // ------------------------------------------------------ softmax, output
@@ -268,50 +347,42 @@ window_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
           }
           vm = w & 0xffu;
         }
-        float s[C::kBN];
-        {
-          uint32_t r[C::kBN / 32][32];
-#pragma unroll
-          for (int c = 0; c < C::kBN / 32; ++c) tc::tmem_ld32(ts + c * 32, r[c]);
-          tc::tmem_wait_ld();
-#pragma unroll
-          for (int c = 0; c < C::kBN / 32; ++c)
-#pragma unroll
-            for (int e = 0; e < 32; ++e) s[c * 32 + e] = __uint_as_float(r[c][e]);
-        }
         // Position of column 0 as if the tile held no first tokens; mask only
-        // where some column is not visible.
+        // where some column is not visible.  (Decided for the whole warp, and
+        // done in tensor memory, word by word, so that the code is short.)
         const int tok0 = tbase + j * C::kBN - 16 * n_first;
-        if (!(tok0 + C::kBN <= lim && tok0 >= lo && tok0 >= tbase && vm == 0xffu)) {
+        if (__any_sync(0xffffffffu, !(tok0 + C::kBN <= lim && tok0 >= lo && tok0 >= tbase &&
+                                      vm == 0xffu))) {
           // Visible columns as bits: the window's range [wa, wb), past the
           // columns of the first tokens' pieces, and the first tokens [0, fe).
           const int cf = max(0, min(16 * n_first - j * C::kBN, C::kBN));
           const int wa = max(lo - tok0, cf), wb = lim - tok0;
           const int fe = cf > 0 ? min(cf, min(a.sinks, lim) - j * C::kBN)
                                 : min(a.sinks, lim) - tok0;
-#pragma unroll
+#pragma unroll 1
           for (int w = 0; w < C::kBN / 32; ++w) {
             const uint32_t loaded = ((vm >> (2 * w)) & 1u ? 0xffffu : 0u) |
                                     ((vm >> (2 * w + 1)) & 1u ? 0xffff0000u : 0u);
             const uint32_t bits = ((bits_below(wb - 32 * w) & ~bits_below(wa - 32 * w)) |
                                    bits_below(fe - 32 * w)) & loaded;
-            if (bits != 0xffffffffu) {
+            if (__all_sync(0xffffffffu, bits == 0xffffffffu)) continue;
+            uint32_t r[32];
+            tc::tmem_ld32(ts + w * 32, r);
+            tc::tmem_wait_ld();
 #pragma unroll
-              for (int c = 0; c < 32; ++c)
-                s[32 * w + c] = (bits >> c) & 1u ? s[32 * w + c] : -CUDART_INF_F;
-            }
+            for (int c = 0; c < 32; ++c) r[c] = (bits >> c) & 1u ? r[c] : 0xff800000u;   // -inf
+            tc::tmem_st32(ts + w * 32, r);
           }
+          tc::tmem_wait_st();
         }
         float mx;
         {
-          float m8[8];
+          uint32_t r[C::kBN / 32][32];
+          float m4[C::kBN / 32];
 #pragma unroll
-          for (int k = 0; k < 8; ++k) m8[k] = fmaxf(s[k], s[8 + k]);
-#pragma unroll
-          for (int col = 16; col < C::kBN; col += 16)
-#pragma unroll
-            for (int k = 0; k < 8; ++k) m8[k] = max3(m8[k], s[col + k], s[col + 8 + k]);
-          mx = max3(max3(m8[0], m8[1], m8[2]), max3(m8[3], m8[4], m8[5]), fmaxf(m8[6], m8[7]));
+          for (int c = 0; c < C::kBN / 32; ++c) tmem_ld32_max(ts + c * 32, r[c], m4[c]);
+          tc::tmem_wait_ld();
+          mx = fmaxf(max3(m4[0], m4[1], m4[2]), m4[3]);
           mx *= a.scale_log2;
         }
         const float m_new = fmaxf(m_used, mx);
@@ -321,7 +392,7 @@ window_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
         const float mu = m_used == -CUDART_INF_F ? 0.f : m_used;
         // S_x(j) has landed, hence PV_x(j-1) too: O_x may be rescaled now.
         if (__any_sync(0xffffffffu, need) && j > 0) {
-#pragma unroll
+#pragma unroll 1
           for (int c = 0; c < D / 32; ++c) {
             uint32_t r[32];
             tc::tmem_ld32(to + c * 32, r);
@@ -341,9 +412,9 @@ window_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
             if (!tc::mbar_wait(BAR(kVFull + (g & 1)), (g >> 1) & 1)) fail();
             const uint32_t vbase = sbase + C::kOffV + (g & 1) * C::kTileBytes +
                                    (t >> 4) * C::kPieceBytes;
-#pragma unroll
+#pragma unroll 1
             for (int h = 0; h < C::kHalves; ++h)
-#pragma unroll
+#pragma unroll 1
               for (int c = 0; c < 8; ++c)
                 asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(vbase + h * 2048 +
                                                                            sw128(t & 15, c)),
@@ -353,29 +424,33 @@ window_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
           }
         }
         // P = exp2(s * scale_log2 - m_used) as bf16 pairs over the first 64
-        // columns of the S row, published in two halves.
+        // columns of the S row (behind the columns still to be read), published
+        // after 96 and after 128 tokens: what is left of PV_x for the chain is
+        // two steps.
         {
           float l8[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
           float r8[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int c16 = 0; c16 < C::kBN / 32; ++c16) {
-            uint32_t pk[16];
+#pragma unroll 1
+          for (int c = 0; c < C::kBN / 32; ++c) {
+            uint32_t r[32], pk[16];
+            tc::tmem_ld32(ts + c * 32, r);
+            tc::tmem_wait_ld();
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
-              const int c = c16 * 16 + e;
               float x0, x1;
-              ffma2(x0, x1, s[2 * c], s[2 * c + 1], a.scale_log2, -mu);
+              ffma2(x0, x1, __uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1]), a.scale_log2,
+                    -mu);
               const float p0 = ex2(x0);
               const float p1 = ex2(x1);
               fadd2(l8[2 * (e & 3)], l8[2 * (e & 3) + 1], p0, p1);
               pk[e] = pack_bf16(p0, p1);
               add_bf16x2_f32(r8[2 * (e & 3)], r8[2 * (e & 3) + 1], pk[e]);
             }
-            tc::tmem_st16(ts + c16 * 16, pk);
-            if (c16 == C::kBN / 64 - 1 || c16 == C::kBN / 32 - 1) {
+            tc::tmem_st16(ts + c * 16, pk);
+            if (c >= 2) {
               tc::tmem_wait_st();
               tc::tc_fence_before();
-              tc::mbar_arrive(BAR((c16 == C::kBN / 32 - 1 ? kPHi : kPLo) + x));
+              tc::mbar_arrive(BAR((c == 2 ? kPLo : kPHi) + x));
             }
           }
           l = l * alpha +
@@ -394,30 +469,27 @@ window_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
         // 32-byte stores write whole sectors where `out` is 32-byte aligned.
         const bool a32 = (reinterpret_cast<uintptr_t>(a.out) & 31u) == 0;
         uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + qrow * D);
-#pragma unroll
-        for (int c2 = 0; c2 < D / 64; ++c2) {
-          uint32_t r[2][32];
-          tc::tmem_ld32(to + c2 * 64, r[0]);
-          tc::tmem_ld32(to + c2 * 64 + 32, r[1]);
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t r[32];
+          tc::tmem_ld32(to + c * 32, r);
           tc::tmem_wait_ld();
           if (valid) {
 #pragma unroll
-            for (int k = 0; k < 2; ++k)
+            for (int v = 0; v < 2; ++v) {
+              uint32_t w[8];
 #pragma unroll
-              for (int v = 0; v < 2; ++v) {
-                uint32_t w[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                  w[e] = pack_bf16(__uint_as_float(r[k][v * 16 + 2 * e]) * inv,
-                                   __uint_as_float(r[k][v * 16 + 2 * e + 1]) * inv);
-                uint32_t* p = dst + (c2 * 2 + k) * 16 + v * 8;
-                if (a32) {
-                  st_global_v8(p, w);
-                } else {
-                  reinterpret_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-                  reinterpret_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
-                }
+              for (int e = 0; e < 8; ++e)
+                w[e] = pack_bf16(__uint_as_float(r[v * 16 + 2 * e]) * inv,
+                                 __uint_as_float(r[v * 16 + 2 * e + 1]) * inv);
+              uint32_t* p = dst + c * 16 + v * 8;
+              if (a32) {
+                st_global_v8(p, w);
+              } else {
+                reinterpret_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+                reinterpret_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
               }
+            }
           }
         }
         if (valid && a.lse != nullptr)
@@ -425,6 +497,7 @@ window_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
       } else if (valid) {
         // Nothing visible (or a CTA that gave up): o = 0, lse = -inf.
         uint4* dst = reinterpret_cast<uint4*>(a.out + qrow * D);
+#pragma unroll 1
         for (int c = 0; c < D / 8; ++c) dst[c] = make_uint4(0, 0, 0, 0);
         if (a.lse != nullptr) a.lse[qrow] = -CUDART_INF_F;
       }
@@ -435,34 +508,36 @@ window_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
     }
   } else if (warp == 0) {
     // ------------------------------------------------------------ MMA issue
-    if (lane == 0) {
+    if (elect_one()) {
       constexpr uint32_t idesc_s = tc::idesc_bf16_f32(128, C::kBN, 0, 0);
       constexpr uint32_t idesc_o = tc::idesc_bf16_f32(128, D, 0, 1);
       uint32_t g = 0, full = 0;
       bool ok = true;
       auto wait = [&](int bar, uint32_t parity) { return tc::mbar_wait(BAR(bar), parity); };
+      // Low words of the descriptors at the buffers' starts (offset 16 for the
+      // unused leading dimension of Q and K, 2048 between V's column halves).
+      const uint32_t q_lo = (sbase >> 4) | (1u << 16);
+      const uint32_t k_lo = ((sbase + C::kOffK) >> 4) | (1u << 16);
+      const uint32_t v_lo = ((sbase + C::kOffV) >> 4) | (128u << 16);
       // S_x of tile n (of the stream) into the S columns of tile x.
       auto issue_s = [&](int x, uint32_t n) {
-        const uint32_t qs = sbase + x * C::kQBytes;
-        const uint32_t ks = sbase + C::kOffK + (n & 1) * C::kTileBytes;
+        const uint32_t ql = q_lo + x * (C::kQBytes >> 4);
+        const uint32_t kl = k_lo + (n & 1) * (C::kTileBytes >> 4);
 #pragma unroll
         for (int k = 0; k < D / 16; ++k)
           // K: [8-row group][half][8 rows][128 B].
-          tc::mma_bf16_ss(
-              tmem + C::col_s(x),
-              tc::smem_desc_sw128(qs + (k >> 2) * (C::kBM * 128) + (k & 3) * 32, 16, 1024),
-              tc::smem_desc_sw128(ks + (k >> 2) * 1024 + (k & 3) * 32, 16, 1024 * C::kHalves),
-              idesc_s, k > 0 ? 1u : 0u);
+          mma_ss(tmem + C::col_s(x), ql + (((k >> 2) * (C::kBM * 128) + (k & 3) * 32) >> 4),
+                 desc_hi(1024), kl + (((k >> 2) * 1024 + (k & 3) * 32) >> 4),
+                 desc_hi(1024 * C::kHalves), idesc_s, k > 0);
         tc::mma_commit(BAR(kSFull + x));
       };
-      // O_x (+)= P_x V over four 16-token steps from k0.
-      auto issue_pv = [&](int x, uint32_t n, int k0, bool fresh) {
-        const uint32_t vs = sbase + C::kOffV + (n & 1) * C::kTileBytes;
+      // O_x (+)= P_x V over the 16-token steps [from, to).
+      auto issue_pv = [&](int x, uint32_t n, auto from, auto to, bool fresh) {
+        const uint32_t vl = v_lo + (n & 1) * (C::kTileBytes >> 4);
 #pragma unroll
-        for (int k = k0; k < k0 + C::kBN / 32; ++k)
-          tc::mma_bf16_ts(tmem + C::col_o(x), tmem + C::col_s(x) + k * 8,
-                          tc::smem_desc_sw128(vs + k * C::kPieceBytes, 2048, 1024), idesc_o,
-                          (!fresh || k > 0) ? 1u : 0u);
+        for (int k = from; k < to; ++k)
+          mma_ts(tmem + C::col_o(x), tmem + C::col_s(x) + k * 8, vl + k * (C::kPieceBytes >> 4),
+                 desc_hi(1024), idesc_o, !fresh || k > 0);
       };
       for (int u = 0; ok; ++u) {
         if (*abort_flag || !wait(kUnitFull + (u & 1), (u >> 1) & 1)) { ok = false; break; }
@@ -473,6 +548,7 @@ window_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
         if (ntiles == 0) continue;
         // First S of both tiles; the queue runs on from the unit before.
         if (!wait(kKFull + (g & 1), (g >> 1) & 1)) { ok = false; break; }
+#pragma unroll 1
         for (int x = 0; x < 2 && ok; ++x) {
           ok = wait(kQFull + x, full & 1);
           if (!ok) break;
@@ -487,13 +563,14 @@ window_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
           const bool more = j + 1 < ntiles;
           if (!wait(kVFull + (g & 1), (g >> 1) & 1)) { ok = false; break; }
           if (more && !wait(kKFull + ((g + 1) & 1), ((g + 1) >> 1) & 1)) { ok = false; break; }
+#pragma unroll
           for (int x = 0; x < 2; ++x) {
             if (!wait(kPLo + x, g & 1)) { ok = false; break; }
             tc::tc_fence_after();
-            issue_pv(x, g, 0, j == 0);
+            issue_pv(x, g, Step<0>(), Step<6>(), j == 0);
             if (!wait(kPHi + x, g & 1)) { ok = false; break; }
             tc::tc_fence_after();
-            issue_pv(x, g, C::kBN / 32, false);
+            issue_pv(x, g, Step<6>(), Step<8>(), false);
             if (more) {
               issue_s(x, g + 1);
               if (j + 2 == ntiles) tc::mma_commit(BAR(kQEmpty + x));
@@ -522,8 +599,9 @@ window_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
       return __all_sync(0xffffffffu, tc::mbar_wait(bar, parity));
     };
     uint32_t gk = 0, gv = 0;          // tiles whose K / V have been issued
-    int blk0 = -1, blk1 = -1;         // block (-1: not loaded) of the lane's piece in tiles gv, gv + 1
-    int off0 = 0, off1 = 0;           // its first token's offset in the block
+    // The lane's pieces in tiles gv and gv + 1: block (-1: not loaded), first
+    // token's offset in it, kv head.
+    int blk0 = -1, blk1 = -1, off0 = 0, off1 = 0;
     int kvh0 = 0, kvh1 = 0;
     int u = 0, j = 0, ntiles = 0;     // the unit that K is in
     int request = 0, kvh = 0, n_first = 0, tbase = 0, pieces = 0;
@@ -532,7 +610,7 @@ window_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
     auto raw_of = [&](int jj) -> int {
       const int v = jj * C::kPieces + lane;
       if (!box || v >= pieces) return -1;
-      const int idx = (v < n_first ? 16 * v : tbase + 16 * (v - n_first)) / a.bs;
+      const int idx = div_bs(v < n_first ? 16 * v : tbase + 16 * (v - n_first), a.bs, a.bs_log2);
       return block_at(a.block_table + static_cast<int64_t>(request) * a.max_blocks, idx,
                       a.max_blocks);
     };
@@ -542,7 +620,7 @@ window_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
       if (do_k && j == ntiles) {
         // The next unit; with a V outstanding, only if it is known already.
         const uint32_t bar = BAR(kUnitFull + (u & 1)), parity = (u >> 1) & 1;
-        const bool known = gv < gk ? __all_sync(0xffffffffu, tc::mbar_try_wait(bar, parity))
+        const bool known = gv < gk ? __all_sync(0xffffffffu, mbar_test(bar, parity))
                                    : wait_all(bar, parity);
         if (!known && gv == gk) { ok = false; break; }
         do_k = false;
@@ -573,7 +651,7 @@ window_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
         const bool mine = box && v < pieces;
         const bool good = mine && r0 >= 0 && r0 < a.num_blocks;
         const int blk = good ? r0 : -1;
-        const int off = (v < n_first ? 16 * v : tbase + 16 * (v - n_first)) % a.bs;
+        const int off = mod_bs(v < n_first ? 16 * v : tbase + 16 * (v - n_first), a.bs, a.bs_log2);
         const unsigned loaded = __ballot_sync(0xffffffffu, good);
         const unsigned bad = __ballot_sync(0xffffffffu, mine && !good);
         if (lane == 0) {
@@ -772,6 +850,7 @@ cudaError_t launch_t(const WindowPrefillLaunch& n, cudaStream_t stream) {
   a.Hkv = n.Hkv;
   a.grp = n.Hq / n.Hkv;
   a.bs = n.bs;
+  a.bs_log2 = block_size_log2(n.bs);
   a.num_blocks = n.num_blocks;
   a.row_tokens = C::kBM / a.grp;
   a.total_q = n.total_q;
@@ -792,17 +871,6 @@ cudaError_t launch_t(const WindowPrefillLaunch& n, cudaStream_t stream) {
   static DeviceFlags attr_set;
   cudaError_t e = set_smem_once(kern, C::kSmemBytes, attr_set);
   if (e != cudaSuccess) return e;
-  // The register hand-over between warpgroups waits for registers that the
-  // launch must actually hold; refuse to launch a build that does not.
-  static const bool regs_ok = [&] {
-    cudaFuncAttributes fa{};
-    if (cudaFuncGetAttributes(&fa, kern) != cudaSuccess) return false;
-    const long long have = static_cast<long long>(fa.numRegs) * C::kThreads;
-    const long long need = 256LL * C::kRegSoftmax + 128LL * C::kRegOther;
-    return fa.numRegs >= static_cast<int>(C::kRegOther) &&
-           fa.numRegs <= static_cast<int>(C::kRegSoftmax) && have >= need;
-  }();
-  if (!regs_ok) return cudaErrorInvalidConfiguration;
   const int per = 2 * a.row_tokens;   // query rows of a unit
   const unsigned tiles = static_cast<unsigned>((n.max_query_len - 1) / per) + 1u;
   return launch_pdl(kern, dim3(tiles, n.Hkv, n.N), dim3(C::kThreads), C::kSmemBytes, stream, q_map,
