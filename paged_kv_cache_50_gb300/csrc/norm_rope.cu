@@ -12,15 +12,17 @@
 // Bound by HBM: every input is read once and every output written once.  A
 // warp takes a token: its rows pass in steps of 32 / (d / 8) rows, d/8 lanes to
 // a row, eight values to a lane.  A lane holds both halves of its pairs (values
-// 4l.. and r/2 + 4l.., two 8-byte loads), so the rotation needs no exchange
-// between lanes and the sum of squares is the only reduction; weight times
-// cosine and sine is formed once per token and kept in registers over its
-// rows; arithmetic is on packed pairs of fp32.  18432 tokens of 32 / 8 heads,
-// d 128 (457 MB): 72.5 us, 6.3 TB/s, 0.93 of the copy rate.  Before: a CTA per
+// 4l.. and r/2 + 4l.., two 8-byte loads; neighbouring pairs come in one of 16),
+// so the rotation needs no exchange between lanes and the sum of squares is the
+// only reduction; weight times cosine and sine is formed once per token and
+// kept in registers over its rows; arithmetic is on packed pairs of fp32.
+// 18432 tokens of 32 / 8 heads, d 128 (457 MB): 71.2 us, 6.4 TB/s, 0.95 of the
+// copy rate; 64 tokens 2.3 us (an empty kernel 2.2).  Before: a CTA per
 // token, 16-byte loads and the other half by shuffles 207 us, a warp per token
 // 131 us (instructions); one loop over all kinds of rows with loads a round
-// ahead 98 us (spilled registers).  An e4m3 pool adds a division per
-// value: 8191 tokens of 64 / 8 heads, d 64 (160 MB): 34.4 us.
+// ahead 98 us (spilled registers).  An e4m3 pool adds a quotient
+// per value: 8191 tokens of 64 / 8 heads, d 64, neighbouring pairs (161 MB): 31.4
+// us, bound by instructions (issue slots 60 % busy) as much as by HBM.
 #include <type_traits>
 
 #include "pa_common.cuh"
@@ -75,10 +77,6 @@ __device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
   return r;
 }
-__device__ __forceinline__ F2 swap2(F2 a) {
-  const float2 f = split(a);
-  return f2(f.y, f.x);
-}
 // Two bf16 (low half first) as fp32.
 __device__ __forceinline__ F2 widen(uint32_t w) {
   return f2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
@@ -120,7 +118,36 @@ constexpr int kFlight = 4;   // steps whose loads are in flight per warp
 
 enum Kind { kQuery, kKey, kValue };
 
-template <int D, bool FP8>
+// Eight values of a lane as two vectors of four, P and Q, whose elements are
+// the pairs to be rotated: two chunks of a row half a rotation apart, or (INTER)
+// the even and the odd elements of 16 bytes.
+struct Pairs {
+  F2 p[2], q[2];
+};
+template <bool INTER>
+__device__ __forceinline__ Pairs widen8(uint4 x) {
+  if (!INTER) return {{widen(x.x), widen(x.y)}, {widen(x.z), widen(x.w)}};
+  auto lo = [](uint32_t w) { return __uint_as_float(w << 16); };
+  auto hi = [](uint32_t w) { return __uint_as_float(w & 0xffff0000u); };
+  return {{f2(lo(x.x), lo(x.y)), f2(lo(x.z), lo(x.w))},
+          {f2(hi(x.x), hi(x.y)), f2(hi(x.z), hi(x.w))}};
+}
+// The eight values in the row's order again, as pairs of neighbours.
+template <bool INTER>
+__device__ __forceinline__ void in_order(const Pairs& y, F2 (&v)[4]) {
+  if constexpr (!INTER) {
+    v[0] = y.p[0], v[1] = y.p[1], v[2] = y.q[0], v[3] = y.q[1];
+  } else {
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const float2 a = split(y.p[e]), b = split(y.q[e]);
+      v[2 * e] = f2(a.x, b.x);
+      v[2 * e + 1] = f2(a.y, b.y);
+    }
+  }
+}
+
+template <int D, bool FP8, bool INTER>
 __global__ void __launch_bounds__(kWarps * 32, 8) norm_rope_kernel(const NormRopeArgs a) {
   constexpr int L = D / 8;              // lanes per row
   constexpr int G = 32 / L;             // rows per step
@@ -134,11 +161,20 @@ __global__ void __launch_bounds__(kWarps * 32, 8) norm_rope_kernel(const NormRop
   if (t >= a.num_tokens) return;   // whole warps
   const int share = static_cast<int>(unit - t * a.shares);
   // The lane's two chunks of four values: the halves of four pairs where they
-  // are rotated, neighbours otherwise.
+  // are rotated and lie apart, neighbours otherwise.
   const int half = a.rot / 2;
   const bool turned = 8 * l < a.rot;
-  const bool apart = !a.interleaved && turned;
-  const int c0 = apart ? l : 2 * l, c1 = apart ? l + half / 4 : 2 * l + 1;
+  const int c0 = !INTER && turned ? l : 2 * l, c1 = !INTER && turned ? l + half / 4 : 2 * l + 1;
+  auto fetch = [&](const __nv_bfloat16* row, bool stream) -> uint4 {
+    if (INTER) {
+      const uint4* p = reinterpret_cast<const uint4*>(row) + l;
+      return stream ? __ldcs(p) : __ldg(p);
+    }
+    const uint2* p = reinterpret_cast<const uint2*>(row);
+    const uint2 x = stream ? __ldcs(p + c0) : __ldg(p + c0);
+    const uint2 y = stream ? __ldcs(p + c1) : __ldg(p + c1);
+    return make_uint4(x.x, x.y, y.x, y.y);
+  };
 
   // Where this token's keys and values go (null: nowhere), and its angles.
   const int64_t slot = a.slots[t];
@@ -166,133 +202,117 @@ __global__ void __launch_bounds__(kWarps * 32, 8) norm_rope_kernel(const NormRop
   int s0 = share * a.per, s1 = s0 + a.per;   // steps left, counted from the kind's first
   auto rows = [&](auto kind_tag, const __nv_bfloat16* src, int H, const __nv_bfloat16* weight) {
     constexpr Kind kind = decltype(kind_tag)::value;
+    constexpr int kOutEl = kind == kQuery ? 2 : kEl;
     const int steps = (H + G - 1) / G;
     const int end = min(s1, steps);
-    // y = rstd (A own + B other): A = w cos, B = -+ w_other sin; [chunk][pair].
-    F2 A[2][2], B[2][2];
+    const int mine = min(end, (H - g + G - 1) / G);   // this lane's rows end here
+    // y = rstd (A own + B other): A = w cos, B = -+ w_other sin.
+    F2 Ap[2], Aq[2], Bp[2], Bq[2];
     if (kind != kValue && s0 < end) {
-      F2 w[2][2];
+      Pairs w = {{f2(1.f, 1.f), f2(1.f, 1.f)}, {f2(1.f, 1.f), f2(1.f, 1.f)}};
+      if (norm) w = widen8<INTER>(fetch(weight, false));
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        w[k][0] = w[k][1] = f2(1.f, 1.f);
-        if (norm) {
-          const uint2 x = __ldg(reinterpret_cast<const uint2*>(weight + 4 * (k ? c1 : c0)));
-          w[k][0] = widen(x.x);
-          w[k][1] = widen(x.y);
-        }
-#pragma unroll
-        for (int e = 0; e < 2; ++e) A[k][e] = w[k][e];
-      }
+      for (int e = 0; e < 2; ++e) Ap[e] = w.p[e], Aq[e] = w.q[e];
       if (turned) {
         const float4 c = __ldg(reinterpret_cast<const float4*>(angles + 4 * l));
         const float4 s = __ldg(reinterpret_cast<const float4*>(angles + half + 4 * l));
-        if (apart) {
-          const F2 cc[2] = {f2(c.x, c.y), f2(c.z, c.w)};
-          const F2 sp[2] = {f2(s.x, s.y), f2(s.z, s.w)};
-          const F2 sn[2] = {f2(-s.x, -s.y), f2(-s.z, -s.w)};
+        const F2 cc[2] = {f2(c.x, c.y), f2(c.z, c.w)};
+        const F2 sp[2] = {f2(s.x, s.y), f2(s.z, s.w)};
+        const F2 sn[2] = {f2(-s.x, -s.y), f2(-s.z, -s.w)};
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            B[0][e] = mul2(w[1][e], sn[e]);
-            B[1][e] = mul2(w[0][e], sp[e]);
-            A[0][e] = mul2(w[0][e], cc[e]);
-            A[1][e] = mul2(w[1][e], cc[e]);
-          }
-        } else {   // pairs 4l .. 4l + 3, inside the lane
-          const float c4[4] = {c.x, c.y, c.z, c.w}, s4[4] = {s.x, s.y, s.z, s.w};
-#pragma unroll
-          for (int k = 0; k < 2; ++k)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              B[k][e] = mul2(swap2(w[k][e]), f2(-s4[2 * k + e], s4[2 * k + e]));
-              A[k][e] = mul2(w[k][e], f2(c4[2 * k + e], c4[2 * k + e]));
-            }
+        for (int e = 0; e < 2; ++e) {
+          Bp[e] = mul2(w.q[e], sn[e]);
+          Bq[e] = mul2(w.p[e], sp[e]);
+          Ap[e] = mul2(w.p[e], cc[e]);
+          Aq[e] = mul2(w.q[e], cc[e]);
         }
       }
     }
+    uint8_t* dst = cell;
+    if (kind == kQuery)
+      dst = reinterpret_cast<uint8_t*>(a.q_out + static_cast<int64_t>(t) * a.Hq * D);
+    else if (kind == kValue)
+      dst += static_cast<int64_t>(a.bs) * a.Hkv * (D * kEl);
     const float scale = kind == kValue ? a.v_scale : a.k_scale, inv = __frcp_rn(scale);
     const bool plain = scale >= 0x1p-100f && scale <= 0x1p100f;
-    uint8_t* dst = kind == kQuery
-                       ? reinterpret_cast<uint8_t*>(a.q_out + static_cast<int64_t>(t) * a.Hq * D)
-                       : cell + (kind == kValue ? static_cast<int64_t>(a.bs) * a.Hkv : 0) * (D * kEl);
     for (int base = s0; base < end; base += kFlight) {
-      uint2 raw[kFlight][2];
+      const __nv_bfloat16* in = src + (base * G + g) * D;
+      uint8_t* to = dst + (base * G + g) * (D * kOutEl);
+      uint4 raw[kFlight];
 #pragma unroll
-      for (int u = 0; u < kFlight; ++u) {
-        const int r = (base + u) * G + g;
-        raw[u][0] = raw[u][1] = make_uint2(0, 0);
-        if (base + u < end && r < H) {
-          const uint2* p = reinterpret_cast<const uint2*>(src + r * D);
-          raw[u][0] = __ldcs(p + c0);
-          raw[u][1] = __ldcs(p + c1);
-        }
-      }
+      for (int u = 0; u < kFlight; ++u)
+        raw[u] = base + u < mine ? fetch(in + u * G * D, true) : make_uint4(0, 0, 0, 0);
 #pragma unroll
       for (int u = 0; u < kFlight; ++u) {
         if (base + u >= end) break;
-        const int r = (base + u) * G + g;
-        const bool store = r < H && (kind == kQuery || keep);
-        const uint2 x0 = raw[u][0], x1 = raw[u][1];
+        const bool store = base + u < mine && (kind == kQuery || keep);
+        const uint4 x = raw[u];
+        uint2* out = reinterpret_cast<uint2*>(to + u * (G * D * kOutEl));
         if (kind == kValue && !FP8) {   // a bit copy
           if (store) {
-            uint2* p = reinterpret_cast<uint2*>(dst + r * (D * 2));
-            p[c0] = x0;
-            p[c1] = x1;
+            if (INTER) {
+              reinterpret_cast<uint4*>(out)[l] = x;
+            } else {
+              out[c0] = make_uint2(x.x, x.y);
+              out[c1] = make_uint2(x.z, x.w);
+            }
           }
           continue;
         }
-        F2 y[2][2] = {{widen(x0.x), widen(x0.y)}, {widen(x1.x), widen(x1.y)}};
+        Pairs y = widen8<INTER>(x);
         if (kind != kValue) {
           float rstd = 1.f;
           if (norm) {
-            F2 s2 = mul2(y[0][0], y[0][0]);
-            s2 = fma2(y[0][1], y[0][1], s2);
-            s2 = fma2(y[1][0], y[1][0], s2);
-            s2 = fma2(y[1][1], y[1][1], s2);
+            F2 s2 = mul2(y.p[0], y.p[0]);
+            s2 = fma2(y.p[1], y.p[1], s2);
+            s2 = fma2(y.q[0], y.q[0], s2);
+            s2 = fma2(y.q[1], y.q[1], s2);
             const float2 f = split(s2);
             float ss = f.x + f.y;
 #pragma unroll
             for (int o = L / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
             rstd = rsqrtf(ss * (1.f / D) + a.eps);
           }
-          F2 z[2][2];
+          const Pairs z = y;
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            z[0][e] = y[0][e];
-            z[1][e] = y[1][e];
-            y[0][e] = mul2(y[0][e], A[0][e]);
-            y[1][e] = mul2(y[1][e], A[1][e]);
+            y.p[e] = mul2(y.p[e], Ap[e]);
+            y.q[e] = mul2(y.q[e], Aq[e]);
           }
-          if (apart) {
+          if (turned) {
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              y[0][e] = fma2(z[1][e], B[0][e], y[0][e]);
-              y[1][e] = fma2(z[0][e], B[1][e], y[1][e]);
-            }
-          } else if (turned) {
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              y[0][e] = fma2(swap2(z[0][e]), B[0][e], y[0][e]);
-              y[1][e] = fma2(swap2(z[1][e]), B[1][e], y[1][e]);
+              y.p[e] = fma2(z.q[e], Bp[e], y.p[e]);
+              y.q[e] = fma2(z.p[e], Bq[e], y.q[e]);
             }
           }
           if (norm) {
             const F2 r2 = f2(rstd, rstd);
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              y[0][e] = mul2(y[0][e], r2);
-              y[1][e] = mul2(y[1][e], r2);
+              y.p[e] = mul2(y.p[e], r2);
+              y.q[e] = mul2(y.q[e], r2);
             }
           }
         }
         if (!store) continue;
+        F2 v[4];
+        in_order<INTER>(y, v);
         if (kind != kQuery && FP8) {
-          uint32_t* p = reinterpret_cast<uint32_t*>(dst + r * D);
-          p[c0] = quant4(y[0][0], y[0][1], scale, inv, plain);
-          p[c1] = quant4(y[1][0], y[1][1], scale, inv, plain);
+          const uint2 codes = make_uint2(quant4(v[0], v[1], scale, inv, plain),
+                                         quant4(v[2], v[3], scale, inv, plain));
+          if (INTER) {
+            out[l] = codes;
+          } else {
+            reinterpret_cast<uint32_t*>(out)[c0] = codes.x;
+            reinterpret_cast<uint32_t*>(out)[c1] = codes.y;
+          }
+        } else if (INTER) {
+          reinterpret_cast<uint4*>(out)[l] =
+              make_uint4(narrow(v[0]), narrow(v[1]), narrow(v[2]), narrow(v[3]));
         } else {
-          uint2* p = reinterpret_cast<uint2*>(dst + r * (D * 2));
-          p[c0] = make_uint2(narrow(y[0][0]), narrow(y[0][1]));
-          p[c1] = make_uint2(narrow(y[1][0]), narrow(y[1][1]));
+          out[c0] = make_uint2(narrow(v[0]), narrow(v[1]));
+          out[c1] = make_uint2(narrow(v[2]), narrow(v[3]));
         }
       }
     }
@@ -302,6 +322,14 @@ __global__ void __launch_bounds__(kWarps * 32, 8) norm_rope_kernel(const NormRop
   rows(std::integral_constant<Kind, kQuery>(), a.q + t * a.q_stride, a.Hq, a.q_weight);
   rows(std::integral_constant<Kind, kKey>(), a.k + t * a.k_stride, a.Hkv, a.k_weight);
   rows(std::integral_constant<Kind, kValue>(), a.v + t * a.v_stride, a.Hkv, nullptr);
+}
+
+template <int D, bool FP8>
+cudaError_t launch_t(const NormRopeArgs& a, unsigned ctas, cudaStream_t stream) {
+  return a.interleaved ? launch_pdl(norm_rope_kernel<D, FP8, true>, dim3(ctas), dim3(kWarps * 32),
+                                    0, stream, a)
+                       : launch_pdl(norm_rope_kernel<D, FP8, false>, dim3(ctas), dim3(kWarps * 32),
+                                    0, stream, a);
 }
 
 }  // namespace
@@ -337,19 +365,17 @@ cudaError_t launch_norm_rope(const NormRopeLaunch& n, cudaStream_t stream) {
   // over several warps, until about 16 warps per SM have work.
   const int rows = 32 / (n.d / 8);
   const int steps = (n.Hq + rows - 1) / rows + 2 * ((n.Hkv + rows - 1) / rows);
-  long long shares = (16LL * n.sm_count + n.num_tokens - 1) / n.num_tokens;
+    long long shares = (16LL * n.sm_count + n.num_tokens - 1) / n.num_tokens;
   if (shares > steps) shares = steps;
   a.per = static_cast<int>((steps + shares - 1) / shares);
   a.shares = (steps + a.per - 1) / a.per;
   a.num_tokens = n.num_tokens;
   // shares > 1 only below 16 tokens per SM: the units fit 32 bits.
   const unsigned units = static_cast<unsigned>(n.num_tokens) * a.shares;
-  const dim3 grid((units + kWarps - 1) / kWarps), block(kWarps * 32);
-  if (n.d == 128)
-    return n.fp8 ? launch_pdl(norm_rope_kernel<128, true>, grid, block, 0, stream, a)
-                 : launch_pdl(norm_rope_kernel<128, false>, grid, block, 0, stream, a);
-  return n.fp8 ? launch_pdl(norm_rope_kernel<64, true>, grid, block, 0, stream, a)
-               : launch_pdl(norm_rope_kernel<64, false>, grid, block, 0, stream, a);
+  const unsigned ctas = (units + kWarps - 1) / kWarps;
+  if (n.d == 128) return n.fp8 ? launch_t<128, true>(a, ctas, stream)
+                               : launch_t<128, false>(a, ctas, stream);
+  return n.fp8 ? launch_t<64, true>(a, ctas, stream) : launch_t<64, false>(a, ctas, stream);
 }
 
 }  // namespace pa
