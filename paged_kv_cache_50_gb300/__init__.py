@@ -531,30 +531,19 @@ def pa_mla_decode(q, kv_cache, block_table, seq_lens, scale, workspace, out=None
 # their checks are compiled (csrc/binding.cpp).
 # ---------------------------------------------------------------------------
 
-def _call_device(t, name: str) -> int:
-    if not isinstance(t, torch.Tensor):
+def _new(stream, like, name, shape, dtype) -> torch.Tensor:
+    """An output tensor beside ``like``, allocated for the stream that the call
+    runs on; ``shape``: an int, or a slice of ``like``'s."""
+    if not isinstance(like, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    dev = t.get_device()
-    if dev < 0:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if dev != torch.cuda.current_device():
-        raise ValueError(f"{name} is on cuda:{dev}, the current device is "
-                         f"cuda:{torch.cuda.current_device()}")
-    return dev
-
-
-def _raw_stream(stream, dev: int) -> int:
-    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
-
-
-def _new(stream, shape, dtype, dev: int) -> torch.Tensor:
-    """An output tensor, allocated for the stream that the call runs on."""
+    if isinstance(shape, slice):
+        shape = like.shape[shape]
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
+        return torch.empty(shape, dtype=dtype, device=like.device)
     if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(stream), device=dev)
+        stream = torch.cuda.ExternalStream(int(stream), device=like.device)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=dev)
+        return torch.empty(shape, dtype=dtype, device=like.device)
 
 
 def pa_plan_step(context_lens, query_lens, block_table, free_blocks, block_size, num_blocks,
@@ -571,27 +560,26 @@ def pa_plan_step(context_lens, query_lens, block_table, free_blocks, block_size,
     given are written and returned.  Tokens past the new ones get position 0
     and slot -1.  ``max_tokens`` defaults to the length of ``slot_mapping`` or
     ``positions``; with neither it must be given."""
-    dev = _call_device(block_table, "block_table")
     if max_tokens is None:
         given = slot_mapping if slot_mapping is not None else positions
         if given is None:
             raise ValueError("max_tokens, slot_mapping or positions must be given")
         max_tokens = given.shape[0]
-    n = block_table.shape[0]
     if query_start_loc is None:
-        query_start_loc = _new(stream, n + 1, torch.int32, dev)
+        query_start_loc = _new(stream, block_table, "block_table", block_table.shape[0] + 1,
+                               torch.int32)
     if seq_lens is None:
-        seq_lens = _new(stream, n, torch.int32, dev)
+        seq_lens = _new(stream, block_table, "block_table", slice(0, 1), torch.int32)
     if positions is None:
-        positions = _new(stream, max_tokens, torch.int32, dev)
+        positions = _new(stream, block_table, "block_table", max_tokens, torch.int32)
     if slot_mapping is None:
-        slot_mapping = _new(stream, max_tokens, torch.int64, dev)
+        slot_mapping = _new(stream, block_table, "block_table", max_tokens, torch.int64)
     if totals is None:
-        totals = _new(stream, 2, torch.int32, dev)
+        totals = _new(stream, block_table, "block_table", 2, torch.int32)
     _check(_binding().plan_step(
-        dev, context_lens, query_lens, free_blocks, free_start, block_table, block_size,
+        context_lens, query_lens, free_blocks, free_start, block_table, block_size,
         num_blocks, max_tokens, query_start_loc, seq_lens, positions, slot_mapping, totals,
-        _raw_stream(stream, dev)), "pa_plan_step")
+        None if stream is None else _stream(stream)), "pa_plan_step")
     return query_start_loc, seq_lens, positions, slot_mapping, totals
 
 
@@ -617,12 +605,12 @@ def pa_qk_norm_rope_cache(q, key, value, kv_cache, slot_mapping, q_weight=None, 
     ``q_weight`` and ``k_weight`` [d] bf16 (neither: no norm), ``cos_sin``
     [max_position, rotary_dim] fp32 (see rope_table; none: no rotation) with
     ``positions`` [T] int32, ``slot_mapping`` [T] int64 (< 0: no cache write)."""
-    dev = _call_device(q, "q")
     if q_out is None:
-        q_out = _new(stream, q.shape, torch.bfloat16, dev)
+        q_out = _new(stream, q, "q", slice(None), torch.bfloat16)
     _check(_binding().norm_rope(
-        dev, q, key, value, kv_cache, slot_mapping, None, q_weight, k_weight, eps, cos_sin,
-        positions, interleaved, q_out, _raw_stream(stream, dev)), "pa_qk_norm_rope_cache")
+        q, key, value, kv_cache, slot_mapping, None, q_weight, k_weight, eps, cos_sin,
+        positions, interleaved, q_out, None if stream is None else _stream(stream)),
+        "pa_qk_norm_rope_cache")
     return q_out
 
 
@@ -631,12 +619,11 @@ def pa_qk_norm_rope_cache_fp8(q, key, value, kv_cache, slot_mapping, k_scale, v_
                               positions=None, interleaved=False, q_out=None, stream=None):
     """pa_qk_norm_rope_cache into an fp8 pool: e4m3 codes of key / k_scale and
     value / v_scale (uint8 or float8_e4m3fn)."""
-    dev = _call_device(q, "q")
     if q_out is None:
-        q_out = _new(stream, q.shape, torch.bfloat16, dev)
+        q_out = _new(stream, q, "q", slice(None), torch.bfloat16)
     _check(_binding().norm_rope(
-        dev, q, key, value, kv_cache, slot_mapping, (k_scale, v_scale), q_weight, k_weight, eps,
-        cos_sin, positions, interleaved, q_out, _raw_stream(stream, dev)),
+        q, key, value, kv_cache, slot_mapping, (k_scale, v_scale), q_weight, k_weight, eps,
+        cos_sin, positions, interleaved, q_out, None if stream is None else _stream(stream)),
         "pa_qk_norm_rope_cache_fp8")
     return q_out
 
@@ -647,14 +634,14 @@ def pa_varlen_fwd_sinks(q, kv_cache, block_table, query_start_loc, seq_lens, max
     """Causal varlen paged attention in which a row at position p sees
     p - sliding_window < p' <= p and p' < num_sinks.  Blocks that no row sees
     are not read.  Returns (out, lse) like pa_varlen_fwd_window."""
-    dev = _call_device(q, "q")
     if out is None:
-        out = _new(stream, q.shape, torch.bfloat16, dev)
+        out = _new(stream, q, "q", slice(None), torch.bfloat16)
     if lse is None and return_lse:
-        lse = _new(stream, q.shape[:2], torch.float32, dev)
+        lse = _new(stream, q, "q", slice(0, 2), torch.float32)
     _check(_binding().varlen_sinks(
-        dev, q, kv_cache, block_table, seq_lens, out, lse, query_start_loc, max_query_len, scale,
-        sliding_window, num_sinks, _raw_stream(stream, dev)), "pa_varlen_fwd_sinks")
+        q, kv_cache, block_table, seq_lens, out, lse, query_start_loc, max_query_len, scale,
+        sliding_window, num_sinks, None if stream is None else _stream(stream)),
+        "pa_varlen_fwd_sinks")
     return out, lse
 
 
@@ -663,14 +650,13 @@ def pa_decode_window(q, kv_cache, block_table, seq_lens, scale, sliding_window, 
     """Decode (q [N, Hq, d], one query per request at its last position) over
     the last ``sliding_window`` and the first ``num_sinks`` cached tokens, in
     one launch without a workspace.  Returns (out [N, Hq, d] bf16, lse [N, Hq])."""
-    dev = _call_device(q, "q")
     if out is None:
-        out = _new(stream, q.shape, torch.bfloat16, dev)
+        out = _new(stream, q, "q", slice(None), torch.bfloat16)
     if lse is None and return_lse:
-        lse = _new(stream, q.shape[:2], torch.float32, dev)
+        lse = _new(stream, q, "q", slice(0, 2), torch.float32)
     _check(_binding().decode_window(
-        dev, q, kv_cache, block_table, seq_lens, out, lse, None, scale, sliding_window, num_sinks,
-        _raw_stream(stream, dev)), "pa_decode_window")
+        q, kv_cache, block_table, seq_lens, out, lse, None, scale, sliding_window, num_sinks,
+        None if stream is None else _stream(stream)), "pa_decode_window")
     return out, lse
 
 
@@ -679,14 +665,14 @@ def pa_decode_window_fp8(q, kv_cache, block_table, seq_lens, scale, k_scale, v_s
                          stream=None):
     """pa_decode_window over an fp8 pool (entries = e4m3 value x k_scale or
     v_scale; uint8 or float8_e4m3fn)."""
-    dev = _call_device(q, "q")
     if out is None:
-        out = _new(stream, q.shape, torch.bfloat16, dev)
+        out = _new(stream, q, "q", slice(None), torch.bfloat16)
     if lse is None and return_lse:
-        lse = _new(stream, q.shape[:2], torch.float32, dev)
+        lse = _new(stream, q, "q", slice(0, 2), torch.float32)
     _check(_binding().decode_window(
-        dev, q, kv_cache, block_table, seq_lens, out, lse, (k_scale, v_scale), scale,
-        sliding_window, num_sinks, _raw_stream(stream, dev)), "pa_decode_window_fp8")
+        q, kv_cache, block_table, seq_lens, out, lse, (k_scale, v_scale), scale,
+        sliding_window, num_sinks, None if stream is None else _stream(stream)),
+        "pa_decode_window_fp8")
     return out, lse
 
 

@@ -3,11 +3,13 @@
 // A step's small calls (a plan of 64 requests, the norms of 64 tokens) run for
 // about 3 us on the GPU, and reading type, device, layout and address of a
 // dozen tensors from Python costs more than that: pa_plan_step took 9.8 us of
-// host time, 3.3 of them in the library.  Each function here takes one entry
+// host time, 3.3 of them in the library (3.0 with these checks).  Each function here takes one entry
 // point's arguments as they come from paged_kv_cache_50_gb300/__init__.py,
 // checks every tensor (TypeError, ValueError), calls the entry point and
 // returns its status.  Nothing is computed or kept here.
 #include <Python.h>
+#include <c10/cuda/CUDAFunctions.h>
+#include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <stdarg.h>
@@ -40,6 +42,20 @@ const char* type_name(at::ScalarType t) {
     case at::kBFloat16: return "torch.bfloat16";
     default: return "torch.uint8";
   }
+}
+
+void same_device(long long dev, long long current, const char* name) {
+  if (dev != current)
+    refuse(PyExc_ValueError, "%s is on cuda:%lld, the current device is cuda:%lld", name, dev,
+           current);
+}
+
+// The call's device: that of `t`, which must be the current one.
+int call_device(const at::Tensor& t, const char* name) {
+  if (!t.is_cuda()) refuse(PyExc_ValueError, "%s must be a CUDA tensor", name);
+  const int dev = t.get_device();
+  same_device(dev, c10::cuda::current_device(), name);
+  return dev;
 }
 
 // Device and type of a tensor on CUDA device `dev`.
@@ -94,10 +110,15 @@ int extent(int64_t v, const char* name) {
   return static_cast<int>(v);
 }
 
-void* pointer(PyObject* o) {   // a stream handle
+void* pointer(PyObject* o) {
   void* p = PyLong_AsVoidPtr(o);
   if (p == nullptr && PyErr_Occurred()) throw Refused();
   return p;
+}
+
+// A stream handle; None: the current stream.
+void* stream_of(PyObject* o, int dev) {
+  return o == Py_None ? c10::cuda::getCurrentCUDAStream(dev).stream() : pointer(o);
 }
 
 // Entry points of the loaded library.
@@ -122,6 +143,16 @@ PyObject* guarded(Py_ssize_t n, Py_ssize_t want, F f) {
   return nullptr;
 }
 
+// (device, current device, name): raises unless they agree.
+PyObject* check_device(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 3, [&]() -> PyObject* {
+    const char* name = PyUnicode_AsUTF8(a[2]);
+    if (name == nullptr) throw Refused();
+    same_device(integer(a[0]), integer(a[1]), name);
+    Py_RETURN_NONE;
+  });
+}
+
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded(n, 6, [&]() -> PyObject* {
     plan_step_fn = reinterpret_cast<decltype(plan_step_fn)>(pointer(a[0]));
@@ -134,36 +165,36 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-// (dev, context_lens, query_lens, free_blocks, free_start | None, block_table,
+// (context_lens, query_lens, free_blocks, free_start | None, block_table,
 //  block_size, num_blocks, max_tokens, query_start_loc, seq_lens, positions,
-//  slot_mapping, totals, stream)
+//  slot_mapping, totals, stream | None)
 PyObject* plan_step(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded(n, 15, [&]() -> PyObject* {
-    const int dev = integer32(a[0], "device");
-    const at::Tensor& table = tensor(a[5], "block_table");
-    const at::Tensor& free = tensor(a[3], "free_blocks");
+  return guarded(n, 14, [&]() -> PyObject* {
+    const at::Tensor& table = tensor(a[4], "block_table");
+    const at::Tensor& free = tensor(a[2], "free_blocks");
     if (table.dim() != 2) refuse(PyExc_ValueError, "block_table must be [num_seqs, max_blocks]");
     if (free.dim() != 1) refuse(PyExc_ValueError, "free_blocks must be [num_free]");
     const int64_t seqs = table.size(0);
-    const int cap = integer32(a[8], "max_tokens");
-    void* ctx = shaped(a[1], "context_lens", at::kInt, dev, {seqs});
-    void* qlen = shaped(a[2], "query_lens", at::kInt, dev, {seqs});
-    void* start = a[4] == Py_None ? nullptr : shaped(a[4], "free_start", at::kInt, dev, {1});
-    void* qsl = shaped(a[9], "query_start_loc", at::kInt, dev, {seqs + 1});
-    void* seq = shaped(a[10], "seq_lens", at::kInt, dev, {seqs});
-    void* pos = shaped(a[11], "positions", at::kInt, dev, {cap});
-    void* slot = shaped(a[12], "slot_mapping", at::kLong, dev, {cap});
-    void* totals = shaped(a[13], "totals", at::kInt, dev, {2});
+    const int cap = integer32(a[7], "max_tokens");
+    const int dev = call_device(table, "block_table");
+    void* ctx = shaped(a[0], "context_lens", at::kInt, dev, {seqs});
+    void* qlen = shaped(a[1], "query_lens", at::kInt, dev, {seqs});
+    void* start = a[3] == Py_None ? nullptr : shaped(a[3], "free_start", at::kInt, dev, {1});
+    void* qsl = shaped(a[8], "query_start_loc", at::kInt, dev, {seqs + 1});
+    void* seq = shaped(a[9], "seq_lens", at::kInt, dev, {seqs});
+    void* pos = shaped(a[10], "positions", at::kInt, dev, {cap});
+    void* slot = shaped(a[11], "slot_mapping", at::kLong, dev, {cap});
+    void* totals = shaped(a[12], "totals", at::kInt, dev, {2});
     using I = int32_t*;
     return PyLong_FromLong(plan_step_fn(
         static_cast<I>(ctx), static_cast<I>(qlen),
         static_cast<I>(dense(free, "free_blocks", at::kInt, dev)), static_cast<I>(start),
         extent(free.size(0), "free_blocks"), extent(seqs, "block_table"),
-        extent(table.size(1), "block_table"), integer32(a[6], "block_size"),
-        integer32(a[7], "num_blocks"), cap,
+        extent(table.size(1), "block_table"), integer32(a[5], "block_size"),
+        integer32(a[6], "num_blocks"), cap,
         static_cast<I>(dense(table, "block_table", at::kInt, dev)), static_cast<I>(qsl),
         static_cast<I>(seq), static_cast<I>(pos), static_cast<int64_t*>(slot),
-        static_cast<I>(totals), pointer(a[14])));
+        static_cast<I>(totals), stream_of(a[13], dev)));
   });
 }
 
@@ -203,59 +234,61 @@ void* token_rows(PyObject* o, const char* name, int64_t tokens, int64_t heads, i
   return t.data_ptr();
 }
 
-// (dev, q, key, value, kv_cache, slot_mapping, (k_scale, v_scale) | None,
+// (q, key, value, kv_cache, slot_mapping, (k_scale, v_scale) | None,
 //  q_weight | None, k_weight | None, eps, cos_sin | None, positions | None,
-//  interleaved, q_out, stream)
+//  interleaved, q_out, stream | None)
 PyObject* norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded(n, 15, [&]() -> PyObject* {
-    const int dev = integer32(a[0], "device");
-    const at::Tensor& q = tensor(a[1], "q");
-    const at::Tensor& pool = tensor(a[4], "kv_cache");
+  return guarded(n, 14, [&]() -> PyObject* {
+    const at::Tensor& q = tensor(a[0], "q");
+    const at::Tensor& pool = tensor(a[3], "kv_cache");
     if (q.dim() != 3) refuse(PyExc_ValueError, "q must be [num_tokens, num_q_heads, head_size]");
     const int64_t tokens = q.size(0), heads = q.size(1), d = q.size(2);
     const pa_shape s = pool_shape(pool, 0, heads, 1);
     if (d != s.head_size) refuse(PyExc_ValueError, "q head_size does not match kv_cache");
+    const int dev = call_device(q, "q");
     int64_t qs, ks, vs;
-    void* qp = token_rows(a[1], "q", tokens, heads, d, dev, &qs);
-    void* kp = token_rows(a[2], "key", tokens, s.num_kv_heads, d, dev, &ks);
-    void* vp = token_rows(a[3], "value", tokens, s.num_kv_heads, d, dev, &vs);
-    void* slots = shaped(a[5], "slot_mapping", at::kLong, dev, {tokens});
-    if ((a[7] == Py_None) != (a[8] == Py_None))
+    void* qp = token_rows(a[0], "q", tokens, heads, d, dev, &qs);
+    void* kp = token_rows(a[1], "key", tokens, s.num_kv_heads, d, dev, &ks);
+    void* vp = token_rows(a[2], "value", tokens, s.num_kv_heads, d, dev, &vs);
+    void* slots = shaped(a[4], "slot_mapping", at::kLong, dev, {tokens});
+    if ((a[6] == Py_None) != (a[7] == Py_None))
       refuse(PyExc_ValueError, "q_weight and k_weight must be given together");
     void *qw = nullptr, *kw = nullptr, *cs = nullptr, *pos = nullptr;
-    if (a[7] != Py_None) {
-      qw = shaped(a[7], "q_weight", at::kBFloat16, dev, {d});
-      kw = shaped(a[8], "k_weight", at::kBFloat16, dev, {d});
+    if (a[6] != Py_None) {
+      qw = shaped(a[6], "q_weight", at::kBFloat16, dev, {d});
+      kw = shaped(a[7], "k_weight", at::kBFloat16, dev, {d});
     }
     int rows = 0, rot = 0;
-    if (a[10] != Py_None) {
-      const at::Tensor& table = tensor(a[10], "cos_sin");
-      if (table.dim() != 2 || a[11] == Py_None)
+    if (a[9] != Py_None) {
+      const at::Tensor& table = tensor(a[9], "cos_sin");
+      if (table.dim() != 2 || a[10] == Py_None)
         refuse(PyExc_ValueError,
                "cos_sin [max_position, rotary_dim] needs positions [num_tokens]");
       rows = extent(table.size(0), "cos_sin");
       rot = extent(table.size(1), "cos_sin");
       cs = dense(table, "cos_sin", at::kFloat, dev);
-      pos = shaped(a[11], "positions", at::kInt, dev, {tokens});
+      pos = shaped(a[10], "positions", at::kInt, dev, {tokens});
     }
-    const int turned = PyObject_IsTrue(a[12]);
+    const int turned = PyObject_IsTrue(a[11]);
     if (turned < 0) throw Refused();
-    void* out = shaped(a[13], "q_out", at::kBFloat16, dev, {tokens, heads, d});
-    const bool fp8 = a[6] != Py_None;
+    void* out = shaped(a[12], "q_out", at::kBFloat16, dev, {tokens, heads, d});
+    const bool fp8 = a[5] != Py_None;
     void* cache = pool_pointer(pool, fp8, dev);
     const int count = extent(tokens, "q");
-    const float eps = real(a[9]);
+    const float eps = real(a[8]);
     if (fp8) {
-      if (!PyTuple_Check(a[6]) || PyTuple_GET_SIZE(a[6]) != 2)
+      if (!PyTuple_Check(a[5]) || PyTuple_GET_SIZE(a[5]) != 2)
         refuse(PyExc_TypeError, "(k_scale, v_scale) expected");
       return PyLong_FromLong(norm_fp8_fn(
           qp, kp, vp, qs, ks, vs, qw, kw, eps, static_cast<float*>(cs), rows, rot, turned,
           static_cast<int32_t*>(pos), cache, static_cast<int64_t*>(slots), count, &s,
-          real(PyTuple_GET_ITEM(a[6], 0)), real(PyTuple_GET_ITEM(a[6], 1)), out, pointer(a[14])));
+          real(PyTuple_GET_ITEM(a[5], 0)), real(PyTuple_GET_ITEM(a[5], 1)), out,
+          stream_of(a[13], dev)));
     }
     return PyLong_FromLong(norm_fn(qp, kp, vp, qs, ks, vs, qw, kw, eps, static_cast<float*>(cs),
                                    rows, rot, turned, static_cast<int32_t*>(pos), cache,
-                                   static_cast<int64_t*>(slots), count, &s, out, pointer(a[14])));
+                                   static_cast<int64_t*>(slots), count, &s, out,
+                                   stream_of(a[13], dev)));
   });
 }
 
@@ -267,9 +300,8 @@ struct Window {
 };
 
 // q, kv_cache, block_table, seq_lens, out, lse | None
-Window window_args(PyObject* dev, PyObject* const* a, bool fp8) {
+Window window_args(PyObject* const* a, bool fp8) {
   Window w;
-  w.dev = integer32(dev, "device");
   const at::Tensor& q = tensor(a[0], "q");
   const at::Tensor& pool = tensor(a[1], "kv_cache");
   const at::Tensor& table = tensor(a[2], "block_table");
@@ -282,6 +314,7 @@ Window window_args(PyObject* dev, PyObject* const* a, bool fp8) {
   w.shape = pool_shape(pool, seq.size(0), q.size(1), table.size(1));
   if (q.size(2) != w.shape.head_size)
     refuse(PyExc_ValueError, "q head_size does not match kv_cache");
+  w.dev = call_device(q, "q");
   w.q = dense(q, "q", at::kBFloat16, w.dev);
   w.pool = pool_pointer(pool, fp8, w.dev);
   w.table = dense(table, "block_table", at::kInt, w.dev);
@@ -291,42 +324,42 @@ Window window_args(PyObject* dev, PyObject* const* a, bool fp8) {
   return w;
 }
 
-// (dev, q, kv_cache, block_table, seq_lens, out, lse | None, query_start_loc,
-//  max_query_len, scale, sliding_window, num_sinks, stream)
+// (q, kv_cache, block_table, seq_lens, out, lse | None, query_start_loc,
+//  max_query_len, scale, sliding_window, num_sinks, stream | None)
 PyObject* varlen_sinks(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded(n, 13, [&]() -> PyObject* {
-    const Window w = window_args(a[0], a + 1, false);
-    void* qsl = shaped(a[7], "query_start_loc", at::kInt, w.dev,
+  return guarded(n, 12, [&]() -> PyObject* {
+    const Window w = window_args(a, false);
+    void* qsl = shaped(a[6], "query_start_loc", at::kInt, w.dev,
                        {static_cast<int64_t>(w.shape.num_seqs) + 1});
     return PyLong_FromLong(sinks_fn(
         w.q, w.pool, static_cast<int32_t*>(w.table), static_cast<int32_t*>(qsl),
-        static_cast<int32_t*>(w.seq), extent(w.rows, "q"), integer32(a[8], "max_query_len"),
-        &w.shape, real(a[9]), integer32(a[10], "sliding_window"), integer32(a[11], "num_sinks"),
-        w.out, static_cast<float*>(w.lse), pointer(a[12])));
+        static_cast<int32_t*>(w.seq), extent(w.rows, "q"), integer32(a[7], "max_query_len"),
+        &w.shape, real(a[8]), integer32(a[9], "sliding_window"), integer32(a[10], "num_sinks"),
+        w.out, static_cast<float*>(w.lse), stream_of(a[11], w.dev)));
   });
 }
 
-// (dev, q, kv_cache, block_table, seq_lens, out, lse | None,
-//  (k_scale, v_scale) | None, scale, sliding_window, num_sinks, stream)
+// (q, kv_cache, block_table, seq_lens, out, lse | None,
+//  (k_scale, v_scale) | None, scale, sliding_window, num_sinks, stream | None)
 PyObject* decode_window(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded(n, 12, [&]() -> PyObject* {
-    const bool fp8 = a[7] != Py_None;
-    const Window w = window_args(a[0], a + 1, fp8);
+  return guarded(n, 11, [&]() -> PyObject* {
+    const bool fp8 = a[6] != Py_None;
+    const Window w = window_args(a, fp8);
     if (w.rows != w.shape.num_seqs) refuse(PyExc_ValueError, "q must hold one row per request");
     int32_t* table = static_cast<int32_t*>(w.table);
     int32_t* seq = static_cast<int32_t*>(w.seq);
     float* lse = static_cast<float*>(w.lse);
-    const float scale = real(a[8]);
-    const int window = integer32(a[9], "sliding_window"), sinks = integer32(a[10], "num_sinks");
+    const float scale = real(a[7]);
+    const int window = integer32(a[8], "sliding_window"), sinks = integer32(a[9], "num_sinks");
     if (fp8) {
-      if (!PyTuple_Check(a[7]) || PyTuple_GET_SIZE(a[7]) != 2)
+      if (!PyTuple_Check(a[6]) || PyTuple_GET_SIZE(a[6]) != 2)
         refuse(PyExc_TypeError, "(k_scale, v_scale) expected");
       return PyLong_FromLong(window_fp8_fn(
-          w.q, w.pool, table, seq, &w.shape, scale, real(PyTuple_GET_ITEM(a[7], 0)),
-          real(PyTuple_GET_ITEM(a[7], 1)), window, sinks, w.out, lse, pointer(a[11])));
+          w.q, w.pool, table, seq, &w.shape, scale, real(PyTuple_GET_ITEM(a[6], 0)),
+          real(PyTuple_GET_ITEM(a[6], 1)), window, sinks, w.out, lse, stream_of(a[10], w.dev)));
     }
     return PyLong_FromLong(window_fn(w.q, w.pool, table, seq, &w.shape, scale, window, sinks,
-                                     w.out, lse, pointer(a[11])));
+                                     w.out, lse, stream_of(a[10], w.dev)));
   });
 }
 
@@ -336,6 +369,7 @@ PyCFunction fast(F f) {
 }
 
 PyMethodDef methods[] = {
+    {"check_device", fast(check_device), METH_FASTCALL, "Refuses a device that is not current."},
     {"bind", fast(bind), METH_FASTCALL, "Takes the library's entry points (addresses)."},
     {"plan_step", fast(plan_step), METH_FASTCALL, "pa_plan_step"},
     {"norm_rope", fast(norm_rope), METH_FASTCALL, "pa_qk_norm_rope_cache, with scales _fp8"},

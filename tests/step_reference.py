@@ -175,11 +175,11 @@ def check_attention(got_o, got_l, ref, d, fp8, vmax, what):
     err = (got_o - o).abs()
     assert torch.isfinite(got_o).all(), f"{what}: non-finite output"
     worst = float((err - tol).max()) if err.numel() else 0.0
-    assert worst <= 0, f"{what}: output beyond its bound by {worst:.3e} (max err {float(err.max()):.3e})"
+    assert worst <= 0, f"{what}: output beyond its bound by {worst:.3e}"
     empty = torch.isneginf(lse)
     assert torch.equal(empty, torch.isneginf(got_l)), f"{what}: -inf pattern"
     assert (got_o[empty] == 0).all(), f"{what}: rows with nothing visible"
     live = ~empty
     ltol = logit[live] + 2.0 ** -20 * (1 + lse[live].abs())
     lerr = (got_l[live] - lse[live]).abs()
-    assert (lerr <= ltol).all(), f"{what}: lse off by {float((lerr - ltol).max()):.3e} beyond its bound"
+    assert (lerr <= ltol).all(), f"{what}: lse beyond its bound by {(lerr - ltol).max():.3e}"

@@ -163,7 +163,8 @@ def test_plan_allocates_its_outputs_and_steps_chain(pa):
     """Two steps in a row, the second from the first one's outputs."""
     ctx, q, table, free, start, nb = make(9, 20, 30, 60, 16, spare_cols=4, spare_free=40)
     tab, fr = i32(table), i32(free)
-    out = pa.pa_plan_step(i32(ctx), i32(q), tab, fr, 16, nb, max_tokens=700, free_start=i32([start]))
+    out = pa.pa_plan_step(i32(ctx), i32(q), tab, fr, 16, nb, max_tokens=700,
+                          free_start=i32([start]))
     one = torch.ones(20, dtype=torch.int32, device="cuda")
     out2 = pa.pa_plan_step(out[1], one, tab, fr, 16, nb, max_tokens=20, free_start=out[4][1:])
     w = ref.plan(ctx, q, table, free, start, 16, nb, 700)
