@@ -37,9 +37,6 @@ def nvcc() -> str:
     return cand
 
 
-CUDA_INCLUDE = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
-
-
 def _sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
 
@@ -68,12 +65,13 @@ def build_binding(force: bool = False, verbose: bool = False) -> str:
     os.makedirs(OUT_DIR, exist_ok=True)
     root = os.path.dirname(torch.__file__)
     inc, lib = os.path.join(root, "include"), os.path.join(root, "lib")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
     tmp = BINDING + f".{os.getpid()}.tmp"
     cmd = [os.environ.get("CXX") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
            "-I", INCLUDE, "-isystem", inc, "-isystem",
            os.path.join(inc, "torch", "csrc", "api", "include"),
-           "-isystem", sysconfig.get_paths()["include"], "-isystem", CUDA_INCLUDE, src, "-o", tmp,
+           "-isystem", sysconfig.get_paths()["include"], "-isystem", cuda, src, "-o", tmp,
            "-L", lib, "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda", f"-Wl,-rpath,{lib}"]
     if verbose:
         print(" ".join(cmd), flush=True)

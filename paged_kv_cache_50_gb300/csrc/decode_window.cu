@@ -81,6 +81,12 @@ __device__ __forceinline__ float ld_remote(uint32_t addr) {
   return v;
 }
 
+#ifdef PA_TEST_HOOKS
+// Test builds only: warp 0 of share g_decode_skip.x of the first request's
+// first kv head does not issue box g_decode_skip.y; {-1, -1} = off.
+__device__ int2 g_decode_skip = {-1, -1};
+#endif
+
 template <class KV, int D, int R, int NT, int W, int MINB>
 __global__ void __launch_bounds__(32 * W, MINB) decode_window_kernel(
     const __grid_constant__ CUtensorMap map, const __grid_constant__ WindowArgs a) {
@@ -123,8 +129,10 @@ __global__ void __launch_bounds__(32 * W, MINB) decode_window_kernel(
     return v < n_first ? 16 * v : wb + 16 * (v - n_first);
   };
   auto visible = [&](int p) { return p < seq && (p >= lo || p < sinks); };
+  // (A plain load: the table may be the previous kernel's output.)
   auto lookup = [&](int n) {
-    return block_at(table, div_bs(token(n), a.bs, a.bs_log2), a.max_blocks);
+    const int idx = div_bs(token(n), a.bs, a.bs_log2);
+    return idx < a.max_blocks ? table[idx] : -1;
   };
   // Block ids of sub-blocks n .. n + kAhead (the copies of the last one go
   // out while sub-block n is worked on).
@@ -154,6 +162,9 @@ __global__ void __launch_bounds__(32 * W, MINB) decode_window_kernel(
     const int n = C::kPair ? h : h >> 1;
     if (lane != 0 || n >= my_n) return;
     const uint32_t bar = bars + 8 * place;
+#ifdef PA_TEST_HOOKS
+    if (warp == 0 && h == g_decode_skip.y && kvh == 0 && i == 0 && s == g_decode_skip.x) return;
+#endif
     if (blk >= 0 && blk < a.num_blocks) {
       const int off = mod_bs(token(n), a.bs, a.bs_log2);
       tc::mbar_arrive_expect_tx(bar, C::kPlaceBytes);
@@ -393,6 +404,14 @@ cudaError_t launch_warps(const DecodeWindowLaunch& n, const WindowArgs& a, int S
 }
 
 }  // namespace
+
+#ifdef PA_TEST_HOOKS
+// Test builds only (not declared in pa.h).
+extern "C" int pa_test_skip_decode_box(int share, int box) {
+  const int2 v = make_int2(share, box);
+  return cudaMemcpyToSymbol(g_decode_skip, &v, sizeof(v)) == cudaSuccess ? 0 : 3;
+}
+#endif
 
 // CTAs per (request, kv head): as many as leave at most two per SM, up to 8,
 // and at least 64 tokens to each.  More CTAs cost more than they bring, since

@@ -61,13 +61,14 @@ __global__ void __launch_bounds__(kPlanThreads) plan_step_kernel(const PlanArgs 
   __shared__ uint32_t s_tok[kStep];   // first token of each request of the step
   __shared__ uint32_t s_blk[kStep];   // its first new block, counted from 0
   __shared__ uint32_t s_wt[32], s_wb[32];
+  // Inputs may be the previous kernel's outputs: plain loads, no read-only path.
   pdl_wait();
   pdl_trigger();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t t0 = blockIdx.x * static_cast<uint32_t>(kPlanThreads);
   const uint32_t t = t0 + tid;   // this thread's token
   const bool mine = t < static_cast<uint32_t>(a.max_tokens);
-  const int start = a.free_start != nullptr ? __ldg(a.free_start) : 0;
+  const int start = a.free_start != nullptr ? *a.free_start : 0;
   uint32_t tok = 0, blk = 0;     // tokens and new blocks of the requests before the step
   bool done = false;
   int bad = 0;
@@ -88,8 +89,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_step_kernel(const PlanArgs 
 #pragma unroll
     for (int k = 0; k < kPer; ++k) {
       const bool in = i0 + k < a.num_seqs;
-      int ctx = in ? __ldg(a.context_lens + i0 + k) : 0;
-      int n = in ? __ldg(a.query_lens + i0 + k) : 0;
+      int ctx = in ? a.context_lens[i0 + k] : 0;
+      int n = in ? a.query_lens[i0 + k] : 0;
       if (ctx < 0 || n < 0) bad |= PA_DEVERR_LENGTH;
       ctx = max(ctx, 0);
       n = max(n, 0);
@@ -170,7 +171,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_step_kernel(const PlanArgs 
           hi = mid - 1;
       }
       const int r = step * kStep + lo;
-      const int c = max(__ldg(a.context_lens + r), 0);
+      const int c = max(a.context_lens[r], 0);
       const int pos = c + static_cast<int>(t - s_tok[lo]);
       const int b = div_bs(pos, a.bs, a.bs_log2), off = mod_bs(pos, a.bs, a.bs_log2);
       const int have = blocks_of(c, a);
@@ -194,7 +195,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_step_kernel(const PlanArgs 
         } else if (f >= a.num_free) {
           bad |= PA_DEVERR_NO_BLOCKS;
         } else {
-          id = __ldg(a.free_blocks + f);
+          id = a.free_blocks[f];
           if (id < 0 || id >= a.num_blocks) {
             bad |= PA_DEVERR_BLOCK_ID;
             id = -1;

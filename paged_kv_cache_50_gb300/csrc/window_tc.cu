@@ -36,14 +36,18 @@
 //    formed by one addition each, and the thread is chosen by elect.sync, so
 //    that they live in uniform registers.
 //
-// Bound by the chain S -> softmax -> PV -> S of a Q tile (~3200 of a 128-token
-// tile pair's ~3300 cycles; its MMAs take 2290) and, at a unit's ends, by mask
-// and output code that is not in the instruction cache.  Measured (d 128, 16
-// requests of U[256, 2048] new tokens, 32 / 8 heads, window 1024, 4 first
-// tokens): 285 us, 1035 TFLOP/s; 8192 tokens of 64 / 8 heads, window 4096: 769
-// us, 1430 TFLOP/s; varlen_tc.cu's kernel with the same mask, one unit per CTA
-// and 128-token steps, took 419 and 1016.  Steps: persistent CTAs 365 / 953;
-// the short loops 318 / 880; descriptors 301 / 818; elect.sync 286 / 778.  Two
+//  * The grid has one slot per 2 x 128 rows of the whole batch and request, not
+//    per request and longest query, and the heads of a slot run side by side (they
+//    read neighbouring parts of the same cache rows).
+//
+// Bound by the chain S -> softmax -> PV -> S of a Q tile (~3200 cycles of a
+// 128-token tile pair; its MMAs take 2290) and, at a unit's ends, by mask and
+// output code that is not in the instruction cache.  Measured (d 128, 16 requests
+// of U[256, 2048] new tokens, 32 / 8 heads, window 1024, 4 first tokens): 275 us,
+// 1073 TFLOP/s; 8192 tokens of 64 / 8 heads, window 4096: 751 us, 1469 TFLOP/s;
+// varlen_tc.cu's kernel with the same mask, one unit per CTA and 128-token steps,
+// took 419 and 1016.  Steps: persistent CTAs 365 / 953; the short loops 318 / 880;
+// descriptors 301 / 818; elect.sync 286 / 778; heads side by side 275 / 751.  Two
 // MMA threads (368 / 1008), the next unit's first S between the last PVs (328 /
 // 915) and one loop for all S (354 / 1012) were slower.
 //
@@ -119,7 +123,7 @@ constexpr int kPieceRing = 4;
 struct Unit {
   int live;       // 0: no more units
   int request, kvh, q0;
-  int rows, tile;   // packed rows of the request, and which two Q tiles of them
+  int qlen, tile;   // query rows of the request, and which two Q tiles of them
   int seq, ctx;
   // The unit sees [oldest, end) and the first tokens: `first` pieces from
   // position 0, then pieces from `base`.
@@ -132,9 +136,9 @@ struct WinArgs {
   const int32_t* block_table;
   const int32_t* qsl;
   const int32_t* seq_lens;
-  int max_blocks, Hq, Hkv, grp, bs, bs_log2, num_blocks;
+  int N, max_blocks, Hq, Hkv, grp, bs, bs_log2, num_blocks;
   int row_tokens;   // query rows of a Q tile: 128 / grp
-  int total_q;
+  int total_q, max_query_len;
   float scale_log2;
   int window, sinks;
   __nv_bfloat16* out;
@@ -216,24 +220,31 @@ __device__ __forceinline__ void clc_request(uint32_t resp, uint32_t bar) {
       "r"(bar)
       : "memory");
 }
-// Whether a launch was cancelled, and the index of its CTA.
-__device__ __forceinline__ bool clc_answer(uint32_t resp, int& x, int& y, int& z) {
+// Whether a launch was cancelled, and the index of its CTA (of a 1-D grid).
+__device__ __forceinline__ bool clc_answer(uint32_t resp, int& x) {
   uint32_t ok;
   asm volatile(
       "{\n"
       ".reg .b128 r;\n"
       ".reg .pred p;\n"
-      "ld.shared.b128 r, [%4];\n"
+      "ld.shared.b128 r, [%2];\n"
       "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n"
       "selp.u32 %0, 1, 0, p;\n"
-      "mov.u32 %1, 0;\nmov.u32 %2, 0;\nmov.u32 %3, 0;\n"
-      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%1, %2, %3, _}, r;\n"
+      "mov.u32 %1, 0;\n"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%1, _, _, _}, r;\n"
       "}\n"
-      : "=r"(ok), "=r"(x), "=r"(y), "=r"(z)
+      : "=r"(ok), "=r"(x)
       : "r"(resp)
       : "memory");
   return ok != 0;
 }
+
+#ifdef PA_TEST_HOOKS
+// Test builds only: the producer of the CTA with index g_window_skip.x issues
+// neither the copies nor the byte count of the K of tile g_window_skip.y, so
+// the waits on it can only end at their poll limit; {-1, -1} = off.
+__device__ int2 g_window_skip = {-1, -1};
+#endif
 
 template <int D>
 __global__ void __launch_bounds__(384, 1)
@@ -317,7 +328,7 @@ window_tc_kernel(const __grid_constant__ CUtensorMap q_map,
       const int live = un->live, ntiles = un->tiles, n_first = un->first, tbase = un->base;
       const int end = un->end, oldest = un->oldest;
       const int qi = (un->tile * 2 + x) * a.row_tokens + t_tok;   // query row of the request
-      const bool valid = row_used && qi * a.grp < un->rows;
+      const bool valid = row_used && qi < un->qlen;
       const int lim = valid ? max(0, min(un->ctx + qi + 1, un->seq)) : 0;
       const int64_t qrow = static_cast<int64_t>(un->q0 + qi) * a.Hq + un->kvh * a.grp + hh;
       __syncwarp();
@@ -611,8 +622,9 @@ window_tc_kernel(const __grid_constant__ CUtensorMap q_map,
       const int v = jj * C::kPieces + lane;
       if (!box || v >= pieces) return -1;
       const int idx = div_bs(v < n_first ? 16 * v : tbase + 16 * (v - n_first), a.bs, a.bs_log2);
-      return block_at(a.block_table + static_cast<int64_t>(request) * a.max_blocks, idx,
-                      a.max_blocks);
+      // (A plain load: the table may be the previous kernel's output.)
+      return idx < a.max_blocks
+                 ? a.block_table[static_cast<int64_t>(request) * a.max_blocks + idx] : -1;
     };
     while (ok && (more || gv < gk)) {
       if (__any_sync(0xffffffffu, *abort_flag != 0)) break;
@@ -649,16 +661,23 @@ window_tc_kernel(const __grid_constant__ CUtensorMap q_map,
         if (gk >= 2 && !wait_all(BAR(kKEmpty + st), ((gk >> 1) - 1) & 1)) { ok = false; break; }
         const int v = j * C::kPieces + lane;
         const bool mine = box && v < pieces;
-        const bool good = mine && r0 >= 0 && r0 < a.num_blocks;
+#ifdef PA_TEST_HOOKS
+        const bool skip = blockIdx.x == static_cast<unsigned>(g_window_skip.x) &&
+                          gk == static_cast<uint32_t>(g_window_skip.y);
+#else
+        constexpr bool skip = false;
+#endif
+        const bool good = mine && r0 >= 0 && r0 < a.num_blocks && !skip;
         const int blk = good ? r0 : -1;
         const int off = mod_bs(v < n_first ? 16 * v : tbase + 16 * (v - n_first), a.bs, a.bs_log2);
         const unsigned loaded = __ballot_sync(0xffffffffu, good);
         const unsigned bad = __ballot_sync(0xffffffffu, mine && !good);
         if (lane == 0) {
-          if (bad != 0u) record_error(a.err, PA_DEVERR_BLOCK_ID);
+          if (bad != 0u && !skip) record_error(a.err, PA_DEVERR_BLOCK_ID);
           piece_ring[gk % kPieceRing] = (gk << 8) | (loaded & 0xffu);
-          tc::mbar_arrive_expect_tx(BAR(kKFull + st),
-                                    static_cast<uint32_t>(__popc(loaded)) * C::kPieceBytes);
+          if (!skip)
+            tc::mbar_arrive_expect_tx(BAR(kKFull + st),
+                                      static_cast<uint32_t>(__popc(loaded)) * C::kPieceBytes);
         }
         __syncwarp();
         // Coordinates: column, token in its 8-group, half (of all heads'), token
@@ -700,43 +719,83 @@ window_tc_kernel(const __grid_constant__ CUtensorMap q_map,
     }
   } else if (warp == 2) {
     // ------------------------------------------------------ units and queries
-    if (lane == 0) {
-      int cx = blockIdx.x, cy = blockIdx.y, cz = blockIdx.z;
-      const uint32_t resp = bars + kOffClc;
-      bool ok = true, asked = false;
-      uint32_t answers = 0, full = 0;
-      auto ask = [&]() {
+    // Slot s of the grid belongs to the last request i with qsl[i] / per + i <=
+    // s (per: query rows of a unit): request i owns at least ceil(qlen / per)
+    // slots from there on, and the grid has total_q / per + N slots, so that a
+    // batch of many short and a few long requests has at most one empty slot
+    // per request.  The request is found by a 32-way search.
+    // The heads of a slot run side by side: they read neighbouring parts of the
+    // same cache rows and queries.
+    int slot = blockIdx.x / a.Hkv, head = blockIdx.x - slot * a.Hkv;
+    const int per = 2 * a.row_tokens;
+    const uint32_t resp = bars + kOffClc;
+    bool ok = true, asked = false;
+    uint32_t answers = 0, full = 0;
+    // Unlike the others, these waits last as long as a unit.
+    auto wait = [&](int bar, uint32_t parity) {
+      for (int n = 0; n < 64; ++n) {
+        if (tc::mbar_wait(BAR(bar), parity)) return true;
+        if (*abort_flag) return false;
+      }
+      return false;
+    };
+    auto ask = [&]() {
+      if (lane == 0) {
         tc::mbar_arrive_expect_tx(BAR(kClc), 16);
         clc_request(resp, BAR(kClc));
-        asked = true;
-      };
-      ask();
-      int u = 0;
-      for (bool live = true; ok && live;) {
-        if (*abort_flag) break;
-        const int q0 = a.qsl[cz], rows = (a.qsl[cz + 1] - q0) * a.grp;
-        const int tile = static_cast<int>(gridDim.x) - 1 - cx;   // late rows first
-        const int qi = tile * 2 * a.row_tokens;                  // the unit's first query row
-        if (qi * a.grp < rows) {
-          const int qlen = rows / a.grp, seq = max(0, a.seq_lens[cz]), ctx = seq - qlen;
-          const int q_last = min(qi + 2 * a.row_tokens, qlen) - 1;
-          // Positions [0, end) and, in the window, from `oldest` on.
-          const int end = max(0, min(ctx + q_last + 1, seq));
-          const int oldest = max(0, ctx + qi + 1 - a.window);
-          int first = (min(a.sinks, end) + 15) >> 4, base = oldest & ~15;
-          if (base <= 16 * first) first = base = 0;
-          const int pieces = first + ((max(0, end - base) + 15) >> 4);
-          const int tiles = (pieces + C::kPieces - 1) / C::kPieces;
-          if (u >= 2 && !tc::mbar_wait(BAR(kUnitEmpty + (u & 1)), ((u >> 1) - 1) & 1)) {
-            ok = false;
-            break;
-          }
+      }
+      asked = true;
+    };
+    ask();
+    int u = 0;
+    for (bool live = true; live;) {
+      if (__any_sync(0xffffffffu, *abort_flag != 0)) {
+        ok = false;
+        break;
+      }
+      int lo = 0, hi = a.N, q0 = 0, q1 = 0, seq = 0;
+      for (;;) {
+        const int step = (hi - lo + 31) / 32, i = lo + lane * step;
+        const bool in = i < hi;
+        const int q = in ? a.qsl[i] : 0;
+        const bool last = step == 1;
+        // In the last round a lane holds its request's row.
+        const int next = in && last ? a.qsl[i + 1] : 0;
+        const int len = in && last ? a.seq_lens[i] : 0;
+        const unsigned below = __ballot_sync(0xffffffffu, in && q / per + i <= slot);
+        const int k = max(31 - __clz(below), 0);
+        lo += k * step;
+        hi = min(lo + step, hi);
+        if (last) {
+          q0 = __shfl_sync(0xffffffffu, q, k);
+          q1 = __shfl_sync(0xffffffffu, next, k);
+          seq = max(0, __shfl_sync(0xffffffffu, len, k));
+          break;
+        }
+      }
+      const int qlen = q1 - q0, tile = slot - (q0 / per + lo), qi = tile * per;   // first query row
+      if (tile >= 0 && qi < min(qlen, a.max_query_len)) {
+        const int ctx = seq - qlen;
+        const int q_last = min(qi + per, qlen) - 1;
+        // Positions [0, end) and, in the window, from `oldest` on.
+        const int end = max(0, min(ctx + q_last + 1, seq));
+        const int oldest = max(0, ctx + qi + 1 - a.window);
+        int first = (min(a.sinks, end) + 15) >> 4, base = oldest & ~15;
+        if (base <= 16 * first) first = base = 0;
+        const int pieces = first + ((max(0, end - base) + 15) >> 4);
+        const int tiles = (pieces + C::kPieces - 1) / C::kPieces;
+        if (u >= 2 &&
+            !__all_sync(0xffffffffu, wait(kUnitEmpty + (u & 1), ((u >> 1) - 1) & 1))) {
+          ok = false;
+          break;
+        }
+        if (lane == 0) {
           volatile Unit* un = unit_slot(u);
           un->live = 1;
-          un->request = cz;
-          un->kvh = cy;
+          un->request = lo;
+          un->kvh = head;
           un->q0 = q0;
-          un->rows = rows;
+          un->qlen = qlen;
           un->tile = tile;
           un->seq = seq;
           un->ctx = ctx;
@@ -747,46 +806,58 @@ window_tc_kernel(const __grid_constant__ CUtensorMap q_map,
           un->pieces = pieces;
           un->tiles = tiles;
           tc::mbar_arrive(BAR(kUnitFull + (u & 1)));
-          ++u;
-          if (tiles > 0) {
-            for (int x = 0; x < 2; ++x) {
-              if (full > 0 && !tc::mbar_wait(BAR(kQEmpty + x), (full - 1) & 1)) {
-                ok = false;
-                break;
-              }
-              // Rows past the request or the batch are fetched too (or zeros):
-              // they are masked.
+        }
+        __syncwarp();
+        ++u;
+        if (tiles > 0) {
+          for (int x = 0; x < 2 && ok; ++x) {
+            if (full > 0 &&
+                !__all_sync(0xffffffffu, wait(kQEmpty + x, (full - 1) & 1))) {
+              ok = false;
+              break;
+            }
+            // Rows past the request or the batch are fetched too (or zeros):
+            // they are masked.
+            if (lane == 0) {
               tc::mbar_arrive_expect_tx(
                   BAR(kQFull + x), static_cast<uint32_t>(a.row_tokens * a.grp) * (D * 2));
               for (int h = 0; h < C::kHalves; ++h)
                 tc::tma_load_3d(sbase + x * C::kQBytes + h * (C::kBM * 128), &q_map,
-                                BAR(kQFull + x), h * 64, cy * a.grp,
+                                BAR(kQFull + x), h * 64, head * a.grp,
                                 min(q0 + qi + x * a.row_tokens, a.total_q));
             }
-            if (!ok) break;
-            ++full;
           }
-        }
-        // The next unit, if a launch is left to take over.
-        if (!tc::mbar_wait(BAR(kClc), answers & 1)) { ok = false; break; }
-        ++answers;
-        asked = false;
-        live = clc_answer(resp, cx, cy, cz);
-        if (live) {
-          tc::fence_proxy_async_smem();   // the answer has been read
-          ask();
+          if (!ok) break;
+          ++full;
         }
       }
-      if (ok && !*abort_flag) {
-        if (u >= 2 && !tc::mbar_wait(BAR(kUnitEmpty + (u & 1)), ((u >> 1) - 1) & 1)) {
-          ok = false;
-        } else {
-          unit_slot(u)->live = 0;
-          unit_slot(u)->tiles = 0;
-          tc::mbar_arrive(BAR(kUnitFull + (u & 1)));
-        }
+      // The next unit, if a launch is left to take over.
+      if (!__all_sync(0xffffffffu, wait(kClc, answers & 1))) {
+        ok = false;
+        break;
       }
-      if (!ok) fail();
+      ++answers;
+      asked = false;
+      int cta;
+      live = clc_answer(resp, cta);
+      slot = cta / a.Hkv;
+      head = cta - slot * a.Hkv;
+      if (live) {
+        tc::fence_proxy_async_smem();   // the answer has been read
+        __syncwarp();
+        ask();
+      }
+    }
+    if (ok && u >= 2)
+      ok = __all_sync(0xffffffffu, wait(kUnitEmpty + (u & 1), ((u >> 1) - 1) & 1));
+    if (lane == 0) {
+      if (ok) {
+        unit_slot(u)->live = 0;
+        unit_slot(u)->tiles = 0;
+        tc::mbar_arrive(BAR(kUnitFull + (u & 1)));
+      } else {
+        fail();
+      }
       // Nothing may land in shared memory any more.
       if (asked) tc::mbar_wait(BAR(kClc), answers & 1);
       if (full > 0)
@@ -847,6 +918,7 @@ cudaError_t launch_t(const WindowPrefillLaunch& n, cudaStream_t stream) {
   a.seq_lens = n.seq_lens;
   a.max_blocks = n.max_blocks;
   a.Hq = n.Hq;
+  a.N = n.N;
   a.Hkv = n.Hkv;
   a.grp = n.Hq / n.Hkv;
   a.bs = n.bs;
@@ -854,6 +926,7 @@ cudaError_t launch_t(const WindowPrefillLaunch& n, cudaStream_t stream) {
   a.num_blocks = n.num_blocks;
   a.row_tokens = C::kBM / a.grp;
   a.total_q = n.total_q;
+  a.max_query_len = n.max_query_len;
   a.scale_log2 = n.scale * kLog2e;
   a.window = n.window;
   a.sinks = n.sinks;
@@ -871,13 +944,22 @@ cudaError_t launch_t(const WindowPrefillLaunch& n, cudaStream_t stream) {
   static DeviceFlags attr_set;
   cudaError_t e = set_smem_once(kern, C::kSmemBytes, attr_set);
   if (e != cudaSuccess) return e;
-  const int per = 2 * a.row_tokens;   // query rows of a unit
-  const unsigned tiles = static_cast<unsigned>((n.max_query_len - 1) / per) + 1u;
-  return launch_pdl(kern, dim3(tiles, n.Hkv, n.N), dim3(C::kThreads), C::kSmemBytes, stream, q_map,
-                    k_map, v_map, a);
+  // Slots of the grid, per head: see the scheduler.
+  const long long ctas = (n.total_q / (2 * a.row_tokens) + static_cast<long long>(n.N)) * n.Hkv;
+  if (ctas > INT_MAX) return cudaErrorInvalidValue;
+  return launch_pdl(kern, dim3(static_cast<unsigned>(ctas)), dim3(C::kThreads), C::kSmemBytes,
+                    stream, q_map, k_map, v_map, a);
 }
 
 }  // namespace
+
+#ifdef PA_TEST_HOOKS
+// Test builds only (not declared in pa.h).
+extern "C" int pa_test_skip_window_tile(int cta, int tile) {
+  const int2 v = make_int2(cta, tile);
+  return cudaMemcpyToSymbol(g_window_skip, &v, sizeof(v)) == cudaSuccess ? 0 : 3;
+}
+#endif
 
 cudaError_t launch_window_prefill(const WindowPrefillLaunch& n, cudaStream_t stream) {
   return n.d == 128 ? launch_t<128>(n, stream) : launch_t<64>(n, stream);

@@ -105,6 +105,8 @@ PREFILL = {
     "late_chunk": ([2100], [70], 12, 4, 128, 16),
     "g128_d64": ([40, 300], [7, 33], 128, 1, 64, 16),
     "g100": ([70, 140], [12, 5], 100, 1, 128, 32),
+    "one_long_many_short": ([5 + k for k in range(70)] + [700] + [40] * 30,
+                            [1] * 70 + [500] + [1] * 30, 8, 4, 64, 16),
     "many_empty": ([1, 400, 2, 3, 1, 30], [1, 400, 1, 2, 1, 1], 8, 4, 64, 16),
 }
 MASKS = [(1, 0), (1, 1), (7, 2), (16, 16), (100, 4), (128, 0), (129, 17), (64, 15), (250, 130),
