@@ -180,7 +180,9 @@ __global__ void __launch_bounds__(kPlanThreads) plan_step_kernel(const PlanArgs 
       if (b < have) {
         // The part-filled last block of the context.
         if (b < a.max_blocks) {
-          id = *entry;
+          // Past L1: other CTAs write entries of the same line, and a kernel that
+          // is launched while this one runs must not find the line there.
+          id = __ldcg(entry);
           if (id < 0 || id >= a.num_blocks) {
             bad |= PA_DEVERR_BLOCK_ID;
             id = -1;

@@ -152,7 +152,7 @@ def window_attention(q, pool, table, qsl, seqs, scale, window, sinks):
                 X[a:b, hs] = mag.masked_fill(~vis[:, None], 0).amax(-1)
                 x = x.masked_fill(~vis[:, None], -math.inf)
                 lse[a:b, hs] = torch.logsumexp(x, -1)
-                w = torch.softmax(x, -1)
+                w = torch.softmax(x, -1).masked_fill(~vis[:, None], 0)   # a row may see nothing
                 o = torch.einsum("tgk,kd->tgd", w, v[:, h])
                 out[a:b, hs] = o
                 B[a:b, hs] = torch.einsum("tgk,kd->tgd", w, v[:, h].abs())

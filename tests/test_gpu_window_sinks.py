@@ -148,6 +148,58 @@ def test_prefill_leaves_other_rows(pa):
     assert (out[130:] == 3.0).all() and (lse[130:] == 5.0).all()
 
 
+def test_prefill_more_queries_than_tokens(pa):
+    """Requests whose queries reach before position 0: those rows see nothing
+    (0, -inf), whole units of them included; the others are aligned to the end."""
+    b = Batch(54, [20, 5, 300, 1], [150, 200, 40, 65], 8, 2, 64, 16, 24, 3, poison=False)
+    o, l = b.prefill(pa)
+    b.check(pa, (o, l), "queries before position 0")
+    assert torch.isneginf(l[:130]).all() and not torch.isneginf(l[130:150]).any()
+
+
+def test_prefill_is_repeatable_and_without_lse(pa):
+    b = Batch(55, *PREFILL["ragged"], 100, 4)
+    o1, l1 = b.prefill(pa)
+    for _ in range(4):
+        o2, l2 = b.prefill(pa)
+        assert torch.equal(o1, o2) and torch.equal(l1, l2)
+    o3, l3 = b.prefill(pa, return_lse=False)
+    assert l3 is None and torch.equal(o1, o3)
+
+
+def test_prefill_captured_and_beside_another(pa):
+    """A captured call replayed with other lengths and inputs, while another
+    stream runs the same kernel on its own batch."""
+    b = Batch(56, [500, 90, 700], [300, 90, 256], 8, 2, 128, 16, 200, 4, poison=False)
+    other = Batch(57, [4000], [2500], 16, 4, 128, 16, 1024, 4)
+    want = other.prefill(pa)
+    out, lse = torch.empty_like(b.q), torch.empty(b.q.shape[:2], device="cuda")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        b.prefill(pa, out=out, lse=lse)
+    for seqs, qlens in (([500, 90, 700], [300, 90, 256]), ([496, 60, 640], [290, 0, 1]),
+                        ([300, 90, 650], [300, 1, 200])):
+        b.seqs = np.array(seqs)
+        b.qsl = np.concatenate([[0], np.cumsum(qlens)])
+        b.dev_seq.copy_(torch.from_numpy(b.seqs.astype(np.int32)))
+        b.dev_qsl.copy_(torch.from_numpy(b.qsl.astype(np.int32)))
+        b.q.normal_()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            for _ in range(3):
+                graph.replay()
+        for _ in range(3):
+            got = other.prefill(pa)
+        torch.cuda.synchronize()
+        n = int(b.qsl[-1])
+        ref.check_attention(out[:n], lse[:n], tuple(t[:n] for t in b.reference()), b.d, False,
+                            b.vmax, f"replay {qlens}")
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert pa.pa_get_device_error() == 0
+
+
 def test_prefill_bad_visible_block_is_masked(pa):
     b = Batch(53, [300], [40], 8, 2, 64, 16, 64, 4, poison=False)
     b.dev_table[0, 17] = 10 ** 6      # positions 272..287: in the window
@@ -203,6 +255,14 @@ def test_decode_is_repeatable_and_without_lse(pa):
         assert torch.equal(o1, o2) and torch.equal(l1, l2)
     o3, l3 = b.decode(pa, return_lse=False)
     assert l3 is None and torch.equal(o1, o3)
+
+
+def test_decode_float8_pool_is_its_codes(pa):
+    b = Batch(67, [900, 33], [1, 1], 16, 4, 128, 16, 200, 20, fp8=True)
+    want = b.decode(pa)
+    b.pool = b.pool.view(torch.float8_e4m3fn)
+    got = b.decode(pa)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
 
 
 def test_decode_unaligned_query_and_output(pa):
