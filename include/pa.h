@@ -403,7 +403,9 @@ pa_status pa_mla_prefill(const void* q, const void* kv_cache, const void* w_kv_b
  *   base_i = free_start + sum_{j < i} (need_j - have_j)
  * the call writes
  *   seq_lens[i] = seq_i;
- *   query_start_loc[0..N]: exclusive prefix sums of query_lens, then the sum T;
+ *   query_start_loc[0..N]: exclusive prefix sums of query_lens, then the sum T,
+ *     none above max_tokens (so that no request's rows leave a buffer of that
+ *     many);
  *   block_table[i, have_i + k] = free_blocks[base_i + k], k < need_i - have_i
  *     (other entries stay as they are);
  *   for token t = query_start_loc[i] + j, j < query_lens[i]:
@@ -413,8 +415,8 @@ pa_status pa_mla_prefill(const void* q, const void* kv_cache, const void* w_kv_b
  *     slot_mapping[t] = -1 (the cache writes skip them);
  *   totals[0] = T, totals[1] = free_start + the number of blocks taken (the
  *     next step's free_start).
- * free_start is a device int32, NULL for 0; totals must not overlap it.
- * Nothing else of the outputs may overlap an input.
+ * free_start is a device int32, NULL for 0.  No output may overlap an input or
+ * another output (PA_ERR_INVALID): two steps in a row take two totals in turn.
  * Refused on the device, without a write out of range:
  *   - a new block when free_blocks (num_free entries) is used up: its table
  *     entry becomes -1, its tokens get slot -1, PA_DEVERR_NO_BLOCKS;
@@ -456,8 +458,9 @@ pa_status pa_plan_step(const int32_t* context_lens, const int32_t* query_lens,
  * q: [num_tokens, Hq, d] bf16 with q_stride elements from token to token (the
  * heads of a token are dense), key and value likewise with Hkv heads: views of
  * one packed projection need no copy.  Strides: multiples of 8, at least H * d.
- * q_out: [num_tokens, Hq, d] bf16, dense; it may be q itself when q is dense,
- * and overlaps no other argument.  cos_sin: [max_position, r] fp32;
+ * q_out: [num_tokens, Hq, d] bf16, dense; it may be q itself when q is dense, and
+ * overlaps no other argument (PA_ERR_INVALID where it reaches into q, key or
+ * value).  cos_sin: [max_position, r] fp32;
  * positions: [num_tokens] int32; with r == 0 both are unused and may be NULL.
  * Supported: head_size in {64, 128}, r a multiple of 16, at most head_size.
  * Data pointers 16-byte aligned.  eps >= 0.  Uses shape->num_q_heads,
@@ -493,6 +496,9 @@ pa_status pa_qk_norm_rope_cache_fp8(const void* q, const void* key, const void* 
  * request sees (between the first tokens and the oldest window) are not
  * read: their table entries and contents may be anything.  A position that
  * one row of a request sees must hold finite values, as for pa_varlen_fwd.
+ * scale is finite and > 0.  Rows of a request past max_query_len or total_q are
+ * not written; positions past the table's columns are not seen
+ * (PA_DEVERR_BLOCK_ID).
  * Supported: head_size in {64, 128}, Hq / Hkv <= 128.
  */
 pa_status pa_varlen_fwd_sinks(const void* q, const void* kv_cache, const int32_t* block_table,
@@ -509,7 +515,8 @@ pa_status pa_varlen_fwd_sinks(const void* q, const void* kv_cache, const int32_t
  * visible tokens are cut over the CTAs of a thread-block cluster, which merge
  * their partial results in shared memory.
  * q, out: [N, Hq, d] bf16; lse: [N, Hq] fp32, nullable.  seq_lens[i] <= 0:
- * out = 0, lse = -inf.  sliding_window >= 1, num_sinks >= 0.
+ * out = 0, lse = -inf.  sliding_window >= 1, num_sinks >= 0, scale finite and >
+ * 0.  Positions past the table's columns are not seen (PA_DEVERR_BLOCK_ID).
  * Supported: head_size in {64, 128}, Hq / Hkv <= 16.  q 4-byte, kv_cache
  * 16-byte, out 2-byte aligned.
  */

@@ -52,6 +52,18 @@ pa_status from_cuda(cudaError_t e) { return e == cudaSuccess ? PA_OK : PA_ERR_CU
 // rows in 4-byte pairs.
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) % n) == 0; }
 
+bool scale_ok(float x) { return x > 0.f && x <= 3.4028234663852886e38f; }
+
+// A range of device memory.
+struct Range {
+  const void* p;
+  size_t bytes;
+};
+bool overlap(const Range& a, const Range& b) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+  return a.bytes > 0 && b.bytes > 0 && (x < y ? y - x < a.bytes : x - y < b.bytes);
+}
+
 // Device address of the error word on the current device (looked up once per
 // device; a host-side symbol is not a device address).
 int* device_error_ptr() {
@@ -274,7 +286,8 @@ pa_status pa_varlen_fwd_sinks(const void* q, const void* kv_cache, const int32_t
                               int total_q, int max_query_len, const pa_shape* shape, float scale,
                               int sliding_window, int num_sinks, void* out, float* lse,
                               void* stream) {
-  if (!shape_ok(shape) || total_q < 0 || max_query_len < 0 || sliding_window < 1 || num_sinks < 0)
+  if (!shape_ok(shape) || total_q < 0 || max_query_len < 0 || sliding_window < 1 ||
+      num_sinks < 0 || !scale_ok(scale))
     return PA_ERR_INVALID;
   if (shape->head_size != 64 && shape->head_size != 128) return PA_ERR_UNSUPPORTED;
   if (shape->num_q_heads / shape->num_kv_heads > 128) return PA_ERR_UNSUPPORTED;
@@ -482,8 +495,6 @@ pa_status pa_decode_splitkv(const void* q, const void* kv_cache, const int32_t* 
       static_cast<cudaStream_t>(stream)));
 }
 
-static bool scale_ok(float x) { return x > 0.f && x <= 3.4028234663852886e38f; }
-
 pa_status pa_reshape_and_cache_fp8(const void* key, const void* value, void* kv_cache,
                                    const int64_t* slot_mapping, int num_tokens,
                                    const pa_shape* shape, float k_scale, float v_scale,
@@ -532,7 +543,8 @@ static pa_status decode_window(const void* q, const void* kv_cache, const int32_
                                const int32_t* seq_lens, const pa_shape* shape, float scale,
                                bool fp8, float k_scale, float v_scale, int sliding_window,
                                int num_sinks, void* out, float* lse, void* stream) {
-  if (!shape_ok(shape) || sliding_window < 1 || num_sinks < 0) return PA_ERR_INVALID;
+  if (!shape_ok(shape) || sliding_window < 1 || num_sinks < 0 || !scale_ok(scale))
+    return PA_ERR_INVALID;
   if (!scale_ok(k_scale) || !scale_ok(v_scale)) return PA_ERR_INVALID;
   if (shape->head_size != 64 && shape->head_size != 128) return PA_ERR_UNSUPPORTED;
   if (shape->num_q_heads / shape->num_kv_heads > 16) return PA_ERR_UNSUPPORTED;
@@ -605,6 +617,16 @@ pa_status pa_plan_step(const int32_t* context_lens, const int32_t* query_lens,
       !aligned(seq_lens, 4) || !aligned(positions, 4) || !aligned(slot_mapping, 8) ||
       !aligned(totals, 4))
     return PA_ERR_INVALID;
+  // Inputs, then outputs: a CTA reads inputs while another writes its outputs.
+  const size_t n4 = static_cast<size_t>(num_seqs) * 4, cap = static_cast<size_t>(max_tokens);
+  const Range ranges[] = {
+      {context_lens, n4}, {query_lens, n4}, {free_blocks, static_cast<size_t>(num_free) * 4},
+      {free_start, free_start != nullptr ? 4u : 0u}, {block_table, n4 * max_blocks_per_seq},
+      {query_start_loc, n4 + 4}, {seq_lens, n4}, {positions, cap * 4}, {slot_mapping, cap * 8},
+      {totals, 8}};
+  for (int out = 4; out < 10; ++out)
+    for (int k = 0; k < out; ++k)
+      if (overlap(ranges[out], ranges[k])) return PA_ERR_INVALID;
   return from_cuda(pa::launch_plan_step(
       context_lens, query_lens, free_blocks, free_start, num_free, num_seqs, max_blocks_per_seq,
       block_size, num_blocks, max_tokens, block_table, query_start_loc, seq_lens, positions,
@@ -642,7 +664,14 @@ static pa_status norm_rope(const void* q, const void* key, const void* value, in
       !aligned(k_weight, 16) || !aligned(cos_sin, 16) || !aligned(kv_cache, 16) ||
       !aligned(q_out, 16) || !aligned(positions, 4) || !aligned(slot_mapping, 8))
     return PA_ERR_INVALID;
-  if (q_out == q && q_stride != qw) return PA_ERR_INVALID;
+  // q_out is q (dense) or lies apart from all three inputs.
+  auto rows = [&](const void* p, int64_t stride, int64_t width) {
+    return Range{p, static_cast<size_t>((num_tokens - 1) * stride + width) * 2};   // bf16
+  };
+  const Range out = rows(q_out, qw, qw);
+  if ((q_out == q ? q_stride != qw && num_tokens > 1 : overlap(out, rows(q, q_stride, qw))) ||
+      overlap(out, rows(key, key_stride, kw)) || overlap(out, rows(value, value_stride, kw)))
+    return PA_ERR_INVALID;
   pa::NormRopeLaunch n{};
   n.q = q;
   n.key = key;

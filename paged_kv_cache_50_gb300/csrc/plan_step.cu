@@ -151,7 +151,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_step_kernel(const PlanArgs 
       s_tok[tid * kPer + k] = et;
       s_blk[tid * kPer + k] = eb;
       if (owner && i0 + k < a.num_seqs) {
-        a.query_start_loc[i0 + k] = static_cast<int32_t>(et);
+        // At most max_tokens: rows of a buffer of that length stay in range.
+        a.query_start_loc[i0 + k] = min(static_cast<int>(et), a.max_tokens);
         a.seq_lens[i0 + k] = seq[k];
       }
       et = sat_add(et, q[k]);
@@ -219,7 +220,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_step_kernel(const PlanArgs 
   if (blockIdx.x == gridDim.x - 1) {
     // The last CTA has walked every request.
     if (tid == 0) {
-      a.query_start_loc[a.num_seqs] = static_cast<int32_t>(tok);
+      a.query_start_loc[a.num_seqs] = min(static_cast<int>(tok), a.max_tokens);
       a.totals[0] = static_cast<int32_t>(tok);
       a.totals[1] = static_cast<int32_t>(sat_add(max(start, 0), blk));
       if (tok > static_cast<uint32_t>(a.max_tokens)) bad |= PA_DEVERR_LENGTH;

@@ -85,7 +85,7 @@ def plan(ctx, qlen, table, free, start, bs, num_blocks, cap):
         seqs.append(c + m)
     if t > cap:
         err |= DEVERR["LENGTH"]
-    return (np.array(qsl, np.int32), np.array(seqs, np.int32), pos, slots,
+    return (np.minimum(qsl, cap).astype(np.int32), np.array(seqs, np.int32), pos, slots,
             np.array([t, at], np.int32), table, err)
 
 

@@ -47,6 +47,23 @@ def test_plan_step_refusals(pa):
         assert _plan(pa, **bad) == pa.PA_ERR_INVALID, bad
 
 
+def test_plan_step_refuses_overlaps(pa):
+    """No output may lie in an input or in another output."""
+    apart = dict(ctx=1 << 12, q=2 << 12, free=3 << 12, start=4 << 12, table=5 << 12, qsl=6 << 12,
+                 seq=7 << 12, pos=8 << 12, slot=9 << 12, totals=10 << 12)
+    size = dict(ctx=8, q=8, free=16, start=4, table=32, qsl=12, seq=8, pos=40, slot=80, totals=8)
+    inputs = ("ctx", "q", "free", "start")
+    for out in apart:
+        for other in apart:
+            if out == other or out in inputs:
+                continue
+            for at in (apart[other], apart[other] + size[other] - 4,
+                       apart[other] - size[out] + 4):
+                if out == "slot" and at % 8:
+                    continue
+                assert _plan(pa, **{**apart, out: at}) == pa.PA_ERR_INVALID, (out, other, at)
+
+
 def _norm(pa, shape=None, fp8=False, **kw):
     f = dict(q=P, k=P, v=P, qs=256, ks=128, vs=128, qw=P, kw=P, eps=1e-6, cs=P, rows=16, rot=64,
              inter=0, pos=P, cache=P, slots=P, n=4)
@@ -70,6 +87,11 @@ def test_norm_rope_refusals(pa, fp8):
                 dict(rot=80), dict(rows=0), dict(eps=-1.0), dict(eps=nan), dict(eps=inf),
                 dict(qs=512, out=P)):   # in place needs dense queries
         assert _norm(pa, fp8=fp8, **bad) == pa.PA_ERR_INVALID, bad
+    # The output in a part of an input: 4 tokens of 512, 256 and 256 bytes.
+    at = dict(q=1 << 12, k=2 << 12, v=3 << 12, out=4 << 12)
+    for name, size in (("q", 2048), ("k", 1024), ("v", 1024)):
+        for off in (16 - 2048, 16, size - 16) + ((0,) if name != "q" else ()):
+            assert _norm(pa, fp8=fp8, **{**at, "out": at[name] + off}) == pa.PA_ERR_INVALID
     for bad in (dict(num_q_heads=0), dict(num_kv_heads=0), dict(head_size=0), dict(block_size=0),
                 dict(block_size=24), dict(num_blocks=0), dict(num_q_heads=70000)):
         assert _norm(pa, _shape(pa, **bad), fp8=fp8) == pa.PA_ERR_INVALID, bad
@@ -87,20 +109,23 @@ def test_windowed_attention_refusals(pa):
     L = pa.lib()
     s = _shape(pa)
 
-    def varlen(shape=s, window=8, sinks=2, ptrs=(P,) * 5, out=P, lse=NULL, total=4):
-        return L.pa_varlen_fwd_sinks(*ptrs, total, 2, ctypes.byref(shape), 0.1, window, sinks, out,
+    def varlen(shape=s, window=8, sinks=2, ptrs=(P,) * 5, out=P, lse=NULL, total=4, scale=0.1):
+        return L.pa_varlen_fwd_sinks(*ptrs, total, 2, ctypes.byref(shape), scale, window, sinks, out,
                                      lse, NULL)
 
-    def decode(shape=s, window=8, sinks=2, ptrs=(P,) * 4, out=P, lse=NULL):
-        return L.pa_decode_window(*ptrs, ctypes.byref(shape), 0.1, window, sinks, out, lse, NULL)
+    def decode(shape=s, window=8, sinks=2, ptrs=(P,) * 4, out=P, lse=NULL, scale=0.1):
+        return L.pa_decode_window(*ptrs, ctypes.byref(shape), scale, window, sinks, out, lse, NULL)
 
-    def decode8(shape=s, window=8, sinks=2, ptrs=(P,) * 4, out=P, lse=NULL, ks=1.0, vs=1.0):
-        return L.pa_decode_window_fp8(*ptrs, ctypes.byref(shape), 0.1, ks, vs, window, sinks, out,
+    def decode8(shape=s, window=8, sinks=2, ptrs=(P,) * 4, out=P, lse=NULL, ks=1.0, vs=1.0,
+                scale=0.1):
+        return L.pa_decode_window_fp8(*ptrs, ctypes.byref(shape), scale, ks, vs, window, sinks, out,
                                       lse, NULL)
 
     for f, n in ((varlen, 5), (decode, 4), (decode8, 4)):
         assert f(window=0) == f(window=-3) == f(sinks=-1) == f(out=NULL) == pa.PA_ERR_INVALID
         assert f(lse=66) == pa.PA_ERR_INVALID
+        for bad in (0.0, -0.1, float("inf"), float("nan")):
+            assert f(scale=bad) == pa.PA_ERR_INVALID
         for k in range(n):
             assert f(ptrs=tuple(NULL if j == k else P for j in range(n))) == pa.PA_ERR_INVALID
             assert f(ptrs=tuple(P + 2 if j == k else P for j in range(n))) == pa.PA_ERR_INVALID

@@ -152,7 +152,7 @@ def test_plan_sums_saturate(pa):
     """Lengths whose sum leaves 32 bits: no wrap, tokens in range, LENGTH."""
     big = 2 ** 31 - 1
     got = run(pa, [0, 0, 0], [big, big, 4], [[1], [2], [3]], [5, 6], 0, 16, 8, 40)
-    assert got[-1] & ref.DEVERR["LENGTH"] and got[0].tolist() == [0, big, big, big]
+    assert got[-1] & ref.DEVERR["LENGTH"] and got[0].tolist() == [0, 40, 40, 40]
     assert got[2].tolist() == list(range(40)) and got[3].tolist()[:16] == list(range(80, 96))
     assert got[3].tolist()[16:] == [-1] * 24
     got = run(pa, [big], [5], [[1]], [5], 0, 16, 8, 5)
@@ -171,6 +171,27 @@ def test_plan_allocates_its_outputs_and_steps_chain(pa):
     w2 = ref.plan(w[1], np.ones(20), w[5], free, int(w[4][1]), 16, nb, 20)
     assert w[-1] == w2[-1] == 0
     compare([t.cpu().numpy() for t in out2] + [tab.cpu().numpy(), pa.pa_get_device_error()], w2)
+
+
+def test_plan_beyond_capacity_keeps_attention_in_range(pa):
+    """A step of more tokens than its buffers hold: attention over the plan's
+    outputs neither leaves them nor touches another row."""
+    ctx, q = np.array([20, 0, 7]), np.array([30, 40, 50])
+    tab, cap = i32(np.full((3, 8), -1)), 64
+    tab[0, :2], tab[2, 0] = i32([0, 1]), 2
+    qsl, seq, pos, slot, tot = pa.pa_plan_step(i32(ctx), i32(q), tab, i32(np.arange(3, 24)), 16, 24,
+                                               max_tokens=cap)
+    assert qsl.tolist() == [0, 30, 64, 64] and tot.tolist()[0] == 120
+    assert pa.pa_get_device_error() == pa.PA_DEVERR_LENGTH
+    pool = torch.randn(24, 2, 16, 2, 64, device="cuda").bfloat16()
+    x = torch.randn(cap + 80, 8, 64, device="cuda").bfloat16()
+    out, lse = torch.full_like(x, 3.0), torch.full((cap + 80, 8), 5.0, device="cuda")
+    pa.pa_varlen_fwd_sinks(x[:cap], pool, tab, qsl, seq, 50, 0.1, 16, 2, out=out[:cap],
+                           lse=lse[:cap])
+    torch.cuda.synchronize()
+    pa.pa_get_device_error()      # the blocks that were never opened
+    assert torch.isfinite(out[:30]).all()
+    assert (out[cap:] == 3.0).all() and (lse[cap:] == 5.0).all()
 
 
 def test_plan_argument_checks(pa):
