@@ -43,6 +43,7 @@ struct WindowArgs {
   const int32_t* block_table;
   const int32_t* seq_lens;
   int max_blocks, Hq, Hkv, bs, bs_log2, num_blocks;
+  int positions;      // of a table row, at most INT_MAX - 64
   float scale_log2;   // scale * k_scale * log2(e)
   float out_scale;    // v_scale
   int window, sinks;
@@ -111,14 +112,17 @@ __global__ void __launch_bounds__(32 * W, MINB) decode_window_kernel(
   }
   __syncwarp();   // each warp uses its own barriers only
   pdl_wait();
-  const int seq = min(max(0, a.seq_lens[i]), INT_MAX - 64);   // sums below stay in range
+  const int seq = max(0, a.seq_lens[i]);
   const int32_t* table = a.block_table + static_cast<int64_t>(i) * a.max_blocks;
   const int lo = seq > a.window ? seq - a.window : 0;
-  const int sinks = min(a.sinks, seq);
+  // What lies past the table's columns has no block and is not walked over.
+  const int end = min(seq, a.positions);
+  if (end < seq && s == 0 && threadIdx.x == 0) record_error(a.err, PA_DEVERR_BLOCK_ID);
+  const int sinks = min(a.sinks, end);
   int n_first = (sinks + 15) >> 4, wb = lo & ~15;
   if (wb <= 16 * n_first) n_first = wb = 0;   // the first tokens reach the window: one run
   // 16-token sub-blocks of the list, and this CTA's share [v0, v1) of them.
-  const int nsb = n_first + static_cast<int>((static_cast<unsigned>(seq - wb) + 15u) >> 4);
+  const int nsb = n_first + ((max(0, end - wb) + 15) >> 4);
   const int per = (nsb + S - 1) / S;
   const int v_begin = min(nsb, s * per), v_end = min(nsb, v_begin + per);
   const int left = v_end - v_begin - warp;
@@ -128,11 +132,11 @@ __global__ void __launch_bounds__(32 * W, MINB) decode_window_kernel(
     const int v = v_begin + warp + n * C::kWarps;
     return v < n_first ? 16 * v : wb + 16 * (v - n_first);
   };
-  auto visible = [&](int p) { return p < seq && (p >= lo || p < sinks); };
+  auto visible = [&](int p) { return p < end && (p >= lo || p < sinks); };
   // (A plain load: the table may be the previous kernel's output.)
   auto lookup = [&](int n) {
     const int idx = div_bs(token(n), a.bs, a.bs_log2);
-    return idx < a.max_blocks ? table[idx] : -1;
+    return table[idx];
   };
   // Block ids of sub-blocks n .. n + kAhead (the copies of the last one go
   // out while sub-block n is worked on).
@@ -456,6 +460,7 @@ cudaError_t launch_decode_window(const DecodeWindowLaunch& n, cudaStream_t strea
   a.err = n.err;
   const long long positions = static_cast<long long>(n.max_blocks) * n.bs;
   const long long visible = std::min(static_cast<long long>(n.window) + n.sinks, positions);
+  a.positions = static_cast<int>(std::min(positions, INT_MAX - 64LL));
   const int S = decode_window_shares(n.N, n.Hkv, visible, n.sm_count);
   const bool wide = n.Hq / n.Hkv > 8;   // groups of 9..16 heads take two n-tiles
   using dec::KvBf16;

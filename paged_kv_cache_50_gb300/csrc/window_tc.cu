@@ -118,12 +118,13 @@ constexpr int kOffClc = 224;                  // response (16, 16-byte aligned)
 constexpr int kOffRing = 240;                 // loaded-piece masks of four tiles (16)
 constexpr int kOffUnits = 256;                // two descriptors
 constexpr int kPieceRing = 4;
+constexpr int kEmptySlots = 256;   // about half a millisecond
 
 // What a unit is (in shared memory, 64 bytes each).
 struct Unit {
   int live;       // 0: no more units
   int request, kvh, q0;
-  int qlen, tile;   // query rows of the request, and which two Q tiles of them
+  int rows, tile;   // query rows of the request, and which two Q tiles of them
   int seq, ctx;
   // The unit sees [oldest, end) and the first tokens: `first` pieces from
   // position 0, then pieces from `base`.
@@ -139,6 +140,7 @@ struct WinArgs {
   int N, max_blocks, Hq, Hkv, grp, bs, bs_log2, num_blocks;
   int row_tokens;   // query rows of a Q tile: 128 / grp
   int total_q, max_query_len;
+  int positions;    // of a table row, at most INT_MAX - 127
   float scale_log2;
   int window, sinks;
   __nv_bfloat16* out;
@@ -328,7 +330,7 @@ window_tc_kernel(const __grid_constant__ CUtensorMap q_map,
       const int live = un->live, ntiles = un->tiles, n_first = un->first, tbase = un->base;
       const int end = un->end, oldest = un->oldest;
       const int qi = (un->tile * 2 + x) * a.row_tokens + t_tok;   // query row of the request
-      const bool valid = row_used && qi < un->qlen;
+      const bool valid = row_used && qi < un->rows;
       const int lim = valid ? max(0, min(un->ctx + qi + 1, un->seq)) : 0;
       const int64_t qrow = static_cast<int64_t>(un->q0 + qi) * a.Hq + un->kvh * a.grp + hh;
       __syncwarp();
@@ -476,7 +478,7 @@ window_tc_kernel(const __grid_constant__ CUtensorMap q_map,
       }
       if (alive && ntiles > 0) {   // warp-uniform
         tc::tc_fence_after();
-        const float inv = lr > 0.f ? 1.f / lr : 0.f;
+        const float inv = lr == 0.f ? 0.f : 1.f / lr;
         // 32-byte stores write whole sectors where `out` is 32-byte aligned.
         const bool a32 = (reinterpret_cast<uintptr_t>(a.out) & 31u) == 0;
         uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + qrow * D);
@@ -504,7 +506,7 @@ window_tc_kernel(const __grid_constant__ CUtensorMap q_map,
           }
         }
         if (valid && a.lse != nullptr)
-          a.lse[qrow] = l > 0.f ? (m_used + log2f(l)) * kLn2 : -CUDART_INF_F;
+          a.lse[qrow] = l == 0.f ? -CUDART_INF_F : (m_used + log2f(l)) * kLn2;
       } else if (valid) {
         // Nothing visible (or a CTA that gave up): o = 0, lse = -inf.
         uint4* dst = reinterpret_cast<uint4*>(a.out + qrow * D);
@@ -731,6 +733,7 @@ window_tc_kernel(const __grid_constant__ CUtensorMap q_map,
     const uint32_t resp = bars + kOffClc;
     bool ok = true, asked = false;
     uint32_t answers = 0, full = 0;
+    int empty = 0;   // empty slots in a row
     // Unlike the others, these waits last as long as a unit.
     auto wait = [&](int bar, uint32_t parity) {
       for (int n = 0; n < 64; ++n) {
@@ -774,16 +777,28 @@ window_tc_kernel(const __grid_constant__ CUtensorMap q_map,
         }
       }
       const int qlen = q1 - q0, tile = slot - (q0 / per + lo), qi = tile * per;   // first query row
-      if (tile >= 0 && qi < min(qlen, a.max_query_len)) {
+      // Rows past max_query_len, or outside the batch, are not touched.
+      const int rows = q0 >= 0 ? min(min(qlen, a.max_query_len), a.total_q - q0) : 0;
+      const bool real = tile >= 0 && qi < rows;
+      // A long run of empty slots is broken by units without rows, so that the
+      // other warps' waits for a unit stay short.
+      empty = real ? 0 : empty + 1;
+      if (real || empty == kEmptySlots) {
+        empty = 0;
         const int ctx = seq - qlen;
-        const int q_last = min(qi + per, qlen) - 1;
-        // Positions [0, end) and, in the window, from `oldest` on.
-        const int end = max(0, min(ctx + q_last + 1, seq));
+        const int q_last = min(qi + per, rows) - 1;
+        // Positions [0, end) and, in the window, from `oldest` on; what lies past
+        // the table's columns has no block and is not walked over.
+        int end = max(0, min(ctx + q_last + 1, seq));
+        if (real && end > a.positions) {
+          if (lane == 0) record_error(a.err, PA_DEVERR_BLOCK_ID);
+          end = a.positions;
+        }
         const int oldest = max(0, ctx + qi + 1 - a.window);
         int first = (min(a.sinks, end) + 15) >> 4, base = oldest & ~15;
         if (base <= 16 * first) first = base = 0;
         const int pieces = first + ((max(0, end - base) + 15) >> 4);
-        const int tiles = (pieces + C::kPieces - 1) / C::kPieces;
+        const int tiles = real ? (pieces + C::kPieces - 1) / C::kPieces : 0;
         if (u >= 2 &&
             !__all_sync(0xffffffffu, wait(kUnitEmpty + (u & 1), ((u >> 1) - 1) & 1))) {
           ok = false;
@@ -795,7 +810,7 @@ window_tc_kernel(const __grid_constant__ CUtensorMap q_map,
           un->request = lo;
           un->kvh = head;
           un->q0 = q0;
-          un->qlen = qlen;
+          un->rows = real ? rows : 0;
           un->tile = tile;
           un->seq = seq;
           un->ctx = ctx;
@@ -927,6 +942,8 @@ cudaError_t launch_t(const WindowPrefillLaunch& n, cudaStream_t stream) {
   a.row_tokens = C::kBM / a.grp;
   a.total_q = n.total_q;
   a.max_query_len = n.max_query_len;
+  a.positions = static_cast<int>(
+      std::min(static_cast<long long>(n.max_blocks) * n.bs, INT_MAX - 127LL));
   a.scale_log2 = n.scale * kLog2e;
   a.window = n.window;
   a.sinks = n.sinks;

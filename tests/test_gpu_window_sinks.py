@@ -148,6 +148,75 @@ def test_prefill_leaves_other_rows(pa):
     assert (out[130:] == 3.0).all() and (lse[130:] == 5.0).all()
 
 
+def test_prefill_rows_past_the_batch(pa):
+    """A last request that reaches past total_q or max_query_len: the rows that
+    exist are computed, the others are left as they were."""
+    b = Batch(58, [60, 200], [40, 90], 8, 2, 64, 16, 32, 4, poison=False)
+    full = b.reference()
+    for T, longest, rows in ((110, 90, [(0, 110)]), (130, 50, [(0, 40), (40, 90)])):
+        out = torch.full((200, 8, 64), 3.0, device="cuda").bfloat16()
+        lse = torch.full((200, 8), 5.0, device="cuda")
+        pa.pa_varlen_fwd_sinks(b.q[:T], b.pool, b.dev_table, b.dev_qsl, b.dev_seq, longest,
+                               b.scale, 32, 4, out=out[:T], lse=lse[:T])
+        done = torch.zeros(200, dtype=torch.bool, device="cuda")
+        for lo, hi in rows:
+            done[lo:hi] = True
+            ref.check_attention(out[lo:hi], lse[lo:hi], tuple(t[lo:hi] for t in full), b.d, False,
+                                b.vmax, f"rows {lo}:{hi}")
+        assert (out[~done] == 3.0).all() and (lse[~done] == 5.0).all()
+    assert pa.pa_get_device_error() == 0
+
+
+def test_prefill_most_requests(pa):
+    """65535 requests and 64 kv heads, nearly all requests without queries."""
+    n, heads, last = 65535, 64, 40
+    seq = torch.full((n,), 16, dtype=torch.int32, device="cuda")
+    qsl = torch.zeros(n + 1, dtype=torch.int32, device="cuda")
+    qsl[1:], qsl[n] = 16, 16 + last      # the first and the last one
+    seq[n - 1] = last
+    table = torch.zeros((n, 3), dtype=torch.int32, device="cuda")
+    table[n - 1] = torch.tensor([1, 2, 3])
+    pool = torch.randn(4, 2, 16, heads, 64, device="cuda").bfloat16()
+    q = torch.randn(16 + last, heads, 64, device="cuda").bfloat16()
+    out, lse = pa.pa_varlen_fwd_sinks(q, pool, table, qsl, seq, last, 0.125, 16, 2)
+    short = torch.tensor([0, 16, 16 + last], dtype=torch.int32, device="cuda")
+    want, wl = pa.pa_varlen_fwd_sinks(q, pool, table[[0, n - 1]], short, seq[[0, n - 1]], last,
+                                      0.125, 16, 2)
+    assert torch.equal(out, want) and torch.equal(lse, wl)
+    assert pa.pa_get_device_error() == 0
+
+
+def test_nan_query_stays_in_its_row(pa):
+    b = Batch(59, [300, 70], [90, 70], 8, 2, 128, 16, 64, 4, poison=False)
+    want, wl = b.prefill(pa)
+    b.q[33, 5, 7] = float("nan")
+    got, gl = b.prefill(pa)
+    assert torch.isnan(got[33, 5]).all() and torch.isnan(gl[33, 5])
+    got[33, 5], gl[33, 5] = want[33, 5], wl[33, 5]
+    assert torch.equal(got, want) and torch.equal(gl, wl)
+
+
+@pytest.mark.parametrize("length", [16 * 21, BIG])
+def test_lengths_past_the_table(pa, length):
+    """Positions past the table's columns are not seen, and not walked over."""
+    b = Batch(68, [300, 40], [1, 1], 8, 2, 64, 16, BIG, 4, poison=False)
+    assert b.dev_table.shape[1] == 20
+    want = Batch(68, [300, 40], [1, 1], 8, 2, 64, 16, BIG, 4, poison=False).decode(pa)
+    b.dev_seq[0] = length
+    b.dev_table[0, 19] = 0        # the last column
+    for call in (b.decode, b.prefill):
+        got = call(pa)
+        assert pa.pa_get_device_error() == pa.PA_DEVERR_BLOCK_ID
+        assert torch.isfinite(got[0]).all() and torch.isfinite(got[1]).all()
+        assert (got[1][1] - want[1][1]).abs().max() < 1e-5
+        b.dev_seq[0] = 320
+        o, l = b.decode(pa)       # what the table holds
+        assert pa.pa_get_device_error() == 0
+        assert (got[1][0] - l[0]).abs().max() < 1e-5
+        assert (got[0].float() - o.float()).abs().max() < 0.02
+        b.dev_seq[0] = length
+
+
 def test_prefill_more_queries_than_tokens(pa):
     """Requests whose queries reach before position 0: those rows see nothing
     (0, -inf), whole units of them included; the others are aligned to the end."""
