@@ -9,24 +9,27 @@
 // The visible tokens form a list of 16-token sub-blocks: ceil(sinks / 16)
 // first ones, then those from lo rounded down to 16 (one run from position 0
 // where the two meet).  Nothing else is read.  One cluster of S CTAs serves
-// one (request, kv head): CTA r takes the r-th share of the list, its four or
-// eight warps sub-blocks in turn, each warp with its own ring of K and V tiles,
-// filled by TMA boxes of 16 token rows of a head (a box is one instruction of
-// one lane; the same ring filled by cp.async took 49.7 us instead of 42.5 on
+// one (request, kv head): CTA r takes the r-th share of the list, its four,
+// eight or sixteen warps sub-blocks in turn, each warp with its own ring of K and V
+// tiles, filled by TMA boxes of 16 token rows of a head (a box is one instruction
+// of one lane; the same ring filled by cp.async took 49.7 us instead of 42.5 on
 // the batch below, its address and mask arithmetic being what a warp spent its
-// time on).  The warps' states are merged in shared memory, the CTAs' in
-// distributed shared memory, every CTA writing a share of the outputs.  A
-// window bounds a request's work, so unlike split-KV decode over a whole
-// context S <= 8 shares are enough, and the second launch and its fp32
-// workspace (written and read once) go.
+// time on).  The warps' states are merged in shared memory.  The CTAs send each
+// other their parts of the outputs (st.async, counted on a barrier of the
+// receiver), and each finishes a share of them.  A window bounds a request's
+// work, so unlike split-KV decode over a whole context S <= 8 shares are enough,
+// and the second launch and its fp32 workspace (written and read once) go.
 //
-// Bound by HBM where the batch fills the GPU, else by latency (lengths ->
-// block ids -> K/V -> merge, one after the other).  Measured (32 / 8 heads,
-// d 128): 64 requests, window 1024 over U[128, 4096] tokens, 242 MB: 41.7 us,
-// 5.8 TB/s; window 4096 over U[1024, 8192], 899 MB: 135.2 us, 6.6 TB/s; an e4m3
-// pool, 128 requests, window 4096, 911 MB: 149 us, 6.1 TB/s (372 warp
-// instructions per 16 tokens, 64 of them conversions); one request of 64 / 8
-// heads, window 4096: 10.1 us.
+// Bound by HBM where the batch fills the GPU, else by latency: one request of 64
+// / 8 heads, window 4096, takes 8.1 us, of which the launch and the set-up are
+// ~2, lengths and block ids 0.5, the first tile 0.9, two to three sub-blocks per
+// warp 2.7 (a sub-block is a chain of ~1600 cycles in a warp, which is why more
+// warps help), the warps' merge 0.6 and the cluster's 1.2.  Fetching the parts from the
+// others between two cluster barriers instead took 1.1 us longer.  Measured (32 / 8
+// heads, d 128): 64 requests, window 1024 over U[128, 4096] tokens, 242 MB: 41.0
+// us, 5.9 TB/s; window 4096 over U[1024, 8192], 899 MB: 135-137 us, 6.6 TB/s; an
+// e4m3 pool, 128 requests, window 4096, 911 MB: 148-151 us, 6.1 TB/s (372 warp
+// instructions per 16 tokens, 64 of them conversions).
 #include <algorithm>
 #include <climits>
 
@@ -42,7 +45,8 @@ struct WindowArgs {
   const __nv_bfloat16* q;
   const int32_t* block_table;
   const int32_t* seq_lens;
-  int max_blocks, Hq, Hkv, bs, bs_log2, num_blocks;
+  int max_blocks, Hq, grp, bs, bs_log2, num_blocks;
+  int out_share;      // outputs (heads x d) of a CTA
   int positions;      // of a table row, at most INT_MAX - 64
   float scale_log2;   // scale * k_scale * log2(e)
   float out_scale;    // v_scale
@@ -68,18 +72,24 @@ struct WindowCfg {
   static constexpr int kWarpBytes = R * kPlaceBytes;   // a multiple of the swizzle atom
   static constexpr int kPipeBytes = kWarps * kWarpBytes;
   static constexpr int kHeads = 8 * NT;
-  // Combine buffer: O rows per warp, then max, sum and divisor per (warp,
-  // head), then the CTA's max, sum and divisor per head.
-  static constexpr int kCombineBytes = (kWarps * kHeads * (KV::kOStride + 3) + 3 * kHeads) * 4;
+  // Combine buffer: O rows per warp, then max (later: factor), sum and divisor
+  // per (warp, head), then the CTA's max, sum and divisor per head (16 bytes).
+  static constexpr int kOffStats = kWarps * kHeads * (KV::kOStride + 3) * 4;
+  static constexpr int kCombineBytes = kOffStats + kHeads * 16;
   static constexpr int kDataBytes = kPipeBytes > kCombineBytes ? kPipeBytes : kCombineBytes;
   static constexpr int kOffBar = (kDataBytes + 7) / 8 * 8;   // [warp][R] barriers
-  static constexpr int kSmemBytes = kOffBar + kWarps * R * 8 + 1024;   // + alignment slack
+  // What the cluster's CTAs send each other, apart from the ring, which a slower
+  // CTA still uses: a barrier, max, sum and divisor per (CTA, head), and a share
+  // of each CTA's O.
+  static constexpr int kOffReceived = (kOffBar + kWarps * R * 8 + 15) / 16 * 16;
+  static constexpr int kSmemBytes = kOffReceived + 1024;   // + alignment slack
+  __host__ __device__ static constexpr int received_bytes(int S, int share) {
+    return 16 + S * kHeads * 16 + S * share * 4;
+  }
 };
-
-__device__ __forceinline__ float ld_remote(uint32_t addr) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-  return v;
+// Outputs of one CTA of a cluster of S, out of `total`: whole 16 bytes.
+__host__ __device__ __forceinline__ int output_share(int total, int S) {
+  return (total / 4 + S - 1) / S * 4;
 }
 
 #ifdef PA_TEST_HOOKS
@@ -98,7 +108,7 @@ __global__ void __launch_bounds__(32 * W, MINB) decode_window_kernel(
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* const smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const int S = gridDim.x, s = blockIdx.x, kvh = blockIdx.y, i = blockIdx.z;   // cluster = grid.x
-  const int grp = a.Hq / a.Hkv;
+  const int grp = a.grp;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int gid = lane >> 2, tid4 = lane & 3;
 
@@ -108,9 +118,11 @@ __global__ void __launch_bounds__(32 * W, MINB) decode_window_kernel(
     tc::tma_prefetch_desc(&map);
 #pragma unroll
     for (int k = 0; k < R; ++k) tc::mbar_init(bars + 8 * k, 1);
+    if (warp == 0) tc::mbar_init(smem_u32(smem) + C::kOffReceived, 1);
     tc::fence_barrier_init();
   }
-  __syncwarp();   // each warp uses its own barriers only
+  __syncwarp();   // each warp uses its own ring's barriers only
+  if (S > 1) tc::cluster_arrive_relaxed();   // the receive barrier is set up
   pdl_wait();
   const int seq = max(0, a.seq_lens[i]);
   const int32_t* table = a.block_table + static_cast<int64_t>(i) * a.max_blocks;
@@ -144,21 +156,6 @@ __global__ void __launch_bounds__(32 * W, MINB) decode_window_kernel(
 #pragma unroll
   for (int n = 0; n <= kAhead; ++n) ids[n] = n < my_n ? lookup(n) : -1;
 
-  uint32_t qf[NT][kK][2];
-  {
-    const __nv_bfloat16* qb =
-        a.q + (static_cast<int64_t>(i) * a.Hq + static_cast<int64_t>(kvh) * grp) * D;
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const int h = nt * 8 + gid;
-#pragma unroll
-      for (int kk = 0; kk < kK; ++kk) {
-        qf[nt][kk][0] = qf[nt][kk][1] = 0u;
-        if (h < grp) KV::load_q(qb + h * D, tid4, kk, qf[nt][kk]);
-      }
-    }
-  }
-
   // Box h into ring place `place`: sub-block h, or the K or V of sub-block
   // h / 2, in block blk.  A box that is not loaded (no such block) completes
   // its barrier all the same.
@@ -191,10 +188,33 @@ __global__ void __launch_bounds__(32 * W, MINB) decode_window_kernel(
     if (++at == R) at = 0, parity ^= 1;
   };
 
-  dec::State<D, NT> st;
-  st.clear();
+  // The first boxes go out before anything else that can wait for them.
 #pragma unroll
   for (int h = 0; h < R - 1; ++h) issue(h, ids[C::kPair ? h : h >> 1], h);
+
+  const int total = grp * D, out_share = a.out_share;
+  const int out_begin = s * out_share, out_n = max(0, min(total - out_begin, out_share));
+  const uint32_t received = smem_u32(smem) + C::kOffReceived;
+  if (S > 1 && threadIdx.x == 0)
+    tc::mbar_arrive_expect_tx(received, static_cast<uint32_t>(S * (out_n * 4 + grp * 16)));
+  __syncwarp();
+  uint32_t qf[NT][kK][2];
+  {
+    const __nv_bfloat16* qb =
+        a.q + (static_cast<int64_t>(i) * a.Hq + static_cast<int64_t>(kvh) * grp) * D;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int h = nt * 8 + gid;
+#pragma unroll
+      for (int kk = 0; kk < kK; ++kk) {
+        qf[nt][kk][0] = qf[nt][kk][1] = 0u;
+        if (h < grp) KV::load_q(qb + h * D, tid4, kk, qf[nt][kk]);
+      }
+    }
+  }
+
+  dec::State<D, NT> st;
+  st.clear();
   for (int n = 0; n < my_n && alive; ++n) {
     const int blk = ids[0];
     const int after = n + kAhead + 1;   // the next block id, a sub-block ahead of its copies
@@ -259,14 +279,13 @@ __global__ void __launch_bounds__(32 * W, MINB) decode_window_kernel(
         if (KV::kRoundedSums) st.lr[nt][j] += __shfl_xor_sync(0xffffffffu, st.lr[nt][j], o);
       }
 
-  // The four warps' states -> this CTA's (max, sum, divisor, O) per head, in
-  // place of warp 0's O rows.
+  // The warps' states, in place of the ring.
   __syncthreads();
   float* obuf = reinterpret_cast<float*>(smem);
   float* mbuf = obuf + C::kWarps * C::kHeads * KV::kOStride;   // [warp][head]
   float* lbuf = mbuf + C::kWarps * C::kHeads;
   float* rbuf = lbuf + C::kWarps * C::kHeads;
-  float* cta = rbuf + C::kWarps * C::kHeads;                   // [3][head]
+  float4* stats = reinterpret_cast<float4*>(smem + C::kOffStats);   // [head]
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -288,66 +307,105 @@ __global__ void __launch_bounds__(32 * W, MINB) decode_window_kernel(
     }
   }
   __syncthreads();
-  for (int idx = threadIdx.x; idx < grp * D; idx += C::kThreads) {
-    const int r = idx / D, e = idx % D;
-    float M = -CUDART_INF_F;
+  // Each warp's factor per head; a head's warps are neighbouring lanes.
+  const int64_t row0 = static_cast<int64_t>(i) * a.Hq + kvh * grp;
+  if (threadIdx.x < C::kWarps * C::kHeads) {   // whole warps
+    const int h = threadIdx.x / C::kWarps, at = threadIdx.x % C::kWarps * C::kHeads + h;
+    float M = mbuf[at];
 #pragma unroll
-    for (int w = 0; w < C::kWarps; ++w) M = fmaxf(M, mbuf[w * C::kHeads + r]);
-    float L = 0.f, LR = 0.f, acc = 0.f;
-    if (M != -CUDART_INF_F) {
+    for (int o = 1; o < C::kWarps; o <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    float f = M == -CUDART_INF_F ? 0.f : fast_exp2(mbuf[at] - M);
+    float L = f * lbuf[at], LR = f * rbuf[at];
 #pragma unroll
-      for (int w = 0; w < C::kWarps; ++w) {
-        const float f = fast_exp2(mbuf[w * C::kHeads + r] - M);
-        L += f * lbuf[w * C::kHeads + r];
-        LR += f * rbuf[w * C::kHeads + r];
-        acc += f * obuf[(w * C::kHeads + r) * KV::kOStride + KV::place(e)];
-      }
+    for (int o = 1; o < C::kWarps; o <<= 1) {
+      L += __shfl_xor_sync(0xffffffffu, L, o);
+      LR += __shfl_xor_sync(0xffffffffu, LR, o);
     }
-    const int64_t row = static_cast<int64_t>(i) * a.Hq + kvh * grp + r;
     if (S == 1) {
-      a.out[row * D + e] = __float2bfloat16_rn(LR == 0.f ? 0.f : acc / LR * a.out_scale);
-      if (e == 0 && a.lse != nullptr)
-        a.lse[row] = L == 0.f ? -CUDART_INF_F : (M + log2f(L)) * kLn2;
-    } else {
-      obuf[r * KV::kOStride + KV::place(e)] = acc;   // only this thread reads it
-      if (e == 0) {
-        cta[r] = M;
-        cta[C::kHeads + r] = L;
-        cta[2 * C::kHeads + r] = LR;
-      }
+      f = LR == 0.f ? 0.f : f / LR * a.out_scale;
+      if (threadIdx.x % C::kWarps == 0 && h < grp && a.lse != nullptr)
+        a.lse[row0 + h] = L == 0.f ? -CUDART_INF_F : (M + log2f(L)) * kLn2;
+    } else if (threadIdx.x % C::kWarps == 0) {
+      stats[h] = make_float4(M, L, LR, 0.f);
     }
+    mbuf[at] = f;
   }
-  if (S == 1) return;
-  tc::cluster_sync();
-  // Merge over the cluster: the outputs are dealt out over its CTAs.
-  const uint32_t o_at = smem_u32(obuf), c_at = smem_u32(cta);
-  for (int idx = s * C::kThreads + threadIdx.x; idx < grp * D; idx += S * C::kThreads) {
-    const int r = idx / D, e = idx % D;
-    const uint32_t oa = o_at + (r * KV::kOStride + KV::place(e)) * 4, ca = c_at + r * 4;
-    float m[kMaxShares], M = -CUDART_INF_F;
+  __syncthreads();
+  auto merged = [&](int idx) {
+    const int r = idx / D, at = KV::place(idx % D);
+    float acc = 0.f;
+#pragma unroll
+    for (int w = 0; w < C::kWarps; ++w)
+      acc = fmaf(mbuf[w * C::kHeads + r], obuf[(w * C::kHeads + r) * KV::kOStride + at], acc);
+    return acc;
+  };
+  if (S == 1) {
+    for (int idx = threadIdx.x; idx < total; idx += C::kThreads)
+      a.out[row0 * D + idx] = __float2bfloat16_rn(merged(idx));
+    return;
+  }
+  // Each CTA makes a share of the outputs.  The others' parts are sent to it, not
+  // fetched: one way instead of a cluster barrier and a round trip, and since
+  // every CTA waits for all that is sent to it, none leaves early.
+  const uint32_t stats_at = received + 16, o_at = stats_at + S * C::kHeads * 16;
+  tc::cluster_wait();   // every CTA's barrier is set up
+  for (int idx = 4 * threadIdx.x; idx < total; idx += 4 * C::kThreads) {
+    const int owner = idx / out_share, r = idx / D, at = KV::place(idx % D);
+    float v[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int w = 0; w < C::kWarps; ++w) {
+      const float f = mbuf[w * C::kHeads + r];
+      const float* o = obuf + (w * C::kHeads + r) * KV::kOStride + at;
+      float x[4];
+      if constexpr (KV::kRoundedSums) {
+        const float4 q = *reinterpret_cast<const float4*>(o);
+        x[0] = q.x, x[1] = q.y, x[2] = q.z, x[3] = q.w;
+      } else {
+        x[0] = o[0], x[1] = o[1], x[2] = o[2], x[3] = o[3];
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = fmaf(f, x[e], v[e]);
+    }
+    tc::st_async_v4(tc::map_to_rank(o_at + (s * out_share + idx - owner * out_share) * 4, owner),
+                    __float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
+                    __float_as_uint(v[3]), tc::map_to_rank(received, owner));
+  }
+  for (int k = threadIdx.x; k < S * grp; k += C::kThreads) {
+    const int to = k / grp, r = k - to * grp;
+    const float4 v = stats[r];
+    tc::st_async_v4(tc::map_to_rank(stats_at + (s * C::kHeads + r) * 16, to), __float_as_uint(v.x),
+                    __float_as_uint(v.y), __float_as_uint(v.z), 0u, tc::map_to_rank(received, to));
+  }
+  // A CTA whose own waits run out sends after at most R + 1 limits.
+  bool got = false;
+  for (int k = 0; k < 4 * R && !got; ++k) got = tc::mbar_wait_cluster(received, 0);
+  if (!got) record_error(a.err, PA_DEVERR_TIMEOUT);
+  const float4* all = reinterpret_cast<const float4*>(smem + C::kOffReceived + 16);   // [CTA][head]
+  const float* parts = reinterpret_cast<const float*>(all + S * C::kHeads);           // [CTA][share]
+  for (int n = threadIdx.x; n < out_n; n += C::kThreads) {
+    const int r = (out_begin + n) / D, e = (out_begin + n) % D;
+    float4 v[kMaxShares];
+    float o[kMaxShares], M = -CUDART_INF_F;
 #pragma unroll
     for (int k = 0; k < kMaxShares; ++k) {
-      m[k] = k < S ? ld_remote(tc::map_to_rank(ca, k)) : -CUDART_INF_F;
-      M = fmaxf(M, m[k]);
+      v[k] = k < S ? all[k * C::kHeads + r] : make_float4(-CUDART_INF_F, 0.f, 0.f, 0.f);
+      o[k] = k < S ? parts[k * out_share + n] : 0.f;
+      M = fmaxf(M, v[k].x);
     }
     float L = 0.f, LR = 0.f, acc = 0.f;
     if (M != -CUDART_INF_F) {
 #pragma unroll
       for (int k = 0; k < kMaxShares; ++k) {
-        if (k < S) {
-          const float f = fast_exp2(m[k] - M);
-          L += f * ld_remote(tc::map_to_rank(ca + C::kHeads * 4, k));
-          LR += f * ld_remote(tc::map_to_rank(ca + 2 * C::kHeads * 4, k));
-          acc += f * ld_remote(tc::map_to_rank(oa, k));
-        }
+        const float f = fast_exp2(v[k].x - M);
+        L += f * v[k].y;
+        LR += f * v[k].z;
+        acc += f * o[k];
       }
     }
-    const int64_t row = static_cast<int64_t>(i) * a.Hq + kvh * grp + r;
-    a.out[row * D + e] = __float2bfloat16_rn(LR == 0.f ? 0.f : acc / LR * a.out_scale);
+    a.out[(row0 + r) * D + e] = __float2bfloat16_rn(LR == 0.f ? 0.f : acc / LR * a.out_scale);
     if (e == 0 && a.lse != nullptr)
-      a.lse[row] = L == 0.f ? -CUDART_INF_F : (M + log2f(L)) * kLn2;
+      a.lse[row0 + r] = L == 0.f ? -CUDART_INF_F : (M + log2f(L)) * kLn2;
   }
-  tc::cluster_sync();   // no CTA leaves while another reads its shared memory
 }
 
 // The pool viewed 5-D, innermost first.  Rows of one column group (128 bytes,
@@ -381,12 +439,15 @@ cudaError_t launch_t(const DecodeWindowLaunch& n, const WindowArgs& a, int S, cu
   CUtensorMap map;
   if (!make_tile_map(&map, n)) return cudaErrorInvalidValue;
   static DeviceFlags smem_set;
-  cudaError_t e = set_smem_once(kern, C::kSmemBytes, smem_set);
+  cudaError_t e = set_smem_once(
+      kern, C::kSmemBytes + C::received_bytes(kMaxShares, output_share(C::kHeads * D, kMaxShares)),
+      smem_set);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(S, n.Hkv, n.N);
   cfg.blockDim = dim3(C::kThreads);
-  cfg.dynamicSmemBytes = C::kSmemBytes;
+  cfg.dynamicSmemBytes =
+      C::kSmemBytes + (S > 1 ? C::received_bytes(S, a.out_share) : 0);
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -403,6 +464,8 @@ cudaError_t launch_t(const DecodeWindowLaunch& n, const WindowArgs& a, int S, cu
 template <class KV, int D, int R, int NT, int MINB>
 cudaError_t launch_warps(const DecodeWindowLaunch& n, const WindowArgs& a, int S, int warps,
                          cudaStream_t stream) {
+  if constexpr (NT == 1)
+    if (warps == 16) return launch_t<KV, D, R, NT, 16, 1>(n, a, S, stream);
   return warps == 8 ? launch_t<KV, D, R, NT, 8, 3 - NT>(n, a, S, stream)
                     : launch_t<KV, D, R, NT, 4, MINB>(n, a, S, stream);
 }
@@ -419,11 +482,10 @@ extern "C" int pa_test_skip_decode_box(int share, int box) {
 
 // CTAs per (request, kv head): as many as leave at most two per SM, up to 8,
 // and at least 64 tokens to each.  More CTAs cost more than they bring, since
-// each pays for its start, its merge and its cluster (an empty call takes 2.6
-// us without a cluster, 4.7 with one of 8, 5.6 with one of 16): 64 requests x 8
-// heads (window 1024) take 42.5 us on one CTA each, 49.4 on two, 54.5 on four;
-// 8 x 8 (window 4096) 62.1 on one, 36.3 on two, 26.7 on four, 27.1 on eight; 1
-// x 8 61.7 on one, 21.2 on four, 13.5 on eight.
+// each pays for its start, its merge and its cluster: 64 requests x 8 heads
+// (window 1024) take 41 us on one CTA each, 49 on two, 54 on four; 8 x 8 (window
+// 4096) 62 on one, 36 on two, 25 on four, 27 on eight; 1 x 8 on eight 8.1, on
+// sixteen (more than a portable cluster) the same.
 int decode_window_shares(int N, int Hkv, long long visible, int sm_count) {
   const long long units = static_cast<long long>(N) * Hkv;
   const long long s =
@@ -431,13 +493,18 @@ int decode_window_shares(int N, int Hkv, long long visible, int sm_count) {
   return s < 1 ? 1 : static_cast<int>(s);
 }
 
-// Warps per CTA: 8 where no SM gets a second CTA, or where a share is long
-// (and registers leave room for two such CTAs); else 4, so that twice as many
-// CTAs are resident.  8 against 4: one request x 8 heads 10.7 us (13.5), 64 x 8
-// at 4100 tokens each 137.5 (140), 128 x 8 over an e4m3 pool 152 (164); but 64
-// x 8 at 1028 tokens 43.2 (42.5), over an e4m3 pool 31.8 (26.8).
+// Warps per CTA.  Where no SM gets a second CTA, 16 (8 for short shares, whose
+// warps would have nothing to do, and for groups of 9 to 16 heads, which need the
+// registers): one request x 8 heads, 512 tokens per share, 8.2 us (8.6 with 8
+// warps, 13.5 with 4), 4 query heads per group 7.5 (8.3); 256 tokens 6.4 with
+// either; 64 tokens 6.1 (5.0).  Else 8 where a share is long (and registers leave
+// room for two such CTAs), 4 otherwise, so that twice as many CTAs are
+// resident: 64 x 8 at 4100 tokens each 137.5 us with 8 (140 with 4), 128 x 8 over
+// an e4m3 pool 152 (164); but 64 x 8 at 1028 tokens 43.2 (42.5), over an e4m3 pool
+// 31.8 (26.8).
 int decode_window_warps(long long ctas, long long share, bool wide, int sm_count) {
-  return ctas <= sm_count || (share >= 4096 && !wide) ? 8 : 4;
+  if (ctas <= sm_count) return share >= 512 && !wide ? 16 : 8;
+  return share >= 4096 && !wide ? 8 : 4;
 }
 
 cudaError_t launch_decode_window(const DecodeWindowLaunch& n, cudaStream_t stream) {
@@ -447,7 +514,7 @@ cudaError_t launch_decode_window(const DecodeWindowLaunch& n, cudaStream_t strea
   a.seq_lens = n.seq_lens;
   a.max_blocks = n.max_blocks;
   a.Hq = n.Hq;
-  a.Hkv = n.Hkv;
+  a.grp = n.Hq / n.Hkv;
   a.bs = n.bs;
   a.bs_log2 = block_size_log2(n.bs);
   a.num_blocks = n.num_blocks;
@@ -462,7 +529,8 @@ cudaError_t launch_decode_window(const DecodeWindowLaunch& n, cudaStream_t strea
   const long long visible = std::min(static_cast<long long>(n.window) + n.sinks, positions);
   a.positions = static_cast<int>(std::min(positions, INT_MAX - 64LL));
   const int S = decode_window_shares(n.N, n.Hkv, visible, n.sm_count);
-  const bool wide = n.Hq / n.Hkv > 8;   // groups of 9..16 heads take two n-tiles
+  a.out_share = output_share(a.grp * n.d, S);
+  const bool wide = a.grp > 8;   // groups of 9..16 heads take two n-tiles
   using dec::KvBf16;
   using dec::KvE4m3;
   const int warps = decode_window_warps(static_cast<long long>(S) * n.Hkv * n.N, visible / S,
