@@ -12,11 +12,11 @@
 // itself: no token waits for a table write.
 //
 // Bound by latency: 131072 tokens are 1.7 MB of traffic.  So one launch, and
-// no CTA waits for another: every CTA owns 1024 tokens and repeats the prefix
-// sums over the requests up to its tokens, 1024 or 4096 requests per step, from
-// L2 (8 bytes per request; 65535 requests are 16 steps).  64 requests and
-// tokens take 3.2 us (an empty kernel 2.2), 4096 requests with 131072 tokens
-// 5.8 us.
+// no CTA waits for another: every CTA owns as many tokens as it has threads and
+// repeats the prefix sums over the requests up to its tokens, from L2 (8 bytes per
+// request; 65535 requests are 16 steps of 4096).  64 requests and tokens take 2.3
+// us (an empty kernel 2.2), 16 requests with 18432 tokens 2.3, 4096 requests with
+// 131072 tokens 5.7.
 // Sums saturate at INT_MAX (min(a + b, INT_MAX) is associative for
 // non-negative values), so bad lengths can neither wrap nor index anything.
 #include <climits>
@@ -27,8 +27,6 @@
 namespace pa {
 
 namespace {
-
-constexpr int kPlanThreads = 1024;   // tokens of a CTA
 
 __device__ __forceinline__ uint32_t sat_add(uint32_t a, uint32_t b) {
   return min(a + b, static_cast<uint32_t>(INT_MAX));   // a, b <= INT_MAX: no wrap
@@ -54,13 +52,14 @@ __device__ __forceinline__ int blocks_of(int x, const PlanArgs& a) {
   return div_bs(x, a.bs, a.bs_log2) + (mod_bs(x, a.bs, a.bs_log2) != 0);
 }
 
-// kPer: requests of a thread in a step of the prefix sums.
-template <int kPer>
+// kPlanThreads: tokens of a CTA; kPer: requests of a thread in a step of the
+// prefix sums.
+template <int kPlanThreads, int kPer>
 __global__ void __launch_bounds__(kPlanThreads) plan_step_kernel(const PlanArgs a) {
-  constexpr int kStep = kPlanThreads * kPer;
+  constexpr int kStep = kPlanThreads * kPer, kWarps = kPlanThreads / 32;
   __shared__ uint32_t s_tok[kStep];   // first token of each request of the step
   __shared__ uint32_t s_blk[kStep];   // its first new block, counted from 0
-  __shared__ uint32_t s_wt[32], s_wb[32];
+  __shared__ uint32_t s_wt[kWarps], s_wb[kWarps];
   // Inputs may be the previous kernel's outputs: plain loads, no read-only path.
   pdl_wait();
   pdl_trigger();
@@ -121,9 +120,9 @@ __global__ void __launch_bounds__(kPlanThreads) plan_step_kernel(const PlanArgs 
     __syncthreads();
     uint32_t bt = 0, bb = 0, st, sb;   // sums of the warps before, and of all warps
     {
-      uint32_t wt = s_wt[lane], wb = s_wb[lane];
+      uint32_t wt = lane < kWarps ? s_wt[lane] : 0, wb = lane < kWarps ? s_wb[lane] : 0;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
+      for (int o = 1; o < kWarps; o <<= 1) {
         const uint32_t yt = __shfl_up_sync(0xffffffffu, wt, o);
         const uint32_t yb = __shfl_up_sync(0xffffffffu, wb, o);
         if (lane >= o) {
@@ -131,8 +130,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_step_kernel(const PlanArgs 
           wb = sat_add(wb, yb);
         }
       }
-      st = __shfl_sync(0xffffffffu, wt, 31);
-      sb = __shfl_sync(0xffffffffu, wb, 31);
+      st = __shfl_sync(0xffffffffu, wt, kWarps - 1);
+      sb = __shfl_sync(0xffffffffu, wb, kWarps - 1);
       const uint32_t pt = __shfl_sync(0xffffffffu, wt, max(warp - 1, 0));
       const uint32_t pb = __shfl_sync(0xffffffffu, wb, max(warp - 1, 0));
       if (warp > 0) {
@@ -245,13 +244,19 @@ cudaError_t launch_plan_step(const int32_t* context_lens, const int32_t* query_l
   const PlanArgs a{context_lens, query_lens, free_blocks, free_start, num_free, num_seqs,
                    max_blocks, bs, block_size_log2(bs), num_blocks, max_tokens, block_table,
                    query_start_loc, seq_lens, positions, slot_mapping, totals, err};
-  const unsigned grid = max_tokens > 0
-                            ? static_cast<unsigned>((max_tokens - 1) / kPlanThreads + 1) : 1u;
-  // One request per thread while a single step holds them all, else four (64
-  // requests 3.2 us against 3.9, 4096 requests 7.4 against 5.8).
-  return num_seqs <= kPlanThreads
-             ? launch_pdl(plan_step_kernel<1>, dim3(grid), dim3(kPlanThreads), 0, stream, a)
-             : launch_pdl(plan_step_kernel<4>, dim3(grid), dim3(kPlanThreads), 0, stream, a);
+  // The smallest CTA whose single step holds all requests, one to a thread (64
+  // requests 2.3 us with 256 threads, 3.0 with 1024; 512 requests 2.9 with 512,
+  // 3.3 with 1024); above, four requests to a thread (4096 requests 5.7 us; one to
+  // a thread in four steps 7.4, eight to one of 512 threads 10.4).
+  auto launch = [&](auto kernel, int threads) {
+    const unsigned grid =
+        max_tokens > 0 ? static_cast<unsigned>((max_tokens - 1) / threads + 1) : 1u;
+    return launch_pdl(kernel, dim3(grid), dim3(threads), 0, stream, a);
+  };
+  if (num_seqs <= 256) return launch(plan_step_kernel<256, 1>, 256);
+  if (num_seqs <= 512) return launch(plan_step_kernel<512, 1>, 512);
+  return num_seqs <= 1024 ? launch(plan_step_kernel<1024, 1>, 1024)
+                          : launch(plan_step_kernel<1024, 4>, 1024);
 }
 
 }  // namespace pa

@@ -72,6 +72,7 @@ def compare(got, want):
 
 @pytest.mark.parametrize("bs", [16, 48, 64])
 @pytest.mark.parametrize("n,q_hi,c_hi", [(1, 1, 0), (1, 1, 40), (3, 5, 39), (64, 1, 4095),
+                                         (256, 3, 50), (257, 9, 80), (512, 1, 99), (513, 4, 70),
                                          (16, 300, 4096), (7, 2500, 100), (1023, 3, 70),
                                          (1024, 2, 70), (1025, 4, 33), (2500, 9, 200)])
 def test_plan_equals_reference(pa, n, q_hi, c_hi, bs):
