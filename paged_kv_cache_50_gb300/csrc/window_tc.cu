@@ -43,13 +43,15 @@
 // Bound by the chain S -> softmax -> PV -> S of a Q tile (~3200 cycles of a
 // 128-token tile pair; its MMAs take 2290) and, at a unit's ends, by mask and
 // output code that is not in the instruction cache.  Measured (d 128, 16 requests
-// of U[256, 2048] new tokens, 32 / 8 heads, window 1024, 4 first tokens): 275 us,
-// 1073 TFLOP/s; 8192 tokens of 64 / 8 heads, window 4096: 751 us, 1469 TFLOP/s;
+// of U[256, 2048] new tokens, 32 / 8 heads, window 1024, 4 first tokens): 281 us,
+// 1050 TFLOP/s; 8192 tokens of 64 / 8 heads, window 4096: 778 us, 1418 TFLOP/s;
 // varlen_tc.cu's kernel with the same mask, one unit per CTA and 128-token steps,
 // took 419 and 1016.  Steps: persistent CTAs 365 / 953; the short loops 318 / 880;
-// descriptors 301 / 818; elect.sync 286 / 778; heads side by side 275 / 751.  Two
-// MMA threads (368 / 1008), the next unit's first S between the last PVs (328 /
-// 915) and one loop for all S (354 / 1012) were slower.
+// descriptors 301 / 818; elect.sync 286 / 778; heads side by side 277 / 768; words
+// without pieces skipped 281 / 778, but 5.2 instead of 6.2 us for three requests of
+// at most 5 tokens.  Two MMA threads (368 / 1008), the next unit's first S between
+// the last PVs (328 / 915), one loop for all S (354 / 1012) and the weights' next
+// word loaded ahead (282 / 790 against 277 / 762) were slower.
 //
 // Warp roles (384 threads): warp 0 MMA issue; warp 1 K/V producer (lane p:
 // piece p); warp 2 units and queries; warp 3 idle; warps 4-7 / 8-11 softmax and
@@ -139,6 +141,7 @@ struct WinArgs {
   const int32_t* seq_lens;
   int N, max_blocks, Hq, Hkv, grp, bs, bs_log2, num_blocks;
   int row_tokens;   // query rows of a Q tile: 128 / grp
+  int hkv_log2, per_log2;   // of Hkv and 2 * row_tokens where powers of two, else -1
   int total_q, max_query_len;
   int positions;    // of a table row, at most INT_MAX - 127
   float scale_log2;
@@ -336,7 +339,6 @@ window_tc_kernel(const __grid_constant__ CUtensorMap q_map,
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(BAR(kUnitEmpty + (u & 1)));
       if (!live) break;
-      const int lo = max(0, lim - a.window);   // first visible position of the window
       // l: the row's sum of weights (for the LSE); lr: the same weights rounded
       // to bf16, as PV multiplies them (the output's divisor).
       float m_used = -CUDART_INF_F, l = 0.f, lr = 0.f;
@@ -360,10 +362,16 @@ window_tc_kernel(const __grid_constant__ CUtensorMap q_map,
           }
           vm = w & 0xffu;
         }
+        // 32-column words of the tile up to its last loaded piece; the others are
+        // not looked at, their weights are zeros (one request of 5 tokens 5.2 us
+        // against 6.2, window 64 110 against 121; full tiles 1 % slower).  Formed
+        // anew from the mask where it is used: a register less over the maxima.
+        auto words = [&]() { return (33 - __clz(vm)) >> 1; };
         // Position of column 0 as if the tile held no first tokens; mask only
         // where some column is not visible.  (Decided for the whole warp, and
         // done in tensor memory, word by word, so that the code is short.)
         const int tok0 = tbase + j * C::kBN - 16 * n_first;
+        const int lo = lim - a.window;   // the window's first position, or below 0
         if (__any_sync(0xffffffffu, !(tok0 + C::kBN <= lim && tok0 >= lo && tok0 >= tbase &&
                                       vm == 0xffu))) {
           // Visible columns as bits: the window's range [wa, wb), past the
@@ -373,7 +381,7 @@ window_tc_kernel(const __grid_constant__ CUtensorMap q_map,
           const int fe = cf > 0 ? min(cf, min(a.sinks, lim) - j * C::kBN)
                                 : min(a.sinks, lim) - tok0;
 #pragma unroll 1
-          for (int w = 0; w < C::kBN / 32; ++w) {
+          for (int w = 0; w < words(); ++w) {
             const uint32_t loaded = ((vm >> (2 * w)) & 1u ? 0xffffu : 0u) |
                                     ((vm >> (2 * w + 1)) & 1u ? 0xffff0000u : 0u);
             const uint32_t bits = ((bits_below(wb - 32 * w) & ~bits_below(wa - 32 * w)) |
@@ -395,6 +403,9 @@ window_tc_kernel(const __grid_constant__ CUtensorMap q_map,
 #pragma unroll
           for (int c = 0; c < C::kBN / 32; ++c) tmem_ld32_max(ts + c * 32, r[c], m4[c]);
           tc::tmem_wait_ld();
+#pragma unroll
+          for (int c = 0; c < C::kBN / 32; ++c)
+            if (c >= words()) m4[c] = -CUDART_INF_F;
           mx = fmaxf(max3(m4[0], m4[1], m4[2]), m4[3]);
           mx *= a.scale_log2;
         }
@@ -444,7 +455,7 @@ window_tc_kernel(const __grid_constant__ CUtensorMap q_map,
           float l8[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
           float r8[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll 1
-          for (int c = 0; c < C::kBN / 32; ++c) {
+          for (int c = 0; c < words(); ++c) {
             uint32_t r[32], pk[16];
             tc::tmem_ld32(ts + c * 32, r);
             tc::tmem_wait_ld();
@@ -459,6 +470,18 @@ window_tc_kernel(const __grid_constant__ CUtensorMap q_map,
               pk[e] = pack_bf16(p0, p1);
               add_bf16x2_f32(r8[2 * (e & 3)], r8[2 * (e & 3) + 1], pk[e]);
             }
+            tc::tmem_st16(ts + c * 16, pk);
+            if (c >= 2) {
+              tc::tmem_wait_st();
+              tc::tc_fence_before();
+              tc::mbar_arrive(BAR((c == 2 ? kPLo : kPHi) + x));
+            }
+          }
+#pragma unroll 1
+          for (int c = words(); c < C::kBN / 32; ++c) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) pk[e] = 0u;
             tc::tmem_st16(ts + c * 16, pk);
             if (c >= 2) {
               tc::tmem_wait_st();
@@ -728,7 +751,7 @@ window_tc_kernel(const __grid_constant__ CUtensorMap q_map,
     // per request.  The request is found by a 32-way search.
     // The heads of a slot run side by side: they read neighbouring parts of the
     // same cache rows and queries.
-    int slot = blockIdx.x / a.Hkv, head = blockIdx.x - slot * a.Hkv;
+    int slot = div_bs(blockIdx.x, a.Hkv, a.hkv_log2), head = blockIdx.x - slot * a.Hkv;
     const int per = 2 * a.row_tokens;
     const uint32_t resp = bars + kOffClc;
     bool ok = true, asked = false;
@@ -765,7 +788,7 @@ window_tc_kernel(const __grid_constant__ CUtensorMap q_map,
         // In the last round a lane holds its request's row.
         const int next = in && last ? a.qsl[i + 1] : 0;
         const int len = in && last ? a.seq_lens[i] : 0;
-        const unsigned below = __ballot_sync(0xffffffffu, in && q / per + i <= slot);
+        const unsigned below = __ballot_sync(0xffffffffu, in && div_bs(q, per, a.per_log2) + i <= slot);
         const int k = max(31 - __clz(below), 0);
         lo += k * step;
         hi = min(lo + step, hi);
@@ -776,7 +799,7 @@ window_tc_kernel(const __grid_constant__ CUtensorMap q_map,
           break;
         }
       }
-      const int qlen = q1 - q0, tile = slot - (q0 / per + lo), qi = tile * per;   // first query row
+      const int qlen = q1 - q0, tile = slot - (div_bs(q0, per, a.per_log2) + lo), qi = tile * per;   // first query row
       // Rows past max_query_len, or outside the batch, are not touched.
       const int rows = q0 >= 0 ? min(min(qlen, a.max_query_len), a.total_q - q0) : 0;
       const bool real = tile >= 0 && qi < rows;
@@ -855,7 +878,7 @@ window_tc_kernel(const __grid_constant__ CUtensorMap q_map,
       asked = false;
       int cta;
       live = clc_answer(resp, cta);
-      slot = cta / a.Hkv;
+      slot = div_bs(cta, a.Hkv, a.hkv_log2);
       head = cta - slot * a.Hkv;
       if (live) {
         tc::fence_proxy_async_smem();   // the answer has been read
@@ -940,6 +963,8 @@ cudaError_t launch_t(const WindowPrefillLaunch& n, cudaStream_t stream) {
   a.bs_log2 = block_size_log2(n.bs);
   a.num_blocks = n.num_blocks;
   a.row_tokens = C::kBM / a.grp;
+  a.hkv_log2 = block_size_log2(n.Hkv);
+  a.per_log2 = block_size_log2(2 * a.row_tokens);
   a.total_q = n.total_q;
   a.max_query_len = n.max_query_len;
   a.positions = static_cast<int>(
