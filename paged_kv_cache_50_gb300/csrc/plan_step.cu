@@ -16,7 +16,7 @@
 // repeats the prefix sums over the requests up to its tokens, from L2 (8 bytes per
 // request; 65535 requests are 16 steps of 4096).  64 requests and tokens take 2.3
 // us (an empty kernel 2.2), 16 requests with 18432 tokens 2.3, 4096 requests with
-// 131072 tokens 5.7.
+// 131072 tokens 4.7.
 // Sums saturate at INT_MAX (min(a + b, INT_MAX) is associative for
 // non-negative values), so bad lengths can neither wrap nor index anything.
 #include <climits>
@@ -45,6 +45,7 @@ struct PlanArgs {
   int64_t* slot_mapping;
   int32_t* totals;
   int* err;
+  bool vectors;   // lengths 16-byte aligned
 };
 
 // ceil(x / bs) without overflow near INT_MAX.
@@ -73,9 +74,12 @@ __global__ void __launch_bounds__(kPlanThreads) plan_step_kernel(const PlanArgs 
   int bad = 0;
   const int steps = (a.num_seqs + kStep - 1) / kStep;
   for (int step = 0; step < steps; ++step) {
-    // Step k's per-request outputs are written by CTA k, the last CTA takes
-    // the rest.
-    const bool owner = blockIdx.x == min(static_cast<unsigned>(step), gridDim.x - 1);
+    // Step k's per-request outputs are written by CTA k, the last CTA takes the
+    // rest; those of a single step of 4096, which every CTA walks, by all CTAs, a
+    // warp's each (one CTA would take 0.9 us longer than the others).
+    const bool owner = blockIdx.x == (kPer > 1 && steps == 1
+                                          ? warp % gridDim.x
+                                          : min(static_cast<unsigned>(step), gridDim.x - 1));
     // Past this CTA's tokens and requests: nothing left to do.
     if (tok >= t0 + kPlanThreads && blockIdx.x != gridDim.x - 1 &&
         (blockIdx.x < static_cast<unsigned>(step) || blockIdx.x >= static_cast<unsigned>(steps)))
@@ -84,12 +88,25 @@ __global__ void __launch_bounds__(kPlanThreads) plan_step_kernel(const PlanArgs 
     // blocks, then the inclusive scans over the step's threads.
     const int i0 = step * kStep + tid * kPer;
     uint32_t q[kPer], fresh[kPer], xt = 0, xb = 0;
-    int seq[kPer];
+    int seq[kPer], cs[kPer], ns[kPer];
+    // (A thread's four lengths by one load: 0.2 us of 4096 requests.)
+    const bool whole = kPer == 4 && a.vectors && i0 + kPer <= a.num_seqs;
+    if (whole) {
+      const int4 c = *reinterpret_cast<const int4*>(a.context_lens + i0);
+      const int4 q4 = *reinterpret_cast<const int4*>(a.query_lens + i0);
+      const int cv[4] = {c.x, c.y, c.z, c.w}, qv[4] = {q4.x, q4.y, q4.z, q4.w};
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) cs[k] = cv[k % 4], ns[k] = qv[k % 4];
+    } else {
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) {
+        cs[k] = i0 + k < a.num_seqs ? a.context_lens[i0 + k] : 0;
+        ns[k] = i0 + k < a.num_seqs ? a.query_lens[i0 + k] : 0;
+      }
+    }
 #pragma unroll
     for (int k = 0; k < kPer; ++k) {
-      const bool in = i0 + k < a.num_seqs;
-      int ctx = in ? a.context_lens[i0 + k] : 0;
-      int n = in ? a.query_lens[i0 + k] : 0;
+      int ctx = cs[k], n = ns[k];
       if (ctx < 0 || n < 0) bad |= PA_DEVERR_LENGTH;
       ctx = max(ctx, 0);
       n = max(n, 0);
@@ -243,11 +260,13 @@ cudaError_t launch_plan_step(const int32_t* context_lens, const int32_t* query_l
                              cudaStream_t stream) {
   const PlanArgs a{context_lens, query_lens, free_blocks, free_start, num_free, num_seqs,
                    max_blocks, bs, block_size_log2(bs), num_blocks, max_tokens, block_table,
-                   query_start_loc, seq_lens, positions, slot_mapping, totals, err};
+                   query_start_loc, seq_lens, positions, slot_mapping, totals, err,
+                   (reinterpret_cast<uintptr_t>(context_lens) |
+                    reinterpret_cast<uintptr_t>(query_lens)) % 16 == 0};
   // The smallest CTA whose single step holds all requests, one to a thread (64
   // requests 2.3 us with 256 threads, 3.0 with 1024; 512 requests 2.9 with 512,
-  // 3.3 with 1024); above, four requests to a thread (4096 requests 5.7 us; one to
-  // a thread in four steps 7.4, eight to one of 512 threads 10.4).
+  // 3.3 with 1024); above, four requests to a thread (4096 requests 4.7 us; with
+  // one to a thread in four steps 1.7 us more, with eight to one of 512 threads 4.7).
   auto launch = [&](auto kernel, int threads) {
     const unsigned grid =
         max_tokens > 0 ? static_cast<unsigned>((max_tokens - 1) / threads + 1) : 1u;

@@ -174,6 +174,22 @@ def test_plan_allocates_its_outputs_and_steps_chain(pa):
     compare([t.cpu().numpy() for t in out2] + [tab.cpu().numpy(), pa.pa_get_device_error()], w2)
 
 
+def test_plan_lengths_at_any_address(pa):
+    """More than 1024 requests whose lengths start 4, 8 or 12 bytes past 16."""
+    ctx, q, table, free, start, nb = make(31, 1500, 5, 60, 16)
+    want = ref.plan(ctx, q, table, free, start, 16, nb, int(q.sum()))
+    for off in (1, 2, 3):
+        buf = torch.zeros((2, 1504), dtype=torch.int32, device="cuda")
+        c, n = buf[0, off:off + 1500], buf[1, off:off + 1500]
+        c.copy_(i32(ctx))
+        n.copy_(i32(q))
+        tab = i32(table)
+        got = pa.pa_plan_step(c, n, tab, i32(free), 16, nb, max_tokens=int(q.sum()),
+                              free_start=i32([start]))
+        compare([t.cpu().numpy() for t in got] + [tab.cpu().numpy(), pa.pa_get_device_error()],
+                want)
+
+
 def test_plan_beyond_capacity_keeps_attention_in_range(pa):
     """A step of more tokens than its buffers hold: attention over the plan's
     outputs neither leaves them nor touches another row."""
