@@ -16,12 +16,12 @@
 // so the rotation needs no exchange between lanes and the sum of squares is the
 // only reduction; weight times cosine and sine is formed once per token and
 // kept in registers over its rows; arithmetic is on packed pairs of fp32.
-// 18432 tokens of 32 / 8 heads, d 128 (457 MB): 71.2 us, 6.4 TB/s, 0.95 of the
+// 18432 tokens of 32 / 8 heads, d 128 (457 MB): 70.2 us, 6.5 TB/s, 0.96 of the
 // copy rate; 64 tokens 2.3 us (an empty kernel 2.2).  Before: a CTA per
 // token, 16-byte loads and the other half by shuffles 207 us, a warp per token
 // 131 us (instructions); one loop over all kinds of rows with loads a round
 // ahead 98 us (spilled registers).  An e4m3 pool adds a quotient
-// per value: 8191 tokens of 64 / 8 heads, d 64, neighbouring pairs (161 MB): 30.9
+// per value: 8191 tokens of 64 / 8 heads, d 64, neighbouring pairs (161 MB): 30.1
 // us, bound by instructions (issue slots 60 % busy) as much as by HBM.
 #include <type_traits>
 
@@ -104,8 +104,8 @@ __device__ __forceinline__ float signed_as(float y, float x) {
 // infinities out of the remainder; those below 2^-20 become a zero whatever
 // their last bits, whose sign (and that of -0) is put back.  Scales outside
 // [2^-100, 2^100], whose reciprocal could leave the normal range, take the
-// division.  In pairs: 18432 tokens of 32 / 8 heads, d 128, 73.8 us; one value
-// at a time, with the range tested instead, 75.6.
+// division.  In pairs: 18432 tokens of 32 / 8 heads, d 128, 72.3 us; one value
+// at a time, with the range tested instead, 2 us more.
 __device__ __forceinline__ float2 quotient(F2 x, float scale, float r, bool plain) {
   float2 f = split(x);
   if (!plain) return make_float2(__fdiv_rn(f.x, scale), __fdiv_rn(f.y, scale));
@@ -177,14 +177,16 @@ __global__ void __launch_bounds__(kWarps * 32, 8) norm_rope_kernel(const NormRop
   const int half = a.rot / 2;
   const bool turned = 8 * l < a.rot;
   const int c0 = !INTER && turned ? l : 2 * l, c1 = !INTER && turned ? l + half / 4 : 2 * l + 1;
-  auto fetch = [&](const __nv_bfloat16* row, bool stream) -> uint4 {
+  // Rows are read once, past L1 (18432 tokens, d 128, 70.2 us, 8191 tokens, d 64,
+  // e4m3 pool, 30.1; with loads that mark their lines as first to go 71.0 and 30.9).
+  auto fetch = [&](const __nv_bfloat16* row, bool once) -> uint4 {
     if (INTER) {
       const uint4* p = reinterpret_cast<const uint4*>(row) + l;
-      return stream ? __ldcs(p) : __ldg(p);
+      return once ? __ldcg(p) : __ldg(p);
     }
     const uint2* p = reinterpret_cast<const uint2*>(row);
-    const uint2 x = stream ? __ldcs(p + c0) : __ldg(p + c0);
-    const uint2 y = stream ? __ldcs(p + c1) : __ldg(p + c1);
+    const uint2 x = once ? __ldcg(p + c0) : __ldg(p + c0);
+    const uint2 y = once ? __ldcg(p + c1) : __ldg(p + c1);
     return make_uint4(x.x, x.y, y.x, y.y);
   };
 
