@@ -560,26 +560,29 @@ def pa_plan_step(context_lens, query_lens, block_table, free_blocks, block_size,
     given are written and returned.  Tokens past the new ones get position 0
     and slot -1.  ``max_tokens`` defaults to the length of ``slot_mapping`` or
     ``positions``; with neither it must be given."""
-    if max_tokens is None:
-        given = slot_mapping if slot_mapping is not None else positions
-        if given is None:
+    if max_tokens is None and slot_mapping is None:   # else slot_mapping's length
+        if positions is None:
             raise ValueError("max_tokens, slot_mapping or positions must be given")
-        max_tokens = given.shape[0]
+        max_tokens = positions.shape[0]
     if query_start_loc is None:
         query_start_loc = _new(stream, block_table, "block_table", block_table.shape[0] + 1,
                                torch.int32)
     if seq_lens is None:
         seq_lens = _new(stream, block_table, "block_table", slice(0, 1), torch.int32)
     if positions is None:
+        if max_tokens is None:
+            max_tokens = slot_mapping.shape[0]
         positions = _new(stream, block_table, "block_table", max_tokens, torch.int32)
     if slot_mapping is None:
         slot_mapping = _new(stream, block_table, "block_table", max_tokens, torch.int64)
     if totals is None:
         totals = _new(stream, block_table, "block_table", 2, torch.int32)
-    _check(_binding().plan_step(
+    rc = (_steps or _binding()).plan_step(
         context_lens, query_lens, free_blocks, free_start, block_table, block_size,
         num_blocks, max_tokens, query_start_loc, seq_lens, positions, slot_mapping, totals,
-        None if stream is None else _stream(stream)), "pa_plan_step")
+        None if stream is None else _stream(stream))
+    if rc:
+        _check(rc, "pa_plan_step")
     return query_start_loc, seq_lens, positions, slot_mapping, totals
 
 
@@ -607,10 +610,11 @@ def pa_qk_norm_rope_cache(q, key, value, kv_cache, slot_mapping, q_weight=None, 
     ``positions`` [T] int32, ``slot_mapping`` [T] int64 (< 0: no cache write)."""
     if q_out is None:
         q_out = _new(stream, q, "q", slice(None), torch.bfloat16)
-    _check(_binding().norm_rope(
+    rc = (_steps or _binding()).norm_rope(
         q, key, value, kv_cache, slot_mapping, None, q_weight, k_weight, eps, cos_sin,
-        positions, interleaved, q_out, None if stream is None else _stream(stream)),
-        "pa_qk_norm_rope_cache")
+        positions, interleaved, q_out, None if stream is None else _stream(stream))
+    if rc:
+        _check(rc, "pa_qk_norm_rope_cache")
     return q_out
 
 
@@ -621,10 +625,11 @@ def pa_qk_norm_rope_cache_fp8(q, key, value, kv_cache, slot_mapping, k_scale, v_
     value / v_scale (uint8 or float8_e4m3fn)."""
     if q_out is None:
         q_out = _new(stream, q, "q", slice(None), torch.bfloat16)
-    _check(_binding().norm_rope(
+    rc = (_steps or _binding()).norm_rope(
         q, key, value, kv_cache, slot_mapping, (k_scale, v_scale), q_weight, k_weight, eps,
-        cos_sin, positions, interleaved, q_out, None if stream is None else _stream(stream)),
-        "pa_qk_norm_rope_cache_fp8")
+        cos_sin, positions, interleaved, q_out, None if stream is None else _stream(stream))
+    if rc:
+        _check(rc, "pa_qk_norm_rope_cache_fp8")
     return q_out
 
 
@@ -638,10 +643,11 @@ def pa_varlen_fwd_sinks(q, kv_cache, block_table, query_start_loc, seq_lens, max
         out = _new(stream, q, "q", slice(None), torch.bfloat16)
     if lse is None and return_lse:
         lse = _new(stream, q, "q", slice(0, 2), torch.float32)
-    _check(_binding().varlen_sinks(
+    rc = (_steps or _binding()).varlen_sinks(
         q, kv_cache, block_table, seq_lens, out, lse, query_start_loc, max_query_len, scale,
-        sliding_window, num_sinks, None if stream is None else _stream(stream)),
-        "pa_varlen_fwd_sinks")
+        sliding_window, num_sinks, None if stream is None else _stream(stream))
+    if rc:
+        _check(rc, "pa_varlen_fwd_sinks")
     return out, lse
 
 
@@ -654,9 +660,11 @@ def pa_decode_window(q, kv_cache, block_table, seq_lens, scale, sliding_window, 
         out = _new(stream, q, "q", slice(None), torch.bfloat16)
     if lse is None and return_lse:
         lse = _new(stream, q, "q", slice(0, 2), torch.float32)
-    _check(_binding().decode_window(
+    rc = (_steps or _binding()).decode_window(
         q, kv_cache, block_table, seq_lens, out, lse, None, scale, sliding_window, num_sinks,
-        None if stream is None else _stream(stream)), "pa_decode_window")
+        None if stream is None else _stream(stream))
+    if rc:
+        _check(rc, "pa_decode_window")
     return out, lse
 
 
@@ -669,10 +677,11 @@ def pa_decode_window_fp8(q, kv_cache, block_table, seq_lens, scale, k_scale, v_s
         out = _new(stream, q, "q", slice(None), torch.bfloat16)
     if lse is None and return_lse:
         lse = _new(stream, q, "q", slice(0, 2), torch.float32)
-    _check(_binding().decode_window(
+    rc = (_steps or _binding()).decode_window(
         q, kv_cache, block_table, seq_lens, out, lse, (k_scale, v_scale), scale,
-        sliding_window, num_sinks, None if stream is None else _stream(stream)),
-        "pa_decode_window_fp8")
+        sliding_window, num_sinks, None if stream is None else _stream(stream))
+    if rc:
+        _check(rc, "pa_decode_window_fp8")
     return out, lse
 
 

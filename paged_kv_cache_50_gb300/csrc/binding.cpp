@@ -166,7 +166,7 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
 }
 
 // (context_lens, query_lens, free_blocks, free_start | None, block_table,
-//  block_size, num_blocks, max_tokens, query_start_loc, seq_lens, positions,
+//  block_size, num_blocks, max_tokens | None, query_start_loc, seq_lens, positions,
 //  slot_mapping, totals, stream | None)
 PyObject* plan_step(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded(n, 14, [&]() -> PyObject* {
@@ -175,7 +175,10 @@ PyObject* plan_step(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (table.dim() != 2) refuse(PyExc_ValueError, "block_table must be [num_seqs, max_blocks]");
     if (free.dim() != 1) refuse(PyExc_ValueError, "free_blocks must be [num_free]");
     const int64_t seqs = table.size(0);
-    const int cap = integer32(a[7], "max_tokens");
+    const at::Tensor& slots = tensor(a[11], "slot_mapping");
+    if (slots.dim() != 1) refuse(PyExc_ValueError, "slot_mapping must be [max_tokens]");
+    const int cap = a[7] == Py_None ? extent(slots.size(0), "slot_mapping")
+                                    : integer32(a[7], "max_tokens");
     const int dev = call_device(table, "block_table");
     void* ctx = shaped(a[0], "context_lens", at::kInt, dev, {seqs});
     void* qlen = shaped(a[1], "query_lens", at::kInt, dev, {seqs});
