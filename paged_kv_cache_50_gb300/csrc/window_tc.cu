@@ -43,15 +43,14 @@
 // Bound by the chain S -> softmax -> PV -> S of a Q tile (~3200 cycles of a
 // 128-token tile pair; its MMAs take 2290) and, at a unit's ends, by mask and
 // output code that is not in the instruction cache.  Measured (d 128, 16 requests
-// of U[256, 2048] new tokens, 32 / 8 heads, window 1024, 4 first tokens): 281 us,
-// 1050 TFLOP/s; 8192 tokens of 64 / 8 heads, window 4096: 778 us, 1418 TFLOP/s;
+// of U[256, 2048] new tokens, 32 / 8 heads, window 1024, 4 first tokens): 277 us,
+// 1066 TFLOP/s; 8192 tokens of 64 / 8 heads, window 4096: 768 us, 1436 TFLOP/s;
 // varlen_tc.cu's kernel with the same mask, one unit per CTA and 128-token steps,
 // took 419 and 1016.  Steps: persistent CTAs 365 / 953; the short loops 318 / 880;
-// descriptors 301 / 818; elect.sync 286 / 778; heads side by side 277 / 768; words
-// without pieces skipped 281 / 778, but 5.2 instead of 6.2 us for three requests of
-// at most 5 tokens.  Two MMA threads (368 / 1008), the next unit's first S between
-// the last PVs (328 / 915), one loop for all S (354 / 1012) and the weights' next
-// word loaded ahead (282 / 790 against 277 / 762) were slower.
+// descriptors 301 / 818; elect.sync 286 / 778; heads side by side 277 / 768.  Two
+// MMA threads (368 / 1008), the next unit's first S between the last PVs (328 /
+// 915), one loop for all S (354 / 1012) and the weights' next word loaded ahead
+// (282 / 790 against 277 / 762) were slower.
 //
 // Warp roles (384 threads): warp 0 MMA issue; warp 1 K/V producer (lane p:
 // piece p); warp 2 units and queries; warp 3 idle; warps 4-7 / 8-11 softmax and
@@ -251,7 +250,8 @@ __device__ __forceinline__ bool clc_answer(uint32_t resp, int& x) {
 __device__ int2 g_window_skip = {-1, -1};
 #endif
 
-template <int D>
+// SKIP: words of a tile without pieces are not looked at.
+template <int D, bool SKIP>
 __global__ void __launch_bounds__(384, 1)
 window_tc_kernel(const __grid_constant__ CUtensorMap q_map,
                  const __grid_constant__ CUtensorMap k_map,
@@ -339,6 +339,7 @@ window_tc_kernel(const __grid_constant__ CUtensorMap q_map,
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(BAR(kUnitEmpty + (u & 1)));
       if (!live) break;
+      const int unit_lo = max(0, lim - a.window);
       // l: the row's sum of weights (for the LSE); lr: the same weights rounded
       // to bf16, as PV multiplies them (the output's divisor).
       float m_used = -CUDART_INF_F, l = 0.f, lr = 0.f;
@@ -362,16 +363,16 @@ window_tc_kernel(const __grid_constant__ CUtensorMap q_map,
           }
           vm = w & 0xffu;
         }
-        // 32-column words of the tile up to its last loaded piece; the others are
-        // not looked at, their weights are zeros (one request of 5 tokens 5.2 us
-        // against 6.2, window 64 110 against 121; full tiles 1 % slower).  Formed
-        // anew from the mask where it is used: a register less over the maxima.
-        auto words = [&]() { return (33 - __clz(vm)) >> 1; };
+        // With SKIP, 32-column words of the tile up to its last loaded piece; the
+        // others' weights are zeros.  Formed anew from the mask where it is used: a
+        // register less over the maxima.
+        auto words = [&]() { return SKIP ? (33 - __clz(vm)) >> 1 : C::kBN / 32; };
         // Position of column 0 as if the tile held no first tokens; mask only
         // where some column is not visible.  (Decided for the whole warp, and
         // done in tensor memory, word by word, so that the code is short.)
         const int tok0 = tbase + j * C::kBN - 16 * n_first;
-        const int lo = lim - a.window;   // the window's first position, or below 0
+        // The window's first position (or one below 0; recomputed for a register).
+        const int lo = SKIP ? lim - a.window : unit_lo;
         if (__any_sync(0xffffffffu, !(tok0 + C::kBN <= lim && tok0 >= lo && tok0 >= tbase &&
                                       vm == 0xffu))) {
           // Visible columns as bits: the window's range [wa, wb), past the
@@ -947,7 +948,7 @@ bool make_k_map(CUtensorMap* map, const void* cache, int nb, int bs, int Hkv, in
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D>
+template <int D, bool SKIP>
 cudaError_t launch_t(const WindowPrefillLaunch& n, cudaStream_t stream) {
   using C = WinCfg<D>;
   WinArgs a{};
@@ -982,7 +983,7 @@ cudaError_t launch_t(const WindowPrefillLaunch& n, cudaStream_t stream) {
       !make_k_map(&k_map, n.cache, n.num_blocks, n.bs, n.Hkv, D) ||
       !make_v_map(&v_map, n.cache, n.num_blocks, n.bs, n.Hkv, D))
     return cudaErrorInvalidValue;
-  auto kern = window_tc_kernel<D>;
+  auto kern = window_tc_kernel<D, SKIP>;
   static DeviceFlags attr_set;
   cudaError_t e = set_smem_once(kern, C::kSmemBytes, attr_set);
   if (e != cudaSuccess) return e;
@@ -1004,7 +1005,15 @@ extern "C" int pa_test_skip_window_tile(int cta, int tile) {
 #endif
 
 cudaError_t launch_window_prefill(const WindowPrefillLaunch& n, cudaStream_t stream) {
-  return n.d == 128 ? launch_t<128>(n, stream) : launch_t<64>(n, stream);
+  if (n.d == 64) return launch_t<64, true>(n, stream);
+  // Where a unit sees a few tiles only, those that end early are many, and their
+  // empty words are worth skipping, which costs a full tile 1.5 % (us with and
+  // without, d 128: three requests of at most 5 tokens 5.2, 6.2; windows of 64 110,
+  // 121, 192 138, 146, 384 164.6, 164.6, 512 189.0, 188.2, 1024 281, 277; d 64: 128 165,
+  // 186, 1024 469, 473).
+  const long long seen = std::min(static_cast<long long>(n.window) + n.sinks,
+                                  static_cast<long long>(n.max_blocks) * n.bs);
+  return seen <= 384 ? launch_t<128, true>(n, stream) : launch_t<128, false>(n, stream);
 }
 
 }  // namespace pa
