@@ -393,14 +393,13 @@ __global__ void __launch_bounds__(32 * W, MINB) decode_window_kernel(
       M = fmaxf(M, v[k].x);
     }
     float L = 0.f, LR = 0.f, acc = 0.f;
-    if (M != -CUDART_INF_F) {
 #pragma unroll
-      for (int k = 0; k < kMaxShares; ++k) {
-        const float f = fast_exp2(v[k].x - M);
-        L += f * v[k].y;
-        LR += f * v[k].z;
-        acc += f * o[k];
-      }
+    for (int k = 0; k < kMaxShares; ++k) {
+      // (Nothing visible: all sums are 0, or NaN where the query is.)
+      const float f = v[k].x == M ? 1.f : fast_exp2(v[k].x - M);
+      L += f * v[k].y;
+      LR += f * v[k].z;
+      acc += f * o[k];
     }
     a.out[(row0 + r) * D + e] = __float2bfloat16_rn(LR == 0.f ? 0.f : acc / LR * a.out_scale);
     if (e == 0 && a.lse != nullptr)

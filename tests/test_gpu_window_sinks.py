@@ -196,6 +196,18 @@ def test_nan_query_stays_in_its_row(pa):
     assert torch.equal(got, want) and torch.equal(gl, wl)
 
 
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "fp8"])
+@pytest.mark.parametrize("window", [64, 4096])
+def test_nan_query_stays_in_its_row_of_decode(pa, window, fp8):
+    b = Batch(69, [4200, 70], [1, 1], 8, 2, 128, 16, window, 4, fp8, poison=False)
+    want, wl = b.decode(pa)
+    b.q[0, 5, 7] = float("nan")
+    got, gl = b.decode(pa)
+    assert torch.isnan(got[0, 5]).all() and torch.isnan(gl[0, 5])
+    got[0, 5], gl[0, 5] = want[0, 5], wl[0, 5]
+    assert torch.equal(got, want) and torch.equal(gl, wl)
+
+
 @pytest.mark.parametrize("length", [16 * 21, BIG])
 def test_lengths_past_the_table(pa, length):
     """Positions past the table's columns are not seen, and not walked over."""
