@@ -559,7 +559,8 @@ def pa_plan_step(context_lens, query_lens, block_table, free_blocks, block_size,
     int64, totals [2] int32 = new tokens, next free_start); buffers that are
     given are written and returned.  Tokens past the new ones get position 0
     and slot -1.  ``max_tokens`` defaults to the length of ``slot_mapping`` or
-    ``positions``; with neither it must be given."""
+    ``positions``; with neither it must be given.  No output may share memory
+    with an input or another output."""
     if max_tokens is None and slot_mapping is None:   # else slot_mapping's length
         if positions is None:
             raise ValueError("max_tokens, slot_mapping or positions must be given")

@@ -221,7 +221,10 @@ __global__ void __launch_bounds__(32 * W, MINB) decode_window_kernel(
     const int fetched = after < my_n ? lookup(after) : -1;
     const int tb = token(n);
     const bool ok = blk >= 0 && blk < a.num_blocks;
-    const bool v0 = ok && visible(tb + gid), v1 = ok && visible(tb + gid + 8);
+    // Most sub-blocks are visible as a whole.
+    const bool whole = ok && tb >= lo && tb + 16 <= end;
+    bool v0 = true, v1 = true;
+    if (!whole) v0 = ok && visible(tb + gid), v1 = ok && visible(tb + gid + 8);
     // The next box goes to the place of the one before this.
     const int before = at == 0 ? R - 1 : at - 1;
     if (C::kPair)
@@ -239,7 +242,7 @@ __global__ void __launch_bounds__(32 * W, MINB) decode_window_kernel(
       arrived();
       vb = wbase + at * C::kPlaceBytes;
     }
-    if (!__all_sync(0xffffffffu, v0 && v1)) {
+    if (__any_sync(0xffffffffu, !whole)) {
       // Weights of unseen tokens are 0, but 0 * NaN is not: clear their rows.
       for (int c = lane; c < 16 * KV::kChunks; c += 32) {
         const int r = c / KV::kChunks;
