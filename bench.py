@@ -637,6 +637,7 @@ def bench_prefill(pa, device, pk, flush, reps=SECONDARY_REPS, check=True):
                                 b.causal_flops(),
                                 profiled_traffic("varlen_tc_chunked_prefill.md",
                                                  kernel_source_sha(["varlen_tc.cu",
+                                                                    "tc_tiles.cuh",
                                                                     "tc_common.cuh"])))}
     if check:
         import oracle

@@ -92,6 +92,12 @@ __host__ __device__ __forceinline__ int output_share(int total, int S) {
   return (total / 4 + S - 1) / S * 4;
 }
 
+// Arrival at a cluster barrier that publishes nothing but what a fence before it
+// does (fence_barrier_init).
+__device__ __forceinline__ void cluster_arrive_relaxed() {
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+}
+
 #ifdef PA_TEST_HOOKS
 // Test builds only: warp 0 of share g_decode_skip.x of the first request's
 // first kv head does not issue box g_decode_skip.y; {-1, -1} = off.
@@ -122,7 +128,7 @@ __global__ void __launch_bounds__(32 * W, MINB) decode_window_kernel(
     tc::fence_barrier_init();
   }
   __syncwarp();   // each warp uses its own ring's barriers only
-  if (S > 1) tc::cluster_arrive_relaxed();   // the receive barrier is set up
+  if (S > 1) cluster_arrive_relaxed();   // the receive barrier is set up
   pdl_wait();
   const int seq = max(0, a.seq_lens[i]);
   const int32_t* table = a.block_table + static_cast<int64_t>(i) * a.max_blocks;
