@@ -377,8 +377,9 @@ window_tc_kernel(const __grid_constant__ CUtensorMap q_map,
                                       vm == 0xffu))) {
           // Visible columns as bits: the window's range [wa, wb), past the
           // columns of the first tokens' pieces, and the first tokens [0, fe).
+          // (Where wb < 0 the window shows nothing, and wb - window could leave 32 bits.)
           const int cf = max(0, min(16 * n_first - j * C::kBN, C::kBN));
-          const int wa = max(lo - tok0, cf), wb = lim - tok0;
+          const int wb = lim - tok0, wa = max(max(wb, 0) - a.window, cf);
           const int fe = cf > 0 ? min(cf, min(a.sinks, lim) - j * C::kBN)
                                 : min(a.sinks, lim) - tok0;
 #pragma unroll 1
@@ -818,7 +819,9 @@ window_tc_kernel(const __grid_constant__ CUtensorMap q_map,
           if (lane == 0) record_error(a.err, PA_DEVERR_BLOCK_ID);
           end = a.positions;
         }
-        const int oldest = max(0, ctx + qi + 1 - a.window);
+        // (A first row before position 0 is held to 0 before the window is taken
+        // off: the difference fits an int whatever the window.)
+        const int oldest = max(0, max(0, ctx + qi + 1) - a.window);
         int first = (min(a.sinks, end) + 15) >> 4, base = oldest & ~15;
         if (base <= 16 * first) first = base = 0;
         const int pieces = first + ((max(0, end - base) + 15) >> 4);
