@@ -100,8 +100,23 @@ __device__ __forceinline__ void cluster_arrive_relaxed() {
 
 #ifdef PA_TEST_HOOKS
 // Test builds only: warp 0 of share g_decode_skip.x of the first request's
-// first kv head does not issue box g_decode_skip.y; {-1, -1} = off.
+// first kv head does not issue box g_decode_skip.y; {-1, -1} = off.  With
+// g_decode_late it issues it after all once the wait for it has run out.
+// g_decode_left: boxes that a warp issued after a wait of its own had run out,
+// and boxes that were still on their way when it had drained its ring.
 __device__ int2 g_decode_skip = {-1, -1};
+__device__ int g_decode_late = 0;
+__device__ int2 g_decode_left = {0, 0};
+__device__ __forceinline__ bool box_landed(uint32_t bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n.reg .pred p;\nmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+      "selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(done)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return done != 0;
+}
 #endif
 
 template <class KV, int D, int R, int NT, int W, int MINB>
@@ -165,12 +180,19 @@ __global__ void __launch_bounds__(32 * W, MINB) decode_window_kernel(
   // Box h into ring place `place`: sub-block h, or the K or V of sub-block
   // h / 2, in block blk.  A box that is not loaded (no such block) completes
   // its barrier all the same.
+  int failed = -1;   // the box whose wait has run out
+#ifdef PA_TEST_HOOKS
+  auto hooked = [&](int h) {
+    return warp == 0 && h == g_decode_skip.y && kvh == 0 && i == 0 && s == g_decode_skip.x;
+  };
+#endif
   auto issue = [&](int h, int blk, int place) {
     const int n = C::kPair ? h : h >> 1;
     if (lane != 0 || n >= my_n) return;
     const uint32_t bar = bars + 8 * place;
 #ifdef PA_TEST_HOOKS
-    if (warp == 0 && h == g_decode_skip.y && kvh == 0 && i == 0 && s == g_decode_skip.x) return;
+    if (failed < 0 && hooked(h)) return;
+    if (failed >= 0 && !hooked(h)) atomicAdd(&g_decode_left.x, 1);
 #endif
     if (blk >= 0 && blk < a.num_blocks) {
       const int off = mod_bs(token(n), a.bs, a.bs_log2);
@@ -185,10 +207,9 @@ __global__ void __launch_bounds__(32 * W, MINB) decode_window_kernel(
       tc::mbar_arrive(bar);
     }
   };
-  bool alive = true;   // no wait has run out
   int at = 0, parity = 0;   // place and barrier parity of the tile worked on
   auto arrived = [&]() {
-    if (!__all_sync(0xffffffffu, tc::mbar_wait(bars + 8 * at, parity))) alive = false;
+    return __all_sync(0xffffffffu, tc::mbar_wait(bars + 8 * at, parity));
   };
   auto next_tile = [&]() {
     if (++at == R) at = 0, parity ^= 1;
@@ -221,7 +242,7 @@ __global__ void __launch_bounds__(32 * W, MINB) decode_window_kernel(
 
   dec::State<D, NT> st;
   st.clear();
-  for (int n = 0; n < my_n && alive; ++n) {
+  for (int n = 0; n < my_n; ++n) {
     const int blk = ids[0];
     const int after = n + kAhead + 1;   // the next block id, a sub-block ahead of its copies
     const int fetched = after < my_n ? lookup(after) : -1;
@@ -237,7 +258,10 @@ __global__ void __launch_bounds__(32 * W, MINB) decode_window_kernel(
       issue(n + R - 1, ids[R - 1], before);
     else
       issue(2 * n + R - 1, ids[(R - 1) >> 1], before);
-    arrived();
+    if (!arrived()) {
+      failed = C::kPair ? n : 2 * n;
+      break;
+    }
     uint32_t pb[NT][2];
     dec::weights<KV, D, NT>(st, wbase + at * C::kPlaceBytes, lane, v0, v1, a.scale_log2, qf, pb);
     uint32_t vb = wbase + at * C::kPlaceBytes + KV::kTileBytes;
@@ -245,7 +269,10 @@ __global__ void __launch_bounds__(32 * W, MINB) decode_window_kernel(
       __syncwarp();   // every lane is done with K(n): its place is free
       issue(2 * n + R, ids[R >> 1], at);
       next_tile();
-      arrived();
+      if (!arrived()) {
+        failed = 2 * n + 1;
+        break;
+      }
       vb = wbase + at * C::kPlaceBytes;
     }
     if (__any_sync(0xffffffffu, !whole)) {
@@ -266,14 +293,29 @@ __global__ void __launch_bounds__(32 * W, MINB) decode_window_kernel(
     for (int k = 0; k < kAhead; ++k) ids[k] = ids[k + 1];
     ids[kAhead] = fetched;
   }
-  if (!alive && lane == 0) {
-    // Given up: the outputs are invalid.  No copy may still be landing when
-    // the CTA goes on, so each place's barrier gets one more bounded wait.
+  if (failed >= 0 && lane == 0) {
+    // Given up: the outputs are invalid.  No copy may still be landing when the
+    // ring becomes the merge buffer and the CTA goes on.  The ring holds the
+    // boxes failed .. failed + R - 1 (as far as there are), in this order from
+    // the place that the warp stands at: each gets one more bounded wait.
     record_error(a.err, PA_DEVERR_TIMEOUT);
-    for (int k = 0; k < R; ++k) {
+#ifdef PA_TEST_HOOKS
+    if (hooked(failed) && g_decode_late) issue(failed, ids[0], at);
+    const int at0 = at, parity0 = parity;
+#endif
+    const int past = min(failed + R, C::kPair ? my_n : 2 * my_n);
+    for (int h = failed; h < past; ++h) {
       tc::mbar_wait(bars + 8 * at, parity);
       next_tile();
     }
+#ifdef PA_TEST_HOOKS
+    at = at0, parity = parity0;
+    for (int h = failed; h < past; ++h) {
+      if (!(hooked(h) && !g_decode_late) && !box_landed(bars + 8 * at, parity))
+        atomicAdd(&g_decode_left.y, 1);
+      next_tile();
+    }
+#endif
   }
   pdl_trigger();
 
@@ -385,7 +427,8 @@ __global__ void __launch_bounds__(32 * W, MINB) decode_window_kernel(
     tc::st_async_v4(tc::map_to_rank(stats_at + (s * C::kHeads + r) * 16, to), __float_as_uint(v.x),
                     __float_as_uint(v.y), __float_as_uint(v.z), 0u, tc::map_to_rank(received, to));
   }
-  // A CTA whose own waits run out sends after at most R + 1 limits.
+  // A CTA that gives up sends at most R + 1 limits after it began the wait that
+  // ran out: that wait, and one for each place of the ring.
   bool got = false;
   for (int k = 0; k < 4 * R && !got; ++k) got = tc::mbar_wait_cluster(received, 0);
   if (!got) record_error(a.err, PA_DEVERR_TIMEOUT);
@@ -484,7 +527,22 @@ cudaError_t launch_warps(const DecodeWindowLaunch& n, const WindowArgs& a, int S
 // Test builds only (not declared in pa.h).
 extern "C" int pa_test_skip_decode_box(int share, int box) {
   const int2 v = make_int2(share, box);
-  return cudaMemcpyToSymbol(g_decode_skip, &v, sizeof(v)) == cudaSuccess ? 0 : 3;
+  const int late = 0;
+  return cudaMemcpyToSymbol(g_decode_skip, &v, sizeof(v)) == cudaSuccess &&
+                 cudaMemcpyToSymbol(g_decode_late, &late, sizeof(late)) == cudaSuccess
+             ? 0 : 3;
+}
+extern "C" int pa_test_late_decode_box(int share, int box) {
+  const int late = 1;
+  const int e = pa_test_skip_decode_box(share, box);
+  return e != 0 || cudaMemcpyToSymbol(g_decode_late, &late, sizeof(late)) != cudaSuccess ? 3 : 0;
+}
+// What g_decode_left has counted since the last call: {issued after, on their way}.
+extern "C" int pa_test_decode_left(int* two) {
+  const int2 none = make_int2(0, 0);
+  return cudaMemcpyFromSymbol(two, g_decode_left, sizeof(none)) == cudaSuccess &&
+                 cudaMemcpyToSymbol(g_decode_left, &none, sizeof(none)) == cudaSuccess
+             ? 0 : 3;
 }
 #endif
 
