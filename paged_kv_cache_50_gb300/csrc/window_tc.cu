@@ -248,6 +248,13 @@ __device__ __forceinline__ bool clc_answer(uint32_t resp, int& x) {
 // neither the copies nor the byte count of the K of tile g_window_skip.y, so
 // the waits on it can only end at their poll limit; {-1, -1} = off.
 __device__ int2 g_window_skip = {-1, -1};
+// The softmax of Q tile 1 in the CTA with index g_window_mute.x does not publish
+// its weights of tile g_window_mute.y (of the CTA's first unit, the last but one),
+// and the next unit's queries for Q tile 0 are fetched only when the wait for Q
+// tile 1's place has run out.  g_window_left: query copies that were still on
+// their way when the CTA took them for landed.
+__device__ int2 g_window_mute = {-1, -1};
+__device__ int g_window_left = 0;
 #endif
 
 // SKIP: words of a tile without pieces are not looked at.
@@ -454,6 +461,16 @@ window_tc_kernel(const __grid_constant__ CUtensorMap q_map,
         // after 96 and after 128 tokens: what is left of PV_x for the chain is
         // two steps.
         {
+          auto publish = [&](int c) {
+            tc::tmem_wait_st();
+            tc::tc_fence_before();
+#ifdef PA_TEST_HOOKS
+            if (x == 1 && blockIdx.x == static_cast<unsigned>(g_window_mute.x) &&
+                g == static_cast<uint32_t>(g_window_mute.y))
+              return;
+#endif
+            tc::mbar_arrive(BAR((c == 2 ? kPLo : kPHi) + x));
+          };
           float l8[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
           float r8[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll 1
@@ -473,11 +490,7 @@ window_tc_kernel(const __grid_constant__ CUtensorMap q_map,
               add_bf16x2_f32(r8[2 * (e & 3)], r8[2 * (e & 3) + 1], pk[e]);
             }
             tc::tmem_st16(ts + c * 16, pk);
-            if (c >= 2) {
-              tc::tmem_wait_st();
-              tc::tc_fence_before();
-              tc::mbar_arrive(BAR((c == 2 ? kPLo : kPHi) + x));
-            }
+            if (c >= 2) publish(c);
           }
 #pragma unroll 1
           for (int c = words(); c < C::kBN / 32; ++c) {
@@ -485,11 +498,7 @@ window_tc_kernel(const __grid_constant__ CUtensorMap q_map,
 #pragma unroll
             for (int e = 0; e < 16; ++e) pk[e] = 0u;
             tc::tmem_st16(ts + c * 16, pk);
-            if (c >= 2) {
-              tc::tmem_wait_st();
-              tc::tc_fence_before();
-              tc::mbar_arrive(BAR((c == 2 ? kPLo : kPHi) + x));
-            }
+            if (c >= 2) publish(c);
           }
           l = l * alpha +
               (((l8[0] + l8[1]) + (l8[2] + l8[3])) + ((l8[4] + l8[5]) + (l8[6] + l8[7])));
@@ -757,7 +766,7 @@ window_tc_kernel(const __grid_constant__ CUtensorMap q_map,
     const int per = 2 * a.row_tokens;
     const uint32_t resp = bars + kOffClc;
     bool ok = true, asked = false;
-    uint32_t answers = 0, full = 0;
+    uint32_t answers = 0, full = 0, fetched = 0;   // fetched: Q tiles, 0 and 1 in turn
     int empty = 0;   // empty slots in a row
     // Unlike the others, these waits last as long as a unit.
     auto wait = [&](int bar, uint32_t parity) {
@@ -852,14 +861,9 @@ window_tc_kernel(const __grid_constant__ CUtensorMap q_map,
         __syncwarp();
         ++u;
         if (tiles > 0) {
-          for (int x = 0; x < 2 && ok; ++x) {
-            if (full > 0 &&
-                !__all_sync(0xffffffffu, wait(kQEmpty + x, (full - 1) & 1))) {
-              ok = false;
-              break;
-            }
-            // Rows past the request or the batch are fetched too (or zeros):
-            // they are masked.
+          // Rows past the request or the batch are fetched too (or zeros): they are
+          // masked.
+          auto fetch = [&](int x) {
             if (lane == 0) {
               tc::mbar_arrive_expect_tx(
                   BAR(kQFull + x), static_cast<uint32_t>(a.row_tokens * a.grp) * (D * 2));
@@ -868,6 +872,21 @@ window_tc_kernel(const __grid_constant__ CUtensorMap q_map,
                                 BAR(kQFull + x), h * 64, head * a.grp,
                                 min(q0 + qi + x * a.row_tokens, a.total_q));
             }
+          };
+#ifdef PA_TEST_HOOKS
+          const bool late = full == 1 && blockIdx.x == static_cast<unsigned>(g_window_mute.x);
+#else
+          constexpr bool late = false;
+#endif
+          for (int x = 0; x < 2 && ok; ++x) {
+            if (full > 0 &&
+                !__all_sync(0xffffffffu, wait(kQEmpty + x, (full - 1) & 1))) {
+              if (late && x == 1) fetch(0);
+              ok = false;
+              break;
+            }
+            if (!late) fetch(x);
+            ++fetched;
           }
           if (!ok) break;
           ++full;
@@ -902,8 +921,15 @@ window_tc_kernel(const __grid_constant__ CUtensorMap q_map,
       }
       // Nothing may land in shared memory any more.
       if (asked) tc::mbar_wait(BAR(kClc), answers & 1);
-      if (full > 0)
-        for (int x = 0; x < 2; ++x) tc::mbar_wait(BAR(kQFull + x), (full - 1) & 1);
+      // (A unit may have been given up between its two Q tiles.)
+      for (int x = 0; x < 2; ++x) {
+        const uint32_t n = (fetched + 1 - x) >> 1;
+        if (n > 0) tc::mbar_wait(BAR(kQFull + x), (n - 1) & 1);
+      }
+#ifdef PA_TEST_HOOKS
+      for (uint32_t n = fetched >= 2 ? fetched - 2 : 0; n < fetched; ++n)
+        if (!mbar_test(BAR(kQFull + (n & 1)), (n >> 1) & 1)) atomicAdd(&g_window_left, 1);
+#endif
     }
   }
 
@@ -1004,6 +1030,17 @@ cudaError_t launch_t(const WindowPrefillLaunch& n, cudaStream_t stream) {
 extern "C" int pa_test_skip_window_tile(int cta, int tile) {
   const int2 v = make_int2(cta, tile);
   return cudaMemcpyToSymbol(g_window_skip, &v, sizeof(v)) == cudaSuccess ? 0 : 3;
+}
+extern "C" int pa_test_mute_window_tile(int cta, int tile) {
+  const int2 v = make_int2(cta, tile);
+  return cudaMemcpyToSymbol(g_window_mute, &v, sizeof(v)) == cudaSuccess ? 0 : 3;
+}
+// What g_window_left has counted since the last call.
+extern "C" int pa_test_window_left(int* copies) {
+  const int none = 0;
+  return cudaMemcpyFromSymbol(copies, g_window_left, sizeof(none)) == cudaSuccess &&
+                 cudaMemcpyToSymbol(g_window_left, &none, sizeof(none)) == cudaSuccess
+             ? 0 : 3;
 }
 #endif
 

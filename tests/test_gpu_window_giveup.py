@@ -34,3 +34,12 @@ def test_decode_leaves_nothing_on_its_way(test_lib):  # noqa: F811
         # Request 0, kv head 0: four query heads.
         assert rec["rows"] and all(r == 0 and h < 4 for r, h in rec["rows"]), rec
         assert rec["after"] == [0, 0, 0, 0] and rec["left_after"] == [0, 0] and rec["same"], rec
+
+
+def test_prefill_leaves_nothing_on_its_way(test_lib):  # noqa: F811
+    for rec in child(test_lib, "window_giveup_prefill_child"):
+        assert rec["plain"] == [0, 0, 0, 0] and rec["plain_left"] == 0, rec
+        assert rec["muted"] == [0, 0, 0, 4] and rec["left"] == 0, rec
+        # The muted unit, and those that the CTA had taken over by then.
+        assert [0, 0] in rec["units"] and len(rec["units"]) <= 4, rec
+        assert rec["after"] == [0, 0, 0, 0] and rec["left_after"] == 0 and rec["same"], rec
