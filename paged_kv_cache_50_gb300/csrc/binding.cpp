@@ -130,6 +130,23 @@ decltype(&pa_varlen_fwd_sinks) sinks_fn;
 decltype(&pa_decode_window) window_fn;
 decltype(&pa_decode_window_fp8) window_fp8_fn;
 
+// The library call itself, without the interpreter's lock: a launch waits where
+// the stream's queue is full, and what it waits for may need another thread of the
+// interpreter.  The arguments are taken beforehand.
+struct Unlocked {
+  PyThreadState* state = PyEval_SaveThread();
+  ~Unlocked() { PyEval_RestoreThread(state); }
+};
+template <class... P, class... A>
+PyObject* call(pa_status (*f)(P...), A... args) {
+  pa_status status;
+  {
+    Unlocked unlocked;
+    status = f(args...);
+  }
+  return PyLong_FromLong(status);
+}
+
 template <class F>
 PyObject* guarded(Py_ssize_t n, Py_ssize_t want, F f) {
   try {
@@ -190,15 +207,14 @@ PyObject* plan_step(PyObject*, PyObject* const* a, Py_ssize_t n) {
     void* slot = shaped(a[11], "slot_mapping", at::kLong, dev, {cap});
     void* totals = shaped(a[12], "totals", at::kInt, dev, {2});
     using I = int32_t*;
-    return PyLong_FromLong(plan_step_fn(
-        static_cast<I>(ctx), static_cast<I>(qlen),
-        static_cast<I>(dense(free, "free_blocks", at::kInt, dev)), static_cast<I>(start),
-        extent(free.size(0), "free_blocks"), extent(seqs, "block_table"),
-        extent(table.size(1), "block_table"), integer32(a[5], "block_size"),
-        integer32(a[6], "num_blocks"), cap,
-        static_cast<I>(dense(table, "block_table", at::kInt, dev)), static_cast<I>(qsl),
-        static_cast<I>(seq), static_cast<I>(pos), static_cast<int64_t*>(slot),
-        static_cast<I>(totals), stream_of(a[13], dev)));
+    return call(plan_step_fn, static_cast<I>(ctx), static_cast<I>(qlen),
+                static_cast<I>(dense(free, "free_blocks", at::kInt, dev)), static_cast<I>(start),
+                extent(free.size(0), "free_blocks"), extent(seqs, "block_table"),
+                extent(table.size(1), "block_table"), integer32(a[5], "block_size"),
+                integer32(a[6], "num_blocks"), cap,
+                static_cast<I>(dense(table, "block_table", at::kInt, dev)), static_cast<I>(qsl),
+                static_cast<I>(seq), static_cast<I>(pos), static_cast<int64_t*>(slot),
+                static_cast<I>(totals), stream_of(a[13], dev));
   });
 }
 
@@ -283,16 +299,14 @@ PyObject* norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (fp8) {
       if (!PyTuple_Check(a[5]) || PyTuple_GET_SIZE(a[5]) != 2)
         refuse(PyExc_TypeError, "(k_scale, v_scale) expected");
-      return PyLong_FromLong(norm_fp8_fn(
-          qp, kp, vp, qs, ks, vs, qw, kw, eps, static_cast<float*>(cs), rows, rot, turned,
-          static_cast<int32_t*>(pos), cache, static_cast<int64_t*>(slots), count, &s,
-          real(PyTuple_GET_ITEM(a[5], 0)), real(PyTuple_GET_ITEM(a[5], 1)), out,
-          stream_of(a[13], dev)));
+      return call(norm_fp8_fn, qp, kp, vp, qs, ks, vs, qw, kw, eps, static_cast<float*>(cs), rows,
+                  rot, turned, static_cast<int32_t*>(pos), cache, static_cast<int64_t*>(slots),
+                  count, &s, real(PyTuple_GET_ITEM(a[5], 0)), real(PyTuple_GET_ITEM(a[5], 1)), out,
+                  stream_of(a[13], dev));
     }
-    return PyLong_FromLong(norm_fn(qp, kp, vp, qs, ks, vs, qw, kw, eps, static_cast<float*>(cs),
-                                   rows, rot, turned, static_cast<int32_t*>(pos), cache,
-                                   static_cast<int64_t*>(slots), count, &s, out,
-                                   stream_of(a[13], dev)));
+    return call(norm_fn, qp, kp, vp, qs, ks, vs, qw, kw, eps, static_cast<float*>(cs), rows, rot,
+                turned, static_cast<int32_t*>(pos), cache, static_cast<int64_t*>(slots), count, &s,
+                out, stream_of(a[13], dev));
   });
 }
 
@@ -335,11 +349,11 @@ PyObject* varlen_sinks(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const Window w = window_args(a, false);
     void* qsl = shaped(a[6], "query_start_loc", at::kInt, w.dev,
                        {static_cast<int64_t>(w.shape.num_seqs) + 1});
-    return PyLong_FromLong(sinks_fn(
-        w.q, w.pool, static_cast<int32_t*>(w.table), static_cast<int32_t*>(qsl),
-        static_cast<int32_t*>(w.seq), extent(w.rows, "q"), integer32(a[7], "max_query_len"),
-        &w.shape, real(a[8]), integer32(a[9], "sliding_window"), integer32(a[10], "num_sinks"),
-        w.out, static_cast<float*>(w.lse), stream_of(a[11], w.dev)));
+    return call(sinks_fn, w.q, w.pool, static_cast<int32_t*>(w.table), static_cast<int32_t*>(qsl),
+                static_cast<int32_t*>(w.seq), extent(w.rows, "q"),
+                integer32(a[7], "max_query_len"), &w.shape, real(a[8]),
+                integer32(a[9], "sliding_window"), integer32(a[10], "num_sinks"), w.out,
+                static_cast<float*>(w.lse), stream_of(a[11], w.dev));
   });
 }
 
@@ -358,12 +372,12 @@ PyObject* decode_window(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (fp8) {
       if (!PyTuple_Check(a[6]) || PyTuple_GET_SIZE(a[6]) != 2)
         refuse(PyExc_TypeError, "(k_scale, v_scale) expected");
-      return PyLong_FromLong(window_fp8_fn(
-          w.q, w.pool, table, seq, &w.shape, scale, real(PyTuple_GET_ITEM(a[6], 0)),
-          real(PyTuple_GET_ITEM(a[6], 1)), window, sinks, w.out, lse, stream_of(a[10], w.dev)));
+      return call(window_fp8_fn, w.q, w.pool, table, seq, &w.shape, scale,
+                  real(PyTuple_GET_ITEM(a[6], 0)), real(PyTuple_GET_ITEM(a[6], 1)), window, sinks,
+                  w.out, lse, stream_of(a[10], w.dev));
     }
-    return PyLong_FromLong(window_fn(w.q, w.pool, table, seq, &w.shape, scale, window, sinks,
-                                     w.out, lse, stream_of(a[10], w.dev)));
+    return call(window_fn, w.q, w.pool, table, seq, &w.shape, scale, window, sinks, w.out, lse,
+                stream_of(a[10], w.dev));
   });
 }
 
