@@ -20,13 +20,18 @@ import ctypes
 import importlib.machinery
 import importlib.util
 import os
+import sysconfig
 import threading
 
 import torch
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "_build", "libpa.so")
-BINDING_PATH = os.path.join(_PKG, "_build", "_binding.so")
+# The compiled checks read torch's tensors by the layout of the headers that they
+# were built with, so their name holds that torch and that interpreter: another
+# one finds them missing, not stale.
+BINDING_PATH = os.path.join(_PKG, "_build", f"_binding.torch-{torch.__version__}"
+                            f"{sysconfig.get_config_var('EXT_SUFFIX')}")
 
 PA_OK, PA_ERR_INVALID, PA_ERR_UNSUPPORTED, PA_ERR_CUDA = 0, 1, 2, 3
 PA_DEVERR_BLOCK_ID, PA_DEVERR_SLOT, PA_DEVERR_TIMEOUT, PA_DEVERR_LENGTH = 1, 2, 4, 8

@@ -2,7 +2,8 @@
 
 Every ``csrc/*.cu`` translation unit is compiled in parallel for sm_103a only
 and linked into ``paged_kv_cache_50_gb300/_build/libpa.so``; the compiled
-argument checks (``csrc/binding.cpp``) become ``_build/_binding.so``.  Run as
+argument checks (``csrc/binding.cpp``) become the package's ``BINDING_PATH``, a file
+for each torch and interpreter that they are compiled against.  Run as
 ``python -m paged_kv_cache_50_gb300.build`` or call :func:`build`.
 """
 
@@ -22,8 +23,6 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OUT_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(OUT_DIR, "libpa.so")
-
-BINDING = os.path.join(OUT_DIR, "_binding.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "--expt-relaxed-constexpr",
@@ -56,17 +55,18 @@ def up_to_date() -> bool:
 def build_binding(force: bool = False, verbose: bool = False) -> str:
     """Compile csrc/binding.cpp (a CPython extension over torch's headers) with
     the host compiler; returns its path."""
+    from paged_kv_cache_50_gb300 import BINDING_PATH
     src = os.path.join(CSRC, "binding.cpp")
     deps = [src, os.path.join(INCLUDE, "pa.h"), os.path.abspath(__file__)]
-    if not force and os.path.exists(BINDING) and all(
-            os.path.getmtime(p) <= os.path.getmtime(BINDING) for p in deps):
-        return BINDING
+    if not force and os.path.exists(BINDING_PATH) and all(
+            os.path.getmtime(p) <= os.path.getmtime(BINDING_PATH) for p in deps):
+        return BINDING_PATH
     import torch
     os.makedirs(OUT_DIR, exist_ok=True)
     root = os.path.dirname(torch.__file__)
     inc, lib = os.path.join(root, "include"), os.path.join(root, "lib")
     cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
-    tmp = BINDING + f".{os.getpid()}.tmp"
+    tmp = BINDING_PATH + f".{os.getpid()}.tmp"
     cmd = [os.environ.get("CXX") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
            "-I", INCLUDE, "-isystem", inc, "-isystem",
@@ -78,8 +78,8 @@ def build_binding(force: bool = False, verbose: bool = False) -> str:
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, BINDING)
-    return BINDING
+    os.replace(tmp, BINDING_PATH)
+    return BINDING_PATH
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=None, out_dir=None,

@@ -1,0 +1,57 @@
+"""The compiled argument checks as a file: which torch and interpreter they
+belong to (no GPU needed; the compiler is a stand-in)."""
+
+import os
+import sysconfig
+import types
+
+import pytest
+import torch
+
+
+@pytest.fixture()
+def built(monkeypatch, tmp_path):
+    """(build module, package, list of compiler calls), the package's file being
+    one in tmp_path; the stand-in compiler writes an empty output."""
+    import paged_kv_cache_50_gb300 as pa
+    from paged_kv_cache_50_gb300 import build
+    calls = []
+
+    def run(cmd, **kw):
+        calls.append(cmd)
+        with open(cmd[cmd.index("-o") + 1], "w"):
+            pass
+        return types.SimpleNamespace(returncode=0, stdout="", stderr="")
+
+    monkeypatch.setattr(build, "subprocess", types.SimpleNamespace(run=run))
+    monkeypatch.setattr(pa, "BINDING_PATH", str(tmp_path / os.path.basename(pa.BINDING_PATH)))
+    return build, pa, calls
+
+
+def test_the_file_names_its_torch_and_interpreter():
+    import paged_kv_cache_50_gb300 as pa
+    name = os.path.basename(pa.BINDING_PATH)
+    assert f"torch-{torch.__version__}" in name
+    assert name.endswith(sysconfig.get_config_var("EXT_SUFFIX"))
+
+
+def test_checks_of_another_torch_are_not_current(built, monkeypatch):
+    build, pa, calls = built
+    assert build.build_binding() == pa.BINDING_PATH and len(calls) == 1
+    assert build.build_binding() == pa.BINDING_PATH and len(calls) == 1     # current
+    there = pa.BINDING_PATH
+    other = there.replace(torch.__version__, "9.9.9+cu999")
+    assert other != there
+    monkeypatch.setattr(pa, "BINDING_PATH", other)
+    assert build.build_binding() == other and len(calls) == 2
+    assert os.path.exists(there) and os.path.exists(other)
+
+
+def test_checks_of_another_torch_are_not_loaded(built, monkeypatch):
+    build, pa, calls = built
+    build.build_binding()
+    monkeypatch.setattr(pa, "_steps", None)
+    monkeypatch.setattr(pa, "BINDING_PATH",
+                        pa.BINDING_PATH.replace(torch.__version__, "9.9.9+cu999"))
+    with pytest.raises(RuntimeError, match="is missing: build it"):
+        pa._binding()
