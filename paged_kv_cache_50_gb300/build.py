@@ -16,6 +16,7 @@ import shutil
 import subprocess
 import sys
 import sysconfig
+import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -52,6 +53,18 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(p) <= t for p in _deps())
 
 
+def binding_headers_missing() -> str:
+    """The first header that the compiled checks need and that is not there, or
+    "": libpa.so and the calls that do without the checks need neither."""
+    import torch
+    for h in (os.path.join(sysconfig.get_paths()["include"], "Python.h"),
+              os.path.join(os.path.dirname(torch.__file__), "include", "torch", "csrc",
+                           "autograd", "python_variable.h")):
+        if not os.path.exists(h):
+            return h
+    return ""
+
+
 def build_binding(force: bool = False, verbose: bool = False) -> str:
     """Compile csrc/binding.cpp (a CPython extension over torch's headers) with
     the host compiler; returns its path."""
@@ -86,8 +99,14 @@ def build(force: bool = False, verbose: bool = False, extra_flags=None, out_dir=
           lib_name="libpa.so") -> str:
     """Compile and link libpa.so; returns its path.  ``out_dir`` / ``lib_name``
     build a variant elsewhere (the tests' timeout variant, with its own
-    defines in ``extra_flags``); the default build never includes one."""
+    defines in ``extra_flags``); the default build never includes one.  Without
+    the Python or torch headers the compiled checks are left out with a warning,
+    and the serving-step calls raise."""
     binding = out_dir is None
+    if binding and binding_headers_missing():
+        warnings.warn(f"{binding_headers_missing()} is missing: the compiled checks of the "
+                      "serving-step calls are not built", RuntimeWarning, stacklevel=2)
+        binding = False
     out_dir = out_dir or OUT_DIR
     lib = os.path.join(out_dir, lib_name)
     if binding:

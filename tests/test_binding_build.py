@@ -55,3 +55,19 @@ def test_checks_of_another_torch_are_not_loaded(built, monkeypatch):
                         pa.BINDING_PATH.replace(torch.__version__, "9.9.9+cu999"))
     with pytest.raises(RuntimeError, match="is missing: build it"):
         pa._binding()
+
+
+def test_library_alone_builds_without_python_headers(built, monkeypatch, tmp_path):
+    """libpa.so, and a warning instead of an error for the checks."""
+    build, pa, calls = built
+    made = []
+    monkeypatch.setattr(build, "_build_lib", lambda lib, *rest: made.append(lib))
+    assert build.binding_headers_missing() == ""
+    build.build()
+    assert made == [build.LIB] and len(calls) == 1
+    monkeypatch.setattr(build, "sysconfig", types.SimpleNamespace(
+        get_paths=lambda: {"include": str(tmp_path)}))
+    os.remove(pa.BINDING_PATH)
+    with pytest.warns(RuntimeWarning, match="Python.h is missing"):
+        assert build.build() == build.LIB
+    assert made == [build.LIB] * 2 and len(calls) == 1
