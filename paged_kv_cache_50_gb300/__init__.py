@@ -129,6 +129,8 @@ def _binding():
     if _steps is None:
         L = lib()
         with _lock:
+            if _steps is not None:      # another first caller was there before
+                return _steps
             if not os.path.exists(BINDING_PATH):
                 raise RuntimeError(f"{BINDING_PATH} is missing: build it with "
                                    "`python -m paged_kv_cache_50_gb300.build`")

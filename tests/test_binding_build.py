@@ -71,3 +71,33 @@ def test_library_alone_builds_without_python_headers(built, monkeypatch, tmp_pat
     with pytest.warns(RuntimeWarning, match="Python.h is missing"):
         assert build.build() == build.LIB
     assert made == [build.LIB] * 2 and len(calls) == 1
+
+
+def test_first_callers_load_the_checks_once(monkeypatch):
+    """Two threads that both find them not loaded yet."""
+    import importlib.machinery
+    import threading
+
+    import paged_kv_cache_50_gb300 as pa
+    from paged_kv_cache_50_gb300 import build
+    build.build()
+    real, loads, both = importlib.machinery.ExtensionFileLoader.exec_module, [], []
+    lib, meet = pa.lib(), threading.Barrier(2)
+
+    def exec_module(self, module):
+        loads.append(1)
+        return real(self, module)
+
+    def first(*args):      # both are past the unlocked test when they come here
+        meet.wait(timeout=60)
+        return lib
+
+    monkeypatch.setattr(importlib.machinery.ExtensionFileLoader, "exec_module", exec_module)
+    monkeypatch.setattr(pa, "_steps", None)
+    monkeypatch.setattr(pa, "lib", first)
+    threads = [threading.Thread(target=lambda: both.append(pa._binding())) for _ in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert len(loads) == 1 and both[0] is both[1] and pa._steps is both[0]
