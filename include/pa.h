@@ -496,7 +496,8 @@ pa_status pa_qk_norm_rope_cache_fp8(const void* q, const void* key, const void* 
  * request sees (between the first tokens and the oldest window) are not
  * read: their table entries and contents may be anything.  A position that
  * one row of a request sees must hold finite values, as for pa_varlen_fwd.
- * scale is finite and > 0.  Rows of a request past max_query_len or total_q are
+ * scale > 0, and scale * log2(e) finite in fp32.  Rows of a request past
+ * max_query_len or total_q are
  * not written; positions past the table's columns are not seen
  * (PA_DEVERR_BLOCK_ID).
  * Supported: head_size in {64, 128}, Hq / Hkv <= 128.
@@ -515,8 +516,8 @@ pa_status pa_varlen_fwd_sinks(const void* q, const void* kv_cache, const int32_t
  * visible tokens are cut over the CTAs of a thread-block cluster, which merge
  * their partial results in shared memory.
  * q, out: [N, Hq, d] bf16; lse: [N, Hq] fp32, nullable.  seq_lens[i] <= 0:
- * out = 0, lse = -inf.  sliding_window >= 1, num_sinks >= 0, scale finite and >
- * 0.  Positions past the table's columns are not seen (PA_DEVERR_BLOCK_ID).
+ * out = 0, lse = -inf.  sliding_window >= 1, num_sinks >= 0, scale > 0 and scale *
+ * log2(e) finite in fp32 (with an fp8 pool scale * k_scale * log2(e)).  Positions past the table's columns are not seen (PA_DEVERR_BLOCK_ID).
  * Supported: head_size in {64, 128}, Hq / Hkv <= 16.  q 4-byte, kv_cache
  * 16-byte, out 2-byte aligned.
  */

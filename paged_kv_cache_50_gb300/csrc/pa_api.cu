@@ -54,6 +54,13 @@ bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p
 
 bool scale_ok(float x) { return x > 0.f && x <= 3.4028234663852886e38f; }
 
+// The windowed kernels multiply logits by scale * k_scale * log2(e) in fp32, which
+// has to stay finite (0 * inf is NaN).
+bool logit_scale_ok(float scale, float k_scale) {
+  return scale_ok(scale) && scale_ok(k_scale) &&
+         scale * k_scale * pa::kLog2e <= 3.4028234663852886e38f;
+}
+
 // A range of device memory.
 struct Range {
   const void* p;
@@ -287,7 +294,7 @@ pa_status pa_varlen_fwd_sinks(const void* q, const void* kv_cache, const int32_t
                               int sliding_window, int num_sinks, void* out, float* lse,
                               void* stream) {
   if (!shape_ok(shape) || total_q < 0 || max_query_len < 0 || sliding_window < 1 ||
-      num_sinks < 0 || !scale_ok(scale))
+      num_sinks < 0 || !logit_scale_ok(scale, 1.f))
     return PA_ERR_INVALID;
   if (shape->head_size != 64 && shape->head_size != 128) return PA_ERR_UNSUPPORTED;
   if (shape->num_q_heads / shape->num_kv_heads > 128) return PA_ERR_UNSUPPORTED;
@@ -543,9 +550,9 @@ static pa_status decode_window(const void* q, const void* kv_cache, const int32_
                                const int32_t* seq_lens, const pa_shape* shape, float scale,
                                bool fp8, float k_scale, float v_scale, int sliding_window,
                                int num_sinks, void* out, float* lse, void* stream) {
-  if (!shape_ok(shape) || sliding_window < 1 || num_sinks < 0 || !scale_ok(scale))
+  if (!shape_ok(shape) || sliding_window < 1 || num_sinks < 0 ||
+      !logit_scale_ok(scale, k_scale) || !scale_ok(v_scale))
     return PA_ERR_INVALID;
-  if (!scale_ok(k_scale) || !scale_ok(v_scale)) return PA_ERR_INVALID;
   if (shape->head_size != 64 && shape->head_size != 128) return PA_ERR_UNSUPPORTED;
   if (shape->num_q_heads / shape->num_kv_heads > 16) return PA_ERR_UNSUPPORTED;
   if (shape->num_seqs == 0) return PA_OK;
