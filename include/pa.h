@@ -123,6 +123,8 @@ pa_status pa_varlen_fwd(const void* q, const void* kv_cache, const int32_t* bloc
  * the row's own included) is the library's.  sliding_window >= 1 (else
  * PA_ERR_INVALID); a window at least as long as every sequence equals
  * pa_varlen_fwd with causal = 1.  Other arguments as for pa_varlen_fwd.
+ * For Hq / Hkv <= 128, pa_varlen_fwd_sinks with num_sinks = 0 computes the same by
+ * a faster kernel (16 requests, window 1024: 275 us against 472).
  */
 pa_status pa_varlen_fwd_window(const void* q, const void* kv_cache, const int32_t* block_table,
                                const int32_t* query_start_loc, const int32_t* seq_lens,
@@ -492,7 +494,8 @@ pa_status pa_qk_norm_rope_cache_fp8(const void* q, const void* key, const void* 
  * Varlen paged attention with a sliding window and a few first tokens that
  * stay visible: pa_varlen_fwd_window in which row j at position p_j sees
  *   p <= p_j and (p > p_j - sliding_window or p < num_sinks).
- * num_sinks >= 0; 0 is pa_varlen_fwd_window's mask.  Blocks that no row of a
+ * num_sinks >= 0; 0 is pa_varlen_fwd_window's mask.  A request may have more
+ * queries than tokens: the rows before position 0 see nothing.  Blocks that no row of a
  * request sees (between the first tokens and the oldest window) are not
  * read: their table entries and contents may be anything.  A position that
  * one row of a request sees must hold finite values, as for pa_varlen_fwd.
@@ -500,7 +503,9 @@ pa_status pa_qk_norm_rope_cache_fp8(const void* q, const void* key, const void* 
  * max_query_len or total_q are
  * not written; positions past the table's columns are not seen
  * (PA_DEVERR_BLOCK_ID).
- * Supported: head_size in {64, 128}, Hq / Hkv <= 128.
+ * Supported: head_size in {64, 128}, Hq / Hkv <= 128, a bf16 pool.  (There is no
+ * prefill over an fp8 pool: pa_qk_norm_rope_cache_fp8 writes whole prompts, but
+ * only decode reads such a pool, so prompts are attended to token by token.)
  */
 pa_status pa_varlen_fwd_sinks(const void* q, const void* kv_cache, const int32_t* block_table,
                               const int32_t* query_start_loc, const int32_t* seq_lens,

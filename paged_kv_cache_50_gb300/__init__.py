@@ -310,7 +310,8 @@ def pa_varlen_fwd(q, kv_cache, block_table, query_start_loc, seq_lens, max_query
 def pa_varlen_fwd_window(q, kv_cache, block_table, query_start_loc, seq_lens, max_query_len,
                          scale, sliding_window, out=None, lse=None, return_lse=True, stream=None):
     """Causal varlen paged attention in which a row at position p sees only
-    p - sliding_window < p' <= p.  Returns (out, lse) like pa_varlen_fwd."""
+    p - sliding_window < p' <= p.  Returns (out, lse) like pa_varlen_fwd.
+    pa_varlen_fwd_sinks with num_sinks 0 computes the same by a faster kernel."""
     T, hq, d = q.shape
     N = seq_lens.shape[0]
     if query_start_loc.shape != (N + 1,):
@@ -646,7 +647,8 @@ def pa_varlen_fwd_sinks(q, kv_cache, block_table, query_start_loc, seq_lens, max
                         stream=None):
     """Causal varlen paged attention in which a row at position p sees
     p - sliding_window < p' <= p and p' < num_sinks.  Blocks that no row sees
-    are not read.  Returns (out, lse) like pa_varlen_fwd_window."""
+    are not read.  The pool is bf16: no prefill reads an fp8 pool.  Returns (out,
+    lse) like pa_varlen_fwd_window."""
     if out is None:
         out = _new(stream, q, "q", slice(None), torch.bfloat16)
     if lse is None and return_lse:

@@ -3,7 +3,7 @@
 // A step's small calls (a plan of 64 requests, the norms of 64 tokens) run for 2
 // to 3 us on the GPU, and reading type, device, layout and address of a dozen
 // tensors from Python costs more than that: a pa_plan_step call took 9.8 us of
-// host time and takes 2.3 with these checks, 1.5 of them the launch.  Each
+// host time and takes 2.5 with these checks, 1.5 of them the launch.  Each
 // function here takes one entry point's arguments as they come from
 // paged_kv_cache_50_gb300/__init__.py, checks every tensor (TypeError,
 // ValueError), calls the entry point and returns its status.  Nothing is computed

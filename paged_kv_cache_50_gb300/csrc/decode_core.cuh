@@ -1,6 +1,8 @@
 // One 16-token sub-block of decode attention for the query heads of one kv
-// group, by one warp: the products and the online softmax of the decode
-// kernels, for a bf16 pool and for a pool of e4m3 codes.
+// group, by one warp: the products and the online softmax of the windowed
+// decode kernel, for a bf16 pool and for a pool of e4m3 codes.  (The split-KV
+// kernels of decode.cu and decode_fp8.cu hold their own, over tiles that
+// cp.async lays out: a change here does not reach them.)
 //
 // The 16 tokens are the M dimension of mma.m16n8k16 and the group's heads its
 // N dimension (8 per n-tile): S^T = K Q^T, softmax over the tokens (two in a

@@ -22,7 +22,12 @@
 // 131 us (instructions); one loop over all kinds of rows with loads a round
 // ahead 98 us (spilled registers).  An e4m3 pool adds a quotient
 // per value: 8191 tokens of 64 / 8 heads, d 64, neighbouring pairs (161 MB): 30.1
-// us, bound by instructions (issue slots 60 % busy) as much as by HBM.
+// us, 0.79 of the copy rate (issue slots 53 % busy).
+// Between a few tokens per SM and several waves of warps (32 per SM: 4864 tokens
+// on 152 SMs) the last, part-filled wave costs most: 32 / 8 heads, d 128, bf16 /
+// e4m3, times the floor of their bytes: 2048 tokens 10.7 / 11.4 us (1.41 / 1.63),
+// 2500 14.6 / 17.1 (1.58 / 2.01), 4096 18.3 / 19.3 (1.21 / 1.39), 5000 26.4 / 27.5
+// (1.43 / 1.62), 8191 33.7 / 34.8 (1.11 / 1.25), 18432 70.3 / 72.3 (1.04 / 1.17).
 #include <type_traits>
 
 #include "pa_common.cuh"

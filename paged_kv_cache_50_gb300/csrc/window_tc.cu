@@ -43,8 +43,9 @@
 // Bound by the chain S -> softmax -> PV -> S of a Q tile (~3200 cycles of a
 // 128-token tile pair; its MMAs take 2290) and, at a unit's ends, by mask and
 // output code that is not in the instruction cache.  Measured (d 128, 16 requests
-// of U[256, 2048] new tokens, 32 / 8 heads, window 1024, 4 first tokens): 277 us,
-// 1066 TFLOP/s; 8192 tokens of 64 / 8 heads, window 4096: 768 us, 1436 TFLOP/s;
+// of U[256, 2048] new tokens, 32 / 8 heads, window 1024, 4 first tokens): the
+// kernel 275-280 us, 1055-1074 TFLOP/s, a call 283-287; 8192 tokens of 64 / 8
+// heads, window 4096: 757-778 us, 1417-1457 TFLOP/s, a call 770;
 // varlen_tc.cu's kernel with the same mask, one unit per CTA and 128-token steps,
 // took 419 and 1016.  Steps: persistent CTAs 365 / 953; the short loops 318 / 880;
 // descriptors 301 / 818; elect.sync 286 / 778; heads side by side 277 / 768.  Two
