@@ -537,6 +537,126 @@ pa_status pa_decode_window_fp8(const void* q, const void* kv_cache, const int32_
                                float k_scale, float v_scale, int sliding_window, int num_sinks,
                                void* out, float* lse, void* stream);
 
+/*
+ * A pool held in 4 bits.  Shape [num_blocks, num_kv_heads, block_size / 16, 2,
+ * 9 * head_size] bytes: for each block, kv head and 16 tokens a tile of keys (index
+ * 0) and one of values (1).  A tile is [16][head_size / 2] bytes of e2m1 codes
+ * (two a byte, the even element in the low half; 0, 0.5, 1, 1.5, 2, 3, 4, 6 and a
+ * sign), then [16][head_size / 16] e4m3 scales, one for each 16 elements.  Element e
+ * of a row stands for code[e] * scale[e / 16] * k_scale (values: v_scale), with the
+ * layer's k_scale and v_scale as for an e4m3 pool.  4.5 bits an element; what one
+ * head reads for 16 tokens is one run of 18 * head_size bytes.  16-byte aligned.
+ *
+ * pa_reshape_and_cache_fp4 -- pa_reshape_and_cache into such a pool.  Each 16
+ * elements x of a head row, with k = k_scale or v_scale, give
+ *   scale = e4m3(min(448, max|x| / k / 6)),  code = e2m1(x / fl32(scale * k)),
+ * quotients in fp32 (IEEE), conversions to nearest even, codes saturating at +-6;
+ * scale 0: codes 0.  A NaN makes the block's scale NaN (0x7F; its elements read as
+ * NaN) and its codes 0; an infinity saturates.
+ * key, value: [num_tokens, Hkv, d] bf16 with key_stride and value_stride elements
+ * from token to token (dense heads; multiples of 8, at least Hkv * d): views of a
+ * packed projection need no copy.  16-byte aligned.  Slots as for
+ * pa_reshape_and_cache.  Supported: head_size in {64, 128}.  Scales finite and > 0.
+ */
+pa_status pa_reshape_and_cache_fp4(const void* key, const void* value, int64_t key_stride,
+                                   int64_t value_stride, void* kv_cache,
+                                   const int64_t* slot_mapping, int num_tokens,
+                                   const pa_shape* shape, float k_scale, float v_scale,
+                                   void* stream);
+
+/*
+ * Decode over a 4-bit pool: one query per request over its first seq_lens[i] tokens,
+ *   out[i, h] = softmax(scale * q[i, h] . K) V,  lse[i, h] natural log,
+ * the context split over CTAs as the library sees fit, the partials merged as
+ * pa_lse_merge does.  max_seq_len >= every seq_lens[i] sizes the splits (tokens of a
+ * longer request are all read by its last split).  workspace: 16-byte aligned, at
+ * least pa_decode_fp4_workspace_bytes(N, Hq, Hkv, d, max_seq_len, 0) bytes on the
+ * device of the call (0: may be NULL); its contents are of no meaning between calls,
+ * and calls that may overlap on the GPU need one each.
+ * Queries and softmax weights enter the tensor cores as f16 (queries exactly for |q|
+ * in [2^-14, 65504], the weights to 2^-11), codes times scales exactly, sums are
+ * fp32.  q, out: [N, Hq, d] bf16; lse: [N, Hq] fp32, nullable.  seq_lens[i] <= 0: out
+ * = 0, lse = -inf.  Contents of tokens past seq_lens[i] do not matter.  Positions
+ * past the table's columns, and blocks outside [0, num_blocks), are not seen
+ * (PA_DEVERR_BLOCK_ID).  scale, k_scale, v_scale > 0, scale * k_scale * log2(e)
+ * finite in fp32.  Supported: head_size in {64, 128}, Hq / Hkv <= 16.  q 4-byte,
+ * kv_cache 16-byte, out 2-byte aligned.
+ */
+size_t pa_decode_fp4_workspace_bytes(int num_seqs, int num_q_heads, int num_kv_heads,
+                                     int head_size, int max_seq_len, int with_scores);
+pa_status pa_decode_fp4(const void* q, const void* kv_cache, const int32_t* block_table,
+                        const int32_t* seq_lens, const pa_shape* shape, float scale, float k_scale,
+                        float v_scale, int max_seq_len, void* workspace, size_t workspace_bytes,
+                        void* out, float* lse, void* stream);
+
+/*
+ * Decode that also accumulates what weight each cached token gets, over a bf16 pool
+ * (the standard layout) or a 4-bit one: out and lse as above, and for p < seq_lens[i]
+ *   scores[i, kvh, p] += sum over the heads h of kv head kvh of
+ *                        exp(scale * q[i, h] . K[p] - lse[i, h])
+ * in fp32 and in the order of the heads (no atomics).  Other entries stay as they
+ * are.  scores: [N, Hkv, score_tokens] fp32, in-out, score_tokens >= max_seq_len; the
+ * caller clears a new request's row.  Tokens past max_seq_len are attended to but get
+ * no sums (PA_DEVERR_LENGTH).  The sums are by request, not by block: requests may
+ * share blocks.  workspace: pa_decode_scores_workspace_bytes(...), for a 4-bit pool
+ * pa_decode_fp4_workspace_bytes(..., 1); 16-byte aligned.
+ */
+size_t pa_decode_scores_workspace_bytes(int num_seqs, int num_q_heads, int num_kv_heads,
+                                        int head_size, int max_seq_len);
+pa_status pa_decode_scores(const void* q, const void* kv_cache, const int32_t* block_table,
+                           const int32_t* seq_lens, const pa_shape* shape, float scale,
+                           int max_seq_len, void* workspace, size_t workspace_bytes, float* scores,
+                           int score_tokens, void* out, float* lse, void* stream);
+pa_status pa_decode_scores_fp4(const void* q, const void* kv_cache, const int32_t* block_table,
+                               const int32_t* seq_lens, const pa_shape* shape, float scale,
+                               float k_scale, float v_scale, int max_seq_len, void* workspace,
+                               size_t workspace_bytes, float* scores, int score_tokens, void* out,
+                               float* lse, void* stream);
+
+/*
+ * Eviction by accumulated weight.  A request with seq_lens[i] > budget is cut to
+ * `budget` tokens, for each kv head by itself: positions p < num_first and p >=
+ * seq_lens[i] - num_recent stay, and of the others those with the highest scores[i,
+ * kvh, p] (of equal ones the lowest positions; NaN counts below everything, -0 as 0).
+ * What stays keeps its order and moves, keys and values, to the places 0 .. budget -
+ * 1 of the request's blocks.  With kept position p_j in place j:
+ *   kept[i, kvh, j] = p_j, new_scores[i, kvh, j] = scores[i, kvh, p_j],
+ *   new_lens[i] = budget, new_scores 0 from there on (to seq_lens[i]; to score_tokens
+ *   where new_scores is not scores).
+ * A request within the budget keeps all: kept[j] = j, then -1; sums copied.
+ * Keys keep the rotation of their old positions: a later token's position is the
+ * caller's count of the tokens seen, its cache slot follows the new length.
+ * Blocks that lie behind the new lengths are pushed in front of the free ones, by
+ * request and column: with F of them free_blocks[free_start - F ..] get their ids
+ * and new_free_start = free_start - F, so that pa_plan_step takes them next.  The
+ * table's entries stay as they are.  free_blocks (num_free entries), free_start and
+ * new_free_start (device int32): all NULL, or none.  Without room for F in front of
+ * free_start (or free_start > num_free) none is pushed, new_free_start = free_start:
+ * PA_DEVERR_LENGTH.
+ * new_lens may be seq_lens, new_scores may be scores, new_free_start may be
+ * free_start (in place); outputs overlap nothing otherwise (PA_ERR_INVALID).
+ * A request's blocks must be its own: a block that two requests (or two columns)
+ * share would be moved in twice.
+ * Refused on the device: a request longer than score_tokens or its table row
+ * (PA_DEVERR_LENGTH) stays as it is, its kept[] as if within the budget; rows of
+ * blocks outside [0, num_blocks) are not moved (PA_DEVERR_BLOCK_ID).
+ * pa_evict: the standard pool with element_bytes 2 (bf16) or 1 (e4m3); pa_evict_fp4:
+ * the 4-bit pool.  budget >= 1, num_first + num_recent <= budget.  scores and
+ * new_scores: [N, Hkv, score_tokens] fp32; kept: [N, Hkv, budget] int32.  Supported:
+ * head_size in {64, 128}.  shape->num_q_heads is not used but must be a multiple of
+ * num_kv_heads.
+ */
+pa_status pa_evict(void* kv_cache, const pa_shape* shape, int element_bytes,
+                   const int32_t* block_table, const int32_t* seq_lens, const float* scores,
+                   int score_tokens, int budget, int num_recent, int num_first, int32_t* new_lens,
+                   float* new_scores, int32_t* kept, int32_t* free_blocks, int num_free,
+                   const int32_t* free_start, int32_t* new_free_start, void* stream);
+pa_status pa_evict_fp4(void* kv_cache, const pa_shape* shape, const int32_t* block_table,
+                       const int32_t* seq_lens, const float* scores, int score_tokens, int budget,
+                       int num_recent, int num_first, int32_t* new_lens, float* new_scores,
+                       int32_t* kept, int32_t* free_blocks, int num_free,
+                       const int32_t* free_start, int32_t* new_free_start, void* stream);
+
 /* Size of the fixed device array pa_decode_noalloc keeps its split partials in. */
 #define PA_NOALLOC_WORKSPACE_BYTES (16u * 1024u * 1024u)
 

@@ -106,6 +106,18 @@ def lib() -> ctypes.CDLL:
         L.pa_varlen_fwd_sinks.argtypes = [P, P, P, P, P, i32, i32, SP, f32, i32, i32, P, P, P]
         L.pa_decode_window.argtypes = [P, P, P, P, SP, f32, i32, i32, P, P, P]
         L.pa_decode_window_fp8.argtypes = [P, P, P, P, SP, f32, f32, f32, i32, i32, P, P, P]
+        size = ctypes.c_size_t
+        L.pa_reshape_and_cache_fp4.argtypes = [P, P, i64, i64, P, P, i32, SP, f32, f32, P]
+        L.pa_decode_fp4_workspace_bytes.argtypes = [i32, i32, i32, i32, i32, i32]
+        L.pa_decode_fp4_workspace_bytes.restype = size
+        L.pa_decode_scores_workspace_bytes.argtypes = [i32, i32, i32, i32, i32]
+        L.pa_decode_scores_workspace_bytes.restype = size
+        L.pa_decode_fp4.argtypes = [P, P, P, P, SP, f32, f32, f32, i32, P, size, P, P, P]
+        L.pa_decode_scores.argtypes = [P, P, P, P, SP, f32, i32, P, size, P, i32, P, P, P]
+        L.pa_decode_scores_fp4.argtypes = [P, P, P, P, SP, f32, f32, f32, i32, P, size, P, i32, P,
+                                           P, P]
+        L.pa_evict.argtypes = [P, SP, i32, P, P, P, i32, i32, i32, i32, P, P, P, P, i32, P, P, P]
+        L.pa_evict_fp4.argtypes = [P, SP, P, P, P, i32, i32, i32, i32, P, P, P, P, i32, P, P, P]
         L.pa_status_string.argtypes = [st]
         L.pa_status_string.restype = ctypes.c_char_p
         L.pa_get_device_error.argtypes = [ctypes.POINTER(ctypes.c_int), P]
@@ -117,7 +129,8 @@ def lib() -> ctypes.CDLL:
                      "pa_cascade_fwd", "pa_mla_cache_write", "pa_mla_expand_kv",
                      "pa_mla_prefill", "pa_plan_step", "pa_qk_norm_rope_cache",
                      "pa_qk_norm_rope_cache_fp8", "pa_varlen_fwd_sinks", "pa_decode_window",
-                     "pa_decode_window_fp8"):
+                     "pa_decode_window_fp8", "pa_reshape_and_cache_fp4", "pa_decode_fp4",
+                     "pa_decode_scores", "pa_decode_scores_fp4", "pa_evict", "pa_evict_fp4"):
             getattr(L, name).restype = st
         _lib = L
         return L
@@ -141,6 +154,9 @@ def _binding():
             m.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
                 L.pa_plan_step, L.pa_qk_norm_rope_cache, L.pa_qk_norm_rope_cache_fp8,
                 L.pa_varlen_fwd_sinks, L.pa_decode_window, L.pa_decode_window_fp8)))
+            m.bind_more(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
+                L.pa_reshape_and_cache_fp4, L.pa_decode_fp4, L.pa_decode_scores,
+                L.pa_decode_scores_fp4, L.pa_evict, L.pa_evict_fp4)))
             _steps = m
     return _steps
 
@@ -539,13 +555,13 @@ def pa_mla_decode(q, kv_cache, block_table, seq_lens, scale, workspace, out=None
 # their checks are compiled (csrc/binding.cpp).
 # ---------------------------------------------------------------------------
 
-def _new(stream, like, name, shape, dtype) -> torch.Tensor:
+def _new(stream, like, name, shape, dtype, more=()) -> torch.Tensor:
     """An output tensor beside ``like``, allocated for the stream that the call
-    runs on; ``shape``: an int, or a slice of ``like``'s."""
+    runs on; ``shape``: an int, or a slice of ``like``'s (with ``more`` behind it)."""
     if not isinstance(like, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if isinstance(shape, slice):
-        shape = like.shape[shape]
+        shape = (*like.shape[shape], *more) if more else like.shape[shape]
     if stream is None:
         return torch.empty(shape, dtype=dtype, device=like.device)
     if not isinstance(stream, torch.cuda.Stream):
@@ -693,6 +709,142 @@ def pa_decode_window_fp8(q, kv_cache, block_table, seq_lens, scale, k_scale, v_s
     if rc:
         _check(rc, "pa_decode_window_fp8")
     return out, lse
+
+
+# ---------------------------------------------------------------------------
+# Longer contexts: a 4-bit pool, sums of the attention weights, eviction.  As
+# for the serving step, every tensor is on one device, the current one.
+# ---------------------------------------------------------------------------
+
+def fp4_pool(num_blocks, block_size, num_kv_heads, head_size, device="cuda"):
+    """A 4-bit pool of zeros: uint8 [num_blocks, num_kv_heads, block_size / 16, 2,
+    9 * head_size], for each 16 tokens of a head the keys' e2m1 codes (two a byte)
+    and e4m3 scales (one for 16 elements), then the values'."""
+    if block_size % 16 or head_size % 16:
+        raise ValueError("block_size and head_size must be multiples of 16")
+    return torch.zeros((num_blocks, num_kv_heads, block_size // 16, 2, 9 * head_size),
+                       dtype=torch.uint8, device=device)
+
+
+def pa_reshape_and_cache_fp4(key, value, kv_cache, slot_mapping, k_scale, v_scale,
+                             stream=None) -> None:
+    """Quantising cache write: key/value [T, Hkv, d] bf16 into a 4-bit pool (see
+    fp4_pool).  Both may be views of one packed projection (dense heads, any token
+    stride that is a multiple of 8)."""
+    rc = (_steps or _binding()).cache_write_fp4(
+        key, value, kv_cache, slot_mapping, k_scale, v_scale,
+        None if stream is None else _stream(stream))
+    if rc:
+        _check(rc, "pa_reshape_and_cache_fp4")
+
+
+def pa_decode_fp4_workspace_bytes(num_seqs, num_q_heads, num_kv_heads, head_size, max_seq_len,
+                                  with_scores=False) -> int:
+    return int(lib().pa_decode_fp4_workspace_bytes(
+        int(num_seqs), int(num_q_heads), int(num_kv_heads), int(head_size), int(max_seq_len),
+        int(bool(with_scores))))
+
+
+def pa_decode_scores_workspace_bytes(num_seqs, num_q_heads, num_kv_heads, head_size,
+                                     max_seq_len) -> int:
+    return int(lib().pa_decode_scores_workspace_bytes(
+        int(num_seqs), int(num_q_heads), int(num_kv_heads), int(head_size), int(max_seq_len)))
+
+
+def _decode_scores(what, q, kv_cache, block_table, seq_lens, scale, scales, scores, workspace, out,
+                   lse, max_seq_len, return_lse, stream):
+    if max_seq_len is None:
+        max_seq_len = _max_seq(seq_lens, None)
+    if out is None:
+        out = _new(stream, q, "q", slice(None), torch.bfloat16)
+    if lse is None and return_lse:
+        lse = _new(stream, q, "q", slice(0, 2), torch.float32)
+    rc = (_steps or _binding()).decode_scores(
+        q, kv_cache, block_table, seq_lens, out, lse, workspace, scores, scales, scale, max_seq_len,
+        None if stream is None else _stream(stream))
+    if rc:
+        _check(rc, what)
+    return out, lse
+
+
+def pa_decode_fp4(q, kv_cache, block_table, seq_lens, scale, k_scale, v_scale, workspace, out=None,
+                  lse=None, max_seq_len=None, return_lse=True, stream=None):
+    """Decode (q [N, Hq, d] bf16, one query per request) over a 4-bit pool (see
+    fp4_pool).  ``workspace``: a uint8 tensor of pa_decode_fp4_workspace_bytes(N, Hq,
+    Hkv, d, max_seq_len) bytes (none needed: None or empty).  ``max_seq_len`` defaults
+    to the longest of ``seq_lens`` (a read from the device).  Returns (out [N, Hq, d]
+    bf16, lse [N, Hq])."""
+    return _decode_scores("pa_decode_fp4", q, kv_cache, block_table, seq_lens, scale,
+                          (k_scale, v_scale), None, workspace, out, lse, max_seq_len, return_lse,
+                          stream)
+
+
+def pa_decode_scores(q, kv_cache, block_table, seq_lens, scale, scores, workspace, out=None,
+                     lse=None, max_seq_len=None, return_lse=True, stream=None):
+    """Decode over a bf16 pool that adds each cached token's attention weight, summed
+    over the query heads of its kv head, to ``scores`` [N, Hkv, score_tokens] fp32
+    (in place; clear a new request's row).  ``workspace``: a uint8 tensor of
+    pa_decode_scores_workspace_bytes(N, Hq, Hkv, d, max_seq_len) bytes.  Returns (out,
+    lse)."""
+    if scores is None:
+        raise TypeError("scores must be a torch.Tensor")
+    return _decode_scores("pa_decode_scores", q, kv_cache, block_table, seq_lens, scale, None,
+                          scores, workspace, out, lse, max_seq_len, return_lse, stream)
+
+
+def pa_decode_scores_fp4(q, kv_cache, block_table, seq_lens, scale, k_scale, v_scale, scores,
+                         workspace, out=None, lse=None, max_seq_len=None, return_lse=True,
+                         stream=None):
+    """pa_decode_scores over a 4-bit pool; ``workspace``:
+    pa_decode_fp4_workspace_bytes(..., with_scores=True) bytes."""
+    if scores is None:
+        raise TypeError("scores must be a torch.Tensor")
+    return _decode_scores("pa_decode_scores_fp4", q, kv_cache, block_table, seq_lens, scale,
+                          (k_scale, v_scale), scores, workspace, out, lse, max_seq_len, return_lse,
+                          stream)
+
+
+def _evict(what, four, kv_cache, block_table, seq_lens, scores, budget, num_recent, num_first,
+           new_lens, new_scores, kept, free_blocks, free_start, new_free_start, stream):
+    new_lens = seq_lens if new_lens is None else new_lens
+    new_scores = scores if new_scores is None else new_scores
+    if kept is None:
+        kept = _new(stream, scores, "scores", slice(0, 2), torch.int32, more=(int(budget),))
+    if free_start is not None and new_free_start is None:
+        new_free_start = free_start
+    rc = (_steps or _binding()).evict(
+        kv_cache, four, block_table, seq_lens, scores, budget, num_recent, num_first, new_lens,
+        new_scores, kept, free_blocks, free_start, new_free_start,
+        None if stream is None else _stream(stream))
+    if rc:
+        _check(rc, what)
+    return new_lens, new_scores, kept
+
+
+def pa_evict(kv_cache, block_table, seq_lens, scores, budget, num_recent=0, num_first=0,
+             new_lens=None, new_scores=None, kept=None, free_blocks=None, free_start=None,
+             new_free_start=None, stream=None):
+    """Cuts requests longer than ``budget`` to that many cached tokens, for each kv
+    head the first ``num_first``, the last ``num_recent`` and the highest ``scores``
+    [N, Hkv, score_tokens] of the rest, moved together in order (in place in
+    ``kv_cache``, bf16 or e4m3).  Returns (new_lens [N], new_scores, kept [N, Hkv,
+    budget] = the position that each place held, -1 past the end); lengths and scores
+    are updated in place unless buffers are given.  With ``free_blocks`` and
+    ``free_start`` ([1] int32, as pa_plan_step takes them) the blocks behind the new
+    lengths are pushed in front of the free ones (``new_free_start``: in place unless
+    given).  A request's blocks must not be shared."""
+    return _evict("pa_evict", False, kv_cache, block_table, seq_lens, scores, budget, num_recent,
+                  num_first, new_lens, new_scores, kept, free_blocks, free_start, new_free_start,
+                  stream)
+
+
+def pa_evict_fp4(kv_cache, block_table, seq_lens, scores, budget, num_recent=0, num_first=0,
+                 new_lens=None, new_scores=None, kept=None, free_blocks=None, free_start=None,
+                 new_free_start=None, stream=None):
+    """pa_evict in a 4-bit pool (see fp4_pool)."""
+    return _evict("pa_evict_fp4", True, kv_cache, block_table, seq_lens, scores, budget,
+                  num_recent, num_first, new_lens, new_scores, kept, free_blocks, free_start,
+                  new_free_start, stream)
 
 
 PA_NOALLOC_WORKSPACE_BYTES = 16 * 1024 * 1024

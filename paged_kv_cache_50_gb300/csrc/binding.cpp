@@ -129,6 +129,12 @@ decltype(&pa_qk_norm_rope_cache_fp8) norm_fp8_fn;
 decltype(&pa_varlen_fwd_sinks) sinks_fn;
 decltype(&pa_decode_window) window_fn;
 decltype(&pa_decode_window_fp8) window_fp8_fn;
+decltype(&pa_reshape_and_cache_fp4) write_fp4_fn;
+decltype(&pa_decode_fp4) decode_fp4_fn;
+decltype(&pa_decode_scores) scores_fn;
+decltype(&pa_decode_scores_fp4) scores_fp4_fn;
+decltype(&pa_evict) evict_fn;
+decltype(&pa_evict_fp4) evict_fp4_fn;
 
 // The library call itself, without the interpreter's lock: a launch waits where
 // the stream's queue is full, and what it waits for may need another thread of the
@@ -179,6 +185,18 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
     sinks_fn = reinterpret_cast<decltype(sinks_fn)>(pointer(a[3]));
     window_fn = reinterpret_cast<decltype(window_fn)>(pointer(a[4]));
     window_fp8_fn = reinterpret_cast<decltype(window_fp8_fn)>(pointer(a[5]));
+    Py_RETURN_NONE;
+  });
+}
+
+PyObject* bind_more(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 6, [&]() -> PyObject* {
+    write_fp4_fn = reinterpret_cast<decltype(write_fp4_fn)>(pointer(a[0]));
+    decode_fp4_fn = reinterpret_cast<decltype(decode_fp4_fn)>(pointer(a[1]));
+    scores_fn = reinterpret_cast<decltype(scores_fn)>(pointer(a[2]));
+    scores_fp4_fn = reinterpret_cast<decltype(scores_fp4_fn)>(pointer(a[3]));
+    evict_fn = reinterpret_cast<decltype(evict_fn)>(pointer(a[4]));
+    evict_fp4_fn = reinterpret_cast<decltype(evict_fp4_fn)>(pointer(a[5]));
     Py_RETURN_NONE;
   });
 }
@@ -381,6 +399,174 @@ PyObject* decode_window(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// The 4-bit pool [num_blocks, num_kv_heads, block_size / 16, 2, 9 * head_size].
+pa_shape pool4_shape(const at::Tensor& pool, int64_t seqs, int64_t heads, int64_t max_blocks) {
+  if (pool.dim() != 5 || pool.size(3) != 2 || pool.size(4) % 9 != 0)
+    refuse(PyExc_ValueError,
+           "kv_cache must be [num_blocks, num_kv_heads, block_size / 16, 2, 9 * head_size]");
+  pa_shape s;
+  s.num_seqs = extent(seqs, "seq_lens");
+  s.num_kv_heads = extent(pool.size(1), "kv_cache");
+  s.num_q_heads = heads < 0 ? s.num_kv_heads : extent(heads, "q");
+  s.head_size = extent(pool.size(4) / 9, "kv_cache");
+  s.block_size = extent(pool.size(2) * 16, "kv_cache");
+  s.num_blocks = extent(pool.size(0), "kv_cache");
+  s.max_blocks_per_seq = extent(max_blocks, "block_table");
+  return s;
+}
+
+// (key, value, kv_cache, slot_mapping, k_scale, v_scale, stream | None)
+PyObject* cache_write_fp4(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 7, [&]() -> PyObject* {
+    const at::Tensor& key = tensor(a[0], "key");
+    const at::Tensor& pool = tensor(a[2], "kv_cache");
+    const pa_shape s = pool4_shape(pool, 0, -1, 1);
+    if (key.dim() != 3)
+      refuse(PyExc_ValueError, "key must be [num_tokens, num_kv_heads, head_size]");
+    const int64_t tokens = key.size(0);
+    const int dev = call_device(key, "key");
+    int64_t ks, vs;
+    void* kp = token_rows(a[0], "key", tokens, s.num_kv_heads, s.head_size, dev, &ks);
+    void* vp = token_rows(a[1], "value", tokens, s.num_kv_heads, s.head_size, dev, &vs);
+    void* slots = shaped(a[3], "slot_mapping", at::kLong, dev, {tokens});
+    return call(write_fp4_fn, kp, vp, ks, vs, dense(pool, "kv_cache", at::kByte, dev),
+                static_cast<int64_t*>(slots), extent(tokens, "key"), &s, real(a[4]), real(a[5]),
+                stream_of(a[6], dev));
+  });
+}
+
+struct Decode {
+  int dev;
+  pa_shape shape;
+  void *q, *pool, *table, *seq, *out, *lse, *workspace, *scores;
+  size_t workspace_bytes;
+  int score_tokens;
+};
+
+// q, kv_cache, block_table, seq_lens, out, lse | None, workspace | None, scores | None
+Decode decode_args(PyObject* const* a, bool four) {
+  Decode w{};
+  const at::Tensor& q = tensor(a[0], "q");
+  const at::Tensor& pool = tensor(a[1], "kv_cache");
+  const at::Tensor& table = tensor(a[2], "block_table");
+  const at::Tensor& seq = tensor(a[3], "seq_lens");
+  if (q.dim() != 3) refuse(PyExc_ValueError, "q must be [num_seqs, num_q_heads, head_size]");
+  if (seq.dim() != 1 || table.dim() != 2 || table.size(0) != seq.size(0))
+    refuse(PyExc_ValueError,
+           "seq_lens must be [num_seqs] and block_table [num_seqs, max_blocks]");
+  w.shape = four ? pool4_shape(pool, seq.size(0), q.size(1), table.size(1))
+                 : pool_shape(pool, seq.size(0), q.size(1), table.size(1));
+  if (q.size(2) != w.shape.head_size)
+    refuse(PyExc_ValueError, "q head_size does not match kv_cache");
+  if (q.size(0) != seq.size(0)) refuse(PyExc_ValueError, "q must hold one row per request");
+  w.dev = call_device(q, "q");
+  w.q = dense(q, "q", at::kBFloat16, w.dev);
+  w.pool = dense(pool, "kv_cache", four ? at::kByte : at::kBFloat16, w.dev);
+  w.table = dense(table, "block_table", at::kInt, w.dev);
+  w.seq = dense(seq, "seq_lens", at::kInt, w.dev);
+  w.out = shaped(a[4], "out", at::kBFloat16, w.dev, {q.size(0), q.size(1), q.size(2)});
+  if (a[5] != Py_None) w.lse = shaped(a[5], "lse", at::kFloat, w.dev, {q.size(0), q.size(1)});
+  if (a[6] != Py_None) {
+    const at::Tensor& ws = tensor(a[6], "workspace");
+    w.workspace = dense(ws, "workspace", at::kByte, w.dev);
+    w.workspace_bytes = static_cast<size_t>(ws.numel());
+  }
+  if (a[7] != Py_None) {
+    const at::Tensor& sc = tensor(a[7], "scores");
+    if (sc.dim() != 3 || sc.size(0) != seq.size(0) || sc.size(1) != w.shape.num_kv_heads)
+      refuse(PyExc_ValueError, "scores must be [num_seqs, num_kv_heads, score_tokens]");
+    w.scores = dense(sc, "scores", at::kFloat, w.dev);
+    w.score_tokens = extent(sc.size(2), "scores");
+  }
+  return w;
+}
+
+// (q, kv_cache, block_table, seq_lens, out, lse | None, workspace | None,
+//  scores | None, (k_scale, v_scale) | None, scale, max_seq_len, stream | None)
+PyObject* decode_scores(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 12, [&]() -> PyObject* {
+    const bool four = a[8] != Py_None;
+    const Decode w = decode_args(a, four);
+    int32_t* table = static_cast<int32_t*>(w.table);
+    int32_t* seq = static_cast<int32_t*>(w.seq);
+    float *lse = static_cast<float*>(w.lse), *scores = static_cast<float*>(w.scores);
+    const float scale = real(a[9]);
+    const int longest = integer32(a[10], "max_seq_len");
+    void* stream = stream_of(a[11], w.dev);
+    if (!four)
+      return call(scores_fn, w.q, w.pool, table, seq, &w.shape, scale, longest, w.workspace,
+                  w.workspace_bytes, scores, w.score_tokens, w.out, lse, stream);
+    if (!PyTuple_Check(a[8]) || PyTuple_GET_SIZE(a[8]) != 2)
+      refuse(PyExc_TypeError, "(k_scale, v_scale) expected");
+    const float ks = real(PyTuple_GET_ITEM(a[8], 0)), vs = real(PyTuple_GET_ITEM(a[8], 1));
+    if (a[7] == Py_None)
+      return call(decode_fp4_fn, w.q, w.pool, table, seq, &w.shape, scale, ks, vs, longest,
+                  w.workspace, w.workspace_bytes, w.out, lse, stream);
+    return call(scores_fp4_fn, w.q, w.pool, table, seq, &w.shape, scale, ks, vs, longest,
+                w.workspace, w.workspace_bytes, scores, w.score_tokens, w.out, lse, stream);
+  });
+}
+
+// (kv_cache, 4-bit, block_table, seq_lens, scores, budget, num_recent, num_first,
+//  new_lens, new_scores, kept, free_blocks | None, free_start | None,
+//  new_free_start | None, stream | None)
+PyObject* evict(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 15, [&]() -> PyObject* {
+    const int four = PyObject_IsTrue(a[1]);
+    if (four < 0) throw Refused();
+    const at::Tensor& pool = tensor(a[0], "kv_cache");
+    const at::Tensor& table = tensor(a[2], "block_table");
+    const at::Tensor& seq = tensor(a[3], "seq_lens");
+    const at::Tensor& sc = tensor(a[4], "scores");
+    if (seq.dim() != 1 || table.dim() != 2 || table.size(0) != seq.size(0))
+      refuse(PyExc_ValueError,
+             "seq_lens must be [num_seqs] and block_table [num_seqs, max_blocks]");
+    const int64_t seqs = seq.size(0);
+    if (!four && (pool.dim() != 5 || pool.size(1) != 2))
+      refuse(PyExc_ValueError,
+             "kv_cache must be [num_blocks, 2, block_size, num_kv_heads, head_size]");
+    const pa_shape s = four ? pool4_shape(pool, seqs, -1, table.size(1))
+                            : pool_shape(pool, seqs, pool.size(3), table.size(1));
+    if (sc.dim() != 3 || sc.size(0) != seqs || sc.size(1) != s.num_kv_heads)
+      refuse(PyExc_ValueError, "scores must be [num_seqs, num_kv_heads, score_tokens]");
+    const int dev = call_device(pool, "kv_cache");
+    const bool bf16 = !four && pool.scalar_type() == at::kBFloat16;
+    void* cache = four   ? dense(pool, "kv_cache", at::kByte, dev)
+                  : bf16 ? dense(pool, "kv_cache", at::kBFloat16, dev)
+                         : pool_pointer(pool, true, dev);
+    using I = int32_t*;
+    I tp = static_cast<I>(dense(table, "block_table", at::kInt, dev));
+    I lp = static_cast<I>(dense(seq, "seq_lens", at::kInt, dev));
+    float* sp = static_cast<float*>(dense(sc, "scores", at::kFloat, dev));
+    const int cap = extent(sc.size(2), "scores"), budget = integer32(a[5], "budget");
+    const int recent = integer32(a[6], "num_recent"), first = integer32(a[7], "num_first");
+    I nl = static_cast<I>(shaped(a[8], "new_lens", at::kInt, dev, {seqs}));
+    float* ns = static_cast<float*>(
+        shaped(a[9], "new_scores", at::kFloat, dev, {seqs, s.num_kv_heads, sc.size(2)}));
+    I kept = static_cast<I>(shaped(a[10], "kept", at::kInt, dev, {seqs, s.num_kv_heads, budget}));
+    I fb = nullptr, fs = nullptr, nf = nullptr;
+    int count = 0;
+    if (a[11] != Py_None) {
+      const at::Tensor& f = tensor(a[11], "free_blocks");
+      if (f.dim() != 1) refuse(PyExc_ValueError, "free_blocks must be [num_free]");
+      if (a[12] == Py_None || a[13] == Py_None)
+        refuse(PyExc_ValueError, "free_blocks needs free_start");
+      fb = static_cast<I>(dense(f, "free_blocks", at::kInt, dev));
+      count = extent(f.size(0), "free_blocks");
+      fs = static_cast<I>(shaped(a[12], "free_start", at::kInt, dev, {1}));
+      nf = static_cast<I>(shaped(a[13], "new_free_start", at::kInt, dev, {1}));
+    } else if (a[12] != Py_None || a[13] != Py_None) {
+      refuse(PyExc_ValueError, "free_start needs free_blocks");
+    }
+    void* stream = stream_of(a[14], dev);
+    if (four)
+      return call(evict_fp4_fn, cache, &s, tp, lp, sp, cap, budget, recent, first, nl, ns, kept, fb,
+                  count, fs, nf, stream);
+    return call(evict_fn, cache, &s, bf16 ? 2 : 1, tp, lp, sp, cap, budget, recent, first, nl, ns,
+                kept, fb, count, fs, nf, stream);
+  });
+}
+
 template <class F>
 PyCFunction fast(F f) {
   return reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f));
@@ -389,6 +575,11 @@ PyCFunction fast(F f) {
 PyMethodDef methods[] = {
     {"check_device", fast(check_device), METH_FASTCALL, "Refuses a device that is not current."},
     {"bind", fast(bind), METH_FASTCALL, "Takes the library's entry points (addresses)."},
+    {"bind_more", fast(bind_more), METH_FASTCALL, "Takes more of them."},
+    {"cache_write_fp4", fast(cache_write_fp4), METH_FASTCALL, "pa_reshape_and_cache_fp4"},
+    {"decode_scores", fast(decode_scores), METH_FASTCALL,
+     "pa_decode_scores, with scales pa_decode_fp4 or pa_decode_scores_fp4"},
+    {"evict", fast(evict), METH_FASTCALL, "pa_evict, pa_evict_fp4"},
     {"plan_step", fast(plan_step), METH_FASTCALL, "pa_plan_step"},
     {"norm_rope", fast(norm_rope), METH_FASTCALL, "pa_qk_norm_rope_cache, with scales _fp8"},
     {"varlen_sinks", fast(varlen_sinks), METH_FASTCALL, "pa_varlen_fwd_sinks"},

@@ -62,7 +62,7 @@ __device__ __forceinline__ uint32_t ld_u32(const __nv_bfloat16* p) {
   return *reinterpret_cast<const uint32_t*>(p);
 }
 
-template <int D, int STAGES, int NT>
+template <int D, int STAGES, int NT, bool LOGITS>
 __global__ void __launch_bounds__(128)
 decode_splitkv_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat16* __restrict__ cache,
                       const int32_t* __restrict__ block_table, const int32_t* __restrict__ seq_lens,
@@ -236,6 +236,19 @@ decode_splitkv_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat16* 
         for (int e = 0; e < 4; ++e) sc[nt][e] = s2[nt][0][e] + s2[nt][1][e];
     }
 
+    if constexpr (LOGITS) {
+      float* dst = ext.logits +
+                   ((static_cast<int64_t>(i) * Hkv + kvh) * ext.logit_tokens + tb + gid) * grp;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int h = nt * 8 + 2 * tid4 + (e & 1), r = gid + 8 * (e >> 1);
+          if (h < grp && tb + r < min(t1, ext.logit_tokens))
+            dst[8 * (e >> 1) * grp + h] = r < lim ? sc[nt][e] * scale_log2 : -CUDART_INF_F;
+        }
+    }
+
     // Online softmax (log2 domain, scale folded in), per head over the 16
     // tokens: two in the lane, the rest across the 8 token lanes.  The
     // reference max moves only when a sub-block's max exceeds it by more than
@@ -359,14 +372,14 @@ decode_splitkv_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat16* 
   }
 }
 
-template <int D, int STAGES, int NT>
+template <int D, int STAGES, int NT, bool LOGITS>
 static cudaError_t launch_decode_t(const void* q, const void* cache, const int32_t* block_table,
                                    const int32_t* seq_lens, int N, int Hq, int Hkv, int bs,
                                    int num_blocks, int max_blocks, float scale, int S, int chunk,
                                    float* ws, int* err, const DecodeExt& ext,
                                    cudaStream_t stream) {
   using C = DecodeCfg<D, STAGES, NT>;
-  auto kern = decode_splitkv_kernel<D, STAGES, NT>;
+  auto kern = decode_splitkv_kernel<D, STAGES, NT, LOGITS>;
   static DeviceFlags attr_set;
   cudaError_t e = set_smem_once(kern, C::kSmemBytes, attr_set);
   if (e != cudaSuccess) return e;
@@ -385,8 +398,13 @@ cudaError_t launch_decode_splitkv(const void* q, const void* cache, const int32_
   const DecodeExt& x = ext != nullptr ? *ext : plain;
   const bool wide = Hq / Hkv > 8;   // groups of 9..16 heads take two n-tiles
 #define PA_DECODE_LAUNCH(DD, ST, NTT)                                                          \
-  return launch_decode_t<DD, ST, NTT>(q, cache, block_table, seq_lens, N, Hq, Hkv, bs,         \
-                                      num_blocks, max_blocks, scale, S, chunk, ws, err, x, stream)
+  return x.logits != nullptr                                                                   \
+             ? launch_decode_t<DD, ST, NTT, true>(q, cache, block_table, seq_lens, N, Hq, Hkv, \
+                                                  bs, num_blocks, max_blocks, scale, S, chunk, \
+                                                  ws, err, x, stream)                          \
+             : launch_decode_t<DD, ST, NTT, false>(q, cache, block_table, seq_lens, N, Hq, Hkv, \
+                                                   bs, num_blocks, max_blocks, scale, S, chunk, \
+                                                   ws, err, x, stream)
   if (d == 128) {
     if (wide) PA_DECODE_LAUNCH(128, 2, 2);
     PA_DECODE_LAUNCH(128, 2, 1);

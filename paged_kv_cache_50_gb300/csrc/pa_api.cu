@@ -604,6 +604,307 @@ pa_status pa_decode_window_fp8(const void* q, const void* kv_cache, const int32_
                        sliding_window, num_sinks, out, lse, stream);
 }
 
+pa_status pa_reshape_and_cache_fp4(const void* key, const void* value, int64_t key_stride,
+                                   int64_t value_stride, void* kv_cache,
+                                   const int64_t* slot_mapping, int num_tokens,
+                                   const pa_shape* shape, float k_scale, float v_scale,
+                                   void* stream) {
+  if (shape == nullptr || num_tokens < 0 || shape->num_kv_heads <= 0 ||
+      shape->num_kv_heads > kMaxGridYZ || shape->head_size <= 0 || shape->block_size <= 0 ||
+      shape->block_size % 16 != 0 || shape->num_blocks <= 0)
+    return PA_ERR_INVALID;
+  if (!scale_ok(k_scale) || !scale_ok(v_scale)) return PA_ERR_INVALID;
+  if (shape->head_size != 64 && shape->head_size != 128) return PA_ERR_UNSUPPORTED;
+  const int64_t width = static_cast<int64_t>(shape->num_kv_heads) * shape->head_size;
+  if (key_stride < width || value_stride < width || key_stride % 8 != 0 || value_stride % 8 != 0)
+    return PA_ERR_INVALID;
+  if (num_tokens == 0) return PA_OK;
+  if (key == nullptr || value == nullptr || kv_cache == nullptr || slot_mapping == nullptr)
+    return PA_ERR_INVALID;
+  if (!aligned(key, 16) || !aligned(value, 16) || !aligned(kv_cache, 16) ||
+      !aligned(slot_mapping, 8))
+    return PA_ERR_INVALID;
+  return from_cuda(pa::launch_cache_write_fp4(
+      key, value, key_stride, value_stride, kv_cache, slot_mapping, num_tokens,
+      shape->num_kv_heads, shape->head_size, shape->block_size, shape->num_blocks, k_scale, v_scale,
+      device_error_ptr(), static_cast<cudaStream_t>(stream)));
+}
+
+// Workspace of a decode call: the splits' partials, then (with sums) the logits.
+static size_t partial_bytes(int num_seqs, int num_q_heads, int splits, int d) {
+  const size_t n = static_cast<size_t>(num_seqs) * num_q_heads * splits * (d + 1) * 4;
+  return (n + 15) / 16 * 16;
+}
+static bool workspace_args_ok(int num_seqs, int num_q_heads, int num_kv_heads, int head_size,
+                              int max_seq_len) {
+  return num_seqs >= 0 && num_q_heads > 0 && num_kv_heads > 0 && head_size > 0 && max_seq_len >= 0;
+}
+// (152 where there is no device to ask, as when a size is planned beforehand.)
+static int sm_count_or_default() {
+  const int n = pa_device_sm_count();
+  return n > 0 ? n : 152;
+}
+
+size_t pa_decode_fp4_workspace_bytes(int num_seqs, int num_q_heads, int num_kv_heads,
+                                     int head_size, int max_seq_len, int with_scores) {
+  if (!workspace_args_ok(num_seqs, num_q_heads, num_kv_heads, head_size, max_seq_len)) return 0;
+  const int S = pa::decode_fp4_splits(num_seqs, num_kv_heads, max_seq_len, sm_count_or_default());
+  if (S == 1 && !with_scores) return 0;
+  return partial_bytes(num_seqs, num_q_heads, S, head_size) +
+         (with_scores ? static_cast<size_t>(num_seqs) * num_q_heads * max_seq_len * 4 : 0);
+}
+
+size_t pa_decode_scores_workspace_bytes(int num_seqs, int num_q_heads, int num_kv_heads,
+                                        int head_size, int max_seq_len) {
+  if (!workspace_args_ok(num_seqs, num_q_heads, num_kv_heads, head_size, max_seq_len)) return 0;
+  const int S = pa_decode_num_kv_splits(num_seqs, num_kv_heads, max_seq_len, sm_count_or_default());
+  return partial_bytes(num_seqs, num_q_heads, S, head_size) +
+         static_cast<size_t>(num_seqs) * num_q_heads * max_seq_len * 4;
+}
+
+// Checks that the decode calls below share; PA_OK with *done where there is nothing to do.
+static pa_status decode_args(const void* q, const void* kv_cache, const int32_t* block_table,
+                             const int32_t* seq_lens, const pa_shape* shape, float scale,
+                             float k_scale, float v_scale, int max_seq_len, const void* out,
+                             const float* lse, bool* done) {
+  *done = false;
+  if (!shape_ok(shape) || max_seq_len < 0 || !logit_scale_ok(scale, k_scale) || !scale_ok(v_scale))
+    return PA_ERR_INVALID;
+  if (shape->head_size != 64 && shape->head_size != 128) return PA_ERR_UNSUPPORTED;
+  if (shape->num_q_heads / shape->num_kv_heads > 16) return PA_ERR_UNSUPPORTED;
+  if (static_cast<long long>(shape->num_seqs) * shape->num_q_heads > INT_MAX) return PA_ERR_INVALID;
+  if (shape->num_seqs == 0) {
+    *done = true;
+    return PA_OK;
+  }
+  if (q == nullptr || kv_cache == nullptr || block_table == nullptr || seq_lens == nullptr ||
+      out == nullptr)
+    return PA_ERR_INVALID;
+  if (!aligned(q, 4) || !aligned(kv_cache, 16) || !aligned(out, 2) || !aligned(lse, 4) ||
+      !aligned(block_table, 4) || !aligned(seq_lens, 4))
+    return PA_ERR_INVALID;
+  return PA_OK;
+}
+
+static pa_status finish_scores(const pa_shape* shape, int S, int max_seq_len, float* ws,
+                               float* logits, const int32_t* seq_lens, float* scores,
+                               int score_tokens, void* out, float* lse, void* stream) {
+  pa::ScoresLaunch m{};
+  m.ws = ws;
+  m.logits = logits;
+  m.logit_tokens = max_seq_len;
+  m.seq_lens = seq_lens;
+  m.N = shape->num_seqs;
+  m.Hq = shape->num_q_heads;
+  m.Hkv = shape->num_kv_heads;
+  m.d = shape->head_size;
+  m.S = S;
+  m.max_seq_len = max_seq_len;
+  m.scores = scores;
+  m.score_tokens = score_tokens;
+  m.out = out;
+  m.lse = lse;
+  m.err = device_error_ptr();
+  return from_cuda(pa::launch_decode_scores(m, static_cast<cudaStream_t>(stream)));
+}
+
+static pa_status decode_fp4(const void* q, const void* kv_cache, const int32_t* block_table,
+                            const int32_t* seq_lens, const pa_shape* shape, float scale,
+                            float k_scale, float v_scale, int max_seq_len, void* workspace,
+                            size_t workspace_bytes, bool with_scores, float* scores,
+                            int score_tokens, void* out, float* lse, void* stream) {
+  bool done;
+  const pa_status s = decode_args(q, kv_cache, block_table, seq_lens, shape, scale, k_scale,
+                                  v_scale, max_seq_len, out, lse, &done);
+  if (s != PA_OK || done) return s;
+  if (with_scores && (scores == nullptr || !aligned(scores, 4) || score_tokens < max_seq_len))
+    return PA_ERR_INVALID;
+  const size_t need =
+      pa_decode_fp4_workspace_bytes(shape->num_seqs, shape->num_q_heads, shape->num_kv_heads,
+                                    shape->head_size, max_seq_len, with_scores);
+  if (need > 0 && (workspace == nullptr || workspace_bytes < need || !aligned(workspace, 16)))
+    return PA_ERR_INVALID;
+  const int S = pa::decode_fp4_splits(shape->num_seqs, shape->num_kv_heads, max_seq_len,
+                                      sm_count_or_default());
+  pa::DecodeFp4Launch n{};
+  n.q = q;
+  n.cache = kv_cache;
+  n.block_table = block_table;
+  n.seq_lens = seq_lens;
+  n.N = shape->num_seqs;
+  n.Hq = shape->num_q_heads;
+  n.Hkv = shape->num_kv_heads;
+  n.d = shape->head_size;
+  n.bs = shape->block_size;
+  n.num_blocks = shape->num_blocks;
+  n.max_blocks = shape->max_blocks_per_seq;
+  n.scale = scale;
+  n.k_scale = k_scale;
+  n.v_scale = v_scale;
+  n.S = S;
+  n.max_seq_len = max_seq_len;
+  n.ws = need > 0 ? static_cast<float*>(workspace) : nullptr;
+  // (Never null with sums, also where no token has logits.)
+  n.logits = with_scores ? reinterpret_cast<float*>(
+                               static_cast<char*>(workspace) +
+                               partial_bytes(n.N, n.Hq, S, n.d))
+                         : nullptr;
+  n.logit_tokens = max_seq_len;
+  n.out = out;
+  n.lse = lse;
+  n.err = device_error_ptr();
+  const cudaError_t e = pa::launch_decode_fp4(n, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return from_cuda(e);
+  if (with_scores)
+    return finish_scores(shape, S, max_seq_len, n.ws, n.logits, seq_lens, scores, score_tokens, out,
+                         lse, stream);
+  if (S == 1) return PA_OK;
+  return from_cuda(pa::launch_lse_merge(n.ws, n.N * n.Hq, S, n.d, out, lse,
+                                        static_cast<cudaStream_t>(stream)));
+}
+
+pa_status pa_decode_fp4(const void* q, const void* kv_cache, const int32_t* block_table,
+                        const int32_t* seq_lens, const pa_shape* shape, float scale, float k_scale,
+                        float v_scale, int max_seq_len, void* workspace, size_t workspace_bytes,
+                        void* out, float* lse, void* stream) {
+  return decode_fp4(q, kv_cache, block_table, seq_lens, shape, scale, k_scale, v_scale, max_seq_len,
+                    workspace, workspace_bytes, false, nullptr, 0, out, lse, stream);
+}
+
+pa_status pa_decode_scores_fp4(const void* q, const void* kv_cache, const int32_t* block_table,
+                               const int32_t* seq_lens, const pa_shape* shape, float scale,
+                               float k_scale, float v_scale, int max_seq_len, void* workspace,
+                               size_t workspace_bytes, float* scores, int score_tokens, void* out,
+                               float* lse, void* stream) {
+  return decode_fp4(q, kv_cache, block_table, seq_lens, shape, scale, k_scale, v_scale, max_seq_len,
+                    workspace, workspace_bytes, true, scores, score_tokens, out, lse, stream);
+}
+
+pa_status pa_decode_scores(const void* q, const void* kv_cache, const int32_t* block_table,
+                           const int32_t* seq_lens, const pa_shape* shape, float scale,
+                           int max_seq_len, void* workspace, size_t workspace_bytes, float* scores,
+                           int score_tokens, void* out, float* lse, void* stream) {
+  bool done;
+  const pa_status s = decode_args(q, kv_cache, block_table, seq_lens, shape, scale, 1.f, 1.f,
+                                  max_seq_len, out, lse, &done);
+  if (s != PA_OK || done) return s;
+  if (scores == nullptr || !aligned(scores, 4) || score_tokens < max_seq_len) return PA_ERR_INVALID;
+  const size_t need =
+      pa_decode_scores_workspace_bytes(shape->num_seqs, shape->num_q_heads, shape->num_kv_heads,
+                                       shape->head_size, max_seq_len);
+  if (workspace == nullptr || workspace_bytes < need || !aligned(workspace, 16))
+    return PA_ERR_INVALID;
+  const int S = pa_decode_num_kv_splits(shape->num_seqs, shape->num_kv_heads, max_seq_len,
+                                        sm_count_or_default());
+  float* ws = static_cast<float*>(workspace);
+  pa::DecodeExt x{0, 0, S, 0};
+  x.logits = reinterpret_cast<float*>(
+      static_cast<char*>(workspace) +
+      partial_bytes(shape->num_seqs, shape->num_q_heads, S, shape->head_size));
+  x.logit_tokens = max_seq_len;
+  const cudaError_t e = pa::launch_decode_splitkv(
+      q, kv_cache, block_table, seq_lens, shape->num_seqs, shape->num_q_heads,
+      shape->num_kv_heads, shape->head_size, shape->block_size, shape->num_blocks,
+      shape->max_blocks_per_seq, scale, S,
+      static_cast<int>(pa::split_chunk(max_seq_len, S, shape->block_size)), ws, device_error_ptr(),
+      static_cast<cudaStream_t>(stream), &x);
+  if (e != cudaSuccess) return from_cuda(e);
+  return finish_scores(shape, S, max_seq_len, ws, x.logits, seq_lens, scores, score_tokens, out, lse,
+                       stream);
+}
+
+static pa_status evict(void* kv_cache, const pa_shape* shape, bool four, int element_bytes,
+                       const int32_t* block_table, const int32_t* seq_lens, const float* scores,
+                       int score_tokens, int budget, int num_recent, int num_first,
+                       int32_t* new_lens, float* new_scores, int32_t* kept, int32_t* free_blocks,
+                       int num_free, const int32_t* free_start, int32_t* new_free_start,
+                       void* stream) {
+  if (!shape_ok(shape) || score_tokens <= 0 || budget < 1 || budget > (1 << 30) ||
+      num_recent < 0 || num_first < 0 || num_recent > budget || num_first > budget - num_recent ||
+      num_free < 0 || (!four && element_bytes != 1 && element_bytes != 2))
+    return PA_ERR_INVALID;
+  if (shape->head_size != 64 && shape->head_size != 128) return PA_ERR_UNSUPPORTED;
+  if (shape->num_seqs == 0) return PA_OK;
+  if (kv_cache == nullptr || block_table == nullptr || seq_lens == nullptr || scores == nullptr ||
+      new_lens == nullptr || new_scores == nullptr || kept == nullptr)
+    return PA_ERR_INVALID;
+  // A free list comes with its two ends, or not at all.
+  if ((free_blocks == nullptr) != (free_start == nullptr) ||
+      (free_blocks == nullptr) != (new_free_start == nullptr))
+    return PA_ERR_INVALID;
+  if (!aligned(kv_cache, 16) || !aligned(block_table, 4) || !aligned(seq_lens, 4) ||
+      !aligned(scores, 4) || !aligned(new_lens, 4) || !aligned(new_scores, 4) ||
+      !aligned(kept, 4) || !aligned(free_blocks, 4) || !aligned(free_start, 4) ||
+      !aligned(new_free_start, 4))
+    return PA_ERR_INVALID;
+  // Inputs, then outputs.  Lengths, sums and the list's start may be updated in place.
+  const size_t n4 = static_cast<size_t>(shape->num_seqs) * 4;
+  const size_t units4 = n4 * shape->num_kv_heads, one = free_start != nullptr ? 4u : 0u;
+  const Range ranges[] = {{block_table, n4 * shape->max_blocks_per_seq},
+                          {seq_lens, n4},
+                          {scores, units4 * score_tokens},
+                          {free_start, one},
+                          {new_lens, n4},
+                          {new_scores, units4 * score_tokens},
+                          {kept, units4 * budget},
+                          {free_blocks, static_cast<size_t>(num_free) * 4},
+                          {new_free_start, one}};
+  for (int out = 4; out < 9; ++out)
+    for (int k = 0; k < out; ++k) {
+      const bool same = (out == 4 && k == 1) || (out == 5 && k == 2) || (out == 8 && k == 3);
+      if (same && ranges[out].p == ranges[k].p) continue;
+      if (overlap(ranges[out], ranges[k])) return PA_ERR_INVALID;
+    }
+  pa::EvictLaunch n{};
+  n.cache = kv_cache;
+  n.block_table = block_table;
+  n.seq_lens = seq_lens;
+  n.scores = scores;
+  n.new_scores = new_scores;
+  n.new_lens = new_lens;
+  n.kept = kept;
+  n.free_blocks = free_blocks;
+  n.free_start = free_start;
+  n.new_free_start = new_free_start;
+  n.num_free = num_free;
+  n.N = shape->num_seqs;
+  n.Hkv = shape->num_kv_heads;
+  n.d = shape->head_size;
+  n.bs = shape->block_size;
+  n.num_blocks = shape->num_blocks;
+  n.max_blocks = shape->max_blocks_per_seq;
+  n.score_tokens = score_tokens;
+  n.budget = budget;
+  n.recent = num_recent;
+  n.first = num_first;
+  n.four = four;
+  n.row_bytes = shape->head_size * element_bytes;
+  n.err = device_error_ptr();
+  n.sm_count = pa_device_sm_count();
+  if (n.sm_count <= 0) return PA_ERR_CUDA;
+  return from_cuda(pa::launch_evict(n, static_cast<cudaStream_t>(stream)));
+}
+
+pa_status pa_evict(void* kv_cache, const pa_shape* shape, int element_bytes,
+                   const int32_t* block_table, const int32_t* seq_lens, const float* scores,
+                   int score_tokens, int budget, int num_recent, int num_first, int32_t* new_lens,
+                   float* new_scores, int32_t* kept, int32_t* free_blocks, int num_free,
+                   const int32_t* free_start, int32_t* new_free_start, void* stream) {
+  return evict(kv_cache, shape, false, element_bytes, block_table, seq_lens, scores, score_tokens,
+               budget, num_recent, num_first, new_lens, new_scores, kept, free_blocks, num_free,
+               free_start, new_free_start, stream);
+}
+
+pa_status pa_evict_fp4(void* kv_cache, const pa_shape* shape, const int32_t* block_table,
+                       const int32_t* seq_lens, const float* scores, int score_tokens, int budget,
+                       int num_recent, int num_first, int32_t* new_lens, float* new_scores,
+                       int32_t* kept, int32_t* free_blocks, int num_free,
+                       const int32_t* free_start, int32_t* new_free_start, void* stream) {
+  return evict(kv_cache, shape, true, 0, block_table, seq_lens, scores, score_tokens, budget,
+               num_recent, num_first, new_lens, new_scores, kept, free_blocks, num_free, free_start,
+               new_free_start, stream);
+}
+
 pa_status pa_plan_step(const int32_t* context_lens, const int32_t* query_lens,
                        const int32_t* free_blocks, const int32_t* free_start, int num_free,
                        int num_seqs, int max_blocks_per_seq, int block_size, int num_blocks,

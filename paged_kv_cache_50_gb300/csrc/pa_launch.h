@@ -23,11 +23,14 @@ cudaError_t launch_reshape_and_cache(const void* key, const void* value, void* c
 // first seq_off tokens, whose blocks are the first table_col0 columns of its
 // row, and split s writes slot ws_slot0 + s of a workspace with ws_slots
 // slots per (request, head).
+// logits (nullable): each token's logits as well, for the weights' sums.
 struct DecodeExt {
   int table_col0;
   int seq_off;
   int ws_slots;
   int ws_slot0;
+  float* logits = nullptr;   // [N, Hkv, logit_tokens, Hq / Hkv], log2 units
+  int logit_tokens = 0;
 };
 
 // Split-KV stage 1; `chunk` = tokens per split (split_chunk in pa_common.cuh).
@@ -132,6 +135,68 @@ struct DecodeWindowLaunch {
   int sm_count;
 };
 cudaError_t launch_decode_window(const DecodeWindowLaunch& n, cudaStream_t stream);
+
+// 4-bit pool: quantising cache write; decode, stage 1, or whole where S == 1 and
+// ws is null.
+cudaError_t launch_cache_write_fp4(const void* key, const void* value, int64_t key_stride,
+                                   int64_t value_stride, void* cache, const int64_t* slot_mapping,
+                                   int num_tokens, int num_kv_heads, int head_size, int block_size,
+                                   int num_blocks, float k_scale, float v_scale, int* err,
+                                   cudaStream_t stream);
+struct DecodeFp4Launch {
+  const void* q;
+  const void* cache;
+  const int32_t* block_table;
+  const int32_t* seq_lens;
+  int N, Hq, Hkv, d, bs, num_blocks, max_blocks;
+  float scale, k_scale, v_scale;
+  int S, max_seq_len;
+  float* ws;          // [N, Hq, S, d + 1], or null
+  float* logits;      // [N, Hkv, logit_tokens, Hq / Hkv], or null
+  int logit_tokens;
+  void* out;
+  float* lse;
+  int* err;
+};
+cudaError_t launch_decode_fp4(const DecodeFp4Launch& n, cudaStream_t stream);
+int decode_fp4_splits(int N, int Hkv, int max_seq_len, int sm_count);
+
+// Merge of the splits, and each token's weights (exp2 of its logit less the row's
+// log-sum-exp, summed over the group's heads) added to scores [N, Hkv, score_tokens].
+struct ScoresLaunch {
+  const float* ws;
+  const float* logits;
+  int logit_tokens;
+  const int32_t* seq_lens;
+  int N, Hq, Hkv, d, S, max_seq_len;
+  float* scores;
+  int score_tokens;
+  void* out;
+  float* lse;
+  int* err;
+};
+cudaError_t launch_decode_scores(const ScoresLaunch& n, cudaStream_t stream);
+
+// Eviction by accumulated weights, and the lengths and blocks behind it.
+struct EvictLaunch {
+  void* cache;
+  const int32_t* block_table;
+  const int32_t* seq_lens;
+  const float* scores;
+  float* new_scores;      // may be scores
+  int32_t* new_lens;      // may be seq_lens
+  int32_t* kept;          // [N, Hkv, budget]
+  int32_t* free_blocks;   // nullable
+  const int32_t* free_start;
+  int32_t* new_free_start;
+  int num_free;
+  int N, Hkv, d, bs, num_blocks, max_blocks, score_tokens, budget, recent, first;
+  bool four;              // 4-bit pool; else rows of row_bytes in the standard layout
+  int row_bytes;
+  int* err;
+  int sm_count;
+};
+cudaError_t launch_evict(const EvictLaunch& n, cudaStream_t stream);
 
 // Step plan: query_start_loc, seq_lens, positions, slot_mapping and new table
 // entries from the requests' lengths.

@@ -1,0 +1,148 @@
+// Split-KV decode, stage 2, with the weights' sums: the LSE merge of the split
+// partials (as merge.cu), and for each cached token p of request i and kv head h
+//   scores[i][h][p] += sum over the group's heads g of exp(x_g[p] - lse_g),
+// x the logits that stage 1 left beside its partials.
+//
+// Stage 1 cannot add the weights itself: a token's weight needs the row's whole
+// sum.  What it leaves is 4 bytes for each token and query head, against 144 (4-bit
+// pool) or 512 (bf16) of keys and values for each token and kv head; for most
+// batches they are still in L2 when this kernel reads them.  A token's sum is
+// formed by one thread in the order of the heads: no atomics, the same result every
+// time.
+//
+// CTA 0 of a (request, kv head) merges the outputs, the others take 1024 tokens
+// each.  Every CTA finds the group's log-sum-exps itself from the splits' (at most a
+// few hundred floats, in L2).
+#include <math_constants.h>
+
+#include "pa_common.cuh"
+#include "pa_launch.h"
+
+namespace pa {
+
+namespace {
+
+constexpr int kScoreThreads = 256;
+constexpr int kScoreTokens = 1024;
+constexpr int kMaxGroup = 16;
+
+struct ScoreArgs {
+  const float* ws;
+  const float* logits;
+  const int32_t* seq_lens;
+  float* scores;
+  __nv_bfloat16* out;
+  float* lse;
+  int* err;
+  int S, Hq, Hkv, grp, max_seq_len;
+  int64_t logit_tokens, score_tokens;
+};
+
+// VW: floats of a token's logits per load.
+template <int D, int VW>
+__global__ void __launch_bounds__(kScoreThreads) decode_scores_kernel(
+    const __grid_constant__ ScoreArgs a) {
+  __shared__ float row_m[kMaxGroup], row_l[kMaxGroup], row_x[kMaxGroup];
+  pdl_wait();
+  pdl_trigger();
+  const int kvh = blockIdx.y, i = blockIdx.z, grp = a.grp;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int seq = max(0, a.seq_lens[i]);
+  // Tokens past max_seq_len have no logits.
+  const int end = min(seq, a.max_seq_len);
+  const int first = (static_cast<int>(blockIdx.x) - 1) * kScoreTokens;
+  if (blockIdx.x > 0 && first >= end) return;
+  if (blockIdx.x == 0 && threadIdx.x == 0 && end < seq) record_error(a.err, PA_DEVERR_LENGTH);
+  const float* base = a.ws + (static_cast<int64_t>(i) * a.Hq + kvh * grp) * a.S * (D + 1);
+  for (int r = warp; r < grp; r += kScoreThreads / 32) {
+    const float* p = base + static_cast<int64_t>(r) * a.S * (D + 1) + D;
+    float m = -CUDART_INF_F;
+    for (int s = lane; s < a.S; s += 32) m = fmaxf(m, p[s * (D + 1)]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    float l = 0.f;
+    for (int s = lane; s < a.S; s += 32) {
+      const float x = p[s * (D + 1)];
+      l += x == -CUDART_INF_F ? 0.f : expf(x - m);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    if (lane == 0) {
+      const float x = l == 0.f ? -CUDART_INF_F : m + logf(l);
+      row_m[r] = m, row_l[r] = l, row_x[r] = x;
+      if (blockIdx.x == 0 && a.lse != nullptr)
+        a.lse[static_cast<int64_t>(i) * a.Hq + kvh * grp + r] = x;
+    }
+  }
+  __syncthreads();
+  if (blockIdx.x == 0) {
+    for (int idx = threadIdx.x; idx < grp * D; idx += kScoreThreads) {
+      const int r = idx / D, e = idx % D;
+      const float* p = base + static_cast<int64_t>(r) * a.S * (D + 1);
+      float acc = 0.f;
+#pragma unroll 4
+      for (int s = 0; s < a.S; ++s) {
+        const float x = p[s * (D + 1) + D];
+        acc += (x == -CUDART_INF_F ? 0.f : expf(x - row_m[r])) * p[s * (D + 1) + e];
+      }
+      a.out[(static_cast<int64_t>(i) * a.Hq + kvh * grp + r) * D + e] =
+          __float2bfloat16_rn(row_l[r] == 0.f ? 0.f : acc / row_l[r]);
+    }
+    return;
+  }
+  const int64_t unit = static_cast<int64_t>(i) * a.Hkv + kvh;
+  const float* x = a.logits + unit * a.logit_tokens * grp;
+  float* sums = a.scores + unit * a.score_tokens;
+  const int last = min(end, first + kScoreTokens);
+  for (int tok = first + threadIdx.x; tok < last; tok += kScoreThreads) {
+    const float* p = x + static_cast<int64_t>(tok) * grp;
+    float w = 0.f;
+    for (int g = 0; g < grp; g += VW) {
+      float v[VW];
+      if constexpr (VW == 4) {
+        const float4 q = __ldcs(reinterpret_cast<const float4*>(p + g));
+        v[0] = q.x, v[1] = q.y, v[2] = q.z, v[3] = q.w;
+      } else {
+        v[0] = __ldcs(p + g);
+      }
+#pragma unroll
+      for (int e = 0; e < VW; ++e)
+        // (A row without visible tokens adds nothing.)
+        w += row_x[g + e] == -CUDART_INF_F ? 0.f : fast_exp2(fmaf(-kLog2e, row_x[g + e], v[e]));
+    }
+    sums[tok] += w;
+  }
+}
+
+template <int D, int VW>
+cudaError_t launch_t(const ScoreArgs& a, int N, cudaStream_t stream) {
+  const long long chunks = (static_cast<long long>(a.max_seq_len) + kScoreTokens - 1) / kScoreTokens;
+  return launch_pdl(decode_scores_kernel<D, VW>,
+                    dim3(static_cast<unsigned>(chunks + 1), a.Hkv, N), dim3(kScoreThreads), 0, stream,
+                    a);
+}
+
+}  // namespace
+
+cudaError_t launch_decode_scores(const ScoresLaunch& n, cudaStream_t stream) {
+  ScoreArgs a{};
+  a.ws = n.ws;
+  a.logits = n.logits;
+  a.seq_lens = n.seq_lens;
+  a.scores = n.scores;
+  a.out = static_cast<__nv_bfloat16*>(n.out);
+  a.lse = n.lse;
+  a.err = n.err;
+  a.S = n.S;
+  a.Hq = n.Hq;
+  a.Hkv = n.Hkv;
+  a.grp = n.Hq / n.Hkv;
+  a.max_seq_len = n.max_seq_len;
+  a.logit_tokens = n.logit_tokens;
+  a.score_tokens = n.score_tokens;
+  const bool four = a.grp % 4 == 0;
+  if (n.d == 128) return four ? launch_t<128, 4>(a, n.N, stream) : launch_t<128, 1>(a, n.N, stream);
+  return four ? launch_t<64, 4>(a, n.N, stream) : launch_t<64, 1>(a, n.N, stream);
+}
+
+}  // namespace pa
