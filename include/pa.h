@@ -657,6 +657,30 @@ pa_status pa_evict_fp4(void* kv_cache, const pa_shape* shape, const int32_t* blo
                        int32_t* kept, int32_t* free_blocks, int num_free,
                        const int32_t* free_start, int32_t* new_free_start, void* stream);
 
+/*
+ * Causal attention over whole prompts that are packed one after another, without a
+ * pool: with rows query_start_loc[i] .. query_start_loc[i + 1] - 1 the prompt i, row
+ * j of it sees its rows <= j,
+ *   out[t, h] = softmax(scale * q[t, h] . K) V,  lse[t, h] natural log,
+ * q head h with kv head h / (Hq / Hkv).  For prompts whose keys and values are at
+ * hand (a projection's output, rotated or not): they may be kept in 8 or 4 bits
+ * afterwards, or not at all.
+ * q: [total_q, Hq, d], key and value: [total_q, Hkv, d] bf16, with q_stride,
+ * key_stride, value_stride elements from token to token (dense heads; multiples of 8,
+ * at least H * d): views of one packed projection need no copy.  out: [total_q, Hq, d]
+ * bf16, dense, overlapping no input (PA_ERR_INVALID); lse: [total_q, Hq] fp32, nullable.
+ * max_query_len >= every prompt's length: rows of a prompt past it, and rows of no
+ * prompt, are not written.  Prompts of length 0 are fine.  Keys and values of a
+ * prompt's own rows must be finite; what lies between or behind the prompts may hold
+ * anything.  scale > 0, scale * log2(e) finite in fp32.
+ * Supported: head_size in {64, 128}, Hq / Hkv <= 128.  Data pointers 16-byte aligned.
+ */
+pa_status pa_prompt_fwd(const void* q, const void* key, const void* value, int64_t q_stride,
+                        int64_t key_stride, int64_t value_stride, const int32_t* query_start_loc,
+                        int num_seqs, int total_q, int max_query_len, int num_q_heads,
+                        int num_kv_heads, int head_size, float scale, void* out, float* lse,
+                        void* stream);
+
 /* Size of the fixed device array pa_decode_noalloc keeps its split partials in. */
 #define PA_NOALLOC_WORKSPACE_BYTES (16u * 1024u * 1024u)
 

@@ -118,6 +118,8 @@ def lib() -> ctypes.CDLL:
                                            P, P]
         L.pa_evict.argtypes = [P, SP, i32, P, P, P, i32, i32, i32, i32, P, P, P, P, i32, P, P, P]
         L.pa_evict_fp4.argtypes = [P, SP, P, P, P, i32, i32, i32, i32, P, P, P, P, i32, P, P, P]
+        L.pa_prompt_fwd.argtypes = [P, P, P, i64, i64, i64, P, i32, i32, i32, i32, i32, i32, f32, P,
+                                    P, P]
         L.pa_status_string.argtypes = [st]
         L.pa_status_string.restype = ctypes.c_char_p
         L.pa_get_device_error.argtypes = [ctypes.POINTER(ctypes.c_int), P]
@@ -130,7 +132,8 @@ def lib() -> ctypes.CDLL:
                      "pa_mla_prefill", "pa_plan_step", "pa_qk_norm_rope_cache",
                      "pa_qk_norm_rope_cache_fp8", "pa_varlen_fwd_sinks", "pa_decode_window",
                      "pa_decode_window_fp8", "pa_reshape_and_cache_fp4", "pa_decode_fp4",
-                     "pa_decode_scores", "pa_decode_scores_fp4", "pa_evict", "pa_evict_fp4"):
+                     "pa_decode_scores", "pa_decode_scores_fp4", "pa_evict", "pa_evict_fp4",
+                     "pa_prompt_fwd"):
             getattr(L, name).restype = st
         _lib = L
         return L
@@ -156,7 +159,7 @@ def _binding():
                 L.pa_varlen_fwd_sinks, L.pa_decode_window, L.pa_decode_window_fp8)))
             m.bind_more(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
                 L.pa_reshape_and_cache_fp4, L.pa_decode_fp4, L.pa_decode_scores,
-                L.pa_decode_scores_fp4, L.pa_evict, L.pa_evict_fp4)))
+                L.pa_decode_scores_fp4, L.pa_evict, L.pa_evict_fp4, L.pa_prompt_fwd)))
             _steps = m
     return _steps
 
@@ -845,6 +848,24 @@ def pa_evict_fp4(kv_cache, block_table, seq_lens, scores, budget, num_recent=0, 
     return _evict("pa_evict_fp4", True, kv_cache, block_table, seq_lens, scores, budget,
                   num_recent, num_first, new_lens, new_scores, kept, free_blocks, free_start,
                   new_free_start, stream)
+
+
+def pa_prompt_fwd(q, key, value, query_start_loc, max_query_len, scale, out=None, lse=None,
+                  return_lse=True, stream=None):
+    """Causal attention over whole prompts packed one after another, without a pool:
+    q [T, Hq, d], key and value [T, Hkv, d] bf16 (views of one packed projection will
+    do: dense heads, any token stride that is a multiple of 8), ``query_start_loc``
+    [N + 1] int32.  Returns (out [T, Hq, d] bf16, lse [T, Hq] fp32 or None)."""
+    if out is None:
+        out = _new(stream, q, "q", slice(None), torch.bfloat16)
+    if lse is None and return_lse:
+        lse = _new(stream, q, "q", slice(0, 2), torch.float32)
+    rc = (_steps or _binding()).prompt_fwd(
+        q, key, value, query_start_loc, max_query_len, scale, out, lse,
+        None if stream is None else _stream(stream))
+    if rc:
+        _check(rc, "pa_prompt_fwd")
+    return out, lse
 
 
 PA_NOALLOC_WORKSPACE_BYTES = 16 * 1024 * 1024

@@ -135,6 +135,7 @@ decltype(&pa_decode_scores) scores_fn;
 decltype(&pa_decode_scores_fp4) scores_fp4_fn;
 decltype(&pa_evict) evict_fn;
 decltype(&pa_evict_fp4) evict_fp4_fn;
+decltype(&pa_prompt_fwd) prompt_fn;
 
 // The library call itself, without the interpreter's lock: a launch waits where
 // the stream's queue is full, and what it waits for may need another thread of the
@@ -190,13 +191,14 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
 }
 
 PyObject* bind_more(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded(n, 6, [&]() -> PyObject* {
+  return guarded(n, 7, [&]() -> PyObject* {
     write_fp4_fn = reinterpret_cast<decltype(write_fp4_fn)>(pointer(a[0]));
     decode_fp4_fn = reinterpret_cast<decltype(decode_fp4_fn)>(pointer(a[1]));
     scores_fn = reinterpret_cast<decltype(scores_fn)>(pointer(a[2]));
     scores_fp4_fn = reinterpret_cast<decltype(scores_fp4_fn)>(pointer(a[3]));
     evict_fn = reinterpret_cast<decltype(evict_fn)>(pointer(a[4]));
     evict_fp4_fn = reinterpret_cast<decltype(evict_fp4_fn)>(pointer(a[5]));
+    prompt_fn = reinterpret_cast<decltype(prompt_fn)>(pointer(a[6]));
     Py_RETURN_NONE;
   });
 }
@@ -567,6 +569,33 @@ PyObject* evict(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// (q, key, value, query_start_loc, max_query_len, scale, out, lse | None, stream | None)
+PyObject* prompt_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 9, [&]() -> PyObject* {
+    const at::Tensor& q = tensor(a[0], "q");
+    const at::Tensor& key = tensor(a[1], "key");
+    const at::Tensor& qsl = tensor(a[3], "query_start_loc");
+    if (q.dim() != 3) refuse(PyExc_ValueError, "q must be [total_q, num_q_heads, head_size]");
+    if (key.dim() != 3)
+      refuse(PyExc_ValueError, "key must be [total_q, num_kv_heads, head_size]");
+    if (qsl.dim() != 1 || qsl.size(0) < 1)
+      refuse(PyExc_ValueError, "query_start_loc must be [num_seqs + 1]");
+    const int64_t tokens = q.size(0), heads = q.size(1), kv = key.size(1), d = q.size(2);
+    const int dev = call_device(q, "q");
+    int64_t qs, ks, vs;
+    void* qp = token_rows(a[0], "q", tokens, heads, d, dev, &qs);
+    void* kp = token_rows(a[1], "key", tokens, kv, d, dev, &ks);
+    void* vp = token_rows(a[2], "value", tokens, kv, d, dev, &vs);
+    void* sp = dense(qsl, "query_start_loc", at::kInt, dev);
+    void* out = shaped(a[6], "out", at::kBFloat16, dev, {tokens, heads, d});
+    void* lse = a[7] == Py_None ? nullptr : shaped(a[7], "lse", at::kFloat, dev, {tokens, heads});
+    return call(prompt_fn, qp, kp, vp, qs, ks, vs, static_cast<int32_t*>(sp),
+                extent(qsl.size(0) - 1, "query_start_loc"), extent(tokens, "q"),
+                integer32(a[4], "max_query_len"), extent(heads, "q"), extent(kv, "key"),
+                extent(d, "q"), real(a[5]), out, static_cast<float*>(lse), stream_of(a[8], dev));
+  });
+}
+
 template <class F>
 PyCFunction fast(F f) {
   return reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f));
@@ -580,6 +609,7 @@ PyMethodDef methods[] = {
     {"decode_scores", fast(decode_scores), METH_FASTCALL,
      "pa_decode_scores, with scales pa_decode_fp4 or pa_decode_scores_fp4"},
     {"evict", fast(evict), METH_FASTCALL, "pa_evict, pa_evict_fp4"},
+    {"prompt_fwd", fast(prompt_fwd), METH_FASTCALL, "pa_prompt_fwd"},
     {"plan_step", fast(plan_step), METH_FASTCALL, "pa_plan_step"},
     {"norm_rope", fast(norm_rope), METH_FASTCALL, "pa_qk_norm_rope_cache, with scales _fp8"},
     {"varlen_sinks", fast(varlen_sinks), METH_FASTCALL, "pa_varlen_fwd_sinks"},

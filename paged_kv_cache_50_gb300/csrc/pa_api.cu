@@ -329,6 +329,60 @@ pa_status pa_varlen_fwd_sinks(const void* q, const void* kv_cache, const int32_t
   return from_cuda(pa::launch_window_prefill(n, static_cast<cudaStream_t>(stream)));
 }
 
+pa_status pa_prompt_fwd(const void* q, const void* key, const void* value, int64_t q_stride,
+                        int64_t key_stride, int64_t value_stride, const int32_t* query_start_loc,
+                        int num_seqs, int total_q, int max_query_len, int num_q_heads,
+                        int num_kv_heads, int head_size, float scale, void* out, float* lse,
+                        void* stream) {
+  if (num_seqs < 0 || num_seqs > kMaxGridYZ || total_q < 0 || max_query_len < 0 ||
+      num_q_heads <= 0 || num_kv_heads <= 0 || num_kv_heads > kMaxGridYZ || head_size <= 0 ||
+      num_q_heads % num_kv_heads != 0 || !logit_scale_ok(scale, 1.f))
+    return PA_ERR_INVALID;
+  if ((head_size != 64 && head_size != 128) || num_q_heads / num_kv_heads > 128)
+    return PA_ERR_UNSUPPORTED;
+  const int64_t qw = static_cast<int64_t>(num_q_heads) * head_size;
+  const int64_t kw = static_cast<int64_t>(num_kv_heads) * head_size;
+  // (A tensor map's strides are below 2^40 bytes.)
+  constexpr int64_t kMost = 1LL << 38;
+  if (q_stride < qw || key_stride < kw || value_stride < kw || q_stride % 8 != 0 ||
+      key_stride % 8 != 0 || value_stride % 8 != 0 || q_stride > kMost || key_stride > kMost ||
+      value_stride > kMost)
+    return PA_ERR_INVALID;
+  if (num_seqs == 0 || total_q == 0 || max_query_len == 0) return PA_OK;
+  if (q == nullptr || key == nullptr || value == nullptr || query_start_loc == nullptr ||
+      out == nullptr)
+    return PA_ERR_INVALID;
+  if (!aligned(q, 16) || !aligned(key, 16) || !aligned(value, 16) || !aligned(out, 16) ||
+      !aligned(lse, 4) || !aligned(query_start_loc, 4))
+    return PA_ERR_INVALID;
+  auto rows = [&](const void* p, int64_t stride, int64_t width) {
+    return Range{p, static_cast<size_t>((total_q - 1) * stride + width) * 2};   // bf16
+  };
+  const Range o = rows(out, qw, qw);
+  if (overlap(o, rows(q, q_stride, qw)) || overlap(o, rows(key, key_stride, kw)) ||
+      overlap(o, rows(value, value_stride, kw)))
+    return PA_ERR_INVALID;
+  pa::PromptLaunch n{};
+  n.q = q;
+  n.key = key;
+  n.value = value;
+  n.q_stride = q_stride;
+  n.key_stride = key_stride;
+  n.value_stride = value_stride;
+  n.qsl = query_start_loc;
+  n.N = num_seqs;
+  n.Hq = num_q_heads;
+  n.Hkv = num_kv_heads;
+  n.d = head_size;
+  n.total_q = total_q;
+  n.max_query_len = max_query_len;
+  n.scale = scale;
+  n.out = out;
+  n.lse = lse;
+  n.err = device_error_ptr();
+  return from_cuda(pa::launch_prompt(n, static_cast<cudaStream_t>(stream)));
+}
+
 int pa_cascade_prefix_splits(int total_q, int num_q_heads, int num_kv_heads,
                              int prefix_tokens, int sm_count) {
   if (total_q <= 0 || num_q_heads <= 0 || num_kv_heads <= 0 || prefix_tokens <= 0) return 1;

@@ -119,6 +119,21 @@ struct WindowPrefillLaunch {
 };
 cudaError_t launch_window_prefill(const WindowPrefillLaunch& n, cudaStream_t stream);
 
+// Causal attention over packed prompts (Hq / Hkv <= 128).
+struct PromptLaunch {
+  const void* q;
+  const void* key;
+  const void* value;
+  int64_t q_stride, key_stride, value_stride;   // elements from token to token
+  const int32_t* qsl;
+  int N, Hq, Hkv, d, total_q, max_query_len;
+  float scale;
+  void* out;    // bf16 [T, Hq, d]
+  float* lse;   // [T, Hq], nullable
+  int* err;
+};
+cudaError_t launch_prompt(const PromptLaunch& n, cudaStream_t stream);
+
 // Decode with a sliding window and first tokens that stay visible, bf16 or
 // e4m3 pool, in one launch.
 struct DecodeWindowLaunch {
