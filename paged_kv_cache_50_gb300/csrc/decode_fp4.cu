@@ -435,7 +435,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) decode_fp4_kernel(c
     } else {
       float* dst = a.ws + ((row0 + r) * a.S + s) * (D + 1);
       dst[e] = y;
-      if (e == 0) dst[D] = ls;
+      // (A NaN row is handed on as +inf, whose weight in the merge is NaN: a maximum
+      // would pass over a NaN.)
+      if (e == 0) dst[D] = ls == ls ? ls : CUDART_INF_F;
     }
   }
 }
