@@ -1,19 +1,28 @@
-// Decode attention over a 4-bit pool (layout: fp4.cuh), stage 1 of two, or alone
-// where the context is not split: o = softmax(scale q K^T) V for one query per
-// request, with K, V = code * scale * k_scale (v_scale).
+// Decode attention over a 4-bit pool (layout: fp4.cuh): o = softmax(scale q K^T) V
+// for one query per request, with K, V = code * scale * k_scale (v_scale).
 //
-// One CTA serves one (split, kv head, request): a producer warp fetches the
-// split's tokens, 16 at a time (keys, values and their scales are one run of 18 d
-// bytes: one bulk copy), into a ring of stages of 32 tokens for each of eight
-// consumer warps.  A consumer warp takes its 32 tokens of a stage as two M = 16
-// tiles of mma.m16n8k16 with the group's query heads as N (8 per n-tile): S^T = K
-// Q^T, one online softmax step over the 32 tokens (two thirds of the shuffles of
-// two steps over 16), O^T += V^T P^T.  Codes are widened to f16 and multiplied by
-// their scales on the way into operand registers (exact); q and the weights are f16.
+// The work is one line of 16-token pieces: request by request, kv head by kv head,
+// token by token.  It is cut into as many equal parts as CTAs are resident, whatever
+// the lengths: a CTA finds its part from the lengths' sum (a scan), and walks over
+// the (request, kv head) units in it.  A unit that lies in one part gives its output
+// at once; of one that is cut the CTAs leave states (o, maximum, sum), which a second
+// kernel merges: two per CTA at most, however long the context.  (One CTA per unit and
+// split, dealt by the hardware, left SMs idle for a quarter of the time on 64 requests
+// of U[128, 4096] tokens, and a quarter of the instructions were in CTAs' ends.)
+//
+// A CTA's eight warps take 32 tokens each in turn.  Each fetches its own: two pieces
+// (keys, values and scales of 16 tokens are one run of 18 d bytes: one bulk copy) into
+// a ring of its own, without a barrier shared by warps.  A warp takes its 32 tokens as
+// two M = 16 tiles of mma.m16n8k16 with the group's query heads as N (8 per n-tile):
+// S^T = K Q^T, one online softmax step over the 32 tokens, O^T += V^T P^T.  Codes are
+// widened to f16 and multiplied by their scales on the way into operand registers
+// (exact); q and the weights are f16.  At a unit's end the warps' states are merged
+// pairwise, lane to lane (a lane holds the same heads and dims in all warps), each
+// state through the ring slot that its warp has just read.
 //
 // Bound by issue slots beside HBM: 2304 bytes for 16 tokens (d = 128) pass in 100
-// cycles of an SM, in which it issues 400 warp instructions, and a sub-block needs 64
-// conversions, 64 scalings and 16 MMAs before anything else.
+// cycles of an SM, in which it issues 400 warp instructions, 200 of them on the ALU,
+// and a piece needs 64 conversions (ALU), 64 scalings and 16 MMAs before anything else.
 #include <math_constants.h>
 
 #include <algorithm>
@@ -27,24 +36,29 @@ namespace pa {
 
 namespace {
 
-constexpr int kConsumers = 8;                      // warps
-constexpr int kThreads = 32 * (kConsumers + 1);
-constexpr int kPieces = 2;                         // 16-token pieces of a warp in a stage
+constexpr int kWarps = 8;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kPieces = 2;                   // 16-token pieces of a warp's slice
+constexpr int kSlice = 16 * kPieces;         // tokens
+constexpr int kStage = kSlice * kWarps;      // tokens of all warps' slices
 
 struct Fp4Args {
   const __nv_bfloat16* q;
   const uint8_t* cache;
   const int32_t* block_table;
   const int32_t* seq_lens;
-  int max_blocks, Hq, Hkv, grp, bs, bs_log2, num_blocks;
-  int S, chunk;       // splits, tokens per split (a multiple of 16)
+  int N, max_blocks, Hq, Hkv, grp, bs, bs_log2, num_blocks;
+  int whole;          // units are not cut: their number is dealt, not their tokens
   int positions;      // of a table row, at most INT_MAX - 1023
   float scale_log2;   // scale * k_scale * log2(e)
   float out_scale;    // v_scale
-  float* ws;          // [N, Hq, S, d + 1], unused where S == 1 and no logits
+  float* parts;       // [CTA][2][grp][d + 2] states of cut units
+  int4* cut;          // [CTA]: (first CTA, request, kv head) of the unit whose end it holds
+  int2* spans;        // [N, Hkv] first and last CTA of a unit, or null
+  float* row_lse;     // [N, Hq] of units that are not cut, with spans
   float* logits;      // [N, Hkv, logit_tokens, grp] (log2 units), or null
   int logit_tokens;
-  __nv_bfloat16* out; // S == 1
+  __nv_bfloat16* out;
   float* lse;
   int* err;
 };
@@ -52,20 +66,16 @@ struct Fp4Args {
 template <int D, int NT>
 struct Fp4Cfg {
   static constexpr int kPairBytes = 2 * fp4::tile_bytes(D);
-  static constexpr int kStageBytes = kConsumers * kPieces * kPairBytes;
-  // Two CTAs per SM.
-  static constexpr int kStages = D == 128 ? 3 : 6;
-  static constexpr int kRingBytes = kStages * kStageBytes;
-  static constexpr int kHeads = 8 * NT;
-  // Rows of the merge buffer: places d + d / 16, an odd number of words apart for
-  // the eight dims that a warp's lanes store at once.
-  static constexpr int kOStride = D == 128 ? 164 : 68;
-  static constexpr int kMergeBytes = kConsumers * kHeads * (kOStride + 2) * 4;
-  static constexpr int kDataBytes = kRingBytes > kMergeBytes ? kRingBytes : kMergeBytes;
-  static constexpr int kOffBar = kDataBytes;              // full[stage], empty[stage]
-  static constexpr int kOffValid = kOffBar + 16 * kStages;   // pieces loaded, a word per stage
-  static constexpr int kSmemBytes = kOffValid + 4 * kStages + 128;
-  __device__ static __forceinline__ int place(int dim) { return dim + (dim >> 4); }
+  static constexpr int kSlotBytes = kPieces * kPairBytes;
+  static constexpr int kCtas = NT == 1 ? 2 : 1;                    // per SM
+  static constexpr int kSlots = (D == 128 ? 3 : 6) * (2 / kCtas);  // of a warp's ring
+  static constexpr int kRingBytes = kWarps * kSlots * kSlotBytes;
+  // A lane's o of one n-tile (D / 4 floats) passes through a slot.
+  static_assert(D / 4 * 128 <= kSlotBytes, "a state's o fits a slot");
+  static constexpr int kOffStats = kRingBytes;                     // [warp][NT][lane] float4
+  static constexpr int kOffBar = kOffStats + kWarps * 32 * 16 * NT;
+  static constexpr int kOffScan = kOffBar + 8 * kWarps * kSlots;
+  static constexpr int kSmemBytes = kOffScan + 128;
 };
 
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
@@ -104,101 +114,198 @@ __device__ __forceinline__ void lds_words(uint32_t a, uint32_t (&w)[N]) {
     asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[0]) : "r"(a));
 }
 
+// Where a CTA (or a warp's fetches, ahead of it) stands in its part of the line.
+struct Walk {
+  int i, h;            // unit
+  int seq, after;      // tokens of request i and of request i + 1
+  int tok, end;        // its tokens in this part
+  long long left;      // pieces (whole: units) of the part from here on
+};
+
+__device__ __forceinline__ int length_of(const Fp4Args& a, int i) {
+  // What lies past the table's columns has no block and is not walked over.
+  return i < a.N ? min(max(0, a.seq_lens[i]), a.positions) : 0;
+}
+// The share of the unit from token `tok` on.
+__device__ __forceinline__ void walk_enter(const Fp4Args& a, Walk& w, int tok) {
+  w.tok = tok;
+  if (a.whole) {
+    w.end = w.seq;
+  } else {
+    const int pieces = (w.seq - tok + 15) >> 4;
+    w.end = w.left < pieces ? tok + 16 * static_cast<int>(w.left) : w.seq;
+  }
+}
+// On to the next unit with tokens; false at the part's end.
+__device__ __forceinline__ bool walk_next(const Fp4Args& a, Walk& w) {
+  w.left -= a.whole ? 1 : (w.end - w.tok + 15) >> 4;
+  if (w.left <= 0) return false;
+  if (++w.h == a.Hkv) {
+    w.h = 0;
+    do {
+      if (++w.i >= a.N) return false;   // (lengths that changed under way)
+      w.seq = w.after;
+      w.after = length_of(a, w.i + 1);
+    } while (w.seq == 0);
+  }
+  walk_enter(a, w, 0);
+  return true;
+}
+
 template <int D, int NT, bool LOGITS>
-__global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) decode_fp4_kernel(const __grid_constant__ Fp4Args a) {
+__global__ void __launch_bounds__(kThreads, Fp4Cfg<D, NT>::kCtas) decode_fp4_kernel(
+    const __grid_constant__ Fp4Args a) {
   using C = Fp4Cfg<D, NT>;
   constexpr int kK = D / 16;          // k-steps of K Q^T = d-tiles of V^T P^T
   constexpr int kWk = D / 32;         // words of a key row in a lane: D / 4 codes
   constexpr int kWv = D / 64;         // words of a value row in a lane: D / 8 codes
   constexpr float kRescale = 8.f;     // log2 units
   extern __shared__ __align__(128) uint8_t smem[];
-  const int s = blockIdx.x, kvh = blockIdx.y, i = blockIdx.z;
+  const int cta = blockIdx.x;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int gid = lane >> 2, tid4 = lane & 3;
   const int grp = a.grp;
-  const uint32_t base = smem_u32(smem);
-  auto full = [&](int st) { return base + C::kOffBar + 16 * st; };
-  auto empty = [&](int st) { return base + C::kOffBar + 16 * st + 8; };
-  volatile uint32_t* valid = reinterpret_cast<volatile uint32_t*>(smem + C::kOffValid);
-
-  if (threadIdx.x == 0) {
+  const uint32_t ring = smem_u32(smem) + warp * C::kSlots * C::kSlotBytes;
+  const uint32_t bars = smem_u32(smem) + C::kOffBar + warp * C::kSlots * 8;
+  if (lane == 0) {
 #pragma unroll
-    for (int st = 0; st < C::kStages; ++st) {
-      tc::mbar_init(full(st), 1);
-      tc::mbar_init(empty(st), kConsumers);
-    }
+    for (int k = 0; k < C::kSlots; ++k) tc::mbar_init(bars + 8 * k, 1);
     tc::fence_barrier_init();
   }
-  __syncthreads();
+  __syncwarp();   // each warp uses its own barriers only
   pdl_wait();
-  const int seq = max(0, a.seq_lens[i]);
-  const int end = min(seq, a.positions);   // what lies past the table's columns has no block
-  if (end < seq && s == 0 && threadIdx.x == 0) record_error(a.err, PA_DEVERR_BLOCK_ID);
-  const long long a0 = static_cast<long long>(s) * a.chunk;
-  const int t0 = static_cast<int>(a0 < end ? a0 : end);
-  const int t1 = static_cast<int>(s == a.S - 1 || a0 + a.chunk > end ? end : a0 + a.chunk);
-  const int pieces = (t1 - t0 + 15) >> 4;
-  const int stages = (pieces + kConsumers * kPieces - 1) / (kConsumers * kPieces);
-  const int64_t row0 = static_cast<int64_t>(i) * a.Hq + kvh * grp;
-  if (pieces == 0 && a.S > 1) {
-    pdl_trigger();
-    for (int idx = threadIdx.x; idx < grp * (D + 1); idx += kThreads) {
-      const int r = idx / (D + 1), e = idx - r * (D + 1);
-      a.ws[((row0 + r) * a.S + s) * (D + 1) + e] = e == D ? -CUDART_INF_F : 0.f;
-    }
-    return;
-  }
+  pdl_trigger();
 
-  float m_r[NT][2], l_r[NT][2], o[NT][kK][4];
+  // ------------------------------------------------------------ the part
+  // A thread sums the pieces of neighbouring requests; the CTA scans the threads' sums.
+  const int chunk = (a.N + kThreads - 1) / kThreads;
+  const int r0 = min(a.N, static_cast<int>(threadIdx.x) * chunk), r1 = min(a.N, r0 + chunk);
+  auto weight = [&](int seq) { return a.whole ? (seq > 0 ? 1 : 0) : (seq + 15) >> 4; };
+  long long mine = 0;
+  for (int i = r0; i < r1; ++i) mine += weight(length_of(a, i));
+  long long upto = mine;
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    m_r[nt][0] = m_r[nt][1] = -CUDART_INF_F;
-    l_r[nt][0] = l_r[nt][1] = 0.f;
-#pragma unroll
-    for (int md = 0; md < kK; ++md)
-      o[nt][md][0] = o[nt][md][1] = o[nt][md][2] = o[nt][md][3] = 0.f;
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += y;
   }
-
-  if (warp == kConsumers) {
-    // ------------------------------------------------------------ producer
-    // Lane l: piece l of a stage (of kConsumers * kPieces); warp w's are w *
-    // kPieces, ....  Block ids are read a stage ahead.
-    const int32_t* table = a.block_table + static_cast<int64_t>(i) * a.max_blocks;
-    const bool box = lane < kConsumers * kPieces;
-    auto lookup = [&](int st) {
-      const int p = st * (kConsumers * kPieces) + lane;
-      // (A plain load: the table may be the previous kernel's output.)
-      return box && p < pieces ? table[div_bs(t0 + 16 * p, a.bs, a.bs_log2)] : -1;
-    };
-    int blk = lookup(0);
-    for (int st = 0; st < stages; ++st) {
-      const int next = st + 1 < stages ? lookup(st + 1) : -1;
-      const int at = st % C::kStages, use = st / C::kStages;
-      if (use > 0 && !__all_sync(0xffffffffu, tc::mbar_wait(empty(at), (use - 1) & 1))) {
-        if (lane == 0) record_error(a.err, PA_DEVERR_TIMEOUT);
-        break;
-      }
-      const int p = st * (kConsumers * kPieces) + lane;
-      const bool mine = box && p < pieces;
-      const bool good = mine && blk >= 0 && blk < a.num_blocks;
-      const unsigned loaded = __ballot_sync(0xffffffffu, good);
-      const unsigned bad = __ballot_sync(0xffffffffu, mine && !good);
-      if (lane == 0) {
-        if (bad != 0u) record_error(a.err, PA_DEVERR_BLOCK_ID);
-        valid[at] = loaded;
-        tc::mbar_arrive_expect_tx(full(at), __popc(loaded) * C::kPairBytes);
-      }
-      __syncwarp();
-      if (good) {
-        const int tok = t0 + 16 * p;
-        const int g = mod_bs(tok, a.bs, a.bs_log2) >> 4;
-        bulk_load(base + at * C::kStageBytes + lane * C::kPairBytes,
-                  a.cache + fp4::pair_at(blk, kvh, g, a.Hkv, a.bs >> 4, D), C::kPairBytes, full(at));
-      }
-      blk = next;
+  long long* scan = reinterpret_cast<long long*>(smem + C::kOffScan);
+  if (lane == 31) scan[warp] = upto;
+  __syncthreads();
+  long long total = 0, before = upto - mine;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) before += scan[w];
+    total += scan[w];
+  }
+  __syncthreads();
+  total *= a.Hkv;
+  before *= a.Hkv;
+  // Parts of equal length, in whole slices.
+  long long share = (total + gridDim.x - 1) / gridDim.x;
+  if (!a.whole) share = (share + kPieces - 1) / kPieces * kPieces;
+  const long long g0 = cta * share, g1 = min(total, g0 + share);
+  if (threadIdx.x == 0) scan[0] = -1;
+  __syncthreads();
+  if (g0 >= before && g0 < before + mine * a.Hkv && g0 < g1) {
+    // The unit that g0 lies in is among this thread's requests.
+    int i = r0;
+    long long at = before;
+    for (; i + 1 < r1; ++i) {
+      const long long n = static_cast<long long>(weight(length_of(a, i))) * a.Hkv;
+      if (g0 < at + n) break;
+      at += n;
     }
-  } else {
-    // ------------------------------------------------------------ consumers
+    scan[0] = i;
+    scan[1] = g0 - at;
+  }
+  __syncthreads();
+  const bool any = scan[0] >= 0;
+  const int first_request = static_cast<int>(scan[0]);
+  const long long inside = scan[1];   // pieces of that request's units before the part
+  if (cta == 0 && threadIdx.x < 32) {
+    bool past = false;
+    for (int i = lane; i < a.N; i += 32) past |= a.seq_lens[i] > a.positions;
+    if (past) record_error(a.err, PA_DEVERR_BLOCK_ID);
+  }
+  // Requests without tokens.
+  for (int i = cta; i < a.N; i += gridDim.x)
+    if (length_of(a, i) == 0) {
+      for (int k = threadIdx.x; k < a.Hq * D; k += kThreads)
+        a.out[static_cast<int64_t>(i) * a.Hq * D + k] = __float2bfloat16_rn(0.f);
+      if (a.lse != nullptr)
+        for (int k = threadIdx.x; k < a.Hq; k += kThreads)
+          a.lse[static_cast<int64_t>(i) * a.Hq + k] = -CUDART_INF_F;
+    }
+  if (a.cut != nullptr && threadIdx.x == 0) a.cut[cta] = make_int4(-1, 0, 0, 0);
+  if (!any) return;
+  Walk at, ahead;
+  at.i = first_request;
+  at.seq = length_of(a, at.i);
+  at.after = length_of(a, at.i + 1);
+  at.left = g1 - g0;
+  {
+    const int n = weight(at.seq);
+    at.h = static_cast<int>(inside / n);
+    walk_enter(a, at, a.whole ? 0 : 16 * static_cast<int>(inside - static_cast<long long>(at.h) * n));
+  }
+  ahead = at;
+  long long pos = g0;   // of the unit's first token in this part
+
+  // ------------------------------------------------------------ fetches
+  int fetch_tok = ahead.tok + warp * kSlice;
+  bool more = true;
+  auto settle = [&]() {   // on to the next slice that is there
+    while (more && fetch_tok >= ahead.end) {
+      more = walk_next(a, ahead);
+      if (more) fetch_tok = ahead.tok + warp * kSlice;
+    }
+  };
+  auto lookup = [&]() {
+    const int tok = fetch_tok + 16 * lane;
+    // (A plain load: the table may be the previous kernel's output.)
+    return more && lane < kPieces && tok < ahead.end
+               ? a.block_table[static_cast<int64_t>(ahead.i) * a.max_blocks +
+                               div_bs(tok, a.bs, a.bs_log2)]
+               : -1;
+  };
+  settle();
+  int blk = lookup();      // of the next slice to be fetched
+  int fill = 0;            // its slot
+  uint32_t loaded = 0;     // kPieces bits per slot: pieces that are there
+  bool ok = true;          // (a warp that gave up fetches no more, and goes on to the barriers)
+  int flying = 0;          // slices on their way
+  auto fetch = [&]() {
+    if (!more || !ok) return;
+    const int tok = fetch_tok + 16 * lane;
+    const bool piece = lane < kPieces && tok < ahead.end;
+    const bool good = piece && blk >= 0 && blk < a.num_blocks;
+    const unsigned there = __ballot_sync(0xffffffffu, good);
+    if (__any_sync(0xffffffffu, piece && !good) && lane == 0) record_error(a.err, PA_DEVERR_BLOCK_ID);
+    loaded = (loaded & ~(3u << (kPieces * fill))) | (there << (kPieces * fill));
+    const uint32_t bar = bars + 8 * fill;
+    if (lane == 0) tc::mbar_arrive_expect_tx(bar, __popc(there) * C::kPairBytes);
+    __syncwarp();
+    if (good) {
+      const int g = mod_bs(tok, a.bs, a.bs_log2) >> 4;
+      bulk_load(ring + fill * C::kSlotBytes + lane * C::kPairBytes,
+                a.cache + fp4::pair_at(blk, ahead.h, g, a.Hkv, a.bs >> 4, D), C::kPairBytes, bar);
+    }
+    if (++fill == C::kSlots) fill = 0;
+    ++flying;
+    fetch_tok += kStage;
+    settle();
+    blk = lookup();
+  };
+  for (int k = 0; k < C::kSlots; ++k) fetch();
+
+  // Source lanes of the P^T operand (tokens 2 tid4 and 2 tid4 + 1 of head gid).
+  const int src_a = 8 * tid4 + (gid >> 1), src_b = src_a + 4;
+  const uint32_t sel = (gid & 1) ? 0x7632u : 0x5410u;
+  int slot = 0, parity = 0;   // of the slice worked on
+  for (bool live = true; live;) {
+    // ---------------------------------------------------------- one unit
+    const int64_t row0 = static_cast<int64_t>(at.i) * a.Hq + at.h * grp;
     uint32_t qf[NT][kK][2];
     {
       const __nv_bfloat16* qb = a.q + row0 * D;
@@ -216,256 +323,402 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) decode_fp4_kernel(c
         }
       }
     }
-    // Source lanes of the P^T operand (tokens 2 tid4 and 2 tid4 + 1 of head gid).
-    const int src_a = 8 * tid4 + (gid >> 1), src_b = src_a + 4;
-    const uint32_t sel = (gid & 1) ? 0x7632u : 0x5410u;
-    bool ok = true;
-    for (int st = 0; st < stages; ++st) {
-      const int at = st % C::kStages;
-      if (!__all_sync(0xffffffffu, tc::mbar_wait(full(at), (st / C::kStages) & 1))) {
-        ok = false;
-        break;
-      }
-      const int p0 = st * (kConsumers * kPieces) + warp * kPieces;
-      const uint32_t here = valid[at] >> (warp * kPieces);
+    float m_r[NT][2], l_r[NT][2], o[NT][kK][4];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      m_r[nt][0] = m_r[nt][1] = -CUDART_INF_F;
+      l_r[nt][0] = l_r[nt][1] = 0.f;
+#pragma unroll
+      for (int md = 0; md < kK; ++md)
+        o[nt][md][0] = o[nt][md][1] = o[nt][md][2] = o[nt][md][3] = 0.f;
+    }
+    int own = -1;   // the slot that the state may pass through
+    for (int tb = at.tok + warp * kSlice; tb < at.end; tb += kStage) {
+      ok = ok && __all_sync(0xffffffffu, tc::mbar_wait(bars + 8 * slot, parity));
+      if (!ok) continue;
+      const uint32_t here = loaded >> (kPieces * slot);
       // Visible tokens of each piece.
       int lim[kPieces];
 #pragma unroll
       for (int p = 0; p < kPieces; ++p)
-        lim[p] = (here >> p) & 1u ? min(16, t1 - (t0 + 16 * (p0 + p))) : 0;
-      // (Logits are written for every token, also where a block is missing.)
-      if (lim[0] > 0 || lim[1] > 0 || (LOGITS && p0 < pieces)) {
-        const uint32_t pair = base + at * C::kStageBytes + warp * kPieces * C::kPairBytes;
-        // S^T = K Q^T: rows = tokens gid, gid + 8; columns = heads.
-        float x[kPieces][NT][4];
+        lim[p] = (here >> p) & 1u ? min(16, at.end - (tb + 16 * p)) : 0;
+      const uint32_t pair = ring + slot * C::kSlotBytes;
+      const bool whole = lim[0] == 16 && lim[1] == 16;
+      // S^T = K Q^T: rows = tokens gid, gid + 8; columns = heads.
+      float x[kPieces][NT][4];
 #pragma unroll
-        for (int p = 0; p < kPieces; ++p) {
-          const uint32_t kb = pair + p * C::kPairBytes, ks = kb + 8 * D;
-          uint32_t k0[kWk], k1[kWk], s0[kK / 4], s1[kK / 4];
-          lds_words(kb + gid * (D / 2) + tid4 * (D / 8), k0);
-          lds_words(kb + (gid + 8) * (D / 2) + tid4 * (D / 8), k1);
-          if constexpr (D == 128) {
-            const uint32_t c0 = fp4::widen_scales(lds_u16(ks + gid * 8 + tid4 * 2));
-            const uint32_t c1 = fp4::widen_scales(lds_u16(ks + (gid + 8) * 8 + tid4 * 2));
-            s0[0] = fp4::both_low(c0), s0[1] = fp4::both_high(c0);
-            s1[0] = fp4::both_low(c1), s1[1] = fp4::both_high(c1);
-          } else {
-            s0[0] = fp4::both_low(fp4::widen_scales(lds_u8(ks + gid * 4 + tid4)));
-            s1[0] = fp4::both_low(fp4::widen_scales(lds_u8(ks + (gid + 8) * 4 + tid4)));
+      for (int p = 0; p < kPieces; ++p) {
+        const uint32_t kb = pair + p * C::kPairBytes, ks = kb + 8 * D;
+        uint32_t k0[kWk], k1[kWk], s0[kK / 4], s1[kK / 4];
+        lds_words(kb + gid * (D / 2) + tid4 * (D / 8), k0);
+        lds_words(kb + (gid + 8) * (D / 2) + tid4 * (D / 8), k1);
+        if constexpr (D == 128) {
+          const uint32_t c0 = fp4::widen_scales(lds_u16(ks + gid * 8 + tid4 * 2));
+          const uint32_t c1 = fp4::widen_scales(lds_u16(ks + (gid + 8) * 8 + tid4 * 2));
+          s0[0] = fp4::both_low(c0), s0[1] = fp4::both_high(c0);
+          s1[0] = fp4::both_low(c1), s1[1] = fp4::both_high(c1);
+        } else {
+          s0[0] = fp4::both_low(fp4::widen_scales(lds_u8(ks + gid * 4 + tid4)));
+          s1[0] = fp4::both_low(fp4::widen_scales(lds_u8(ks + (gid + 8) * 4 + tid4)));
+        }
+        float s2[NT][2][4];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            s2[nt][h][0] = s2[nt][h][1] = s2[nt][h][2] = s2[nt][h][3] = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWk; ++w) {
+          uint32_t f0[4], f1[4];
+          fp4::widen8(k0[w], f0);
+          fp4::widen8(k1[w], f1);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t am[4] = {
+                fp4::mul2(f0[2 * h], s0[w / 2]), fp4::mul2(f1[2 * h], s1[w / 2]),
+                fp4::mul2(f0[2 * h + 1], s0[w / 2]), fp4::mul2(f1[2 * h + 1], s1[w / 2])};
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+              mma_f16_16816(s2[nt][h], am, qf[nt][2 * w + h][0], qf[nt][2 * w + h][1]);
           }
-          float s2[NT][2][4];
+        }
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-              s2[nt][h][0] = s2[nt][h][1] = s2[nt][h][2] = s2[nt][h][3] = 0.f;
+          for (int e = 0; e < 4; ++e)
+            x[p][nt][e] = (s2[nt][0][e] + s2[nt][1][e]) * a.scale_log2;
+      }
+      if (!whole) {
 #pragma unroll
-          for (int w = 0; w < kWk; ++w) {
-            uint32_t f0[4], f1[4];
-            fp4::widen8(k0[w], f0);
-            fp4::widen8(k1[w], f1);
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const uint32_t am[4] = {
-                  fp4::mul2(f0[2 * h], s0[w / 2]), fp4::mul2(f1[2 * h], s1[w / 2]),
-                  fp4::mul2(f0[2 * h + 1], s0[w / 2]), fp4::mul2(f1[2 * h + 1], s1[w / 2])};
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt)
-                mma_f16_16816(s2[nt][h], am, qf[nt][2 * w + h][0], qf[nt][2 * w + h][1]);
-            }
-          }
-          const bool v0 = gid < lim[p], v1 = gid + 8 < lim[p];
+        for (int p = 0; p < kPieces; ++p)
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              x[p][nt][e] = (e < 2 ? v0 : v1) ? (s2[nt][0][e] + s2[nt][1][e]) * a.scale_log2
-                                              : -CUDART_INF_F;
-          if constexpr (LOGITS) {
-            const int tok = t0 + 16 * (p0 + p) + gid;
-            float* dst = a.logits + ((static_cast<int64_t>(i) * a.Hkv + kvh) * a.logit_tokens + tok) * grp;
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const int h = nt * 8 + 2 * tid4 + (e & 1);
-                if (h < grp && tok + 8 * (e >> 1) < min(t1, a.logit_tokens))
-                  dst[8 * (e >> 1) * grp + h] = x[p][nt][e];
-              }
-          }
-        }
-        // Online softmax in the log2 domain; the reference maximum moves only when
-        // the 32 tokens' exceeds it by more than kRescale, so that weights stay < 2^8.
-        uint32_t pb[kPieces][NT][2];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          float pr[kPieces][4];
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            float mx = fmaxf(fmaxf(x[0][nt][j], x[0][nt][2 + j]), fmaxf(x[1][nt][j], x[1][nt][2 + j]));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-            if (mx > m_r[nt][j] + kRescale) {
-              const float alpha = fast_exp2(m_r[nt][j] - mx);   // 0 when the old one is -inf
-              m_r[nt][j] = mx;
-              l_r[nt][j] *= alpha;
-#pragma unroll
-              for (int md = 0; md < kK; ++md) {
-                o[nt][md][j] *= alpha;
-                o[nt][md][2 + j] *= alpha;
-              }
-            }
-            const float mu = m_r[nt][j] == -CUDART_INF_F ? 0.f : m_r[nt][j];
-#pragma unroll
-            for (int p = 0; p < kPieces; ++p) {
-              pr[p][j] = fast_exp2(x[p][nt][j] - mu);
-              pr[p][2 + j] = fast_exp2(x[p][nt][2 + j] - mu);
-              l_r[nt][j] += pr[p][j] + pr[p][2 + j];
-            }
-          }
-#pragma unroll
-          for (int p = 0; p < kPieces; ++p) {
-            const uint32_t u_lo = pack_f16(pr[p][0], pr[p][1]);   // token gid, heads 2 tid4, + 1
-            const uint32_t u_hi = pack_f16(pr[p][2], pr[p][3]);   // token gid + 8
-            const uint32_t xa = __shfl_sync(0xffffffffu, u_lo, src_a);
-            const uint32_t xb = __shfl_sync(0xffffffffu, u_lo, src_b);
-            const uint32_t ya = __shfl_sync(0xffffffffu, u_hi, src_a);
-            const uint32_t yb = __shfl_sync(0xffffffffu, u_hi, src_b);
-            pb[p][nt][0] = __byte_perm(xa, xb, sel);
-            pb[p][nt][1] = __byte_perm(ya, yb, sel);
-          }
-        }
-        // O^T += V^T P^T: a lane's codes are d / 8 neighbouring ones of the value rows
-        // 2 tid4, + 1, + 8, + 9; two tokens' codes are interleaved by halves of bytes.
+              if (gid + 8 * (e >> 1) >= lim[p]) x[p][nt][e] = -CUDART_INF_F;
+      }
+      if constexpr (LOGITS) {
+        // (Of every token, also where a block is missing.)
+        const int64_t unit = static_cast<int64_t>(at.i) * a.Hkv + at.h;
 #pragma unroll
         for (int p = 0; p < kPieces; ++p) {
-          const uint32_t vb = pair + p * C::kPairBytes + fp4::tile_bytes(D), vs = vb + 8 * D;
-          uint32_t v[4][kWv], sc[4];
+          const int tok = tb + 16 * p + gid;
+          float* dst = a.logits + (unit * a.logit_tokens + tok) * grp;
 #pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const int row = 2 * tid4 + (r & 1) + 8 * (r >> 1);
-            lds_words(vb + row * (D / 2) + gid * (D / 16), v[r]);
-            sc[r] = lds_u8(vs + row * (D / 16) + (D == 128 ? gid : gid >> 1));
-            // The weight of a token that is not there is 0, its codes are finite
-            // whatever the bytes, but its scale need not be.
-            if (row >= lim[p]) sc[r] = 0u;
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int h = nt * 8 + 2 * tid4 + (e & 1);
+              if (h < grp && tok + 8 * (e >> 1) < min(at.end, a.logit_tokens))
+                dst[8 * (e >> 1) * grp + h] = x[p][nt][e];
+            }
+        }
+      }
+      // Online softmax in the log2 domain; the reference maximum moves only when the
+      // 32 tokens' exceeds it by more than kRescale, so that weights stay < 2^8.
+      uint32_t pb[kPieces][NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float pr[kPieces][4];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          float mx = fmaxf(fmaxf(x[0][nt][j], x[0][nt][2 + j]), fmaxf(x[1][nt][j], x[1][nt][2 + j]));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+          if (mx > m_r[nt][j] + kRescale) {
+            const float alpha = fast_exp2(m_r[nt][j] - mx);   // 0 when the old one is -inf
+            m_r[nt][j] = mx;
+            l_r[nt][j] *= alpha;
+#pragma unroll
+            for (int md = 0; md < kK; ++md) {
+              o[nt][md][j] *= alpha;
+              o[nt][md][2 + j] *= alpha;
+            }
           }
-          const uint32_t sab = fp4::widen_scales(sc[0] | (sc[1] << 8));
-          const uint32_t scd = fp4::widen_scales(sc[2] | (sc[3] << 8));
+          const float mu = m_r[nt][j] == -CUDART_INF_F ? 0.f : m_r[nt][j];
 #pragma unroll
-          for (int w = 0; w < kWv; ++w) {
-            constexpr uint32_t kLow = 0x0f0f0f0fu;
-            uint32_t ab[2][4], cd[2][4];   // [even, odd element][word byte]
-            fp4::widen8((v[0][w] & kLow) | ((v[1][w] << 4) & ~kLow), ab[0]);
-            fp4::widen8(((v[0][w] >> 4) & kLow) | (v[1][w] & ~kLow), ab[1]);
-            fp4::widen8((v[2][w] & kLow) | ((v[3][w] << 4) & ~kLow), cd[0]);
-            fp4::widen8(((v[2][w] >> 4) & kLow) | (v[3][w] & ~kLow), cd[1]);
+          for (int p = 0; p < kPieces; ++p) {
+            pr[p][j] = fast_exp2(x[p][nt][j] - mu);
+            pr[p][2 + j] = fast_exp2(x[p][nt][2 + j] - mu);
+            l_r[nt][j] += pr[p][j] + pr[p][2 + j];
+          }
+        }
 #pragma unroll
-            for (int b = 0; b < 4; ++b) {
-              const uint32_t am[4] = {fp4::mul2(ab[0][b], sab), fp4::mul2(ab[1][b], sab),
-                                      fp4::mul2(cd[0][b], scd), fp4::mul2(cd[1][b], scd)};
+        for (int p = 0; p < kPieces; ++p) {
+          const uint32_t u_lo = pack_f16(pr[p][0], pr[p][1]);   // token gid, heads 2 tid4, + 1
+          const uint32_t u_hi = pack_f16(pr[p][2], pr[p][3]);   // token gid + 8
+          const uint32_t xa = __shfl_sync(0xffffffffu, u_lo, src_a);
+          const uint32_t xb = __shfl_sync(0xffffffffu, u_lo, src_b);
+          const uint32_t ya = __shfl_sync(0xffffffffu, u_hi, src_a);
+          const uint32_t yb = __shfl_sync(0xffffffffu, u_hi, src_b);
+          pb[p][nt][0] = __byte_perm(xa, xb, sel);
+          pb[p][nt][1] = __byte_perm(ya, yb, sel);
+        }
+      }
+      // O^T += V^T P^T: a lane's codes are d / 8 neighbouring ones of the value rows 2
+      // tid4, + 1, + 8, + 9; two tokens' codes are interleaved by halves of bytes.
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt)
-                mma_f16_16816(o[nt][4 * w + b], am, pb[p][nt][0], pb[p][nt][1]);
+      for (int p = 0; p < kPieces; ++p) {
+        const uint32_t vb = pair + p * C::kPairBytes + fp4::tile_bytes(D), vs = vb + 8 * D;
+        uint32_t v[4][kWv], sc[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int row = 2 * tid4 + (r & 1) + 8 * (r >> 1);
+          lds_words(vb + row * (D / 2) + gid * (D / 16), v[r]);
+          sc[r] = lds_u8(vs + row * (D / 16) + (D == 128 ? gid : gid >> 1));
+        }
+        if (!whole) {
+          // The weight of a token that is not there is 0, its codes are finite whatever
+          // the bytes, but its scale need not be.
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            if (2 * tid4 + (r & 1) + 8 * (r >> 1) >= lim[p]) sc[r] = 0u;
+        }
+        const uint32_t sab = fp4::widen_scales(sc[0] | (sc[1] << 8));
+        const uint32_t scd = fp4::widen_scales(sc[2] | (sc[3] << 8));
+#pragma unroll
+        for (int w = 0; w < kWv; ++w) {
+          constexpr uint32_t kLow = 0x0f0f0f0fu;
+          uint32_t ab[2][4], cd[2][4];   // [even, odd element][word byte]
+          fp4::widen8((v[0][w] & kLow) | ((v[1][w] << 4) & ~kLow), ab[0]);
+          fp4::widen8(((v[0][w] >> 4) & kLow) | (v[1][w] & ~kLow), ab[1]);
+          fp4::widen8((v[2][w] & kLow) | ((v[3][w] << 4) & ~kLow), cd[0]);
+          fp4::widen8(((v[2][w] >> 4) & kLow) | (v[3][w] & ~kLow), cd[1]);
+#pragma unroll
+          for (int b = 0; b < 4; ++b) {
+            const uint32_t am[4] = {fp4::mul2(ab[0][b], sab), fp4::mul2(ab[1][b], sab),
+                                    fp4::mul2(cd[0][b], scd), fp4::mul2(cd[1][b], scd)};
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+              mma_f16_16816(o[nt][4 * w + b], am, pb[p][nt][0], pb[p][nt][1]);
+          }
+        }
+      }
+      __syncwarp();   // every lane has read the slot
+      --flying;
+      if (tb + kStage < at.end)
+        fetch();
+      else
+        own = slot;
+      if (++slot == C::kSlots) slot = 0, parity ^= 1;
+    }
+
+    // ---------------------------------------------------------- its end
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int k = 4; k < 32; k <<= 1) l_r[nt][j] += __shfl_xor_sync(0xffffffffu, l_r[nt][j], k);
+    // Eight states to one in three rounds: the upper half's warps hand theirs to the
+    // lower half's.  A warp without tokens has m = -inf and l = 0, and no o.
+    float4* stats = reinterpret_cast<float4*>(smem + C::kOffStats);
+    int* slots = reinterpret_cast<int*>(smem + C::kOffScan);   // [warp] slot of its o, or -1
+#pragma unroll 1
+    for (int half = kWarps / 2; half > 0; half >>= 1) {
+      const bool gives = warp >= half && warp < 2 * half;
+      if (gives) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+          stats[(warp * NT + nt) * 32 + lane] =
+              make_float4(m_r[nt][0], m_r[nt][1], l_r[nt][0], l_r[nt][1]);
+        if (lane == 0) slots[warp] = own;
+      }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        if (nt > 0) __syncthreads();   // the slot's first contents have been read
+        if (gives && own >= 0) {
+          float4* dst = reinterpret_cast<float4*>(smem + (warp * C::kSlots + own) * C::kSlotBytes);
+#pragma unroll
+          for (int md = 0; md < kK; ++md)
+            dst[md * 32 + lane] = make_float4(o[nt][md][0], o[nt][md][1], o[nt][md][2], o[nt][md][3]);
+        }
+        __syncthreads();
+        if (warp < half) {
+          const int other = warp + half, from = slots[other];
+          if (from >= 0) {   // warp-uniform
+            const float4 s4 = stats[(other * NT + nt) * 32 + lane];
+            const float4* src =
+                reinterpret_cast<const float4*>(smem + (other * C::kSlots + from) * C::kSlotBytes);
+            const float om[2] = {s4.x, s4.y}, ol[2] = {s4.z, s4.w};
+            float f[2], g[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const float M = fmaxf(m_r[nt][j], om[j]);
+              // (Equal, also where both are -inf: 1.)
+              f[j] = m_r[nt][j] == M ? 1.f : fast_exp2(m_r[nt][j] - M);
+              g[j] = om[j] == M ? 1.f : fast_exp2(om[j] - M);
+              m_r[nt][j] = M;
+              l_r[nt][j] = f[j] * l_r[nt][j] + g[j] * ol[j];
+            }
+#pragma unroll
+            for (int md = 0; md < kK; ++md) {
+              const float4 y = src[md * 32 + lane];
+              o[nt][md][0] = fmaf(g[0], y.x, f[0] * o[nt][md][0]);
+              o[nt][md][1] = fmaf(g[1], y.y, f[1] * o[nt][md][1]);
+              o[nt][md][2] = fmaf(g[0], y.z, f[0] * o[nt][md][2]);
+              o[nt][md][3] = fmaf(g[1], y.w, f[1] * o[nt][md][3]);
             }
           }
         }
       }
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(empty(at));
     }
-    if (!ok && lane == 0) record_error(a.err, PA_DEVERR_TIMEOUT);
-  }
-  pdl_trigger();
-
-  // Every copy has landed: a stage was waited for by all consumers, or a wait has run
-  // out; then the producer's last stages get one more bounded wait each.
-  if (warp == kConsumers && lane == 0)
-    for (int st = max(0, stages - C::kStages); st < stages; ++st)
-      tc::mbar_wait(full(st % C::kStages), (st / C::kStages) & 1);
+    __syncthreads();   // read, before a slot or a state is written again
+    if (own >= 0) {
+      tc::fence_proxy_async_smem();   // the state lay where the copy will land
+      __syncwarp();
+      fetch();
+    }
+    const bool starts = at.tok == 0, ends = at.end == at.seq;
+    if (warp == 0) {
+      // A lane's dims of a head are D / 8 neighbouring ones.
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-#pragma unroll
-      for (int k = 4; k < 32; k <<= 1) l_r[nt][j] += __shfl_xor_sync(0xffffffffu, l_r[nt][j], k);
-  __syncthreads();
-  float* obuf = reinterpret_cast<float*>(smem);
-  float* mbuf = obuf + kConsumers * C::kHeads * C::kOStride;   // [warp][head]
-  float* lbuf = mbuf + kConsumers * C::kHeads;
-  if (warp < kConsumers) {
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-      for (int md = 0; md < kK; ++md)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int h = nt * 8 + 2 * tid4 + (e & 1), dim = gid * (D / 8) + 2 * md + (e >> 1);
-          obuf[(warp * C::kHeads + h) * C::kOStride + C::place(dim)] = o[nt][md][e];
-        }
-      if (gid == 0) {
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          mbuf[warp * C::kHeads + nt * 8 + 2 * tid4 + j] = m_r[nt][j];
-          lbuf[warp * C::kHeads + nt * 8 + 2 * tid4 + j] = l_r[nt][j];
+          const int r = nt * 8 + 2 * tid4 + j;
+          if (r >= grp) continue;
+          const float L = l_r[nt][j], m = m_r[nt][j];
+          if (starts && ends) {
+            const float f = L == 0.f ? 0.f : a.out_scale / L;
+            __nv_bfloat16* dst = a.out + (row0 + r) * D + gid * (D / 8);
+            uint32_t w[kK];
+#pragma unroll
+            for (int md = 0; md < kK; ++md) w[md] = pack_bf16(o[nt][md][j] * f, o[nt][md][2 + j] * f);
+            if ((reinterpret_cast<uintptr_t>(a.out) & 15u) == 0) {
+#pragma unroll
+              for (int k = 0; k < D / 64; ++k)
+                reinterpret_cast<uint4*>(dst)[k] =
+                    make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+            } else {
+#pragma unroll
+              for (int md = 0; md < kK; ++md) {
+                dst[2 * md] = __float2bfloat16_rn(o[nt][md][j] * f);
+                dst[2 * md + 1] = __float2bfloat16_rn(o[nt][md][2 + j] * f);
+              }
+            }
+            if (gid == 0) {
+              const float x = L == 0.f ? -CUDART_INF_F : (m + log2f(L)) * kLn2;
+              if (a.lse != nullptr) a.lse[row0 + r] = x;
+              if (a.spans != nullptr) a.row_lse[row0 + r] = x;
+            }
+          } else {
+            float* dst = a.parts + ((static_cast<int64_t>(cta) * 2 + starts) * grp + r) * (D + 2);
+#pragma unroll
+            for (int md = 0; md < kK; ++md)
+              *reinterpret_cast<float2*>(dst + gid * (D / 8) + 2 * md) =
+                  make_float2(o[nt][md][j], o[nt][md][2 + j]);
+            if (gid == 0) dst[D] = m, dst[D + 1] = L;
+          }
         }
+      if (lane == 0) {
+        if (!starts && ends)
+          a.cut[cta] = make_int4(static_cast<int>((pos - (at.tok >> 4)) / share), at.i, at.h, 0);
+        if (starts && a.spans != nullptr)
+          a.spans[static_cast<int64_t>(at.i) * a.Hkv + at.h] = make_int2(
+              cta, ends ? cta : static_cast<int>((pos + ((at.seq + 15) >> 4) - 1) / share));
       }
     }
+    pos += a.whole ? 1 : (at.end - at.tok + 15) >> 4;
+    live = walk_next(a, at);
   }
-  __syncthreads();
-  for (int idx = threadIdx.x; idx < grp * D; idx += kThreads) {
-    const int r = idx / D, e = idx % D;
-    float M = -CUDART_INF_F;
-#pragma unroll
-    for (int w = 0; w < kConsumers; ++w) M = fmaxf(M, mbuf[w * C::kHeads + r]);
-    float L = 0.f, acc = 0.f;
-#pragma unroll
-    for (int w = 0; w < kConsumers; ++w) {
-      const float mw = mbuf[w * C::kHeads + r];
-      const float f = mw == -CUDART_INF_F ? 1.f : fast_exp2(mw - M);   // (its sums are 0, or NaN)
-      L += f * lbuf[w * C::kHeads + r];
-      acc += f * obuf[(w * C::kHeads + r) * C::kOStride + C::place(e)];
-    }
-    const float y = L == 0.f ? 0.f : acc / L * a.out_scale;
-    const float ls = L == 0.f ? -CUDART_INF_F : (M + log2f(L)) * kLn2;
-    if (a.ws == nullptr) {
-      a.out[(row0 + r) * D + e] = __float2bfloat16_rn(y);
-      if (e == 0 && a.lse != nullptr) a.lse[row0 + r] = ls;
-    } else {
-      float* dst = a.ws + ((row0 + r) * a.S + s) * (D + 1);
-      dst[e] = y;
-      // (A NaN row is handed on as +inf, whose weight in the merge is NaN: a maximum
-      // would pass over a NaN.)
-      if (e == 0) dst[D] = ls == ls ? ls : CUDART_INF_F;
+  if (!ok && lane == 0) {
+    // Given up: the outputs are invalid.  No copy may still be landing when the CTA
+    // exits: what is on its way gets one more bounded wait each.
+    record_error(a.err, PA_DEVERR_TIMEOUT);
+    for (int k = 0; k < flying; ++k) {
+      tc::mbar_wait(bars + 8 * slot, parity);
+      if (++slot == C::kSlots) slot = 0, parity ^= 1;
     }
   }
 }
 
+// The states of a cut unit, one CTA for each CTA that holds a unit's end: the first
+// CTA's second state, then the following CTAs' first states up to this one's.
+template <int D>
+__global__ void __launch_bounds__(128) decode_fp4_merge_kernel(
+    const __grid_constant__ Fp4Args a) {
+  pdl_wait();
+  pdl_trigger();
+  const int c1 = blockIdx.x;
+  const int4 u = a.cut[c1];
+  if (u.x < 0) return;
+  const int e = threadIdx.x % D;
+  for (int r = threadIdx.x / D; r < a.grp; r += 128 / D) {
+    auto state = [&](int c) {
+      return a.parts + ((static_cast<int64_t>(c) * 2 + (c == u.x)) * a.grp + r) * (D + 2);
+    };
+    float M = -CUDART_INF_F;
+    for (int c = u.x; c <= c1; ++c) M = fmaxf(M, state(c)[D]);
+    float L = 0.f, acc = 0.f;
+#pragma unroll 4
+    for (int c = u.x; c <= c1; ++c) {
+      const float* s = state(c);
+      const float f = s[D] == M ? 1.f : fast_exp2(s[D] - M);
+      L += f * s[D + 1];
+      acc += f * s[e];
+    }
+    const int64_t row = static_cast<int64_t>(u.y) * a.Hq + u.z * a.grp + r;
+    a.out[row * D + e] = __float2bfloat16_rn(L == 0.f ? 0.f : acc / L * a.out_scale);
+    if (e == 0 && a.lse != nullptr)
+      a.lse[row] = L == 0.f ? -CUDART_INF_F : (M + log2f(L)) * kLn2;
+  }
+}
+
 template <int D, int NT, bool LOGITS>
-cudaError_t launch_t(const Fp4Args& a, int N, cudaStream_t stream) {
+cudaError_t launch_t(const Fp4Args& a, int ctas, cudaStream_t stream) {
   using C = Fp4Cfg<D, NT>;
   auto kern = decode_fp4_kernel<D, NT, LOGITS>;
   static DeviceFlags smem_set;
   cudaError_t e = set_smem_once(kern, C::kSmemBytes, smem_set);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kern, dim3(a.S, a.Hkv, N), dim3(kThreads), C::kSmemBytes, stream, a);
+  e = launch_pdl(kern, dim3(ctas), dim3(kThreads), C::kSmemBytes, stream, a);
+  if (e != cudaSuccess || a.whole || a.spans != nullptr) return e;
+  return launch_pdl(decode_fp4_merge_kernel<D>, dim3(ctas), dim3(128), 0, stream, a);
 }
 template <int D, int NT>
-cudaError_t launch_n(const Fp4Args& a, int N, cudaStream_t stream) {
-  return a.logits != nullptr ? launch_t<D, NT, true>(a, N, stream)
-                             : launch_t<D, NT, false>(a, N, stream);
+cudaError_t launch_n(const Fp4Args& a, int ctas, cudaStream_t stream) {
+  return a.logits != nullptr ? launch_t<D, NT, true>(a, ctas, stream)
+                             : launch_t<D, NT, false>(a, ctas, stream);
 }
+
+size_t up16(size_t n) { return (n + 15) / 16 * 16; }
+
+// CTAs that are resident at once, but no more than there are slices or units.
+int decode_fp4_ctas(int N, int Hq, int Hkv, int max_seq_len, int sm_count) {
+  const long long units = static_cast<long long>(N) * Hkv;
+  const long long slices = units * ((static_cast<long long>(max_seq_len) + kSlice - 1) / kSlice);
+  const long long most = static_cast<long long>(Hq / Hkv > 8 ? 1 : 2) * sm_count;
+  return static_cast<int>(std::max(1LL, std::min(most, std::max(units, slices))));
+}
+
+// Units are not cut where the longest is at most two rounds of a CTA's warps: a second
+// launch would cost more than the balance brings.
+bool decode_fp4_whole(int max_seq_len) { return max_seq_len <= 2 * kStage; }
 
 }  // namespace
 
-// Splits of the context: about six CTAs for each SM (two are resident), of at least
-// 256 tokens, so that a batch of mixed lengths evens out.
-int decode_fp4_splits(int N, int Hkv, int max_seq_len, int sm_count) {
-  const long long units = static_cast<long long>(N) * Hkv;
-  const long long want = (6LL * sm_count + units - 1) / std::max(1LL, units);
-  const long long most = (static_cast<long long>(max_seq_len) + 255) / 256;
-  return static_cast<int>(std::max(1LL, std::min({want, most, 64LL})));
+Fp4Workspace decode_fp4_workspace(int N, int Hq, int Hkv, int d, int max_seq_len, bool sums,
+                                  int sm_count) {
+  Fp4Workspace w{};
+  const size_t n = static_cast<size_t>(N);
+  const int ctas = decode_fp4_ctas(N, Hq, Hkv, max_seq_len, sm_count);
+  if (!decode_fp4_whole(max_seq_len)) {
+    w.cut = w.bytes;
+    w.bytes += static_cast<size_t>(ctas) * sizeof(int4);
+    w.parts = w.bytes;
+    w.bytes += up16(static_cast<size_t>(ctas) * 2 * (Hq / Hkv) * (d + 2) * 4);
+  }
+  if (sums) {
+    w.spans = w.bytes;
+    w.bytes += up16(n * Hkv * sizeof(int2));
+    w.row_lse = w.bytes;
+    w.bytes += up16(n * Hq * 4);
+    w.logits = w.bytes;
+    w.bytes += n * Hq * max_seq_len * 4;
+  }
+  return w;
 }
 
 cudaError_t launch_decode_fp4(const DecodeFp4Launch& n, cudaStream_t stream) {
@@ -474,6 +727,7 @@ cudaError_t launch_decode_fp4(const DecodeFp4Launch& n, cudaStream_t stream) {
   a.cache = static_cast<const uint8_t*>(n.cache);
   a.block_table = n.block_table;
   a.seq_lens = n.seq_lens;
+  a.N = n.N;
   a.max_blocks = n.max_blocks;
   a.Hq = n.Hq;
   a.Hkv = n.Hkv;
@@ -481,21 +735,55 @@ cudaError_t launch_decode_fp4(const DecodeFp4Launch& n, cudaStream_t stream) {
   a.bs = n.bs;
   a.bs_log2 = block_size_log2(n.bs);
   a.num_blocks = n.num_blocks;
-  a.S = n.S;
-  a.chunk = static_cast<int>(split_chunk(n.max_seq_len, n.S, 16));
+  a.whole = decode_fp4_whole(n.max_seq_len);
   a.positions = static_cast<int>(
       std::min(static_cast<long long>(n.max_blocks) * n.bs, INT_MAX - 1023LL));
   a.scale_log2 = n.scale * n.k_scale * kLog2e;
   a.out_scale = n.v_scale;
-  a.ws = n.ws;
-  a.logits = n.logits;
-  a.logit_tokens = n.logit_tokens;
+  const Fp4Workspace w =
+      decode_fp4_workspace(n.N, n.Hq, n.Hkv, n.d, n.max_seq_len, n.scores != nullptr, n.sm_count);
+  char* ws = static_cast<char*>(n.workspace);
+  if (!a.whole) {
+    a.cut = reinterpret_cast<int4*>(ws + w.cut);
+    a.parts = reinterpret_cast<float*>(ws + w.parts);
+  }
+  if (n.scores != nullptr) {
+    a.spans = reinterpret_cast<int2*>(ws + w.spans);
+    a.row_lse = reinterpret_cast<float*>(ws + w.row_lse);
+    a.logits = reinterpret_cast<float*>(ws + w.logits);
+    a.logit_tokens = n.max_seq_len;
+  }
   a.out = static_cast<__nv_bfloat16*>(n.out);
   a.lse = n.lse;
   a.err = n.err;
+  const int ctas = decode_fp4_ctas(n.N, n.Hq, n.Hkv, n.max_seq_len, n.sm_count);
   const bool wide = a.grp > 8;   // groups of 9 to 16 heads take two n-tiles
-  if (n.d == 128) return wide ? launch_n<128, 2>(a, n.N, stream) : launch_n<128, 1>(a, n.N, stream);
-  return wide ? launch_n<64, 2>(a, n.N, stream) : launch_n<64, 1>(a, n.N, stream);
+  cudaError_t e;
+  if (n.d == 128)
+    e = wide ? launch_n<128, 2>(a, ctas, stream) : launch_n<128, 1>(a, ctas, stream);
+  else
+    e = wide ? launch_n<64, 2>(a, ctas, stream) : launch_n<64, 1>(a, ctas, stream);
+  if (e != cudaSuccess || n.scores == nullptr) return e;
+  ScoresLaunch m{};
+  m.parts = a.parts;
+  m.spans = a.spans;
+  m.row_lse = a.row_lse;
+  m.out_scale = n.v_scale;
+  m.logits = a.logits;
+  m.logit_tokens = n.max_seq_len;
+  m.seq_lens = n.seq_lens;
+  m.positions = a.positions;
+  m.N = n.N;
+  m.Hq = n.Hq;
+  m.Hkv = n.Hkv;
+  m.d = n.d;
+  m.max_seq_len = n.max_seq_len;
+  m.scores = n.scores;
+  m.score_tokens = n.score_tokens;
+  m.out = n.out;
+  m.lse = n.lse;
+  m.err = n.err;
+  return launch_decode_scores(m, stream);
 }
 
 }  // namespace pa

@@ -702,10 +702,9 @@ static int sm_count_or_default() {
 size_t pa_decode_fp4_workspace_bytes(int num_seqs, int num_q_heads, int num_kv_heads,
                                      int head_size, int max_seq_len, int with_scores) {
   if (!workspace_args_ok(num_seqs, num_q_heads, num_kv_heads, head_size, max_seq_len)) return 0;
-  const int S = pa::decode_fp4_splits(num_seqs, num_kv_heads, max_seq_len, sm_count_or_default());
-  if (S == 1 && !with_scores) return 0;
-  return partial_bytes(num_seqs, num_q_heads, S, head_size) +
-         (with_scores ? static_cast<size_t>(num_seqs) * num_q_heads * max_seq_len * 4 : 0);
+  return pa::decode_fp4_workspace(num_seqs, num_q_heads, num_kv_heads, head_size, max_seq_len,
+                                  with_scores != 0, sm_count_or_default())
+      .bytes;
 }
 
 size_t pa_decode_scores_workspace_bytes(int num_seqs, int num_q_heads, int num_kv_heads,
@@ -740,28 +739,6 @@ static pa_status decode_args(const void* q, const void* kv_cache, const int32_t*
   return PA_OK;
 }
 
-static pa_status finish_scores(const pa_shape* shape, int S, int max_seq_len, float* ws,
-                               float* logits, const int32_t* seq_lens, float* scores,
-                               int score_tokens, void* out, float* lse, void* stream) {
-  pa::ScoresLaunch m{};
-  m.ws = ws;
-  m.logits = logits;
-  m.logit_tokens = max_seq_len;
-  m.seq_lens = seq_lens;
-  m.N = shape->num_seqs;
-  m.Hq = shape->num_q_heads;
-  m.Hkv = shape->num_kv_heads;
-  m.d = shape->head_size;
-  m.S = S;
-  m.max_seq_len = max_seq_len;
-  m.scores = scores;
-  m.score_tokens = score_tokens;
-  m.out = out;
-  m.lse = lse;
-  m.err = device_error_ptr();
-  return from_cuda(pa::launch_decode_scores(m, static_cast<cudaStream_t>(stream)));
-}
-
 static pa_status decode_fp4(const void* q, const void* kv_cache, const int32_t* block_table,
                             const int32_t* seq_lens, const pa_shape* shape, float scale,
                             float k_scale, float v_scale, int max_seq_len, void* workspace,
@@ -778,8 +755,6 @@ static pa_status decode_fp4(const void* q, const void* kv_cache, const int32_t* 
                                     shape->head_size, max_seq_len, with_scores);
   if (need > 0 && (workspace == nullptr || workspace_bytes < need || !aligned(workspace, 16)))
     return PA_ERR_INVALID;
-  const int S = pa::decode_fp4_splits(shape->num_seqs, shape->num_kv_heads, max_seq_len,
-                                      sm_count_or_default());
   pa::DecodeFp4Launch n{};
   n.q = q;
   n.cache = kv_cache;
@@ -795,26 +770,15 @@ static pa_status decode_fp4(const void* q, const void* kv_cache, const int32_t* 
   n.scale = scale;
   n.k_scale = k_scale;
   n.v_scale = v_scale;
-  n.S = S;
   n.max_seq_len = max_seq_len;
-  n.ws = need > 0 ? static_cast<float*>(workspace) : nullptr;
-  // (Never null with sums, also where no token has logits.)
-  n.logits = with_scores ? reinterpret_cast<float*>(
-                               static_cast<char*>(workspace) +
-                               partial_bytes(n.N, n.Hq, S, n.d))
-                         : nullptr;
-  n.logit_tokens = max_seq_len;
+  n.workspace = workspace;
+  n.scores = scores;
+  n.score_tokens = score_tokens;
   n.out = out;
   n.lse = lse;
   n.err = device_error_ptr();
-  const cudaError_t e = pa::launch_decode_fp4(n, static_cast<cudaStream_t>(stream));
-  if (e != cudaSuccess) return from_cuda(e);
-  if (with_scores)
-    return finish_scores(shape, S, max_seq_len, n.ws, n.logits, seq_lens, scores, score_tokens, out,
-                         lse, stream);
-  if (S == 1) return PA_OK;
-  return from_cuda(pa::launch_lse_merge(n.ws, n.N * n.Hq, S, n.d, out, lse,
-                                        static_cast<cudaStream_t>(stream)));
+  n.sm_count = sm_count_or_default();
+  return from_cuda(pa::launch_decode_fp4(n, static_cast<cudaStream_t>(stream)));
 }
 
 pa_status pa_decode_fp4(const void* q, const void* kv_cache, const int32_t* block_table,
@@ -863,8 +827,24 @@ pa_status pa_decode_scores(const void* q, const void* kv_cache, const int32_t* b
       static_cast<int>(pa::split_chunk(max_seq_len, S, shape->block_size)), ws, device_error_ptr(),
       static_cast<cudaStream_t>(stream), &x);
   if (e != cudaSuccess) return from_cuda(e);
-  return finish_scores(shape, S, max_seq_len, ws, x.logits, seq_lens, scores, score_tokens, out, lse,
-                       stream);
+  pa::ScoresLaunch m{};
+  m.ws = ws;
+  m.S = S;
+  m.out_scale = 1.f;
+  m.logits = x.logits;
+  m.logit_tokens = max_seq_len;
+  m.seq_lens = seq_lens;
+  m.N = shape->num_seqs;
+  m.Hq = shape->num_q_heads;
+  m.Hkv = shape->num_kv_heads;
+  m.d = shape->head_size;
+  m.max_seq_len = max_seq_len;
+  m.scores = scores;
+  m.score_tokens = score_tokens;
+  m.out = out;
+  m.lse = lse;
+  m.err = device_error_ptr();
+  return from_cuda(pa::launch_decode_scores(m, static_cast<cudaStream_t>(stream)));
 }
 
 static pa_status evict(void* kv_cache, const pa_shape* shape, bool four, int element_bytes,

@@ -151,8 +151,7 @@ struct DecodeWindowLaunch {
 };
 cudaError_t launch_decode_window(const DecodeWindowLaunch& n, cudaStream_t stream);
 
-// 4-bit pool: quantising cache write; decode, stage 1, or whole where S == 1 and
-// ws is null.
+// 4-bit pool: quantising cache write, and decode with or without the weights' sums.
 cudaError_t launch_cache_write_fp4(const void* key, const void* value, int64_t key_stride,
                                    int64_t value_stride, void* cache, const int64_t* slot_mapping,
                                    int num_tokens, int num_kv_heads, int head_size, int block_size,
@@ -165,25 +164,39 @@ struct DecodeFp4Launch {
   const int32_t* seq_lens;
   int N, Hq, Hkv, d, bs, num_blocks, max_blocks;
   float scale, k_scale, v_scale;
-  int S, max_seq_len;
-  float* ws;          // [N, Hq, S, d + 1], or null
-  float* logits;      // [N, Hkv, logit_tokens, Hq / Hkv], or null
-  int logit_tokens;
+  int max_seq_len;
+  void* workspace;    // decode_fp4_workspace's bytes
+  float* scores;      // [N, Hkv, score_tokens], or null: no sums
+  int score_tokens;
   void* out;
   float* lse;
   int* err;
+  int sm_count;
 };
 cudaError_t launch_decode_fp4(const DecodeFp4Launch& n, cudaStream_t stream);
-int decode_fp4_splits(int N, int Hkv, int max_seq_len, int sm_count);
+// Offsets in the workspace, and its size.
+struct Fp4Workspace {
+  size_t cut, parts, spans, row_lse, logits, bytes;
+};
+Fp4Workspace decode_fp4_workspace(int N, int Hq, int Hkv, int d, int max_seq_len, bool sums,
+                                  int sm_count);
 
-// Merge of the splits, and each token's weights (exp2 of its logit less the row's
-// log-sum-exp, summed over the group's heads) added to scores [N, Hkv, score_tokens].
+// Merge of what stage 1 left, and each token's weights (exp2 of its logit less the
+// row's log-sum-exp, summed over the group's heads) added to scores [N, Hkv,
+// score_tokens].  Stage 1 left either S partials of each row (ws), or outputs and
+// log-sum-exps of the units that were not cut and states of those that were (spans).
 struct ScoresLaunch {
-  const float* ws;
+  const float* ws;        // [N, Hq, S, d + 1], or null:
+  int S;
+  const float* parts;     // [CTA][2][Hq / Hkv][d + 2]
+  const int2* spans;      // [N, Hkv] first and last CTA
+  const float* row_lse;   // [N, Hq]
+  float out_scale;
   const float* logits;
   int logit_tokens;
   const int32_t* seq_lens;
-  int N, Hq, Hkv, d, S, max_seq_len;
+  int positions;          // with spans: of a table row
+  int N, Hq, Hkv, d, max_seq_len;
   float* scores;
   int score_tokens;
   void* out;

@@ -1,5 +1,6 @@
-// Split-KV decode, stage 2, with the weights' sums: the LSE merge of the split
-// partials (as merge.cu), and for each cached token p of request i and kv head h
+// Decode's second stage with the weights' sums: the merge of what the first left
+// (split partials, as merge.cu takes them, or the states of decode_fp4.cu's cut units),
+// and for each cached token p of request i and kv head h
 //   scores[i][h][p] += sum over the group's heads g of exp(x_g[p] - lse_g),
 // x the logits that stage 1 left beside its partials.
 //
@@ -28,6 +29,11 @@ constexpr int kMaxGroup = 16;
 
 struct ScoreArgs {
   const float* ws;
+  const float* parts;
+  const int2* spans;
+  const float* row_lse;
+  float out_scale;
+  int positions;
   const float* logits;
   const int32_t* seq_lens;
   float* scores;
@@ -42,55 +48,79 @@ struct ScoreArgs {
 template <int D, int VW>
 __global__ void __launch_bounds__(kScoreThreads) decode_scores_kernel(
     const __grid_constant__ ScoreArgs a) {
+  // Per row: the states' maximum, their sum, and the log-sum-exp.
   __shared__ float row_m[kMaxGroup], row_l[kMaxGroup], row_x[kMaxGroup];
   pdl_wait();
   pdl_trigger();
   const int kvh = blockIdx.y, i = blockIdx.z, grp = a.grp;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int seq = max(0, a.seq_lens[i]);
+  const bool cut = a.spans != nullptr;
+  int seq = max(0, a.seq_lens[i]);
+  if (cut) seq = min(seq, a.positions);   // (what lies past them has no logits)
   // Tokens past max_seq_len have no logits.
   const int end = min(seq, a.max_seq_len);
   const int first = (static_cast<int>(blockIdx.x) - 1) * kScoreTokens;
   if (blockIdx.x > 0 && first >= end) return;
   if (blockIdx.x == 0 && threadIdx.x == 0 && end < seq) record_error(a.err, PA_DEVERR_LENGTH);
-  const float* base = a.ws + (static_cast<int64_t>(i) * a.Hq + kvh * grp) * a.S * (D + 1);
+  const int64_t unit = static_cast<int64_t>(i) * a.Hkv + kvh;
+  const int64_t row0 = static_cast<int64_t>(i) * a.Hq + kvh * grp;
+  // State s of row r: D values, then (split partials, normalised) the log-sum-exp, or
+  // (cut units, log2 units) maximum and sum.
+  int states = a.S;
+  int2 span = make_int2(0, 0);
+  if (cut) {
+    if (seq == 0) return;   // its outputs are there already
+    span = a.spans[unit];
+    states = span.y - span.x + 1;
+  }
+  auto state = [&](int r, int s) {
+    return cut ? a.parts + ((static_cast<int64_t>(span.x + s) * 2 + (s == 0)) * grp + r) * (D + 2)
+               : a.ws + ((row0 + r) * a.S + s) * (D + 1);
+  };
+  const bool done = cut && states == 1;   // ... and these
+  if (done && blockIdx.x == 0) return;
   for (int r = warp; r < grp; r += kScoreThreads / 32) {
-    const float* p = base + static_cast<int64_t>(r) * a.S * (D + 1) + D;
-    float m = -CUDART_INF_F;
-    for (int s = lane; s < a.S; s += 32) m = fmaxf(m, p[s * (D + 1)]);
+    float m = -CUDART_INF_F, l = 0.f, x;
+    if (done) {
+      x = a.row_lse[row0 + r];
+    } else {
+      for (int s = lane; s < states; s += 32) m = fmaxf(m, state(r, s)[D]);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    float l = 0.f;
-    for (int s = lane; s < a.S; s += 32) {
-      const float x = p[s * (D + 1)];
-      l += x == -CUDART_INF_F ? 0.f : expf(x - m);
+      for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+      for (int s = lane; s < states; s += 32) {
+        const float* p = state(r, s);
+        if (cut)
+          l += (p[D] == m ? 1.f : fast_exp2(p[D] - m)) * p[D + 1];
+        else
+          l += p[D] == -CUDART_INF_F ? 0.f : expf(p[D] - m);
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+      x = l == 0.f ? -CUDART_INF_F : cut ? (m + log2f(l)) * kLn2 : m + logf(l);
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
     if (lane == 0) {
-      const float x = l == 0.f ? -CUDART_INF_F : m + logf(l);
       row_m[r] = m, row_l[r] = l, row_x[r] = x;
-      if (blockIdx.x == 0 && a.lse != nullptr)
-        a.lse[static_cast<int64_t>(i) * a.Hq + kvh * grp + r] = x;
+      if (blockIdx.x == 0 && a.lse != nullptr) a.lse[row0 + r] = x;
     }
   }
   __syncthreads();
   if (blockIdx.x == 0) {
     for (int idx = threadIdx.x; idx < grp * D; idx += kScoreThreads) {
       const int r = idx / D, e = idx % D;
-      const float* p = base + static_cast<int64_t>(r) * a.S * (D + 1);
+      const float m = row_m[r];
       float acc = 0.f;
 #pragma unroll 4
-      for (int s = 0; s < a.S; ++s) {
-        const float x = p[s * (D + 1) + D];
-        acc += (x == -CUDART_INF_F ? 0.f : expf(x - row_m[r])) * p[s * (D + 1) + e];
+      for (int s = 0; s < states; ++s) {
+        const float* p = state(r, s);
+        const float f = cut ? (p[D] == m ? 1.f : fast_exp2(p[D] - m))
+                            : p[D] == -CUDART_INF_F ? 0.f : expf(p[D] - m);
+        acc += f * p[e];
       }
-      a.out[(static_cast<int64_t>(i) * a.Hq + kvh * grp + r) * D + e] =
-          __float2bfloat16_rn(row_l[r] == 0.f ? 0.f : acc / row_l[r]);
+      a.out[(row0 + r) * D + e] =
+          __float2bfloat16_rn(row_l[r] == 0.f ? 0.f : acc / row_l[r] * a.out_scale);
     }
     return;
   }
-  const int64_t unit = static_cast<int64_t>(i) * a.Hkv + kvh;
   const float* x = a.logits + unit * a.logit_tokens * grp;
   float* sums = a.scores + unit * a.score_tokens;
   const int last = min(end, first + kScoreTokens);
@@ -127,6 +157,11 @@ cudaError_t launch_t(const ScoreArgs& a, int N, cudaStream_t stream) {
 cudaError_t launch_decode_scores(const ScoresLaunch& n, cudaStream_t stream) {
   ScoreArgs a{};
   a.ws = n.ws;
+  a.parts = n.parts;
+  a.spans = n.spans;
+  a.row_lse = n.row_lse;
+  a.out_scale = n.out_scale;
+  a.positions = n.positions;
   a.logits = n.logits;
   a.seq_lens = n.seq_lens;
   a.scores = n.scores;

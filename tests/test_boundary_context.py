@@ -37,12 +37,15 @@ def test_write_refusals(pa):
 
 
 def test_workspace_sizes(pa):
-    # One split of a short context needs none; sums always need the logits.
+    # Short contexts need none; longer ones two states for each CTA, at most two CTAs
+    # for each SM; sums always need the logits, a log-sum-exp for each row and a pair of
+    # numbers for each (request, kv head).
     assert pa.pa_decode_fp4_workspace_bytes(64, 32, 8, 128, 200) == 0
     assert pa.pa_decode_fp4_workspace_bytes(64, 32, 8, 128, 200, True) == \
-        64 * 32 * 129 * 4 + 64 * 32 * 200 * 4
-    assert pa.pa_decode_fp4_workspace_bytes(1, 64, 8, 128, 131072) % 16 == 0
-    assert pa.pa_decode_fp4_workspace_bytes(1, 64, 8, 128, 131072) >= 64 * 129 * 4
+        64 * 8 * 8 + 64 * 32 * 4 + 64 * 32 * 200 * 4
+    n = pa.pa_decode_fp4_workspace_bytes(1, 64, 8, 128, 131072)
+    assert n % 16 == 0 and 0 < n <= 304 * (16 + 2 * 8 * 130 * 4)
+    assert pa.pa_decode_fp4_workspace_bytes(4096, 64, 8, 128, 131072) == n
     n = pa.pa_decode_scores_workspace_bytes(3, 6, 2, 64, 1000)
     assert n == (3 * 6 * 2 * 65 * 4 + 15) // 16 * 16 + 3 * 6 * 1000 * 4
     for bad in ((-1, 4, 2, 64, 10), (1, 0, 2, 64, 10), (1, 4, 0, 64, 10), (1, 4, 2, 0, 10),
