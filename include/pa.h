@@ -571,8 +571,8 @@ pa_status pa_reshape_and_cache_fp4(const void* key, const void* value, int64_t k
  * pa_lse_merge does.  max_seq_len >= every seq_lens[i] sizes the splits (tokens of a
  * longer request are all read by its last split).  workspace: 16-byte aligned, at
  * least pa_decode_fp4_workspace_bytes(N, Hq, Hkv, d, max_seq_len, 0) bytes on the
- * device of the call (0: may be NULL); its contents are of no meaning between calls,
- * and calls that may overlap on the GPU need one each.
+ * device of the call; its contents are of no meaning between calls, and calls that may
+ * overlap on the GPU need one each.
  * Queries and softmax weights enter the tensor cores as f16 (queries exactly for |q|
  * in [2^-14, 65504], the weights to 2^-11), codes times scales exactly, sums are
  * fp32.  q, out: [N, Hq, d] bf16; lse: [N, Hq] fp32, nullable.  seq_lens[i] <= 0: out

@@ -774,9 +774,8 @@ def pa_decode_fp4(q, kv_cache, block_table, seq_lens, scale, k_scale, v_scale, w
                   lse=None, max_seq_len=None, return_lse=True, stream=None):
     """Decode (q [N, Hq, d] bf16, one query per request) over a 4-bit pool (see
     fp4_pool).  ``workspace``: a uint8 tensor of pa_decode_fp4_workspace_bytes(N, Hq,
-    Hkv, d, max_seq_len) bytes (none needed: None or empty).  ``max_seq_len`` defaults
-    to the longest of ``seq_lens`` (a read from the device).  Returns (out [N, Hq, d]
-    bf16, lse [N, Hq])."""
+    Hkv, d, max_seq_len) bytes.  ``max_seq_len`` defaults to the longest of ``seq_lens``
+    (a read from the device).  Returns (out [N, Hq, d] bf16, lse [N, Hq])."""
     return _decode_scores("pa_decode_fp4", q, kv_cache, block_table, seq_lens, scale,
                           (k_scale, v_scale), None, workspace, out, lse, max_seq_len, return_lse,
                           stream)

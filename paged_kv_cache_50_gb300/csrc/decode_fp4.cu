@@ -3,22 +3,22 @@
 //
 // The work is one line of 16-token pieces: request by request, kv head by kv head,
 // token by token.  It is cut into as many equal parts as CTAs are resident, whatever
-// the lengths: a CTA finds its part from the lengths' sum (a scan), and walks over
-// the (request, kv head) units in it.  A unit that lies in one part gives its output
-// at once; of one that is cut the CTAs leave states (o, maximum, sum), which a second
-// kernel merges: two per CTA at most, however long the context.  (One CTA per unit and
-// split, dealt by the hardware, left SMs idle for a quarter of the time on 64 requests
-// of U[128, 4096] tokens, and a quarter of the instructions were in CTAs' ends.)
+// the lengths, and a part into eight for the CTA's warps: each finds its place from the
+// lengths' sum (a scan) and walks over the (request, kv head) units in it by itself.  A
+// unit that lies with one warp gives its output at once.  Of one that is cut the warps
+// keep states (o, maximum, sum), which the CTA merges at its end, and what is cut
+// between CTAs a second kernel: two states per CTA at most, however long the context.
+// (One CTA per unit and split, dealt by the hardware, left SMs idle for a quarter of
+// the time on 64 requests of U[128, 4096] tokens, with a quarter of the instructions in
+// CTAs' ends; a CTA's warps side by side in one unit waited for each other at each
+// unit's end, longest where requests are short: 65 us against 52.)
 //
-// A CTA's eight warps take 32 tokens each in turn.  Each fetches its own: two pieces
-// (keys, values and scales of 16 tokens are one run of 18 d bytes: one bulk copy) into
-// a ring of its own, without a barrier shared by warps.  A warp takes its 32 tokens as
-// two M = 16 tiles of mma.m16n8k16 with the group's query heads as N (8 per n-tile):
-// S^T = K Q^T, one online softmax step over the 32 tokens, O^T += V^T P^T.  Codes are
-// widened to f16 and multiplied by their scales on the way into operand registers
-// (exact); q and the weights are f16.  At a unit's end the warps' states are merged
-// pairwise, lane to lane (a lane holds the same heads and dims in all warps), each
-// state through the ring slot that its warp has just read.
+// A warp fetches its own slices of 32 tokens: two pieces (keys, values and scales of 16
+// tokens are one run of 18 d bytes: one bulk copy) into a ring of its own.  It takes
+// them as two M = 16 tiles of mma.m16n8k16 with the group's query heads as N (8 per
+// n-tile): S^T = K Q^T, one online softmax step over the 32 tokens, O^T += V^T P^T.
+// Codes are widened to f16 and multiplied by their scales on the way into operand
+// registers (exact); q and the weights are f16.
 //
 // Bound by issue slots beside HBM: 2304 bytes for 16 tokens (d = 128) pass in 100
 // cycles of an SM, in which it issues 400 warp instructions, 200 of them on the ALU,
@@ -40,7 +40,6 @@ constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kPieces = 2;                   // 16-token pieces of a warp's slice
 constexpr int kSlice = 16 * kPieces;         // tokens
-constexpr int kStage = kSlice * kWarps;      // tokens of all warps' slices
 
 struct Fp4Args {
   const __nv_bfloat16* q;
@@ -48,11 +47,12 @@ struct Fp4Args {
   const int32_t* block_table;
   const int32_t* seq_lens;
   int N, max_blocks, Hq, Hkv, grp, bs, bs_log2, num_blocks;
-  int whole;          // units are not cut: their number is dealt, not their tokens
+  int whole;          // units are not cut between CTAs
   int positions;      // of a table row, at most INT_MAX - 1023
   float scale_log2;   // scale * k_scale * log2(e)
   float out_scale;    // v_scale
-  float* parts;       // [CTA][2][grp][d + 2] states of cut units
+  float4* held;       // [CTA][warp] states of units that began with an earlier warp
+  float* parts;       // [CTA][2][grp][d + 2] states of units that are cut between CTAs
   int4* cut;          // [CTA]: (first CTA, request, kv head) of the unit whose end it holds
   int2* spans;        // [N, Hkv] first and last CTA of a unit, or null
   float* row_lse;     // [N, Hq] of units that are not cut, with spans
@@ -70,12 +70,26 @@ struct Fp4Cfg {
   static constexpr int kCtas = NT == 1 ? 2 : 1;                    // per SM
   static constexpr int kSlots = (D == 128 ? 3 : 6) * (2 / kCtas);  // of a warp's ring
   static constexpr int kRingBytes = kWarps * kSlots * kSlotBytes;
-  // A lane's o of one n-tile (D / 4 floats) passes through a slot.
-  static_assert(D / 4 * 128 <= kSlotBytes, "a state's o fits a slot");
-  static constexpr int kOffStats = kRingBytes;                     // [warp][NT][lane] float4
-  static constexpr int kOffBar = kOffStats + kWarps * 32 * 16 * NT;
-  static constexpr int kOffScan = kOffBar + 8 * kWarps * kSlots;
-  static constexpr int kSmemBytes = kOffScan + 128;
+  // A state: for each n-tile o, then maxima and sums, 16 bytes a lane at a time.
+  static constexpr int kStateVecs = NT * (D / 16 + 1) * 32;
+  static_assert(kStateVecs * 16 <= kSlots * kSlotBytes, "a state fits a warp's ring");
+  static constexpr int kOffBar = kRingBytes;
+  static constexpr int kOffPlaces = kOffBar + 8 * kWarps * kSlots;
+  static constexpr int kSmemBytes = kOffPlaces + 512;
+};
+
+// Where in the line something is: a request and the pieces before it in that request's
+// units.
+struct Place {
+  long long inside;
+  int i, pad;
+};
+// What a warp has kept for the CTA's merge.
+struct Kept {
+  long long begin;     // of the unit, in the line
+  int i, h;
+  int where;           // 0: nothing, 1: in memory, 2: in the warp's ring
+  int ends;
 };
 
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
@@ -114,12 +128,12 @@ __device__ __forceinline__ void lds_words(uint32_t a, uint32_t (&w)[N]) {
     asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[0]) : "r"(a));
 }
 
-// Where a CTA (or a warp's fetches, ahead of it) stands in its part of the line.
+// Where a warp (or its fetches, ahead of it) stands in its part of the line.
 struct Walk {
   int i, h;            // unit
   int seq, after;      // tokens of request i and of request i + 1
   int tok, end;        // its tokens in this part
-  long long left;      // pieces (whole: units) of the part from here on
+  int left;            // pieces of the part from here on
 };
 
 __device__ __forceinline__ int length_of(const Fp4Args& a, int i) {
@@ -127,18 +141,13 @@ __device__ __forceinline__ int length_of(const Fp4Args& a, int i) {
   return i < a.N ? min(max(0, a.seq_lens[i]), a.positions) : 0;
 }
 // The share of the unit from token `tok` on.
-__device__ __forceinline__ void walk_enter(const Fp4Args& a, Walk& w, int tok) {
+__device__ __forceinline__ void walk_enter(Walk& w, int tok) {
   w.tok = tok;
-  if (a.whole) {
-    w.end = w.seq;
-  } else {
-    const int pieces = (w.seq - tok + 15) >> 4;
-    w.end = w.left < pieces ? tok + 16 * static_cast<int>(w.left) : w.seq;
-  }
+  w.end = w.left < ((w.seq - tok + 15) >> 4) ? tok + 16 * w.left : w.seq;
 }
 // On to the next unit with tokens; false at the part's end.
 __device__ __forceinline__ bool walk_next(const Fp4Args& a, Walk& w) {
-  w.left -= a.whole ? 1 : (w.end - w.tok + 15) >> 4;
+  w.left -= (w.end - w.tok + 15) >> 4;
   if (w.left <= 0) return false;
   if (++w.h == a.Hkv) {
     w.h = 0;
@@ -148,9 +157,117 @@ __device__ __forceinline__ bool walk_next(const Fp4Args& a, Walk& w) {
       w.after = length_of(a, w.i + 1);
     } while (w.seq == 0);
   }
-  walk_enter(a, w, 0);
+  walk_enter(w, 0);
   return true;
 }
+
+// A warp's running state; a lane holds the heads nt * 8 + 2 tid4 + {0, 1}, and of each
+// the D / 8 neighbouring dims from gid * (D / 8) on.
+template <int D, int NT>
+struct Fp4State {
+  float m[NT][2], l[NT][2], o[NT][D / 16][4];
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      m[nt][0] = m[nt][1] = -CUDART_INF_F;
+      l[nt][0] = l[nt][1] = 0.f;
+#pragma unroll
+      for (int md = 0; md < D / 16; ++md)
+        o[nt][md][0] = o[nt][md][1] = o[nt][md][2] = o[nt][md][3] = 0.f;
+    }
+  }
+  // To and from 16 bytes a lane at a time.
+  __device__ __forceinline__ void store(float4* p, int lane) const {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int md = 0; md < D / 16; ++md)
+        p[(nt * (D / 16 + 1) + md) * 32 + lane] =
+            make_float4(o[nt][md][0], o[nt][md][1], o[nt][md][2], o[nt][md][3]);
+      p[(nt * (D / 16 + 1) + D / 16) * 32 + lane] =
+          make_float4(m[nt][0], m[nt][1], l[nt][0], l[nt][1]);
+    }
+  }
+  __device__ __forceinline__ void merge(const float4* p, int lane) {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const float4 s4 = p[(nt * (D / 16 + 1) + D / 16) * 32 + lane];
+      const float om[2] = {s4.x, s4.y}, ol[2] = {s4.z, s4.w};
+      float f[2], g[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const float M = fmaxf(m[nt][j], om[j]);
+        // (Equal, also where both are -inf: 1.)
+        f[j] = m[nt][j] == M ? 1.f : fast_exp2(m[nt][j] - M);
+        g[j] = om[j] == M ? 1.f : fast_exp2(om[j] - M);
+        m[nt][j] = M;
+        l[nt][j] = f[j] * l[nt][j] + g[j] * ol[j];
+      }
+#pragma unroll
+      for (int md = 0; md < D / 16; ++md) {
+        const float4 y = p[(nt * (D / 16 + 1) + md) * 32 + lane];
+        o[nt][md][0] = fmaf(g[0], y.x, f[0] * o[nt][md][0]);
+        o[nt][md][1] = fmaf(g[1], y.y, f[1] * o[nt][md][1]);
+        o[nt][md][2] = fmaf(g[0], y.z, f[0] * o[nt][md][2]);
+        o[nt][md][3] = fmaf(g[1], y.w, f[1] * o[nt][md][3]);
+      }
+    }
+  }
+  // The finished rows of unit (i, h).
+  __device__ __forceinline__ void output(const Fp4Args& a, int i, int h, int lane) const {
+    const int gid = lane >> 2, tid4 = lane & 3;
+    const int64_t row0 = static_cast<int64_t>(i) * a.Hq + h * a.grp;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int r = nt * 8 + 2 * tid4 + j;
+        if (r >= a.grp) continue;
+        const float f = l[nt][j] == 0.f ? 0.f : a.out_scale / l[nt][j];
+        __nv_bfloat16* dst = a.out + (row0 + r) * D + gid * (D / 8);
+        if ((reinterpret_cast<uintptr_t>(a.out) & 15u) == 0) {
+#pragma unroll
+          for (int k = 0; k < D / 64; ++k) {
+            uint32_t w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              w[e] = pack_bf16(o[nt][4 * k + e][j] * f, o[nt][4 * k + e][2 + j] * f);
+            reinterpret_cast<uint4*>(dst)[k] = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        } else {
+#pragma unroll
+          for (int md = 0; md < D / 16; ++md) {
+            dst[2 * md] = __float2bfloat16_rn(o[nt][md][j] * f);
+            dst[2 * md + 1] = __float2bfloat16_rn(o[nt][md][2 + j] * f);
+          }
+        }
+        if (gid == 0) {
+          const float x = l[nt][j] == 0.f ? -CUDART_INF_F : (m[nt][j] + log2f(l[nt][j])) * kLn2;
+          if (a.lse != nullptr) a.lse[row0 + r] = x;
+          if (a.spans != nullptr) a.row_lse[row0 + r] = x;
+        }
+      }
+    if (a.spans != nullptr && lane == 0)
+      a.spans[static_cast<int64_t>(i) * a.Hkv + h] = make_int2(blockIdx.x, blockIdx.x);
+  }
+  // ... or, of a unit that is cut between CTAs, for the second kernel: [grp][d + 2].
+  __device__ __forceinline__ void part(float* to, int grp, int lane) const {
+    const int gid = lane >> 2, tid4 = lane & 3;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int r = nt * 8 + 2 * tid4 + j;
+        if (r >= grp) continue;
+        float* dst = to + r * (D + 2);
+#pragma unroll
+        for (int md = 0; md < D / 16; ++md)
+          *reinterpret_cast<float2*>(dst + gid * (D / 8) + 2 * md) =
+              make_float2(o[nt][md][j], o[nt][md][2 + j]);
+        if (gid == 0) *reinterpret_cast<float2*>(dst + D) = make_float2(m[nt][j], l[nt][j]);
+      }
+  }
+};
 
 template <int D, int NT, bool LOGITS>
 __global__ void __launch_bounds__(kThreads, Fp4Cfg<D, NT>::kCtas) decode_fp4_kernel(
@@ -180,7 +297,7 @@ __global__ void __launch_bounds__(kThreads, Fp4Cfg<D, NT>::kCtas) decode_fp4_ker
   // A thread sums the pieces of neighbouring requests; the CTA scans the threads' sums.
   const int chunk = (a.N + kThreads - 1) / kThreads;
   const int r0 = min(a.N, static_cast<int>(threadIdx.x) * chunk), r1 = min(a.N, r0 + chunk);
-  auto weight = [&](int seq) { return a.whole ? (seq > 0 ? 1 : 0) : (seq + 15) >> 4; };
+  auto weight = [&](int seq) { return (seq + 15) >> 4; };
   long long mine = 0;
   for (int i = r0; i < r1; ++i) mine += weight(length_of(a, i));
   long long upto = mine;
@@ -189,7 +306,7 @@ __global__ void __launch_bounds__(kThreads, Fp4Cfg<D, NT>::kCtas) decode_fp4_ker
     const long long y = __shfl_up_sync(0xffffffffu, upto, o);
     if (lane >= o) upto += y;
   }
-  long long* scan = reinterpret_cast<long long*>(smem + C::kOffScan);
+  long long* scan = reinterpret_cast<long long*>(smem + C::kOffPlaces);
   if (lane == 31) scan[warp] = upto;
   __syncthreads();
   long long total = 0, before = upto - mine;
@@ -201,28 +318,51 @@ __global__ void __launch_bounds__(kThreads, Fp4Cfg<D, NT>::kCtas) decode_fp4_ker
   __syncthreads();
   total *= a.Hkv;
   before *= a.Hkv;
+  mine *= a.Hkv;
   // Parts of equal length, in whole slices.
-  long long share = (total + gridDim.x - 1) / gridDim.x;
-  if (!a.whole) share = (share + kPieces - 1) / kPieces * kPieces;
-  const long long g0 = cta * share, g1 = min(total, g0 + share);
-  if (threadIdx.x == 0) scan[0] = -1;
-  __syncthreads();
-  if (g0 >= before && g0 < before + mine * a.Hkv && g0 < g1) {
-    // The unit that g0 lies in is among this thread's requests.
+  const long long share = ((total + gridDim.x - 1) / gridDim.x + kPieces - 1) / kPieces * kPieces;
+  long long g0 = min(total, cta * share), g1 = min(total, g0 + share);
+  Place* places = reinterpret_cast<Place*>(smem + C::kOffPlaces);   // [kWarps]
+  // The place of position g (< total), found by the thread that has its request.
+  auto locate = [&](long long g, Place* to) {
+    if (g < before || g >= before + mine) return;
     int i = r0;
     long long at = before;
     for (; i + 1 < r1; ++i) {
       const long long n = static_cast<long long>(weight(length_of(a, i))) * a.Hkv;
-      if (g0 < at + n) break;
+      if (g < at + n) break;
       at += n;
     }
-    scan[0] = i;
-    scan[1] = g0 - at;
+    *to = Place{g - at, i, 0};
+  };
+  if (a.whole) {
+    // The units that begin in the part.
+    const long long edge[2] = {g0, g1};
+    for (int k = 0; k < 2; ++k)
+      if (edge[k] < total) locate(edge[k], &places[k]);
+    __syncthreads();
+    long long up[2];
+    for (int k = 0; k < 2; ++k) {
+      up[k] = edge[k];
+      if (edge[k] < total) {
+        const int n = weight(length_of(a, places[k].i));
+        up[k] += (n - places[k].inside % n) % n;
+      }
+    }
+    __syncthreads();
+    g0 = up[0], g1 = up[1];
   }
+  const long long per = ((g1 - g0 + kWarps - 1) / kWarps + kPieces - 1) / kPieces * kPieces;
+  for (int w = 0; w < kWarps; ++w)
+    if (g0 + w * per < g1) locate(g0 + w * per, &places[w]);
   __syncthreads();
-  const bool any = scan[0] >= 0;
-  const int first_request = static_cast<int>(scan[0]);
-  const long long inside = scan[1];   // pieces of that request's units before the part
+  const long long w0 = g0 + warp * per, w1 = min(g1, w0 + per);
+  const bool any = w0 < w1;
+  const Place place = places[warp];
+  __syncthreads();
+  Kept* kept = reinterpret_cast<Kept*>(smem + C::kOffPlaces);   // [kWarps][unit began before, begins]
+  if (lane < 2) kept[2 * warp + lane].where = 0;
+  __syncwarp();
   if (cta == 0 && threadIdx.x < 32) {
     bool past = false;
     for (int i = lane; i < a.N; i += 32) past |= a.seq_lens[i] > a.positions;
@@ -237,64 +377,61 @@ __global__ void __launch_bounds__(kThreads, Fp4Cfg<D, NT>::kCtas) decode_fp4_ker
         for (int k = threadIdx.x; k < a.Hq; k += kThreads)
           a.lse[static_cast<int64_t>(i) * a.Hq + k] = -CUDART_INF_F;
     }
-  if (a.cut != nullptr && threadIdx.x == 0) a.cut[cta] = make_int4(-1, 0, 0, 0);
-  if (!any) return;
-  Walk at, ahead;
-  at.i = first_request;
-  at.seq = length_of(a, at.i);
-  at.after = length_of(a, at.i + 1);
-  at.left = g1 - g0;
-  {
+  if (!a.whole && threadIdx.x == 0) a.cut[cta] = make_int4(-1, 0, 0, 0);
+  Walk at{};
+  if (any) {
+    at.i = place.i;
+    at.seq = length_of(a, at.i);
+    at.after = length_of(a, at.i + 1);
+    at.left = static_cast<int>(min(w1 - w0, static_cast<long long>(INT_MAX)));
     const int n = weight(at.seq);
-    at.h = static_cast<int>(inside / n);
-    walk_enter(a, at, a.whole ? 0 : 16 * static_cast<int>(inside - static_cast<long long>(at.h) * n));
+    at.h = static_cast<int>(place.inside / n);
+    walk_enter(at, 16 * static_cast<int>(place.inside - static_cast<long long>(at.h) * n));
   }
-  ahead = at;
-  long long pos = g0;   // of the unit's first token in this part
+  Walk ahead = at;
+  long long pos = w0;   // of the unit's first token in this part
 
   // ------------------------------------------------------------ fetches
-  int fetch_tok = ahead.tok + warp * kSlice;
-  bool more = true;
-  auto settle = [&]() {   // on to the next slice that is there
-    while (more && fetch_tok >= ahead.end) {
-      more = walk_next(a, ahead);
-      if (more) fetch_tok = ahead.tok + warp * kSlice;
-    }
-  };
+  const int groups = a.bs >> 4;
+  const int64_t head_bytes = static_cast<int64_t>(groups) * C::kPairBytes;
+  const int64_t block_bytes = head_bytes * a.Hkv;
+  bool more = any;
+  // The lane's piece of the next slice to be fetched (lanes < kPieces), and its block.
+  int tok = ahead.tok + 16 * lane;
+  const uint8_t* head = a.cache + ahead.h * head_bytes;
+  const int32_t* table = a.block_table + static_cast<int64_t>(ahead.i) * a.max_blocks;
   auto lookup = [&]() {
-    const int tok = fetch_tok + 16 * lane;
     // (A plain load: the table may be the previous kernel's output.)
-    return more && lane < kPieces && tok < ahead.end
-               ? a.block_table[static_cast<int64_t>(ahead.i) * a.max_blocks +
-                               div_bs(tok, a.bs, a.bs_log2)]
-               : -1;
+    return more && lane < kPieces && tok < ahead.end ? table[div_bs(tok, a.bs, a.bs_log2)] : -1;
   };
-  settle();
-  int blk = lookup();      // of the next slice to be fetched
+  int blk = lookup();
   int fill = 0;            // its slot
   uint32_t loaded = 0;     // kPieces bits per slot: pieces that are there
-  bool ok = true;          // (a warp that gave up fetches no more, and goes on to the barriers)
+  bool ok = true;          // (a warp that gave up fetches no more)
   int flying = 0;          // slices on their way
   auto fetch = [&]() {
     if (!more || !ok) return;
-    const int tok = fetch_tok + 16 * lane;
     const bool piece = lane < kPieces && tok < ahead.end;
     const bool good = piece && blk >= 0 && blk < a.num_blocks;
     const unsigned there = __ballot_sync(0xffffffffu, good);
-    if (__any_sync(0xffffffffu, piece && !good) && lane == 0) record_error(a.err, PA_DEVERR_BLOCK_ID);
+    if (piece && !good) record_error(a.err, PA_DEVERR_BLOCK_ID);
     loaded = (loaded & ~(3u << (kPieces * fill))) | (there << (kPieces * fill));
     const uint32_t bar = bars + 8 * fill;
     if (lane == 0) tc::mbar_arrive_expect_tx(bar, __popc(there) * C::kPairBytes);
     __syncwarp();
-    if (good) {
-      const int g = mod_bs(tok, a.bs, a.bs_log2) >> 4;
+    if (good)
       bulk_load(ring + fill * C::kSlotBytes + lane * C::kPairBytes,
-                a.cache + fp4::pair_at(blk, ahead.h, g, a.Hkv, a.bs >> 4, D), C::kPairBytes, bar);
-    }
+                head + blk * block_bytes + (mod_bs(tok, a.bs, a.bs_log2) >> 4) * C::kPairBytes,
+                C::kPairBytes, bar);
     if (++fill == C::kSlots) fill = 0;
     ++flying;
-    fetch_tok += kStage;
-    settle();
+    tok += kSlice;
+    if (tok - 16 * lane >= ahead.end) {
+      more = walk_next(a, ahead);
+      tok = 16 * lane;   // (a part's later units are entered at their start)
+      head = a.cache + ahead.h * head_bytes;
+      table = a.block_table + static_cast<int64_t>(ahead.i) * a.max_blocks;
+    }
     blk = lookup();
   };
   for (int k = 0; k < C::kSlots; ++k) fetch();
@@ -303,7 +440,8 @@ __global__ void __launch_bounds__(kThreads, Fp4Cfg<D, NT>::kCtas) decode_fp4_ker
   const int src_a = 8 * tid4 + (gid >> 1), src_b = src_a + 4;
   const uint32_t sel = (gid & 1) ? 0x7632u : 0x5410u;
   int slot = 0, parity = 0;   // of the slice worked on
-  for (bool live = true; live;) {
+  Fp4State<D, NT> st;
+  for (bool live = any; live;) {
     // ---------------------------------------------------------- one unit
     const int64_t row0 = static_cast<int64_t>(at.i) * a.Hq + at.h * grp;
     uint32_t qf[NT][kK][2];
@@ -323,17 +461,8 @@ __global__ void __launch_bounds__(kThreads, Fp4Cfg<D, NT>::kCtas) decode_fp4_ker
         }
       }
     }
-    float m_r[NT][2], l_r[NT][2], o[NT][kK][4];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      m_r[nt][0] = m_r[nt][1] = -CUDART_INF_F;
-      l_r[nt][0] = l_r[nt][1] = 0.f;
-#pragma unroll
-      for (int md = 0; md < kK; ++md)
-        o[nt][md][0] = o[nt][md][1] = o[nt][md][2] = o[nt][md][3] = 0.f;
-    }
-    int own = -1;   // the slot that the state may pass through
-    for (int tb = at.tok + warp * kSlice; tb < at.end; tb += kStage) {
+    st.clear();
+    for (int tb = at.tok; tb < at.end; tb += kSlice) {
       ok = ok && __all_sync(0xffffffffu, tc::mbar_wait(bars + 8 * slot, parity));
       if (!ok) continue;
       const uint32_t here = loaded >> (kPieces * slot);
@@ -426,22 +555,22 @@ __global__ void __launch_bounds__(kThreads, Fp4Cfg<D, NT>::kCtas) decode_fp4_ker
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-          if (mx > m_r[nt][j] + kRescale) {
-            const float alpha = fast_exp2(m_r[nt][j] - mx);   // 0 when the old one is -inf
-            m_r[nt][j] = mx;
-            l_r[nt][j] *= alpha;
+          if (mx > st.m[nt][j] + kRescale) {
+            const float alpha = fast_exp2(st.m[nt][j] - mx);   // 0 when the old one is -inf
+            st.m[nt][j] = mx;
+            st.l[nt][j] *= alpha;
 #pragma unroll
             for (int md = 0; md < kK; ++md) {
-              o[nt][md][j] *= alpha;
-              o[nt][md][2 + j] *= alpha;
+              st.o[nt][md][j] *= alpha;
+              st.o[nt][md][2 + j] *= alpha;
             }
           }
-          const float mu = m_r[nt][j] == -CUDART_INF_F ? 0.f : m_r[nt][j];
+          const float mu = st.m[nt][j] == -CUDART_INF_F ? 0.f : st.m[nt][j];
 #pragma unroll
           for (int p = 0; p < kPieces; ++p) {
             pr[p][j] = fast_exp2(x[p][nt][j] - mu);
             pr[p][2 + j] = fast_exp2(x[p][nt][2 + j] - mu);
-            l_r[nt][j] += pr[p][j] + pr[p][2 + j];
+            st.l[nt][j] += pr[p][j] + pr[p][2 + j];
           }
         }
 #pragma unroll
@@ -491,16 +620,13 @@ __global__ void __launch_bounds__(kThreads, Fp4Cfg<D, NT>::kCtas) decode_fp4_ker
                                     fp4::mul2(cd[0][b], scd), fp4::mul2(cd[1][b], scd)};
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
-              mma_f16_16816(o[nt][4 * w + b], am, pb[p][nt][0], pb[p][nt][1]);
+              mma_f16_16816(st.o[nt][4 * w + b], am, pb[p][nt][0], pb[p][nt][1]);
           }
         }
       }
       __syncwarp();   // every lane has read the slot
       --flying;
-      if (tb + kStage < at.end)
-        fetch();
-      else
-        own = slot;
+      fetch();
       if (++slot == C::kSlots) slot = 0, parity ^= 1;
     }
 
@@ -510,160 +636,119 @@ __global__ void __launch_bounds__(kThreads, Fp4Cfg<D, NT>::kCtas) decode_fp4_ker
 #pragma unroll
       for (int j = 0; j < 2; ++j)
 #pragma unroll
-        for (int k = 4; k < 32; k <<= 1) l_r[nt][j] += __shfl_xor_sync(0xffffffffu, l_r[nt][j], k);
-    // Eight states to one in three rounds: the upper half's warps hand theirs to the
-    // lower half's.  A warp without tokens has m = -inf and l = 0, and no o.
-    float4* stats = reinterpret_cast<float4*>(smem + C::kOffStats);
-    int* slots = reinterpret_cast<int*>(smem + C::kOffScan);   // [warp] slot of its o, or -1
-#pragma unroll 1
-    for (int half = kWarps / 2; half > 0; half >>= 1) {
-      const bool gives = warp >= half && warp < 2 * half;
-      if (gives) {
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-          stats[(warp * NT + nt) * 32 + lane] =
-              make_float4(m_r[nt][0], m_r[nt][1], l_r[nt][0], l_r[nt][1]);
-        if (lane == 0) slots[warp] = own;
-      }
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        if (nt > 0) __syncthreads();   // the slot's first contents have been read
-        if (gives && own >= 0) {
-          float4* dst = reinterpret_cast<float4*>(smem + (warp * C::kSlots + own) * C::kSlotBytes);
-#pragma unroll
-          for (int md = 0; md < kK; ++md)
-            dst[md * 32 + lane] = make_float4(o[nt][md][0], o[nt][md][1], o[nt][md][2], o[nt][md][3]);
-        }
-        __syncthreads();
-        if (warp < half) {
-          const int other = warp + half, from = slots[other];
-          if (from >= 0) {   // warp-uniform
-            const float4 s4 = stats[(other * NT + nt) * 32 + lane];
-            const float4* src =
-                reinterpret_cast<const float4*>(smem + (other * C::kSlots + from) * C::kSlotBytes);
-            const float om[2] = {s4.x, s4.y}, ol[2] = {s4.z, s4.w};
-            float f[2], g[2];
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              const float M = fmaxf(m_r[nt][j], om[j]);
-              // (Equal, also where both are -inf: 1.)
-              f[j] = m_r[nt][j] == M ? 1.f : fast_exp2(m_r[nt][j] - M);
-              g[j] = om[j] == M ? 1.f : fast_exp2(om[j] - M);
-              m_r[nt][j] = M;
-              l_r[nt][j] = f[j] * l_r[nt][j] + g[j] * ol[j];
-            }
-#pragma unroll
-            for (int md = 0; md < kK; ++md) {
-              const float4 y = src[md * 32 + lane];
-              o[nt][md][0] = fmaf(g[0], y.x, f[0] * o[nt][md][0]);
-              o[nt][md][1] = fmaf(g[1], y.y, f[1] * o[nt][md][1]);
-              o[nt][md][2] = fmaf(g[0], y.z, f[0] * o[nt][md][2]);
-              o[nt][md][3] = fmaf(g[1], y.w, f[1] * o[nt][md][3]);
-            }
-          }
-        }
-      }
-    }
-    __syncthreads();   // read, before a slot or a state is written again
-    if (own >= 0) {
-      tc::fence_proxy_async_smem();   // the state lay where the copy will land
-      __syncwarp();
-      fetch();
-    }
+        for (int k = 4; k < 32; k <<= 1)
+          st.l[nt][j] += __shfl_xor_sync(0xffffffffu, st.l[nt][j], k);
     const bool starts = at.tok == 0, ends = at.end == at.seq;
-    if (warp == 0) {
-      // A lane's dims of a head are D / 8 neighbouring ones.
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int r = nt * 8 + 2 * tid4 + j;
-          if (r >= grp) continue;
-          const float L = l_r[nt][j], m = m_r[nt][j];
-          if (starts && ends) {
-            const float f = L == 0.f ? 0.f : a.out_scale / L;
-            __nv_bfloat16* dst = a.out + (row0 + r) * D + gid * (D / 8);
-            uint32_t w[kK];
-#pragma unroll
-            for (int md = 0; md < kK; ++md) w[md] = pack_bf16(o[nt][md][j] * f, o[nt][md][2 + j] * f);
-            if ((reinterpret_cast<uintptr_t>(a.out) & 15u) == 0) {
-#pragma unroll
-              for (int k = 0; k < D / 64; ++k)
-                reinterpret_cast<uint4*>(dst)[k] =
-                    make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
-            } else {
-#pragma unroll
-              for (int md = 0; md < kK; ++md) {
-                dst[2 * md] = __float2bfloat16_rn(o[nt][md][j] * f);
-                dst[2 * md + 1] = __float2bfloat16_rn(o[nt][md][2 + j] * f);
-              }
-            }
-            if (gid == 0) {
-              const float x = L == 0.f ? -CUDART_INF_F : (m + log2f(L)) * kLn2;
-              if (a.lse != nullptr) a.lse[row0 + r] = x;
-              if (a.spans != nullptr) a.row_lse[row0 + r] = x;
-            }
-          } else {
-            float* dst = a.parts + ((static_cast<int64_t>(cta) * 2 + starts) * grp + r) * (D + 2);
-#pragma unroll
-            for (int md = 0; md < kK; ++md)
-              *reinterpret_cast<float2*>(dst + gid * (D / 8) + 2 * md) =
-                  make_float2(o[nt][md][j], o[nt][md][2 + j]);
-            if (gid == 0) dst[D] = m, dst[D + 1] = L;
-          }
-        }
-      if (lane == 0) {
-        if (!starts && ends)
-          a.cut[cta] = make_int4(static_cast<int>((pos - (at.tok >> 4)) / share), at.i, at.h, 0);
-        if (starts && a.spans != nullptr)
-          a.spans[static_cast<int64_t>(at.i) * a.Hkv + at.h] = make_int2(
-              cta, ends ? cta : static_cast<int>((pos + ((at.seq + 15) >> 4) - 1) / share));
-      }
-    }
-    pos += a.whole ? 1 : (at.end - at.tok + 15) >> 4;
+    const Walk was = at;
     live = walk_next(a, at);
+    if (starts && ends) {
+      st.output(a, was.i, was.h, lane);
+    } else {
+      // Kept until all warps are done: the last one in the ring, which is free by then.
+      if (live)
+        st.store(a.held + static_cast<int64_t>(cta * kWarps + warp) * C::kStateVecs, lane);
+      else if (ok)
+        st.store(reinterpret_cast<float4*>(smem + warp * C::kSlots * C::kSlotBytes), lane);
+      if (lane == 0)
+        kept[2 * warp + starts] = Kept{pos - (was.tok >> 4), was.i, was.h, live ? 1 : 2, ends};
+    }
+    pos += (was.end - was.tok + 15) >> 4;
   }
   if (!ok && lane == 0) {
-    // Given up: the outputs are invalid.  No copy may still be landing when the CTA
-    // exits: what is on its way gets one more bounded wait each.
+    // Given up: the outputs are invalid.  No copy may still be landing when the ring is
+    // read as a state or the CTA exits: what is on its way gets one more bounded wait each.
     record_error(a.err, PA_DEVERR_TIMEOUT);
     for (int k = 0; k < flying; ++k) {
       tc::mbar_wait(bars + 8 * slot, parity);
       if (++slot == C::kSlots) slot = 0, parity ^= 1;
     }
   }
+  __syncthreads();
+  // ------------------------------------------------------------ units cut between warps
+  // Run 0: the unit that began in an earlier CTA; run k: the one that begins with warp
+  // k - 1 and goes on.  A run is the state that begins it and the first states of the
+  // warps behind, up to one that ends.
+  auto state_of = [&](int w, int where) {
+    return where == 1 ? a.held + static_cast<int64_t>(cta * kWarps + w) * C::kStateVecs
+                      : reinterpret_cast<const float4*>(smem + w * C::kSlots * C::kSlotBytes);
+  };
+  for (int run = warp; run <= kWarps; run += kWarps) {
+    const int from = run == 0 ? 0 : run - 1;
+    const Kept first = kept[2 * from + (run > 0)];
+    if (first.where == 0) continue;   // warp-uniform
+    st.clear();
+    st.merge(state_of(from, first.where), lane);
+    bool ends = first.ends;
+    for (int w = from + 1; w < kWarps && !ends; ++w) {
+      const Kept next = kept[2 * w];
+      if (next.where == 0) break;
+      st.merge(state_of(w, next.where), lane);
+      ends = next.ends;
+    }
+    const bool starts = run > 0;
+    if (starts && ends) {
+      st.output(a, first.i, first.h, lane);
+      continue;
+    }
+    st.part(a.parts + (static_cast<int64_t>(cta) * 2 + starts) * grp * (D + 2), grp, lane);
+    if (lane != 0) continue;
+    if (ends) a.cut[cta] = make_int4(static_cast<int>(first.begin / share), first.i, first.h, 0);
+    if (starts && a.spans != nullptr)
+      a.spans[static_cast<int64_t>(first.i) * a.Hkv + first.h] = make_int2(
+          cta, static_cast<int>((first.begin + weight(length_of(a, first.i)) - 1) / share));
+  }
 }
 
-// The states of a cut unit, one CTA for each CTA that holds a unit's end: the first
-// CTA's second state, then the following CTAs' first states up to this one's.
+// The states of a cut unit, one CTA for each CTA that holds a unit's end and each head:
+// the first CTA's second state, then the following CTAs' first states up to this one's.
 template <int D>
-__global__ void __launch_bounds__(128) decode_fp4_merge_kernel(
-    const __grid_constant__ Fp4Args a) {
+__global__ void __launch_bounds__(D) decode_fp4_merge_kernel(const __grid_constant__ Fp4Args a) {
+  __shared__ float factor[D];
+  __shared__ float red[2][D / 32];
   pdl_wait();
   pdl_trigger();
-  const int c1 = blockIdx.x;
+  const int c1 = blockIdx.x, r = blockIdx.y, e = threadIdx.x;
   const int4 u = a.cut[c1];
   if (u.x < 0) return;
-  const int e = threadIdx.x % D;
-  for (int r = threadIdx.x / D; r < a.grp; r += 128 / D) {
-    auto state = [&](int c) {
-      return a.parts + ((static_cast<int64_t>(c) * 2 + (c == u.x)) * a.grp + r) * (D + 2);
-    };
-    float M = -CUDART_INF_F;
-    for (int c = u.x; c <= c1; ++c) M = fmaxf(M, state(c)[D]);
-    float L = 0.f, acc = 0.f;
-#pragma unroll 4
-    for (int c = u.x; c <= c1; ++c) {
-      const float* s = state(c);
-      const float f = s[D] == M ? 1.f : fast_exp2(s[D] - M);
-      L += f * s[D + 1];
-      acc += f * s[e];
-    }
-    const int64_t row = static_cast<int64_t>(u.y) * a.Hq + u.z * a.grp + r;
-    a.out[row * D + e] = __float2bfloat16_rn(L == 0.f ? 0.f : acc / L * a.out_scale);
-    if (e == 0 && a.lse != nullptr)
-      a.lse[row] = L == 0.f ? -CUDART_INF_F : (M + log2f(L)) * kLn2;
+  const int warp = e >> 5, lane = e & 31;
+  auto state = [&](int c) {
+    return a.parts + ((static_cast<int64_t>(c) * 2 + (c == u.x)) * a.grp + r) * (D + 2);
+  };
+  // D states at a time (more than a few dozen are rare).
+  float M = -CUDART_INF_F, L = 0.f, acc = 0.f;
+  for (int c0 = u.x; c0 <= c1; c0 += D) {
+    const bool mine = c0 + e <= c1;
+    const float m = mine ? state(c0 + e)[D] : -CUDART_INF_F;
+    const float l = mine ? state(c0 + e)[D + 1] : 0.f;
+    float mx = m;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    if (lane == 0) red[0][warp] = mx;
+    __syncthreads();
+    float top = M;
+#pragma unroll
+    for (int w = 0; w < D / 32; ++w) top = fmaxf(top, red[0][w]);
+    const float f = m == top ? 1.f : fast_exp2(m - top);
+    factor[e] = f;
+    float sum = mine ? f * l : 0.f;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (lane == 0) red[1][warp] = sum;
+    __syncthreads();
+    const float old = M == top ? 1.f : fast_exp2(M - top);
+    L *= old;
+    acc *= old;
+#pragma unroll
+    for (int w = 0; w < D / 32; ++w) L += red[1][w];
+    const int n = min(D, c1 - c0 + 1);
+#pragma unroll 8
+    for (int k = 0; k < n; ++k) acc += factor[k] * state(c0 + k)[e];
+    M = top;
+    __syncthreads();
   }
+  const int64_t row = static_cast<int64_t>(u.y) * a.Hq + u.z * a.grp + r;
+  a.out[row * D + e] = __float2bfloat16_rn(L == 0.f ? 0.f : acc / L * a.out_scale);
+  if (e == 0 && a.lse != nullptr) a.lse[row] = L == 0.f ? -CUDART_INF_F : (M + log2f(L)) * kLn2;
 }
 
 template <int D, int NT, bool LOGITS>
@@ -675,7 +760,7 @@ cudaError_t launch_t(const Fp4Args& a, int ctas, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   e = launch_pdl(kern, dim3(ctas), dim3(kThreads), C::kSmemBytes, stream, a);
   if (e != cudaSuccess || a.whole || a.spans != nullptr) return e;
-  return launch_pdl(decode_fp4_merge_kernel<D>, dim3(ctas), dim3(128), 0, stream, a);
+  return launch_pdl(decode_fp4_merge_kernel<D>, dim3(ctas, a.grp), dim3(D), 0, stream, a);
 }
 template <int D, int NT>
 cudaError_t launch_n(const Fp4Args& a, int ctas, cudaStream_t stream) {
@@ -693,9 +778,12 @@ int decode_fp4_ctas(int N, int Hq, int Hkv, int max_seq_len, int sm_count) {
   return static_cast<int>(std::max(1LL, std::min(most, std::max(units, slices))));
 }
 
-// Units are not cut where the longest is at most two rounds of a CTA's warps: a second
-// launch would cost more than the balance brings.
-bool decode_fp4_whole(int max_seq_len) { return max_seq_len <= 2 * kStage; }
+// Units are not cut between CTAs where the longest is at most two slices for each warp:
+// a second launch would cost more than the balance brings.
+bool decode_fp4_whole(int max_seq_len) { return max_seq_len <= 2 * kSlice * kWarps; }
+size_t decode_fp4_held(int ctas, int grp, int d) {
+  return static_cast<size_t>(ctas) * kWarps * (grp > 8 ? 2 : 1) * (d / 16 + 1) * 512;
+}
 
 }  // namespace
 
@@ -704,6 +792,8 @@ Fp4Workspace decode_fp4_workspace(int N, int Hq, int Hkv, int d, int max_seq_len
   Fp4Workspace w{};
   const size_t n = static_cast<size_t>(N);
   const int ctas = decode_fp4_ctas(N, Hq, Hkv, max_seq_len, sm_count);
+  w.held = w.bytes;
+  w.bytes += decode_fp4_held(ctas, Hq / Hkv, d);
   if (!decode_fp4_whole(max_seq_len)) {
     w.cut = w.bytes;
     w.bytes += static_cast<size_t>(ctas) * sizeof(int4);
@@ -743,6 +833,7 @@ cudaError_t launch_decode_fp4(const DecodeFp4Launch& n, cudaStream_t stream) {
   const Fp4Workspace w =
       decode_fp4_workspace(n.N, n.Hq, n.Hkv, n.d, n.max_seq_len, n.scores != nullptr, n.sm_count);
   char* ws = static_cast<char*>(n.workspace);
+  a.held = reinterpret_cast<float4*>(ws + w.held);
   if (!a.whole) {
     a.cut = reinterpret_cast<int4*>(ws + w.cut);
     a.parts = reinterpret_cast<float*>(ws + w.parts);

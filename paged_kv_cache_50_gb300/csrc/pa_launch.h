@@ -176,7 +176,7 @@ struct DecodeFp4Launch {
 cudaError_t launch_decode_fp4(const DecodeFp4Launch& n, cudaStream_t stream);
 // Offsets in the workspace, and its size.
 struct Fp4Workspace {
-  size_t cut, parts, spans, row_lse, logits, bytes;
+  size_t held, cut, parts, spans, row_lse, logits, bytes;
 };
 Fp4Workspace decode_fp4_workspace(int N, int Hq, int Hkv, int d, int max_seq_len, bool sums,
                                   int sm_count);

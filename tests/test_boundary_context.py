@@ -37,15 +37,17 @@ def test_write_refusals(pa):
 
 
 def test_workspace_sizes(pa):
-    # Short contexts need none; longer ones two states for each CTA, at most two CTAs
-    # for each SM; sums always need the logits, a log-sum-exp for each row and a pair of
-    # numbers for each (request, kv head).
-    assert pa.pa_decode_fp4_workspace_bytes(64, 32, 8, 128, 200) == 0
+    # A state for each of eight warps of at most two CTAs for each SM; longer contexts two
+    # more for each CTA, whatever the batch; sums a log-sum-exp for each row, a pair of
+    # numbers for each (request, kv head) and the logits.
+    held = 304 * 8 * 9 * 512
+    assert pa.pa_decode_fp4_workspace_bytes(64, 32, 8, 128, 200) == held
     assert pa.pa_decode_fp4_workspace_bytes(64, 32, 8, 128, 200, True) == \
-        64 * 8 * 8 + 64 * 32 * 4 + 64 * 32 * 200 * 4
+        held + 64 * 8 * 8 + 64 * 32 * 4 + 64 * 32 * 200 * 4
     n = pa.pa_decode_fp4_workspace_bytes(1, 64, 8, 128, 131072)
-    assert n % 16 == 0 and 0 < n <= 304 * (16 + 2 * 8 * 130 * 4)
+    assert n == held + 304 * (16 + 2 * 8 * 130 * 4)
     assert pa.pa_decode_fp4_workspace_bytes(4096, 64, 8, 128, 131072) == n
+    assert pa.pa_decode_fp4_workspace_bytes(1, 2, 1, 64, 16) == 8 * 5 * 512
     n = pa.pa_decode_scores_workspace_bytes(3, 6, 2, 64, 1000)
     assert n == (3 * 6 * 2 * 65 * 4 + 15) // 16 * 16 + 3 * 6 * 1000 * 4
     for bad in ((-1, 4, 2, 64, 10), (1, 0, 2, 64, 10), (1, 4, 0, 64, 10), (1, 4, 2, 0, 10),

@@ -187,11 +187,10 @@ def test_decode_long(pa):
 
 
 def test_decode_many_requests(pa):
-    """The largest batch, one split, without a workspace."""
+    """The largest batch."""
     rng = np.random.default_rng(11)
     c = Cache(10, rng.integers(0, 40, 65535), 2, 1, 64, 16)
-    assert c.workspace(pa).numel() == 0
-    out, lse = c.decode(pa, workspace=None)
+    out, lse = c.decode(pa)
     some = np.arange(0, 65535, 131)
     c.q, c.table, c.seqs = c.q[some], c.table[some], c.seqs[some]
     c.check((out[some], lse[some]), "65535 requests")
