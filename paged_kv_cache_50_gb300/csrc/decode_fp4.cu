@@ -30,7 +30,7 @@
 
 #include "fp4.cuh"
 #include "pa_launch.h"
-#include "tc_common.cuh"
+#include "tc_tiles.cuh"
 
 namespace pa {
 
@@ -392,47 +392,60 @@ __global__ void __launch_bounds__(kThreads, Fp4Cfg<D, NT>::kCtas) decode_fp4_ker
   long long pos = w0;   // of the unit's first token in this part
 
   // ------------------------------------------------------------ fetches
-  const int groups = a.bs >> 4;
-  const int64_t head_bytes = static_cast<int64_t>(groups) * C::kPairBytes;
+  // Addresses are made for 32 pieces of a unit at a time, a lane's each: the block ids
+  // are asked for with the last slice before, and turned into addresses with the next.
+  const int64_t head_bytes = static_cast<int64_t>(a.bs >> 4) * C::kPairBytes;
   const int64_t block_bytes = head_bytes * a.Hkv;
   bool more = any;
-  // The lane's piece of the next slice to be fetched (lanes < kPieces), and its block.
-  int tok = ahead.tok + 16 * lane;
-  const uint8_t* head = a.cache + ahead.h * head_bytes;
-  const int32_t* table = a.block_table + static_cast<int64_t>(ahead.i) * a.max_blocks;
+  int tok = ahead.tok;     // of the next slice to be fetched
+  int blk = -1, next = 0;  // the lane's block id; pieces of the 32 that are used up
+  bool fresh = true;       // ... and whether it has been turned into an address
+  uint32_t valid = 0;      // pieces of the 32 that are there
+  const uint8_t* src = nullptr;
   auto lookup = [&]() {
+    const int t = tok + 16 * lane;
     // (A plain load: the table may be the previous kernel's output.)
-    return more && lane < kPieces && tok < ahead.end ? table[div_bs(tok, a.bs, a.bs_log2)] : -1;
+    blk = more && t < ahead.end ? a.block_table[static_cast<int64_t>(ahead.i) * a.max_blocks +
+                                                div_bs(t, a.bs, a.bs_log2)]
+                                : -1;
+    fresh = true;
+    next = 0;
   };
-  int blk = lookup();
-  int fill = 0;            // its slot
+  lookup();
+  int fill = 0;            // the slot that it goes to
   uint32_t loaded = 0;     // kPieces bits per slot: pieces that are there
   bool ok = true;          // (a warp that gave up fetches no more)
   int flying = 0;          // slices on their way
   auto fetch = [&]() {
     if (!more || !ok) return;
-    const bool piece = lane < kPieces && tok < ahead.end;
-    const bool good = piece && blk >= 0 && blk < a.num_blocks;
-    const unsigned there = __ballot_sync(0xffffffffu, good);
-    if (piece && !good) record_error(a.err, PA_DEVERR_BLOCK_ID);
+    if (fresh) {
+      const bool good = blk >= 0 && blk < a.num_blocks;
+      if (!good && tok + 16 * lane < ahead.end) record_error(a.err, PA_DEVERR_BLOCK_ID);
+      valid = __ballot_sync(0xffffffffu, good);
+      src = a.cache + ahead.h * head_bytes + (good ? blk : 0) * block_bytes +
+            (mod_bs(tok + 16 * lane, a.bs, a.bs_log2) >> 4) * C::kPairBytes;
+      fresh = false;
+    }
+    const uint32_t there = (valid >> next) & 3u;
+    const uint64_t from = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(src), next + lane);
     loaded = (loaded & ~(3u << (kPieces * fill))) | (there << (kPieces * fill));
     const uint32_t bar = bars + 8 * fill;
     if (lane == 0) tc::mbar_arrive_expect_tx(bar, __popc(there) * C::kPairBytes);
     __syncwarp();
-    if (good)
+    if ((there >> lane) & 1u)
       bulk_load(ring + fill * C::kSlotBytes + lane * C::kPairBytes,
-                head + blk * block_bytes + (mod_bs(tok, a.bs, a.bs_log2) >> 4) * C::kPairBytes,
-                C::kPairBytes, bar);
+                reinterpret_cast<const void*>(from), C::kPairBytes, bar);
     if (++fill == C::kSlots) fill = 0;
     ++flying;
     tok += kSlice;
-    if (tok - 16 * lane >= ahead.end) {
+    next += kPieces;
+    if (tok >= ahead.end) {
       more = walk_next(a, ahead);
-      tok = 16 * lane;   // (a part's later units are entered at their start)
-      head = a.cache + ahead.h * head_bytes;
-      table = a.block_table + static_cast<int64_t>(ahead.i) * a.max_blocks;
+      tok = 0;             // (a part's later units are entered at their start)
+      lookup();
+    } else if (next == 32) {
+      lookup();
     }
-    blk = lookup();
   };
   for (int k = 0; k < C::kSlots; ++k) fetch();
 
@@ -473,23 +486,25 @@ __global__ void __launch_bounds__(kThreads, Fp4Cfg<D, NT>::kCtas) decode_fp4_ker
         lim[p] = (here >> p) & 1u ? min(16, at.end - (tb + 16 * p)) : 0;
       const uint32_t pair = ring + slot * C::kSlotBytes;
       const bool whole = lim[0] == 16 && lim[1] == 16;
+      // All loads of keys first: what follows waits for them once.
+      uint32_t kw[kPieces][2][kWk], ksc[kPieces][2];
+#pragma unroll
+      for (int p = 0; p < kPieces; ++p) {
+        const uint32_t kb = pair + p * C::kPairBytes, ks = kb + 8 * D;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int row = gid + 8 * h;
+          ksc[p][h] = D == 128 ? lds_u16(ks + row * 8 + tid4 * 2) : lds_u8(ks + row * 4 + tid4);
+          lds_words(kb + row * (D / 2) + tid4 * (D / 8), kw[p][h]);
+        }
+      }
       // S^T = K Q^T: rows = tokens gid, gid + 8; columns = heads.
       float x[kPieces][NT][4];
 #pragma unroll
       for (int p = 0; p < kPieces; ++p) {
-        const uint32_t kb = pair + p * C::kPairBytes, ks = kb + 8 * D;
-        uint32_t k0[kWk], k1[kWk], s0[kK / 4], s1[kK / 4];
-        lds_words(kb + gid * (D / 2) + tid4 * (D / 8), k0);
-        lds_words(kb + (gid + 8) * (D / 2) + tid4 * (D / 8), k1);
-        if constexpr (D == 128) {
-          const uint32_t c0 = fp4::widen_scales(lds_u16(ks + gid * 8 + tid4 * 2));
-          const uint32_t c1 = fp4::widen_scales(lds_u16(ks + (gid + 8) * 8 + tid4 * 2));
-          s0[0] = fp4::both_low(c0), s0[1] = fp4::both_high(c0);
-          s1[0] = fp4::both_low(c1), s1[1] = fp4::both_high(c1);
-        } else {
-          s0[0] = fp4::both_low(fp4::widen_scales(lds_u8(ks + gid * 4 + tid4)));
-          s1[0] = fp4::both_low(fp4::widen_scales(lds_u8(ks + (gid + 8) * 4 + tid4)));
-        }
+        const uint32_t c0 = fp4::widen_scales(ksc[p][0]), c1 = fp4::widen_scales(ksc[p][1]);
+        const uint32_t s0[2] = {fp4::both_low(c0), fp4::both_high(c0)};
+        const uint32_t s1[2] = {fp4::both_low(c1), fp4::both_high(c1)};
         float s2[NT][2][4];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -499,8 +514,8 @@ __global__ void __launch_bounds__(kThreads, Fp4Cfg<D, NT>::kCtas) decode_fp4_ker
 #pragma unroll
         for (int w = 0; w < kWk; ++w) {
           uint32_t f0[4], f1[4];
-          fp4::widen8(k0[w], f0);
-          fp4::widen8(k1[w], f1);
+          fp4::widen8(kw[p][0][w], f0);
+          fp4::widen8(kw[p][1][w], f1);
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const uint32_t am[4] = {
@@ -516,6 +531,18 @@ __global__ void __launch_bounds__(kThreads, Fp4Cfg<D, NT>::kCtas) decode_fp4_ker
 #pragma unroll
           for (int e = 0; e < 4; ++e)
             x[p][nt][e] = (s2[nt][0][e] + s2[nt][1][e]) * a.scale_log2;
+      }
+      // ... and of values, under the softmax.
+      uint32_t v[kPieces][4][kWv], vsc[kPieces][4];
+#pragma unroll
+      for (int p = 0; p < kPieces; ++p) {
+        const uint32_t vb = pair + p * C::kPairBytes + fp4::tile_bytes(D), vs = vb + 8 * D;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int row = 2 * tid4 + (r & 1) + 8 * (r >> 1);
+          vsc[p][r] = lds_u8(vs + row * (D / 16) + (D == 128 ? gid : gid >> 1));
+          lds_words(vb + row * (D / 2) + gid * (D / 16), v[p][r]);
+        }
       }
       if (!whole) {
 #pragma unroll
@@ -548,16 +575,20 @@ __global__ void __launch_bounds__(kThreads, Fp4Cfg<D, NT>::kCtas) decode_fp4_ker
       uint32_t pb[kPieces][NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        float pr[kPieces][4];
+        float pr[kPieces][4], mx[2];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          float mx = fmaxf(fmaxf(x[0][nt][j], x[0][nt][2 + j]), fmaxf(x[1][nt][j], x[1][nt][2 + j]));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-          if (mx > st.m[nt][j] + kRescale) {
-            const float alpha = fast_exp2(st.m[nt][j] - mx);   // 0 when the old one is -inf
-            st.m[nt][j] = mx;
+          float y = fmaxf(fmaxf(x[0][nt][j], x[0][nt][2 + j]), fmaxf(x[1][nt][j], x[1][nt][2 + j]));
+          y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 4));
+          y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 8));
+          mx[j] = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 16));
+        }
+        if (__any_sync(0xffffffffu, mx[0] > st.m[nt][0] + kRescale || mx[1] > st.m[nt][1] + kRescale)) {
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const bool up = mx[j] > st.m[nt][j] + kRescale;
+            const float alpha = up ? ex2(st.m[nt][j] - mx[j]) : 1.f;   // 0 when the old one is -inf
+            if (up) st.m[nt][j] = mx[j];
             st.l[nt][j] *= alpha;
 #pragma unroll
             for (int md = 0; md < kK; ++md) {
@@ -565,11 +596,14 @@ __global__ void __launch_bounds__(kThreads, Fp4Cfg<D, NT>::kCtas) decode_fp4_ker
               st.o[nt][md][2 + j] *= alpha;
             }
           }
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
           const float mu = st.m[nt][j] == -CUDART_INF_F ? 0.f : st.m[nt][j];
 #pragma unroll
           for (int p = 0; p < kPieces; ++p) {
-            pr[p][j] = fast_exp2(x[p][nt][j] - mu);
-            pr[p][2 + j] = fast_exp2(x[p][nt][2 + j] - mu);
+            pr[p][j] = ex2(x[p][nt][j] - mu);
+            pr[p][2 + j] = ex2(x[p][nt][2 + j] - mu);
             st.l[nt][j] += pr[p][j] + pr[p][2 + j];
           }
         }
@@ -589,31 +623,23 @@ __global__ void __launch_bounds__(kThreads, Fp4Cfg<D, NT>::kCtas) decode_fp4_ker
       // tid4, + 1, + 8, + 9; two tokens' codes are interleaved by halves of bytes.
 #pragma unroll
       for (int p = 0; p < kPieces; ++p) {
-        const uint32_t vb = pair + p * C::kPairBytes + fp4::tile_bytes(D), vs = vb + 8 * D;
-        uint32_t v[4][kWv], sc[4];
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int row = 2 * tid4 + (r & 1) + 8 * (r >> 1);
-          lds_words(vb + row * (D / 2) + gid * (D / 16), v[r]);
-          sc[r] = lds_u8(vs + row * (D / 16) + (D == 128 ? gid : gid >> 1));
-        }
         if (!whole) {
           // The weight of a token that is not there is 0, its codes are finite whatever
           // the bytes, but its scale need not be.
 #pragma unroll
           for (int r = 0; r < 4; ++r)
-            if (2 * tid4 + (r & 1) + 8 * (r >> 1) >= lim[p]) sc[r] = 0u;
+            if (2 * tid4 + (r & 1) + 8 * (r >> 1) >= lim[p]) vsc[p][r] = 0u;
         }
-        const uint32_t sab = fp4::widen_scales(sc[0] | (sc[1] << 8));
-        const uint32_t scd = fp4::widen_scales(sc[2] | (sc[3] << 8));
+        const uint32_t sab = fp4::widen_scales(vsc[p][0] | (vsc[p][1] << 8));
+        const uint32_t scd = fp4::widen_scales(vsc[p][2] | (vsc[p][3] << 8));
 #pragma unroll
         for (int w = 0; w < kWv; ++w) {
           constexpr uint32_t kLow = 0x0f0f0f0fu;
           uint32_t ab[2][4], cd[2][4];   // [even, odd element][word byte]
-          fp4::widen8((v[0][w] & kLow) | ((v[1][w] << 4) & ~kLow), ab[0]);
-          fp4::widen8(((v[0][w] >> 4) & kLow) | (v[1][w] & ~kLow), ab[1]);
-          fp4::widen8((v[2][w] & kLow) | ((v[3][w] << 4) & ~kLow), cd[0]);
-          fp4::widen8(((v[2][w] >> 4) & kLow) | (v[3][w] & ~kLow), cd[1]);
+          fp4::widen8((v[p][0][w] & kLow) | ((v[p][1][w] << 4) & ~kLow), ab[0]);
+          fp4::widen8(((v[p][0][w] >> 4) & kLow) | (v[p][1][w] & ~kLow), ab[1]);
+          fp4::widen8((v[p][2][w] & kLow) | ((v[p][3][w] << 4) & ~kLow), cd[0]);
+          fp4::widen8(((v[p][2][w] >> 4) & kLow) | (v[p][3][w] & ~kLow), cd[1]);
 #pragma unroll
           for (int b = 0; b < 4; ++b) {
             const uint32_t am[4] = {fp4::mul2(ab[0][b], sab), fp4::mul2(ab[1][b], sab),
