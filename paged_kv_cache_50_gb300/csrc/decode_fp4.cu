@@ -40,6 +40,10 @@ constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kPieces = 2;                   // 16-token pieces of a warp's slice
 constexpr int kSlice = 16 * kPieces;         // tokens
+// What a unit's start and end cost a warp, in pieces: it counts on the line in front of
+// the unit's tokens.  (128 requests of U[1, 8191]
+// tokens, 64-wide heads: 100 us with 0, 94 with 2, 90 with 4 to 8.)
+constexpr int kExtra = 6;
 
 struct Fp4Args {
   const __nv_bfloat16* q;
@@ -128,26 +132,35 @@ __device__ __forceinline__ void lds_words(uint32_t a, uint32_t (&w)[N]) {
     asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[0]) : "r"(a));
 }
 
+// x / n; 64-bit divisions take a hundred instructions.
+__device__ __forceinline__ long long quotient(long long x, long long n) {
+  return (x | n) <= INT_MAX ? static_cast<int>(x) / static_cast<int>(n) : x / n;
+}
+
 // Where a warp (or its fetches, ahead of it) stands in its part of the line.
 struct Walk {
   int i, h;            // unit
   int seq, after;      // tokens of request i and of request i + 1
   int tok, end;        // its tokens in this part
-  int left;            // pieces of the part from here on
+  int left;            // of the part behind the unit
 };
 
 __device__ __forceinline__ int length_of(const Fp4Args& a, int i) {
   // What lies past the table's columns has no block and is not walked over.
   return i < a.N ? min(max(0, a.seq_lens[i]), a.positions) : 0;
 }
-// The share of the unit from token `tok` on.
-__device__ __forceinline__ void walk_enter(Walk& w, int tok) {
-  w.tok = tok;
-  w.end = w.left < ((w.seq - tok + 15) >> 4) ? tok + 16 * w.left : w.seq;
+// Enters the unit at `at` on its stretch of the line (kExtra, then its pieces); false
+// where the part ends before its tokens.
+__device__ __forceinline__ bool walk_enter(Walk& w, int at) {
+  const int skip = max(0, kExtra - at), from = max(0, at - kExtra);
+  const int pieces = ((w.seq + 15) >> 4) - from, mine = w.left - skip;
+  w.tok = 16 * from;
+  w.end = mine < pieces ? 16 * (from + mine) : w.seq;
+  w.left -= skip + pieces;
+  return mine > 0;
 }
 // On to the next unit with tokens; false at the part's end.
 __device__ __forceinline__ bool walk_next(const Fp4Args& a, Walk& w) {
-  w.left -= (w.end - w.tok + 15) >> 4;
   if (w.left <= 0) return false;
   if (++w.h == a.Hkv) {
     w.h = 0;
@@ -157,8 +170,7 @@ __device__ __forceinline__ bool walk_next(const Fp4Args& a, Walk& w) {
       w.after = length_of(a, w.i + 1);
     } while (w.seq == 0);
   }
-  walk_enter(w, 0);
-  return true;
+  return walk_enter(w, 0);
 }
 
 // A warp's running state; a lane holds the heads nt * 8 + 2 tid4 + {0, 1}, and of each
@@ -176,7 +188,7 @@ struct Fp4State {
         o[nt][md][0] = o[nt][md][1] = o[nt][md][2] = o[nt][md][3] = 0.f;
     }
   }
-  // To and from 16 bytes a lane at a time.
+  // 16 bytes a lane at a time.
   __device__ __forceinline__ void store(float4* p, int lane) const {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -186,31 +198,6 @@ struct Fp4State {
             make_float4(o[nt][md][0], o[nt][md][1], o[nt][md][2], o[nt][md][3]);
       p[(nt * (D / 16 + 1) + D / 16) * 32 + lane] =
           make_float4(m[nt][0], m[nt][1], l[nt][0], l[nt][1]);
-    }
-  }
-  __device__ __forceinline__ void merge(const float4* p, int lane) {
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const float4 s4 = p[(nt * (D / 16 + 1) + D / 16) * 32 + lane];
-      const float om[2] = {s4.x, s4.y}, ol[2] = {s4.z, s4.w};
-      float f[2], g[2];
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const float M = fmaxf(m[nt][j], om[j]);
-        // (Equal, also where both are -inf: 1.)
-        f[j] = m[nt][j] == M ? 1.f : fast_exp2(m[nt][j] - M);
-        g[j] = om[j] == M ? 1.f : fast_exp2(om[j] - M);
-        m[nt][j] = M;
-        l[nt][j] = f[j] * l[nt][j] + g[j] * ol[j];
-      }
-#pragma unroll
-      for (int md = 0; md < D / 16; ++md) {
-        const float4 y = p[(nt * (D / 16 + 1) + md) * 32 + lane];
-        o[nt][md][0] = fmaf(g[0], y.x, f[0] * o[nt][md][0]);
-        o[nt][md][1] = fmaf(g[1], y.y, f[1] * o[nt][md][1]);
-        o[nt][md][2] = fmaf(g[0], y.z, f[0] * o[nt][md][2]);
-        o[nt][md][3] = fmaf(g[1], y.w, f[1] * o[nt][md][3]);
-      }
     }
   }
   // The finished rows of unit (i, h).
@@ -250,23 +237,6 @@ struct Fp4State {
     if (a.spans != nullptr && lane == 0)
       a.spans[static_cast<int64_t>(i) * a.Hkv + h] = make_int2(blockIdx.x, blockIdx.x);
   }
-  // ... or, of a unit that is cut between CTAs, for the second kernel: [grp][d + 2].
-  __device__ __forceinline__ void part(float* to, int grp, int lane) const {
-    const int gid = lane >> 2, tid4 = lane & 3;
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int r = nt * 8 + 2 * tid4 + j;
-        if (r >= grp) continue;
-        float* dst = to + r * (D + 2);
-#pragma unroll
-        for (int md = 0; md < D / 16; ++md)
-          *reinterpret_cast<float2*>(dst + gid * (D / 8) + 2 * md) =
-              make_float2(o[nt][md][j], o[nt][md][2 + j]);
-        if (gid == 0) *reinterpret_cast<float2*>(dst + D) = make_float2(m[nt][j], l[nt][j]);
-      }
-  }
 };
 
 template <int D, int NT, bool LOGITS>
@@ -294,76 +264,98 @@ __global__ void __launch_bounds__(kThreads, Fp4Cfg<D, NT>::kCtas) decode_fp4_ker
   pdl_trigger();
 
   // ------------------------------------------------------------ the part
-  // A thread sums the pieces of neighbouring requests; the CTA scans the threads' sums.
-  const int chunk = (a.N + kThreads - 1) / kThreads;
-  const int r0 = min(a.N, static_cast<int>(threadIdx.x) * chunk), r1 = min(a.N, r0 + chunk);
-  auto weight = [&](int seq) { return (seq + 15) >> 4; };
+  // (Code that runs once is slow, it is fetched as it goes: loops are kept as loops.)
+  // Requests are dealt over the threads that scan, neighbouring ones to each: those of a
+  // warp by itself where they are few, else those of the CTA.
+  const bool few = a.N <= 256;
+  const int scanner = few ? lane : threadIdx.x, scanners = few ? 32 : kThreads;
+  const int chunk = (a.N + scanners - 1) / scanners;
+  const int r0 = min(a.N, scanner * chunk), r1 = min(a.N, r0 + chunk);
+  auto weight = [&](int seq) { return seq > 0 ? kExtra + ((seq + 15) >> 4) : 0; };
   long long mine = 0;
   for (int i = r0; i < r1; ++i) mine += weight(length_of(a, i));
-  long long upto = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, upto, o);
-    if (lane >= o) upto += y;
-  }
-  long long* scan = reinterpret_cast<long long*>(smem + C::kOffPlaces);
-  if (lane == 31) scan[warp] = upto;
-  __syncthreads();
-  long long total = 0, before = upto - mine;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    if (w < warp) before += scan[w];
-    total += scan[w];
-  }
-  __syncthreads();
-  total *= a.Hkv;
-  before *= a.Hkv;
   mine *= a.Hkv;
-  // Parts of equal length, in whole slices.
-  const long long share = ((total + gridDim.x - 1) / gridDim.x + kPieces - 1) / kPieces * kPieces;
-  long long g0 = min(total, cta * share), g1 = min(total, g0 + share);
-  Place* places = reinterpret_cast<Place*>(smem + C::kOffPlaces);   // [kWarps]
-  // The place of position g (< total), found by the thread that has its request.
-  auto locate = [&](long long g, Place* to) {
-    if (g < before || g >= before + mine) return;
-    int i = r0;
-    long long at = before;
-    for (; i + 1 < r1; ++i) {
-      const long long n = static_cast<long long>(weight(length_of(a, i))) * a.Hkv;
-      if (g < at + n) break;
-      at += n;
+  long long before = mine;
+#pragma unroll 1
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, before, o);
+    if (lane >= o) before += y;
+  }
+  long long total = __shfl_sync(0xffffffffu, before, 31);
+  before -= mine;
+  Place* found = reinterpret_cast<Place*>(smem + C::kOffPlaces);   // (not few: for one warp at a time)
+  if (!few) {
+    long long* scan = reinterpret_cast<long long*>(smem + C::kOffPlaces);
+    if (lane == 31) scan[warp] = total;
+    __syncthreads();
+    total = 0;
+#pragma unroll 1
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) before += scan[w];
+      total += scan[w];
     }
-    *to = Place{g - at, i, 0};
+  }
+  // The place of position g < total.  Few: g is the warp's own; else the CTA's, one
+  // after another.
+  auto locate = [&](long long g) {
+    const bool here = g >= before && g < before + mine;
+    int i = r0;
+    long long in = g - before;
+    if (few) {
+      const int src = __ffs(__ballot_sync(0xffffffffu, here)) - 1;
+      i = __shfl_sync(0xffffffffu, i, src);
+      in = __shfl_sync(0xffffffffu, in, src);
+    }
+    if (few || here)
+      for (; i + 1 < a.N; ++i) {
+        const long long n = static_cast<long long>(weight(length_of(a, i))) * a.Hkv;
+        if (in < n) break;
+        in -= n;
+      }
+    Place p{in, i, 0};
+    if (!few) {
+      __syncthreads();   // the last one has been read
+      if (here) *found = p;
+      __syncthreads();
+      p = *found;
+    }
+    return p;
   };
+  // Parts of equal length, in whole slices.
+  const long long share = (quotient(total + gridDim.x - 1, gridDim.x) + kPieces - 1) / kPieces * kPieces;
+  long long g0 = min(total, cta * share), g1 = min(total, g0 + share);
   if (a.whole) {
     // The units that begin in the part.
-    const long long edge[2] = {g0, g1};
-    for (int k = 0; k < 2; ++k)
-      if (edge[k] < total) locate(edge[k], &places[k]);
-    __syncthreads();
-    long long up[2];
+#pragma unroll 1
     for (int k = 0; k < 2; ++k) {
-      up[k] = edge[k];
-      if (edge[k] < total) {
-        const int n = weight(length_of(a, places[k].i));
-        up[k] += (n - places[k].inside % n) % n;
+      long long& g = k == 0 ? g0 : g1;
+      if (g < total) {
+        const Place p = locate(g);
+        const int n = weight(length_of(a, p.i));
+        const int in = static_cast<int>(p.inside - quotient(p.inside, n) * n);
+        g += in > 0 ? n - in : 0;
       }
     }
-    __syncthreads();
-    g0 = up[0], g1 = up[1];
   }
   const long long per = ((g1 - g0 + kWarps - 1) / kWarps + kPieces - 1) / kPieces * kPieces;
-  for (int w = 0; w < kWarps; ++w)
-    if (g0 + w * per < g1) locate(g0 + w * per, &places[w]);
-  __syncthreads();
   const long long w0 = g0 + warp * per, w1 = min(g1, w0 + per);
-  const bool any = w0 < w1;
-  const Place place = places[warp];
-  __syncthreads();
+  bool any = w0 < w1;
+  Place place{};
+  if (few) {
+    if (any) place = locate(w0);
+  } else {
+#pragma unroll 1
+    for (int w = 0; w < kWarps; ++w)
+      if (g0 + w * per < g1) {   // CTA-uniform
+        const Place p = locate(g0 + w * per);
+        if (w == warp) place = p;
+      }
+    __syncthreads();   // the last place has been read
+  }
   Kept* kept = reinterpret_cast<Kept*>(smem + C::kOffPlaces);   // [kWarps][unit began before, begins]
   if (lane < 2) kept[2 * warp + lane].where = 0;
   __syncwarp();
-  if (cta == 0 && threadIdx.x < 32) {
+  if (cta == 0 && warp == 0) {
     bool past = false;
     for (int i = lane; i < a.N; i += 32) past |= a.seq_lens[i] > a.positions;
     if (past) record_error(a.err, PA_DEVERR_BLOCK_ID);
@@ -379,17 +371,19 @@ __global__ void __launch_bounds__(kThreads, Fp4Cfg<D, NT>::kCtas) decode_fp4_ker
     }
   if (!a.whole && threadIdx.x == 0) a.cut[cta] = make_int4(-1, 0, 0, 0);
   Walk at{};
+  long long pos = 0;   // of the unit's first token in the line
   if (any) {
     at.i = place.i;
     at.seq = length_of(a, at.i);
     at.after = length_of(a, at.i + 1);
     at.left = static_cast<int>(min(w1 - w0, static_cast<long long>(INT_MAX)));
     const int n = weight(at.seq);
-    at.h = static_cast<int>(place.inside / n);
-    walk_enter(at, 16 * static_cast<int>(place.inside - static_cast<long long>(at.h) * n));
+    at.h = static_cast<int>(quotient(place.inside, n));
+    const int in = static_cast<int>(place.inside - static_cast<long long>(at.h) * n);
+    any = walk_enter(at, in);
+    pos = w0 - in + kExtra;
   }
   Walk ahead = at;
-  long long pos = w0;   // of the unit's first token in this part
 
   // ------------------------------------------------------------ fetches
   // Addresses are made for 32 pieces of a unit at a time, a lane's each: the block ids
@@ -447,6 +441,7 @@ __global__ void __launch_bounds__(kThreads, Fp4Cfg<D, NT>::kCtas) decode_fp4_ker
       lookup();
     }
   };
+#pragma unroll 1
   for (int k = 0; k < C::kSlots; ++k) fetch();
 
   // Source lanes of the P^T operand (tokens 2 tid4 and 2 tid4 + 1 of head gid).
@@ -454,26 +449,27 @@ __global__ void __launch_bounds__(kThreads, Fp4Cfg<D, NT>::kCtas) decode_fp4_ker
   const uint32_t sel = (gid & 1) ? 0x7632u : 0x5410u;
   int slot = 0, parity = 0;   // of the slice worked on
   Fp4State<D, NT> st;
-  for (bool live = any; live;) {
-    // ---------------------------------------------------------- one unit
-    const int64_t row0 = static_cast<int64_t>(at.i) * a.Hq + at.h * grp;
-    uint32_t qf[NT][kK][2];
-    {
-      const __nv_bfloat16* qb = a.q + row0 * D;
+  // The unit's queries, as the B operand.
+  uint32_t qf[NT][kK][2];
+  auto queries = [&]() {
+    const __nv_bfloat16* qb =
+        a.q + (static_cast<int64_t>(at.i) * a.Hq + at.h * grp) * D + tid4 * (D / 4);
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        const int h = nt * 8 + gid;
+    for (int nt = 0; nt < NT; ++nt) {
+      const int h = nt * 8 + gid;
 #pragma unroll
-        for (int kk = 0; kk < kK; ++kk) {
-          qf[nt][kk][0] = qf[nt][kk][1] = 0u;
-          if (h < grp) {
-            const __nv_bfloat16* p = qb + h * D + tid4 * (D / 4) + kk * 4;
-            qf[nt][kk][0] = q_pair(p);
-            qf[nt][kk][1] = q_pair(p + 2);
-          }
+      for (int kk = 0; kk < kK; ++kk) {
+        qf[nt][kk][0] = qf[nt][kk][1] = 0u;
+        if (h < grp) {
+          qf[nt][kk][0] = q_pair(qb + h * D + kk * 4);
+          qf[nt][kk][1] = q_pair(qb + h * D + kk * 4 + 2);
         }
       }
     }
+  };
+  for (bool live = any; live;) {
+    // ---------------------------------------------------------- one unit
+    queries();
     st.clear();
     for (int tb = at.tok; tb < at.end; tb += kSlice) {
       ok = ok && __all_sync(0xffffffffu, tc::mbar_wait(bars + 8 * slot, parity));
@@ -498,40 +494,49 @@ __global__ void __launch_bounds__(kThreads, Fp4Cfg<D, NT>::kCtas) decode_fp4_ker
           lds_words(kb + row * (D / 2) + tid4 * (D / 8), kw[p][h]);
         }
       }
-      // S^T = K Q^T: rows = tokens gid, gid + 8; columns = heads.
-      float x[kPieces][NT][4];
+      // S^T = K Q^T: rows = tokens gid, gid + 8; columns = heads.  Pieces and even and
+      // odd k-steps in turn: four chains of MMAs.
+      uint32_t ks[kPieces][2][2];
 #pragma unroll
-      for (int p = 0; p < kPieces; ++p) {
-        const uint32_t c0 = fp4::widen_scales(ksc[p][0]), c1 = fp4::widen_scales(ksc[p][1]);
-        const uint32_t s0[2] = {fp4::both_low(c0), fp4::both_high(c0)};
-        const uint32_t s1[2] = {fp4::both_low(c1), fp4::both_high(c1)};
-        float s2[NT][2][4];
+      for (int p = 0; p < kPieces; ++p)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t c = fp4::widen_scales(ksc[p][h]);
+          ks[p][h][0] = fp4::both_low(c), ks[p][h][1] = fp4::both_high(c);
+        }
+      float s2[kPieces][NT][2][4];
+#pragma unroll
+      for (int p = 0; p < kPieces; ++p)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int h = 0; h < 2; ++h)
-            s2[nt][h][0] = s2[nt][h][1] = s2[nt][h][2] = s2[nt][h][3] = 0.f;
+            s2[p][nt][h][0] = s2[p][nt][h][1] = s2[p][nt][h][2] = s2[p][nt][h][3] = 0.f;
 #pragma unroll
-        for (int w = 0; w < kWk; ++w) {
+      for (int w = 0; w < kWk; ++w)
+#pragma unroll
+        for (int p = 0; p < kPieces; ++p) {
           uint32_t f0[4], f1[4];
           fp4::widen8(kw[p][0][w], f0);
           fp4::widen8(kw[p][1][w], f1);
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const uint32_t am[4] = {
-                fp4::mul2(f0[2 * h], s0[w / 2]), fp4::mul2(f1[2 * h], s1[w / 2]),
-                fp4::mul2(f0[2 * h + 1], s0[w / 2]), fp4::mul2(f1[2 * h + 1], s1[w / 2])};
+                fp4::mul2(f0[2 * h], ks[p][0][w / 2]), fp4::mul2(f1[2 * h], ks[p][1][w / 2]),
+                fp4::mul2(f0[2 * h + 1], ks[p][0][w / 2]), fp4::mul2(f1[2 * h + 1], ks[p][1][w / 2])};
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
-              mma_f16_16816(s2[nt][h], am, qf[nt][2 * w + h][0], qf[nt][2 * w + h][1]);
+              mma_f16_16816(s2[p][nt][h], am, qf[nt][2 * w + h][0], qf[nt][2 * w + h][1]);
           }
         }
+      float x[kPieces][NT][4];
+#pragma unroll
+      for (int p = 0; p < kPieces; ++p)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            x[p][nt][e] = (s2[nt][0][e] + s2[nt][1][e]) * a.scale_log2;
-      }
+            x[p][nt][e] = (s2[p][nt][0][e] + s2[p][nt][1][e]) * a.scale_log2;
       // ... and of values, under the softmax.
       uint32_t v[kPieces][4][kWv], vsc[kPieces][4];
 #pragma unroll
@@ -676,9 +681,9 @@ __global__ void __launch_bounds__(kThreads, Fp4Cfg<D, NT>::kCtas) decode_fp4_ker
       else if (ok)
         st.store(reinterpret_cast<float4*>(smem + warp * C::kSlots * C::kSlotBytes), lane);
       if (lane == 0)
-        kept[2 * warp + starts] = Kept{pos - (was.tok >> 4), was.i, was.h, live ? 1 : 2, ends};
+        kept[2 * warp + starts] = Kept{pos, was.i, was.h, live ? 1 : 2, ends};
     }
-    pos += (was.end - was.tok + 15) >> 4;
+    pos += kExtra + ((was.seq + 15) >> 4);
   }
   if (!ok && lane == 0) {
     // Given up: the outputs are invalid.  No copy may still be landing when the ring is
@@ -698,55 +703,93 @@ __global__ void __launch_bounds__(kThreads, Fp4Cfg<D, NT>::kCtas) decode_fp4_ker
     return where == 1 ? a.held + static_cast<int64_t>(cta * kWarps + w) * C::kStateVecs
                       : reinterpret_cast<const float4*>(smem + w * C::kSlots * C::kSlotBytes);
   };
-  for (int run = warp; run <= kWarps; run += kWarps) {
+  // A warp takes a d-tile of each run.
+#pragma unroll 1
+  for (int run = 0; run <= kWarps; ++run) {
     const int from = run == 0 ? 0 : run - 1;
     const Kept first = kept[2 * from + (run > 0)];
-    if (first.where == 0) continue;   // warp-uniform
-    st.clear();
-    st.merge(state_of(from, first.where), lane);
-    bool ends = first.ends;
-    for (int w = from + 1; w < kWarps && !ends; ++w) {
-      const Kept next = kept[2 * w];
-      if (next.where == 0) break;
-      st.merge(state_of(w, next.where), lane);
-      ends = next.ends;
-    }
+    if (first.where == 0 || warp >= kK) continue;   // warp-uniform
     const bool starts = run > 0;
-    if (starts && ends) {
-      st.output(a, first.i, first.h, lane);
-      continue;
+    bool ends = false;
+#pragma unroll 1
+    for (int nt = 0; nt < NT; ++nt) {
+      float M[2] = {-CUDART_INF_F, -CUDART_INF_F}, L[2] = {0.f, 0.f}, y[4] = {0.f, 0.f, 0.f, 0.f};
+      ends = false;
+#pragma unroll 1
+      for (int w = from; w < kWarps && !ends; ++w) {
+        const Kept* k = &kept[2 * w + (w == from && starts)];
+        const int where = k->where;
+        if (where == 0) break;
+        ends = k->ends;
+        const float4* p = state_of(w, where) + nt * (kK + 1) * 32 + lane;
+        const float4 ml = p[kK * 32], o = p[warp * 32];
+        const float m[2] = {ml.x, ml.y}, l[2] = {ml.z, ml.w}, v[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const float top = fmaxf(M[j], m[j]);
+          // (Equal, also where both are -inf: 1.)
+          const float f = M[j] == top ? 1.f : ex2(M[j] - top), g = m[j] == top ? 1.f : ex2(m[j] - top);
+          M[j] = top;
+          L[j] = f * L[j] + g * l[j];
+          y[j] = f * y[j] + g * v[j];
+          y[2 + j] = f * y[2 + j] + g * v[2 + j];
+        }
+      }
+#pragma unroll 1
+      for (int j = 0; j < 2; ++j) {
+        const int r = nt * 8 + 2 * tid4 + j, dim = gid * (D / 8) + 2 * warp;
+        const float l = j ? L[1] : L[0], m = j ? M[1] : M[0];
+        const float y0 = j ? y[1] : y[0], y1 = j ? y[3] : y[2];
+        if (r >= grp) continue;
+        if (starts && ends) {
+          const int64_t row = static_cast<int64_t>(first.i) * a.Hq + first.h * grp + r;
+          const float f = l == 0.f ? 0.f : a.out_scale / l;
+          a.out[row * D + dim] = __float2bfloat16_rn(y0 * f);
+          a.out[row * D + dim + 1] = __float2bfloat16_rn(y1 * f);
+          if (gid == 0 && warp == 0) {
+            const float x = l == 0.f ? -CUDART_INF_F : (m + log2f(l)) * kLn2;
+            if (a.lse != nullptr) a.lse[row] = x;
+            if (a.spans != nullptr) a.row_lse[row] = x;
+          }
+        } else {
+          float* dst = a.parts + ((static_cast<int64_t>(cta) * 2 + starts) * grp + r) * (D + 2);
+          *reinterpret_cast<float2*>(dst + dim) = make_float2(y0, y1);
+          if (gid == 0 && warp == 0) *reinterpret_cast<float2*>(dst + D) = make_float2(m, l);
+        }
+      }
     }
-    st.part(a.parts + (static_cast<int64_t>(cta) * 2 + starts) * grp * (D + 2), grp, lane);
-    if (lane != 0) continue;
-    if (ends) a.cut[cta] = make_int4(static_cast<int>(first.begin / share), first.i, first.h, 0);
+    if (warp != 0 || lane != 0) continue;
+    if (!starts && ends)
+      a.cut[cta] = make_int4(static_cast<int>(quotient(first.begin, share)), first.i, first.h, 0);
     if (starts && a.spans != nullptr)
       a.spans[static_cast<int64_t>(first.i) * a.Hkv + first.h] = make_int2(
-          cta, static_cast<int>((first.begin + weight(length_of(a, first.i)) - 1) / share));
+          cta, ends ? cta
+                    : static_cast<int>(quotient(first.begin + ((length_of(a, first.i) + 15) >> 4) - 1,
+                                             share)));
   }
 }
 
 // The states of a cut unit, one CTA for each CTA that holds a unit's end and each head:
 // the first CTA's second state, then the following CTAs' first states up to this one's.
-template <int D>
-__global__ void __launch_bounds__(D) decode_fp4_merge_kernel(const __grid_constant__ Fp4Args a) {
+template <int D, int kAhead>
+__device__ __forceinline__ void merge_cut(const Fp4Args& a, const int4& u, int c1, int r) {
+  static_assert(kAhead <= D, "a thread for each state");
   __shared__ float factor[D];
   __shared__ float red[2][D / 32];
-  pdl_wait();
-  pdl_trigger();
-  const int c1 = blockIdx.x, r = blockIdx.y, e = threadIdx.x;
-  const int4 u = a.cut[c1];
-  if (u.x < 0) return;
-  const int warp = e >> 5, lane = e & 31;
+  const int e = threadIdx.x, warp = e >> 5, lane = e & 31;
   auto state = [&](int c) {
     return a.parts + ((static_cast<int64_t>(c) * 2 + (c == u.x)) * a.grp + r) * (D + 2);
   };
-  // D states at a time (more than a few dozen are rare).
+  // kAhead states at a time, everything asked for at once.
   float M = -CUDART_INF_F, L = 0.f, acc = 0.f;
-  for (int c0 = u.x; c0 <= c1; c0 += D) {
-    const bool mine = c0 + e <= c1;
-    const float m = mine ? state(c0 + e)[D] : -CUDART_INF_F;
-    const float l = mine ? state(c0 + e)[D + 1] : 0.f;
-    float mx = m;
+  for (int c0 = u.x; c0 <= c1; c0 += kAhead) {
+    const bool mine = e < kAhead && c0 + e <= c1;
+    const float2 ml = mine ? *reinterpret_cast<const float2*>(state(c0 + e) + D)
+                           : make_float2(-CUDART_INF_F, 0.f);
+    float v[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) v[k] = c0 + k <= c1 ? state(c0 + k)[e] : 0.f;
+    float mx = ml.x;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
     if (lane == 0) red[0][warp] = mx;
@@ -754,27 +797,40 @@ __global__ void __launch_bounds__(D) decode_fp4_merge_kernel(const __grid_consta
     float top = M;
 #pragma unroll
     for (int w = 0; w < D / 32; ++w) top = fmaxf(top, red[0][w]);
-    const float f = m == top ? 1.f : fast_exp2(m - top);
+    // (Equal, also where all are -inf: 1.)
+    const float f = !mine ? 0.f : ml.x == top ? 1.f : ex2(ml.x - top);
     factor[e] = f;
-    float sum = mine ? f * l : 0.f;
+    float sum = mine ? f * ml.y : 0.f;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     if (lane == 0) red[1][warp] = sum;
     __syncthreads();
-    const float old = M == top ? 1.f : fast_exp2(M - top);
+    const float old = M == top ? 1.f : ex2(M - top);
     L *= old;
     acc *= old;
 #pragma unroll
     for (int w = 0; w < D / 32; ++w) L += red[1][w];
-    const int n = min(D, c1 - c0 + 1);
-#pragma unroll 8
-    for (int k = 0; k < n; ++k) acc += factor[k] * state(c0 + k)[e];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k)
+      if (c0 + k <= c1) acc += factor[k] * v[k];
     M = top;
     __syncthreads();
   }
   const int64_t row = static_cast<int64_t>(u.y) * a.Hq + u.z * a.grp + r;
   a.out[row * D + e] = __float2bfloat16_rn(L == 0.f ? 0.f : acc / L * a.out_scale);
   if (e == 0 && a.lse != nullptr) a.lse[row] = L == 0.f ? -CUDART_INF_F : (M + log2f(L)) * kLn2;
+}
+template <int D>
+__global__ void __launch_bounds__(D) decode_fp4_merge_kernel(const __grid_constant__ Fp4Args a) {
+  pdl_wait();
+  pdl_trigger();
+  const int c1 = blockIdx.x;
+  const int4 u = a.cut[c1];
+  if (u.x < 0) return;
+  if (c1 - u.x < 4)
+    merge_cut<D, 4>(a, u, c1, blockIdx.y);
+  else
+    merge_cut<D, 40>(a, u, c1, blockIdx.y);
 }
 
 template <int D, int NT, bool LOGITS>
@@ -800,7 +856,7 @@ size_t up16(size_t n) { return (n + 15) / 16 * 16; }
 int decode_fp4_ctas(int N, int Hq, int Hkv, int max_seq_len, int sm_count) {
   const long long units = static_cast<long long>(N) * Hkv;
   const long long slices = units * ((static_cast<long long>(max_seq_len) + kSlice - 1) / kSlice);
-  const long long most = static_cast<long long>(Hq / Hkv > 8 ? 1 : 2) * sm_count;
+    const long long most = static_cast<long long>(Hq / Hkv > 8 ? 1 : 2) * sm_count;
   return static_cast<int>(std::max(1LL, std::min(most, std::max(units, slices))));
 }
 
