@@ -6,25 +6,28 @@
 // order and moves to the places 0 .. budget - 1 of the request: attention over the
 // cache needs nothing but the new length.  Blocks behind it go back to the free list.
 //
-// One cluster of up to 8 CTAs serves one (request, kv head).
+// One cluster of up to 16 CTAs serves one (request, kv head); a CTA has a part of the
+// tokens, whose ranks it keeps in shared memory.
 //  1. The lowest sum that stays is found by its bits, eight at a time: a histogram
-//     in each CTA's shared memory over its part of the tokens, summed over the cluster.
-//  2. Each CTA counts what stays in its part; the parts' offsets come from the
-//     cluster, and the positions are written to kept[].
-//  3. Rows move in steps of kRows per CTA.  A kept row's source never lies before its
-//     place, and places of a step only hold sources of this step and of earlier ones:
-//     so a step's rows are all read (into registers) before any is written, with one
-//     barrier of the cluster between, and no other order is needed.  Rows that stay
-//     where they are (all before the first one that goes) are not touched.
+//     in each CTA's shared memory over its part, summed over the cluster.
+//  2. Each warp counts what stays in its share of the part; with the offsets of the
+//     warps and CTAs before it, it writes the positions to kept[], by ballots.
+//  3. Rows move in steps: a CTA copies its rows of a step into a ring in shared memory
+//     (cp.async), several steps ahead, and from there to their places.  A kept row's
+//     source never lies before its place, and the places of a step hold sources of this
+//     step and of earlier ones only: so a step is written when all CTAs have it in their
+//     rings, one barrier of the cluster for each, and no other order is needed.  A thread
+//     reads what it has copied itself.  Rows that stay where they are (all before the
+//     first one that goes) are not touched.
 // A second, small kernel writes the new lengths and pushes the blocks.
 //
-// Bound by HBM (each moved row is read and written once) for batches; the selection
-// reads the sums four times from L2.
+// Bound by HBM (each moved row is read and written once).
 #include <cooperative_groups.h>
 #include <math_constants.h>
 
 #include <algorithm>
 #include <climits>
+#include <mutex>
 
 #include "fp4.cuh"
 #include "pa_launch.h"
@@ -36,8 +39,11 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
+constexpr int kPer = 4;                     // 16-byte vectors of a thread in a step
+constexpr int kSteps = 5;                   // steps in the ring
+constexpr int kMaxCtas = 16;
 
 struct EvictArgs {
   uint8_t* cache;
@@ -60,11 +66,11 @@ __device__ __forceinline__ uint32_t rank_of(float x) {
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-// A cached row of one head in 16-byte vectors (kVecs) and, for the 4-bit pool, the
-// two rows' scales (kTail words).
-template <int ROW>   // bytes of a key (or value): 256, 128, 64; 4-bit: codes 64, 32
+// A cached row of one head, key and value, in 16-byte vectors (kVecs) and, for the
+// 4-bit pool, the key's and the value's scales (kTail bytes each).
+template <int ROW>   // bytes of a key (or value): 256, 128, 64
 struct Plain {
-  static constexpr int kVecs = 2 * ROW / 16;   // keys and values
+  static constexpr int kVecs = 2 * ROW / 16;
   static constexpr int kTail = 0;
   __device__ static __forceinline__ uint8_t* vec(const EvictArgs& a, int64_t blk, int off, int head,
                                                  int v) {
@@ -78,53 +84,47 @@ struct Plain {
 template <int D>
 struct Four {
   static constexpr int kVecs = 2 * (D / 2) / 16;
-  static constexpr int kTail = 2 * (D / 16) / 4;   // words
+  static constexpr int kTail = D / 16;
+  __device__ static __forceinline__ uint8_t* tile(const EvictArgs& a, int64_t blk, int off, int head,
+                                                  int kv) {
+    return a.cache + fp4::pair_at(blk, head, off >> 4, a.Hkv, a.bs >> 4, D) + kv * fp4::tile_bytes(D);
+  }
   __device__ static __forceinline__ uint8_t* vec(const EvictArgs& a, int64_t blk, int off, int head,
                                                  int v) {
-    const int kv = v / (D / 32), c = v % (D / 32);
-    return a.cache + fp4::pair_at(blk, head, off >> 4, a.Hkv, a.bs >> 4, D) +
-           kv * fp4::tile_bytes(D) + (off & 15) * (D / 2) + c * 16;
+    return tile(a, blk, off, head, v / (D / 32)) + (off & 15) * (D / 2) + v % (D / 32) * 16;
   }
   __device__ static __forceinline__ uint8_t* tail(const EvictArgs& a, int64_t blk, int off, int head,
-                                                  int w) {
-    const int kv = w / (D / 64), c = w % (D / 64);
-    return a.cache + fp4::pair_at(blk, head, off >> 4, a.Hkv, a.bs >> 4, D) +
-           kv * fp4::tile_bytes(D) + 8 * D + (off & 15) * (D / 16) + c * 4;
+                                                  int kv) {
+    return tile(a, blk, off, head, kv) + 8 * D + (off & 15) * (D / 16);
   }
 };
+template <class Row>
+struct Ring {
+  static constexpr int kRows = kThreads * kPer / Row::kVecs;   // of a CTA in a step
+  static constexpr int kOffTail = kThreads * kPer * 16;
+  static constexpr int kOffSum = kOffTail + kRows * 2 * Row::kTail;
+  static constexpr int kStepBytes = (kOffSum + kRows * 4 + 15) / 16 * 16;
+  static constexpr int kBytes = kSteps * kStepBytes;
+  static constexpr int kKeys = kBytes / 4;                     // ranks that fit it
+};
 
-// Exclusive prefix sum of v over the CTA, and the total.
-__device__ __forceinline__ int block_scan(int v, int* warp_sums, int& total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int x = v;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x += y;
-  }
-  if (lane == 31) warp_sums[warp] = x;
-  __syncthreads();
-  int before = 0;
-  total = 0;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    const int y = warp_sums[w];
-    if (w < warp) before += y;
-    total += y;
-  }
-  __syncthreads();
-  return before + x - v;
+template <int BYTES>
+__device__ __forceinline__ void copy_async(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(BYTES) : "memory");
 }
 
 template <class Row>
-__global__ void __launch_bounds__(kThreads) evict_kernel(const __grid_constant__ EvictArgs a) {
+__global__ void __launch_bounds__(kThreads, 2) evict_kernel(const __grid_constant__ EvictArgs a) {
+  using R = Ring<Row>;
+  extern __shared__ __align__(16) uint8_t smem[];   // the part's ranks, then the ring
   __shared__ int hist[256];
   __shared__ int merged[256];
-  __shared__ int warp_sums[kWarps];
   __shared__ int counts[3];   // this part's tokens above the threshold, at it; first place that moves
+  __shared__ int warp_counts[2][kWarps];
   __shared__ uint32_t pick[2];   // threshold's bits so far, how many at or above it are wanted
   const int kvh = blockIdx.y, i = blockIdx.z;
   const int C = gridDim.x, c = blockIdx.x;   // cluster = grid.x
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   cg::cluster_group cluster = cg::this_cluster();
   pdl_wait();
   pdl_trigger();
@@ -153,38 +153,50 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const __grid_constant__
   const int lo = a.first, hi = seq - a.recent, want = a.budget - a.first - a.recent;
   const int per = (seq + C - 1) / C;
   const int b = min(seq, c * per), e = min(seq, b + per);
+  uint32_t* keys = reinterpret_cast<uint32_t*>(smem);
+  const bool held = per <= R::kKeys;   // (else they are read again)
+  if (held) {
+#pragma unroll 4
+    for (int p = b + threadIdx.x; p < e; p += kThreads) keys[p - b] = rank_of(scores[p]);
+  }
+  auto rank_at = [&](int p) { return held ? keys[p - b] : rank_of(scores[p]); };
   uint32_t prefix = 0;
   int left = want;   // of those that share the prefix
   if (want > 0) {
+#pragma unroll 1
     for (int shift = 24; shift >= 0; shift -= 8) {
-      for (int k = threadIdx.x; k < 256; k += kThreads) hist[k] = 0;
+      hist[threadIdx.x] = 0;
       __syncthreads();
+#pragma unroll 4
       for (int p = max(b, lo) + threadIdx.x; p < min(e, hi); p += kThreads) {
-        const uint32_t u = rank_of(scores[p]);
+        const uint32_t u = rank_at(p);
         if (shift == 24 || (u >> (shift + 8)) == (prefix >> (shift + 8)))
           atomicAdd(&hist[(u >> shift) & 255], 1);
       }
       cluster.sync();
-      if (threadIdx.x < 256) {
+      {
         int n = 0;
+#pragma unroll 8
         for (int k = 0; k < C; ++k) n += cluster.map_shared_rank(hist, k)[threadIdx.x];
         merged[threadIdx.x] = n;
       }
       cluster.sync();   // (the parts are read before they are cleared)
       // The highest digit at which the counts from above reach `left`.
-      if (threadIdx.x < 32) {
+      if (warp == 0) {
         int mine = 0;   // digits 255 - 8 lane ... 248 - 8 lane
-        for (int k = 0; k < 8; ++k) mine += merged[255 - 8 * threadIdx.x - k];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) mine += merged[255 - 8 * lane - k];
         int x = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
           const int y = __shfl_up_sync(0xffffffffu, x, o);
-          if (static_cast<int>(threadIdx.x) >= o) x += y;
+          if (lane >= o) x += y;
         }
         if (x >= left && x - mine < left) {
           int above = x - mine;
+#pragma unroll 1
           for (int k = 0; k < 8; ++k) {
-            const int digit = 255 - 8 * threadIdx.x - k, n = merged[digit];
+            const int digit = 255 - 8 * lane - k, n = merged[digit];
             if (above + n >= left) {
               pick[0] = prefix | (static_cast<uint32_t>(digit) << shift);
               pick[1] = left - above;
@@ -198,112 +210,160 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const __grid_constant__
       prefix = pick[0];
       left = static_cast<int>(pick[1]);
     }
+  } else {
+    __syncthreads();   // (the ranks are there)
   }
   // What stays: first, recent, ranks above the threshold, and the first `left` at it.
-  if (threadIdx.x < 3) counts[threadIdx.x] = threadIdx.x == 2 ? INT_MAX : 0;
-  __syncthreads();
   auto level = [&](int p) {   // 2: stays, 1: at the threshold, 0: goes
     if (p < lo || p >= hi) return 2;
     if (want == 0) return 0;
-    const uint32_t u = rank_of(scores[p]);
+    const uint32_t u = rank_at(p);
     return u > prefix ? 2 : u == prefix ? 1 : 0;
   };
+  // A warp's share of the part, in whole 32s.
+  const int share = ((e - b + kWarps - 1) / kWarps + 31) / 32 * 32;
+  const int wb = min(e, b + warp * share), we = min(e, wb + share);
   int sure = 0, at = 0;
-  for (int p = b + threadIdx.x; p < e; p += kThreads) {
+#pragma unroll 4
+  for (int p = wb + lane; p < we; p += 32) {
     const int l = level(p);
     sure += l == 2;
     at += l == 1;
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    sure += __shfl_xor_sync(0xffffffffu, sure, o);
-    at += __shfl_xor_sync(0xffffffffu, at, o);
-  }
-  if ((threadIdx.x & 31) == 0) {
-    atomicAdd(&counts[0], sure);
-    atomicAdd(&counts[1], at);
+  sure = __reduce_add_sync(0xffffffffu, sure);
+  at = __reduce_add_sync(0xffffffffu, at);
+  if (lane == 0) warp_counts[0][warp] = sure, warp_counts[1][warp] = at;
+  __syncthreads();
+  if (threadIdx.x < 2) {
+    int n = 0;
+    for (int w = 0; w < kWarps; ++w) n += warp_counts[threadIdx.x][w];
+    counts[threadIdx.x] = n;
+  } else if (threadIdx.x == 2) {
+    counts[2] = INT_MAX;
   }
   cluster.sync();
-  int place = 0, tied = 0;   // before this part
+  int before = 0, tied = 0;   // sure and tied tokens before this warp's
+#pragma unroll 8
   for (int k = 0; k < c; ++k) {
     const int* other = cluster.map_shared_rank(counts, k);
-    place += other[0];
+    before += other[0];
     tied += other[1];
   }
-  place += min(tied, left);
-  for (int p0 = b; p0 < e; p0 += kThreads) {
-    const int p = p0 + threadIdx.x;
-    const int l = p < e ? level(p) : 0;
-    int n1, n2;
-    const int t = block_scan(l == 1, warp_sums, n1);
-    const bool stays = l == 2 || (l == 1 && tied + t < left);
-    const int j = block_scan(stays, warp_sums, n2);
-    if (stays) {
-      kept[place + j] = p;
-      if (place + j != p) atomicMin(&counts[2], place + j);
+  for (int w = 0; w < warp; ++w) before += warp_counts[0][w], tied += warp_counts[1][w];
+  int moved = INT_MAX;   // the first place whose row moves
+#pragma unroll 2
+  for (int p0 = wb; p0 < we; p0 += 32) {
+    const int p = p0 + lane;
+    const int l = p < we ? level(p) : 0;
+    const unsigned below = (1u << lane) - 1u;
+    const unsigned twos = __ballot_sync(0xffffffffu, l == 2), ones = __ballot_sync(0xffffffffu, l == 1);
+    const int t = tied + __popc(ones & below);
+    const int j = before + __popc(twos & below) + min(t, left);
+    if (l == 2 || (l == 1 && t < left)) {
+      kept[j] = p;
+      if (j != p) moved = min(moved, j);
     }
-    place += n2;
-    tied += n1;
+    before += __popc(twos);
+    tied += __popc(ones);
   }
-  cluster.sync();   // kept[] is complete, and seen by the cluster
+  moved = __reduce_min_sync(0xffffffffu, moved);
+  if (lane == 0 && moved != INT_MAX) atomicMin(&counts[2], moved);
+  cluster.sync();   // kept[] is complete, and seen by the cluster; the ranks are not needed
 
   // ------------------------------------------------------------ rows
-  int from = INT_MAX;   // the first place whose row moves
+  int from = INT_MAX;
+#pragma unroll 8
   for (int k = 0; k < C; ++k) from = min(from, cluster.map_shared_rank(counts, k)[2]);
-  // Sums, in the same steps as rows below where they may share memory.
-  constexpr int kLanes = Row::kVecs;                  // threads of a row
-  constexpr int kRows = kThreads / kLanes;            // rows of a round
-  constexpr int kRounds = 8;                          // rounds of a step
-  const int r = threadIdx.x / kLanes, v = threadIdx.x % kLanes;
-  const int step = C * kRows * kRounds;
-  for (int j0 = min(from, a.budget); j0 < a.budget; j0 += step) {
-    uint4 row[kRounds];
-    uint32_t tail[kRounds];
-    float sum[kRounds];
-    uint8_t* to[kRounds];
-    uint8_t* to_tail[kRounds];
+  from = min(from, a.budget);
+  // Step s, row q of this CTA: place from + (s C + c) kRows + q.
+  const uint32_t ring = smem_u32(smem);
+  const int r = threadIdx.x / Row::kVecs, v = threadIdx.x % Row::kVecs;
+  constexpr int kPass = kThreads / Row::kVecs;   // rows that the threads cover at once
+  const int steps = (a.budget - from + C * R::kRows - 1) / (C * R::kRows);
+  auto place = [&](int s, int k) { return from + (s * C + c) * R::kRows + k * kPass + r; };
+  int source[kPer];   // of the next step to be fetched
+  auto look = [&](int s) {
 #pragma unroll
-    for (int k = 0; k < kRounds; ++k) {
-      const int j = j0 + (k * C + c) * kRows + r;
-      to[k] = nullptr;
-      if (j < a.budget) {
-        const int p = kept[j];
-        sum[k] = scores[p];
-        const int sb = table[div_bs(p, a.bs, a.bs_log2)], db = table[div_bs(j, a.bs, a.bs_log2)];
-        const int so = mod_bs(p, a.bs, a.bs_log2), dof = mod_bs(j, a.bs, a.bs_log2);
-        if (sb >= 0 && sb < a.num_blocks && db >= 0 && db < a.num_blocks) {
-          row[k] = *reinterpret_cast<const uint4*>(Row::vec(a, sb, so, kvh, v));
-          to[k] = Row::vec(a, db, dof, kvh, v);
-          if constexpr (Row::kTail > 0) {
-            if (v < Row::kTail) {
-              tail[k] = *reinterpret_cast<const uint32_t*>(Row::tail(a, sb, so, kvh, v));
-              to_tail[k] = Row::tail(a, db, dof, kvh, v);
-            }
-          }
-        } else if (v == 0) {
-          record_error(a.err, PA_DEVERR_BLOCK_ID);
+    for (int k = 0; k < kPer; ++k) {
+      const int j = place(s, k);
+      source[k] = s < steps && j < a.budget ? kept[j] : -1;
+    }
+  };
+  auto fetch = [&](int s) {
+    const uint32_t to = ring + s % kSteps * R::kStepBytes;
+    int blk[kPer];
+#pragma unroll
+    for (int k = 0; k < kPer; ++k)
+      blk[k] = source[k] >= 0 ? table[div_bs(source[k], a.bs, a.bs_log2)] : -1;
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+      const int p = source[k], q = k * kPass + r;
+      if (p < 0) continue;
+      if (v == 0) copy_async<4>(to + R::kOffSum + q * 4, scores + p);
+      if (blk[k] < 0 || blk[k] >= a.num_blocks) continue;
+      const int off = mod_bs(p, a.bs, a.bs_log2);
+      cp_async_16(to + (k * kThreads + threadIdx.x) * 16, Row::vec(a, blk[k], off, kvh, v), 16);
+      if constexpr (Row::kTail > 0)
+        if (v < 2)
+          copy_async<Row::kTail>(to + R::kOffTail + (q * 2 + v) * Row::kTail,
+                                 Row::tail(a, blk[k], off, kvh, v));
+    }
+    look(s + 1);
+  };
+  look(0);
+#pragma unroll 1
+  for (int s = 0; s < kSteps - 1; ++s) {
+    if (s < steps) fetch(s);
+    cp_async_commit();
+  }
+#pragma unroll 1
+  for (int s = 0; s < steps; ++s) {
+    cp_async_wait<kSteps - 2>();
+    // Every row of the step has been read.
+    if (C > 1)
+      cluster.sync();
+    else
+      __syncthreads();
+    const uint8_t* held_step = smem + s % kSteps * R::kStepBytes;
+    int blk[kPer], p[kPer];
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+      const int j = place(s, k);
+      p[k] = j < a.budget ? kept[j] : -1;
+      blk[k] = j < a.budget ? table[div_bs(j, a.bs, a.bs_log2)] : -1;
+    }
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+      const int j = place(s, k), q = k * kPass + r;
+      if (p[k] < 0) continue;
+      if (v == 0) fresh[j] = *reinterpret_cast<const float*>(held_step + R::kOffSum + q * 4);
+      const int sb = table[div_bs(p[k], a.bs, a.bs_log2)];
+      if (blk[k] < 0 || blk[k] >= a.num_blocks || sb < 0 || sb >= a.num_blocks) {
+        if (v == 0) record_error(a.err, PA_DEVERR_BLOCK_ID);
+        continue;
+      }
+      const int off = mod_bs(j, a.bs, a.bs_log2);
+      *reinterpret_cast<uint4*>(Row::vec(a, blk[k], off, kvh, v)) =
+          *reinterpret_cast<const uint4*>(held_step + (k * kThreads + threadIdx.x) * 16);
+      if constexpr (Row::kTail > 0)
+        if (v < 2) {
+          uint8_t* to = Row::tail(a, blk[k], off, kvh, v);
+          const uint8_t* got = held_step + R::kOffTail + (q * 2 + v) * Row::kTail;
+          if constexpr (Row::kTail == 8)
+            *reinterpret_cast<uint2*>(to) = *reinterpret_cast<const uint2*>(got);
+          else
+            *reinterpret_cast<uint32_t*>(to) = *reinterpret_cast<const uint32_t*>(got);
         }
-      }
     }
-    cluster.sync();   // every row of the step has been read
-#pragma unroll
-    for (int k = 0; k < kRounds; ++k) {
-      const int j = j0 + (k * C + c) * kRows + r;
-      if (j < a.budget && v == 0) fresh[j] = sum[k];
-      if (to[k] != nullptr) {
-        *reinterpret_cast<uint4*>(to[k]) = row[k];
-        if constexpr (Row::kTail > 0)
-          if (v < Row::kTail) *reinterpret_cast<uint32_t*>(to_tail[k]) = tail[k];
-      }
-    }
+    if (s + kSteps - 1 < steps) fetch(s + kSteps - 1);
+    cp_async_commit();
   }
   if (fresh != scores)
-    for (int j = tid; j < min(from, a.budget); j += all) fresh[j] = scores[j];
+    for (int j = tid; j < from; j += all) fresh[j] = scores[j];
   // (The sums behind the budget have been read: by the last step's barrier, or, where no
   // row moved, there was none to read.)
-  for (int64_t p = a.budget + tid; p < (fresh != scores ? a.score_tokens : static_cast<int64_t>(seq));
-       p += all)
-    fresh[p] = 0.f;
+  const int64_t clear = fresh != scores ? a.score_tokens : static_cast<int64_t>(seq);
+  for (int64_t p = a.budget + tid; p < clear; p += all) fresh[p] = 0.f;
   cluster.sync();   // no CTA leaves while others read its shared memory
 }
 
@@ -320,42 +380,56 @@ struct BlocksArgs {
 };
 
 // New lengths; the blocks behind them go in front of free_start, by request and column.
-// One CTA: a scan over the requests, 1024 at a time.
-__global__ void __launch_bounds__(1024) evict_blocks_kernel(const __grid_constant__ BlocksArgs a) {
+// One cluster, whose CTAs each sum all requests' blocks and then take a range of them:
+// lengths may be updated in place, so nothing is written before all have read them.
+constexpr int kBlockCtas = 8;
+constexpr int kBlockThreads = 1024;
+__global__ void __launch_bounds__(kBlockThreads) evict_blocks_kernel(
+    const __grid_constant__ BlocksArgs a) {
   __shared__ int sums[32];
-  __shared__ unsigned long long total_s;
+  __shared__ unsigned long long totals[2];   // all blocks; those of requests before the range
+  __shared__ int list[3][kBlockThreads];     // of a round's requests: blocks, first column, place
+  cg::cluster_group cluster = cg::this_cluster();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (threadIdx.x < 2) totals[threadIdx.x] = 0;
+  __syncthreads();
   pdl_wait();
   pdl_trigger();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   auto ceil_bs = [&](int x) { return x > 0 ? div_bs(x - 1, a.bs, a.bs_log2) + 1 : 0; };
   auto lens = [&](int i, int& seq, int& keep) {
-    seq = i < a.num_seqs ? max(0, a.seq_lens[i]) : 0;
+    seq = max(0, a.seq_lens[i]);
     const bool refused = seq > a.score_tokens || seq > static_cast<int64_t>(a.max_blocks) * a.bs;
     keep = refused ? seq : min(seq, a.budget);
     return refused ? 0 : ceil_bs(seq) - ceil_bs(keep);
   };
-  if (threadIdx.x == 0) total_s = 0;
-  __syncthreads();
-  unsigned long long mine = 0;
-  for (int i = threadIdx.x; i < a.num_seqs; i += 1024) {
-    int seq, keep;
-    mine += lens(i, seq, keep);
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
-  if (lane == 0 && mine != 0) atomicAdd(&total_s, mine);
-  __syncthreads();
-  const long long total = static_cast<long long>(total_s);
-  const int start = a.free_start != nullptr ? *a.free_start : 0;
-  const bool room = a.free_blocks != nullptr && start >= total && start <= a.num_free;
-  if (threadIdx.x == 0 && a.free_blocks != nullptr && total > 0 && !room)
-    record_error(a.err, PA_DEVERR_LENGTH);
-  int before = room ? static_cast<int>(start - total) : 0;
-  __syncthreads();
-  for (int i0 = 0; i0 < a.num_seqs; i0 += 1024) {
-    const int i = i0 + threadIdx.x;
+  const int per = (a.num_seqs + kBlockCtas - 1) / kBlockCtas;
+  const int r0 = min(a.num_seqs, static_cast<int>(blockIdx.x) * per), r1 = min(a.num_seqs, r0 + per);
+  unsigned long long mine = 0, early = 0;
+  for (int i = threadIdx.x; i < a.num_seqs; i += kBlockThreads) {
     int seq, keep;
     const int n = lens(i, seq, keep);
+    mine += n;
+    if (i < r0) early += n;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    mine += __shfl_xor_sync(0xffffffffu, mine, o);
+    early += __shfl_xor_sync(0xffffffffu, early, o);
+  }
+  if (lane == 0 && mine != 0) atomicAdd(&totals[0], mine);
+  if (lane == 0 && early != 0) atomicAdd(&totals[1], early);
+  const int start = a.free_start != nullptr ? *a.free_start : 0;
+  __syncthreads();
+  const long long total = static_cast<long long>(totals[0]);
+  const bool room = a.free_blocks != nullptr && start >= total && start <= a.num_free;
+  if (blockIdx.x == 0 && threadIdx.x == 0 && a.free_blocks != nullptr && total > 0 && !room)
+    record_error(a.err, PA_DEVERR_LENGTH);
+  int before = room ? static_cast<int>(start - total + static_cast<long long>(totals[1])) : 0;
+  cluster.sync();
+  for (int i0 = r0; i0 < r1; i0 += kBlockThreads) {
+    const int i = i0 + threadIdx.x, count = min(kBlockThreads, r1 - i0);
+    int seq = 0, keep = 0, n = 0;
+    if (i < r1) n = lens(i, seq, keep);
     int x = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -364,36 +438,83 @@ __global__ void __launch_bounds__(1024) evict_blocks_kernel(const __grid_constan
     }
     if (lane == 31) sums[warp] = x;
     __syncthreads();
-    int base = before, chunk = 0;
+    int base = before;
     for (int w = 0; w < 32; ++w) {
       if (w < warp) base += sums[w];
-      chunk += sums[w];
+      before += sums[w];
     }
+    list[0][threadIdx.x] = n;
+    list[1][threadIdx.x] = ceil_bs(keep);
+    list[2][threadIdx.x] = base + x - n;
+    if (i < r1) a.new_lens[i] = keep;
     __syncthreads();
-    // A warp's requests in turn, their columns by its lanes.
-    const int at = base + x - n, col0 = ceil_bs(keep);
+    // A request's blocks are copied by a warp, or, where the requests are few, by all.
+    const bool few = count < 32;
+    const int width = few ? kBlockThreads : 32;
     if (room)
-      for (int k = 0; k < 32; ++k) {
-        const int cols = __shfl_sync(0xffffffffu, n, k);
-        const int to = __shfl_sync(0xffffffffu, at, k), from = __shfl_sync(0xffffffffu, col0, k);
-        const int64_t row = static_cast<int64_t>(i0 + warp * 32 + k) * a.max_blocks + from;
-        for (int q = lane; q < cols; q += 32) {
-          const int blk = a.block_table[row + q];
+      for (int k = few ? 0 : warp; k < count; k += few ? 1 : 32) {
+        const int cols = list[0][k], to = list[2][k];
+        const int32_t* row = a.block_table + static_cast<int64_t>(i0 + k) * a.max_blocks + list[1][k];
+#pragma unroll 4
+        for (int q = few ? threadIdx.x : lane; q < cols; q += width) {
+          const int blk = row[q];
           if (blk < 0 || blk >= a.num_blocks) record_error(a.err, PA_DEVERR_BLOCK_ID);
           a.free_blocks[to + q] = blk;
         }
       }
-    if (i < a.num_seqs) a.new_lens[i] = keep;
-    before += chunk;
+    __syncthreads();
   }
-  if (threadIdx.x == 0 && a.new_free_start != nullptr) *a.new_free_start = room ? static_cast<int>(start - total) : start;
+  if (blockIdx.x == 0 && threadIdx.x == 0 && a.new_free_start != nullptr)
+    *a.new_free_start = room ? static_cast<int>(start - total) : start;
+}
+
+// Whether clusters of 16 are there to be had (they are not portable).
+template <class Row>
+bool wide_clusters() {
+  static std::mutex mu;
+  static int known[64] = {};   // 1: yes, 2: no
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
+  std::lock_guard<std::mutex> lock(mu);
+  if (known[dev] == 0) {
+    known[dev] = 2;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(kMaxCtas);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = Ring<Row>::kBytes;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = kMaxCtas;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaFuncSetAttribute(evict_kernel<Row>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) ==
+            cudaSuccess &&
+        cudaOccupancyMaxActiveClusters(&n, evict_kernel<Row>, &cfg) == cudaSuccess) {
+      if (n >= 4) known[dev] = 1;
+    } else {
+      cudaGetLastError();   // (a refused size is no error of the call)
+    }
+  }
+  return known[dev] == 1;
 }
 
 template <class Row>
-cudaError_t launch_rows(const EvictArgs& a, int N, int C, cudaStream_t stream) {
+cudaError_t launch_rows(const EvictArgs& a, int N, int sm_count, cudaStream_t stream) {
+  static DeviceFlags smem_set;
+  cudaError_t e = set_smem_once(evict_kernel<Row>, Ring<Row>::kBytes, smem_set);
+  if (e != cudaSuccess) return e;
+  // CTAs per (request, kv head): a power of two, as many as leave eight CTAs for each SM
+  // (four rounds of two), but none with less than a step of rows.
+  const long long units = static_cast<long long>(N) * a.Hkv;
+  const int most = wide_clusters<Row>() ? kMaxCtas : 8;
+  int C = 1;
+  while (C < most && 2 * C * units <= 8LL * sm_count && 2LL * C * Ring<Row>::kRows <= a.budget) C *= 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(C, a.Hkv, N);
   cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = Ring<Row>::kBytes;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -428,20 +549,16 @@ cudaError_t launch_evict(const EvictLaunch& n, cudaStream_t stream) {
   a.recent = n.recent;
   a.first = n.first;
   a.d = n.d;
-  // CTAs per (request, kv head): as many as leave two per SM, a power of two up to 8.
-  const long long units = static_cast<long long>(n.N) * n.Hkv;
-  int C = 1;
-  while (C < 8 && 2 * C * units <= 2LL * n.sm_count) C *= 2;
   cudaError_t e;
   if (n.four)
-    e = n.d == 128 ? launch_rows<Four<128>>(a, n.N, C, stream)
-                   : launch_rows<Four<64>>(a, n.N, C, stream);
+    e = n.d == 128 ? launch_rows<Four<128>>(a, n.N, n.sm_count, stream)
+                   : launch_rows<Four<64>>(a, n.N, n.sm_count, stream);
   else if (n.row_bytes == 256)
-    e = launch_rows<Plain<256>>(a, n.N, C, stream);
+    e = launch_rows<Plain<256>>(a, n.N, n.sm_count, stream);
   else if (n.row_bytes == 128)
-    e = launch_rows<Plain<128>>(a, n.N, C, stream);
+    e = launch_rows<Plain<128>>(a, n.N, n.sm_count, stream);
   else
-    e = launch_rows<Plain<64>>(a, n.N, C, stream);
+    e = launch_rows<Plain<64>>(a, n.N, n.sm_count, stream);
   if (e != cudaSuccess) return e;
   BlocksArgs f{};
   f.block_table = n.block_table;
@@ -459,7 +576,19 @@ cudaError_t launch_evict(const EvictLaunch& n, cudaStream_t stream) {
   f.num_blocks = n.num_blocks;
   f.budget = n.budget;
   f.score_tokens = n.score_tokens;
-  return launch_pdl(evict_blocks_kernel, dim3(1), dim3(1024), 0, stream, f);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(kBlockCtas);
+  cfg.blockDim = dim3(kBlockThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = kBlockCtas;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, evict_blocks_kernel, f);
 }
 
 }  // namespace pa
