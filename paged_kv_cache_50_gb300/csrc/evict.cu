@@ -39,10 +39,8 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256;   // that move rows (a CTA has more: see Ring)
 constexpr int kWarps = kThreads / 32;
-constexpr int kPer = 4;                     // 16-byte vectors of a thread in a step
-constexpr int kSteps = 5;                   // steps in the ring
 constexpr int kMaxCtas = 16;
 
 struct EvictArgs {
@@ -67,45 +65,58 @@ __device__ __forceinline__ uint32_t rank_of(float x) {
 }
 
 // A cached row of one head, key and value, in 16-byte vectors (kVecs) and, for the
-// 4-bit pool, the key's and the value's scales (kTail bytes each).
+// 4-bit pool, the key's and the value's scales (kTail bytes each): byte offsets in the
+// pool of the row's first vector and (behind that) first scales, and from there of the
+// others, the same for every row.
 template <int ROW>   // bytes of a key (or value): 256, 128, 64
 struct Plain {
   static constexpr int kVecs = 2 * ROW / 16;
   static constexpr int kTail = 0;
-  __device__ static __forceinline__ uint8_t* vec(const EvictArgs& a, int64_t blk, int off, int head,
-                                                 int v) {
-    const int kv = v / (ROW / 16), c = v % (ROW / 16);
-    return a.cache + (((blk * 2 + kv) * a.bs + off) * a.Hkv + head) * ROW + c * 16;
+  static constexpr int kPer = 4, kSteps = 5;
+  __device__ static __forceinline__ int64_t row(const EvictArgs& a, int64_t blk, int off, int head) {
+    return ((blk * 2 * a.bs + off) * a.Hkv + head) * ROW;
   }
-  __device__ static __forceinline__ uint8_t* tail(const EvictArgs& a, int64_t, int, int, int) {
-    return a.cache;
+  __device__ static __forceinline__ int tail(int) { return 0; }
+  __device__ static __forceinline__ int64_t vec(const EvictArgs& a, int v) {
+    return static_cast<int64_t>(v / (ROW / 16)) * a.bs * a.Hkv * ROW + v % (ROW / 16) * 16;
   }
 };
 template <int D>
 struct Four {
   static constexpr int kVecs = 2 * (D / 2) / 16;
   static constexpr int kTail = D / 16;
-  __device__ static __forceinline__ uint8_t* tile(const EvictArgs& a, int64_t blk, int off, int head,
-                                                  int kv) {
-    return a.cache + fp4::pair_at(blk, head, off >> 4, a.Hkv, a.bs >> 4, D) + kv * fp4::tile_bytes(D);
+  static constexpr int kPer = 2, kSteps = 6;   // (more rows to a vector: longer lists)
+  __device__ static __forceinline__ int64_t row(const EvictArgs& a, int64_t blk, int off, int head) {
+    return fp4::pair_at(blk, head, off >> 4, a.Hkv, a.bs >> 4, D) + (off & 15) * (D / 2);
   }
-  __device__ static __forceinline__ uint8_t* vec(const EvictArgs& a, int64_t blk, int off, int head,
-                                                 int v) {
-    return tile(a, blk, off, head, v / (D / 32)) + (off & 15) * (D / 2) + v % (D / 32) * 16;
+  __device__ static __forceinline__ int tail(int off) {
+    return 8 * D + (off & 15) * (D / 16 - D / 2);
   }
-  __device__ static __forceinline__ uint8_t* tail(const EvictArgs& a, int64_t blk, int off, int head,
-                                                  int kv) {
-    return tile(a, blk, off, head, kv) + 8 * D + (off & 15) * (D / 16);
+  __device__ static __forceinline__ int64_t vec(const EvictArgs&, int v) {
+    return v / (D / 32) * fp4::tile_bytes(D) + v % (D / 32) * 16;
   }
+  static constexpr int kTile = fp4::tile_bytes(D);   // from the key's to the value's
+};
+// What is moved: from and to (offsets in the pool, -1: not there), the position, and
+// where the scales are.
+struct Move {
+  int64_t from, to;
+  int p;
+  int16_t from_tail, to_tail;
 };
 template <class Row>
 struct Ring {
+  // 16-byte vectors of a thread in a step, and steps in the ring.
+  static constexpr int kPer = Row::kPer, kSteps = Row::kSteps;
   static constexpr int kRows = kThreads * kPer / Row::kVecs;   // of a CTA in a step
   static constexpr int kOffTail = kThreads * kPer * 16;
   static constexpr int kOffSum = kOffTail + kRows * 2 * Row::kTail;
   static constexpr int kStepBytes = (kOffSum + kRows * 4 + 15) / 16 * 16;
-  static constexpr int kBytes = kSteps * kStepBytes;
+  static constexpr int kOffMoves = kSteps * kStepBytes;        // lists of kSteps + 1 steps
+  static constexpr int kBytes = kOffMoves + (kSteps + 1) * kRows * static_cast<int>(sizeof(Move));
   static constexpr int kKeys = kBytes / 4;                     // ranks that fit it
+  // Warps beside the kThreads that move rows: they make the lists.
+  static constexpr int kAll = kThreads + (kRows + 31) / 32 * 32;
 };
 
 template <int BYTES>
@@ -114,8 +125,9 @@ __device__ __forceinline__ void copy_async(uint32_t dst, const void* src) {
 }
 
 template <class Row>
-__global__ void __launch_bounds__(kThreads, 2) evict_kernel(const __grid_constant__ EvictArgs a) {
+__global__ void __launch_bounds__(Ring<Row>::kAll, 2) evict_kernel(const __grid_constant__ EvictArgs a) {
   using R = Ring<Row>;
+  constexpr int kPer = R::kPer, kSteps = R::kSteps;
   extern __shared__ __align__(16) uint8_t smem[];   // the part's ranks, then the ring
   __shared__ int hist[256];
   __shared__ int merged[256];
@@ -125,6 +137,7 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const __grid_constan
   const int kvh = blockIdx.y, i = blockIdx.z;
   const int C = gridDim.x, c = blockIdx.x;   // cluster = grid.x
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const bool mover = threadIdx.x < kThreads;
   cg::cluster_group cluster = cg::this_cluster();
   pdl_wait();
   pdl_trigger();
@@ -134,7 +147,7 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const __grid_constan
   float* fresh = a.new_scores + unit * a.score_tokens;
   int32_t* kept = a.kept + unit * a.budget;
   const int32_t* table = a.block_table + static_cast<int64_t>(i) * a.max_blocks;
-  const int tid = c * kThreads + threadIdx.x, all = C * kThreads;
+  const int tid = c * R::kAll + threadIdx.x, all = C * R::kAll;
 
   // A length past the sums or the table: nothing is done to the request.
   const bool refused = seq > a.score_tokens || seq > static_cast<int64_t>(a.max_blocks) * a.bs;
@@ -157,7 +170,7 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const __grid_constan
   const bool held = per <= R::kKeys;   // (else they are read again)
   if (held) {
 #pragma unroll 4
-    for (int p = b + threadIdx.x; p < e; p += kThreads) keys[p - b] = rank_of(scores[p]);
+    for (int p = b + threadIdx.x; p < e; p += R::kAll) keys[p - b] = rank_of(scores[p]);
   }
   auto rank_at = [&](int p) { return held ? keys[p - b] : rank_of(scores[p]); };
   uint32_t prefix = 0;
@@ -165,16 +178,16 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const __grid_constan
   if (want > 0) {
 #pragma unroll 1
     for (int shift = 24; shift >= 0; shift -= 8) {
-      hist[threadIdx.x] = 0;
+      if (mover) hist[threadIdx.x] = 0;
       __syncthreads();
 #pragma unroll 4
-      for (int p = max(b, lo) + threadIdx.x; p < min(e, hi); p += kThreads) {
+      for (int p = max(b, lo) + threadIdx.x; p < min(e, hi); p += R::kAll) {
         const uint32_t u = rank_at(p);
         if (shift == 24 || (u >> (shift + 8)) == (prefix >> (shift + 8)))
           atomicAdd(&hist[(u >> shift) & 255], 1);
       }
       cluster.sync();
-      {
+      if (mover) {
         int n = 0;
 #pragma unroll 8
         for (int k = 0; k < C; ++k) n += cluster.map_shared_rank(hist, k)[threadIdx.x];
@@ -222,7 +235,7 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const __grid_constan
   };
   // A warp's share of the part, in whole 32s.
   const int share = ((e - b + kWarps - 1) / kWarps + 31) / 32 * 32;
-  const int wb = min(e, b + warp * share), we = min(e, wb + share);
+  const int wb = mover ? min(e, b + warp * share) : e, we = min(e, wb + share);
   int sure = 0, at = 0;
 #pragma unroll 4
   for (int p = wb + lane; p < we; p += 32) {
@@ -232,7 +245,7 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const __grid_constan
   }
   sure = __reduce_add_sync(0xffffffffu, sure);
   at = __reduce_add_sync(0xffffffffu, at);
-  if (lane == 0) warp_counts[0][warp] = sure, warp_counts[1][warp] = at;
+  if (mover && lane == 0) warp_counts[0][warp] = sure, warp_counts[1][warp] = at;
   __syncthreads();
   if (threadIdx.x < 2) {
     int n = 0;
@@ -249,7 +262,7 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const __grid_constan
     before += other[0];
     tied += other[1];
   }
-  for (int w = 0; w < warp; ++w) before += warp_counts[0][w], tied += warp_counts[1][w];
+  for (int w = 0; w < min(warp, kWarps); ++w) before += warp_counts[0][w], tied += warp_counts[1][w];
   int moved = INT_MAX;   // the first place whose row moves
 #pragma unroll 2
   for (int p0 = wb; p0 < we; p0 += 32) {
@@ -275,79 +288,102 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const __grid_constan
 #pragma unroll 8
   for (int k = 0; k < C; ++k) from = min(from, cluster.map_shared_rank(counts, k)[2]);
   from = min(from, a.budget);
-  // Step s, row q of this CTA: place from + (s C + c) kRows + q.
+  // Step s, row q of this CTA: place from + (s C + c) kRows + q.  The warps behind the
+  // movers make the lists, a thread for each row: a step's position, then its blocks,
+  // then its addresses, each a turn of the loop after the one before, so that none is
+  // waited for.
   const uint32_t ring = smem_u32(smem);
+  Move* moves = reinterpret_cast<Move*>(smem + R::kOffMoves);
   const int r = threadIdx.x / Row::kVecs, v = threadIdx.x % Row::kVecs;
   constexpr int kPass = kThreads / Row::kVecs;   // rows that the threads cover at once
   const int steps = (a.budget - from + C * R::kRows - 1) / (C * R::kRows);
-  auto place = [&](int s, int k) { return from + (s * C + c) * R::kRows + k * kPass + r; };
-  int source[kPer];   // of the next step to be fetched
-  auto look = [&](int s) {
-#pragma unroll
-    for (int k = 0; k < kPer; ++k) {
-      const int j = place(s, k);
-      source[k] = s < steps && j < a.budget ? kept[j] : -1;
+  const int q0 = static_cast<int>(threadIdx.x) - kThreads;
+  auto place = [&](int s) { return from + (s * C + c) * R::kRows + q0; };
+  int p1 = -1;                      // of the step after the next to be listed
+  int p2 = -1, sb = -1, db = -1;    // of the next
+  auto list = [&](int s) {          // the list of step s, blocks of s + 1, positions of s + 2
+    if (s >= 0) {
+      Move m{-1, -1, p2, 0, 0};
+      if (p2 >= 0) {
+        const int j = place(s);
+        if (sb >= 0 && sb < a.num_blocks && db >= 0 && db < a.num_blocks) {
+          const int so = mod_bs(p2, a.bs, a.bs_log2), dof = mod_bs(j, a.bs, a.bs_log2);
+          m.from = Row::row(a, sb, so, kvh);
+          m.to = Row::row(a, db, dof, kvh);
+          m.from_tail = static_cast<int16_t>(Row::tail(so));
+          m.to_tail = static_cast<int16_t>(Row::tail(dof));
+        } else {
+          record_error(a.err, PA_DEVERR_BLOCK_ID);
+        }
+      }
+      moves[s % (kSteps + 1) * R::kRows + q0] = m;
     }
+    p2 = p1;
+    if (p2 >= 0) {
+      sb = table[div_bs(p2, a.bs, a.bs_log2)];
+      db = table[div_bs(place(s + 1), a.bs, a.bs_log2)];
+    }
+    const int j = place(s + 2);
+    p1 = s + 2 < steps && j < a.budget ? kept[j] : -1;
   };
+  const int64_t mine = Row::vec(a, v);
   auto fetch = [&](int s) {
     const uint32_t to = ring + s % kSteps * R::kStepBytes;
-    int blk[kPer];
-#pragma unroll
-    for (int k = 0; k < kPer; ++k)
-      blk[k] = source[k] >= 0 ? table[div_bs(source[k], a.bs, a.bs_log2)] : -1;
+    const Move* m = moves + s % (kSteps + 1) * R::kRows;
 #pragma unroll
     for (int k = 0; k < kPer; ++k) {
-      const int p = source[k], q = k * kPass + r;
-      if (p < 0) continue;
-      if (v == 0) copy_async<4>(to + R::kOffSum + q * 4, scores + p);
-      if (blk[k] < 0 || blk[k] >= a.num_blocks) continue;
-      const int off = mod_bs(p, a.bs, a.bs_log2);
-      cp_async_16(to + (k * kThreads + threadIdx.x) * 16, Row::vec(a, blk[k], off, kvh, v), 16);
+      const int q = k * kPass + r;
+      const int64_t src = m[q].from;
+      if (v == 0 && m[q].p >= 0) copy_async<4>(to + R::kOffSum + q * 4, scores + m[q].p);
+      if (src < 0) continue;
+      cp_async_16(to + (k * kThreads + threadIdx.x) * 16, a.cache + src + mine, 16);
       if constexpr (Row::kTail > 0)
         if (v < 2)
           copy_async<Row::kTail>(to + R::kOffTail + (q * 2 + v) * Row::kTail,
-                                 Row::tail(a, blk[k], off, kvh, v));
+                                 a.cache + src + m[q].from_tail + v * Row::kTile);
     }
-    look(s + 1);
   };
-  look(0);
+  if (!mover) {
 #pragma unroll 1
-  for (int s = 0; s < kSteps - 1; ++s) {
-    if (s < steps) fetch(s);
-    cp_async_commit();
+    for (int s = -2; s < kSteps; ++s) list(s);
+  }
+  __syncthreads();
+  if (mover) {
+#pragma unroll 1
+    for (int s = 0; s < kSteps - 1; ++s) {
+      if (s < steps) fetch(s);
+      cp_async_commit();
+    }
   }
 #pragma unroll 1
   for (int s = 0; s < steps; ++s) {
     cp_async_wait<kSteps - 2>();
-    // Every row of the step has been read.
-    if (C > 1)
-      cluster.sync();
-    else
-      __syncthreads();
-    const uint8_t* held_step = smem + s % kSteps * R::kStepBytes;
-    int blk[kPer], p[kPer];
-#pragma unroll
-    for (int k = 0; k < kPer; ++k) {
-      const int j = place(s, k);
-      p[k] = j < a.budget ? kept[j] : -1;
-      blk[k] = j < a.budget ? table[div_bs(j, a.bs, a.bs_log2)] : -1;
+    // Every row of the step has been read.  (Nothing is published: what has been read
+    // is in shared memory, and may be written over.)
+    if (C > 1) {
+      asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+      tc::cluster_wait();
     }
+    __syncthreads();   // (and the next list is there)
+    if (!mover) {
+      list(s + kSteps);
+      continue;
+    }
+    const uint8_t* held_step = smem + s % kSteps * R::kStepBytes;
+    const Move* m = moves + s % (kSteps + 1) * R::kRows;
 #pragma unroll
     for (int k = 0; k < kPer; ++k) {
-      const int j = place(s, k), q = k * kPass + r;
-      if (p[k] < 0) continue;
-      if (v == 0) fresh[j] = *reinterpret_cast<const float*>(held_step + R::kOffSum + q * 4);
-      const int sb = table[div_bs(p[k], a.bs, a.bs_log2)];
-      if (blk[k] < 0 || blk[k] >= a.num_blocks || sb < 0 || sb >= a.num_blocks) {
-        if (v == 0) record_error(a.err, PA_DEVERR_BLOCK_ID);
-        continue;
-      }
-      const int off = mod_bs(j, a.bs, a.bs_log2);
-      *reinterpret_cast<uint4*>(Row::vec(a, blk[k], off, kvh, v)) =
+      const int q = k * kPass + r;
+      const int64_t dst = m[q].to;
+      if (v == 0 && m[q].p >= 0)
+        fresh[from + (s * C + c) * R::kRows + q] =
+            *reinterpret_cast<const float*>(held_step + R::kOffSum + q * 4);
+      if (dst < 0) continue;
+      *reinterpret_cast<uint4*>(a.cache + dst + mine) =
           *reinterpret_cast<const uint4*>(held_step + (k * kThreads + threadIdx.x) * 16);
       if constexpr (Row::kTail > 0)
         if (v < 2) {
-          uint8_t* to = Row::tail(a, blk[k], off, kvh, v);
+          uint8_t* to = a.cache + dst + m[q].to_tail + v * Row::kTile;
           const uint8_t* got = held_step + R::kOffTail + (q * 2 + v) * Row::kTail;
           if constexpr (Row::kTail == 8)
             *reinterpret_cast<uint2*>(to) = *reinterpret_cast<const uint2*>(got);
@@ -480,7 +516,7 @@ bool wide_clusters() {
     known[dev] = 2;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(kMaxCtas);
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(Ring<Row>::kAll);
     cfg.dynamicSmemBytes = Ring<Row>::kBytes;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -513,7 +549,7 @@ cudaError_t launch_rows(const EvictArgs& a, int N, int sm_count, cudaStream_t st
   while (C < most && 2 * C * units <= 8LL * sm_count && 2LL * C * Ring<Row>::kRows <= a.budget) C *= 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(C, a.Hkv, N);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(Ring<Row>::kAll);
   cfg.dynamicSmemBytes = Ring<Row>::kBytes;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
