@@ -9,11 +9,13 @@
 // One cluster of up to 16 CTAs serves one (request, kv head); a CTA has a part of the
 // tokens, whose ranks it keeps in shared memory.
 //  1. The lowest sum that stays is found by its bits, eight at a time: a histogram
-//     in each CTA's shared memory over its part, summed over the cluster.
+//     in each CTA's shared memory over its part, summed over the cluster, one barrier of
+//     the cluster for each (two histograms in turn).
 //  2. Each warp counts what stays in its share of the part; with the offsets of the
 //     warps and CTAs before it, it writes the positions to kept[], by ballots.
 //  3. Rows move in steps: a CTA copies its rows of a step into a ring in shared memory
-//     (cp.async), several steps ahead, and from there to their places.  A kept row's
+//     (cp.async), several steps ahead, and from there to their places, by lists of
+//     addresses that warps of their own make.  A kept row's
 //     source never lies before its place, and the places of a step hold sources of this
 //     step and of earlier ones only: so a step is written when all CTAs have it in their
 //     rings, one barrier of the cluster for each, and no other order is needed.  A thread
@@ -21,7 +23,10 @@
 //     first one that goes) are not touched.
 // A second, small kernel writes the new lengths and pushes the blocks.
 //
-// Bound by HBM (each moved row is read and written once).
+// Bound by HBM in the long run (each moved row is read and written once): 64 requests in
+// bf16 move 667 MB in 150 us.  One long stream has no more than 96 CTAs (8 clusters of 12)
+// and is bound by their chains of barriers: 58 us, of them 9 for the ranks' loads, 11 for
+// the four histograms, 8 for the list and the first rows, 21 for the rows.
 #include <cooperative_groups.h>
 #include <math_constants.h>
 
@@ -39,9 +44,8 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kThreads = 256;   // that move rows (a CTA has more: see Ring)
-constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCtas = 16;
+constexpr int kMaxWarps = 24;
 
 struct EvictArgs {
   uint8_t* cache;
@@ -67,12 +71,16 @@ __device__ __forceinline__ uint32_t rank_of(float x) {
 // A cached row of one head, key and value, in 16-byte vectors (kVecs) and, for the
 // 4-bit pool, the key's and the value's scales (kTail bytes each): byte offsets in the
 // pool of the row's first vector and (behind that) first scales, and from there of the
-// others, the same for every row.
+// others, the same for every row.  kMovers threads move kPer vectors each in a step, with
+// kSteps steps in flight, kCtas CTAs to an SM: a step's time is the chain of a warp's
+// instructions, so threads are many and steps are large.  (64 requests in bf16: 2 CTAs
+// with 5 steps 185 us, 3 with 4: 160, 4 with 3: 177.  A stream of the 4-bit pool: 256
+// threads with 4 vectors 64 us, 512 with 2: 58, 512 with 1: 69.)
 template <int ROW>   // bytes of a key (or value): 256, 128, 64
 struct Plain {
   static constexpr int kVecs = 2 * ROW / 16;
   static constexpr int kTail = 0;
-  static constexpr int kPer = 4, kSteps = 5;
+  static constexpr int kMovers = 256, kPer = 4, kSteps = 4, kCtas = 3, kSpread = 2;
   __device__ static __forceinline__ int64_t row(const EvictArgs& a, int64_t blk, int off, int head) {
     return ((blk * 2 * a.bs + off) * a.Hkv + head) * ROW;
   }
@@ -85,7 +93,7 @@ template <int D>
 struct Four {
   static constexpr int kVecs = 2 * (D / 2) / 16;
   static constexpr int kTail = D / 16;
-  static constexpr int kPer = 2, kSteps = 6;   // (more rows to a vector: longer lists)
+  static constexpr int kMovers = 512, kPer = 2, kSteps = 4, kCtas = 2, kSpread = 1;
   __device__ static __forceinline__ int64_t row(const EvictArgs& a, int64_t blk, int off, int head) {
     return fp4::pair_at(blk, head, off >> 4, a.Hkv, a.bs >> 4, D) + (off & 15) * (D / 2);
   }
@@ -106,8 +114,7 @@ struct Move {
 };
 template <class Row>
 struct Ring {
-  // 16-byte vectors of a thread in a step, and steps in the ring.
-  static constexpr int kPer = Row::kPer, kSteps = Row::kSteps;
+  static constexpr int kThreads = Row::kMovers, kPer = Row::kPer, kSteps = Row::kSteps;
   static constexpr int kRows = kThreads * kPer / Row::kVecs;   // of a CTA in a step
   static constexpr int kOffTail = kThreads * kPer * 16;
   static constexpr int kOffSum = kOffTail + kRows * 2 * Row::kTail;
@@ -116,7 +123,8 @@ struct Ring {
   static constexpr int kBytes = kOffMoves + (kSteps + 1) * kRows * static_cast<int>(sizeof(Move));
   static constexpr int kKeys = kBytes / 4;                     // ranks that fit it
   // Warps beside the kThreads that move rows: they make the lists.
-  static constexpr int kAll = kThreads + (kRows + 31) / 32 * 32;
+  static constexpr int kAll = kThreads + kRows;
+  static_assert(kRows % 32 == 0, "whole warps, a thread for each row of a step");
 };
 
 template <int BYTES>
@@ -124,19 +132,136 @@ __device__ __forceinline__ void copy_async(uint32_t dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(BYTES) : "memory");
 }
 
+constexpr uint32_t kStays = 0xffffffffu;   // (above every rank)
+
+struct Shared {
+  int hist[2][256];
+  __align__(16) int merged[256];
+  int counts[3];   // this part's tokens above the threshold, at it; first place that moves
+  int warp_counts[2][kMaxWarps];
+};
+
+// What stays of a CTA's part [b, e), whose ranks `rank` gives: above a threshold, or at it
+// and among the first there.  Writes kept[], and counts[2] of the cluster's CTAs.
+template <class Row, class Rank>
+__device__ __forceinline__ void select(const EvictArgs& a, cg::cluster_group& cluster, Rank rank,
+                                       int b, int e, int want, int32_t* kept, Shared& sh) {
+  constexpr int kAll = Ring<Row>::kAll, kWarps = kAll / 32;
+  static_assert(kWarps <= kMaxWarps);
+  const int C = gridDim.x, c = blockIdx.x;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  uint32_t prefix = want > 0 ? 0u : kStays - 1;
+  int left = want;   // of those that share the prefix
+  if (threadIdx.x < 256) sh.hist[0][threadIdx.x] = 0;
+  __syncthreads();   // (and the ranks are there)
+  if (want > 0) {
+#pragma unroll 1
+    for (int shift = 24; shift >= 0; shift -= 8) {
+      int* hist = sh.hist[shift >> 3 & 1 ^ 1];
+#pragma unroll 4
+      for (int p = b + threadIdx.x; p < e; p += kAll) {
+        const uint32_t u = rank(p);
+        if (u != kStays && (shift == 24 || (u >> (shift + 8)) == (prefix >> (shift + 8))))
+          atomicAdd(&hist[(u >> shift) & 255], 1);
+      }
+      cluster.sync();
+      // (The other histogram was read before this barrier.)
+      if (threadIdx.x < 256) {
+        int n = 0;
+#pragma unroll 8
+        for (int k = 0; k < C; ++k) n += cluster.map_shared_rank(hist, k)[threadIdx.x];
+        sh.merged[255 - threadIdx.x] = n;
+        sh.hist[shift >> 3 & 1][threadIdx.x] = 0;
+      }
+      __syncthreads();
+      // The highest digit at which the counts from above reach `left`, in each warp.
+      int n[8];   // digits 255 - 8 lane ... 248 - 8 lane
+      *reinterpret_cast<int4*>(n) = reinterpret_cast<const int4*>(sh.merged)[2 * lane];
+      *reinterpret_cast<int4*>(n + 4) = reinterpret_cast<const int4*>(sh.merged)[2 * lane + 1];
+#pragma unroll
+      for (int k = 1; k < 8; ++k) n[k] += n[k - 1];
+      int x = n[7];
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      int above = x - n[7], digit = 255 - 8 * lane;
+      const int short_of = left - above;
+#pragma unroll
+      for (int k = 0; k < 7; ++k)
+        if (n[k] < short_of) above = x - n[7] + n[k], digit = 254 - 8 * lane - k;
+      const int hit = __ffs(__ballot_sync(0xffffffffu, x >= left)) - 1;
+      prefix |= static_cast<uint32_t>(__shfl_sync(0xffffffffu, digit, hit)) << shift;
+      left -= __shfl_sync(0xffffffffu, above, hit);
+      __syncthreads();   // (merged[] is written again)
+    }
+  }
+  // A warp's share of the part, in whole 32s.
+  const int share = ((e - b + kWarps - 1) / kWarps + 31) / 32 * 32;
+  const int wb = min(e, b + warp * share), we = min(e, wb + share);
+  int before = 0, tied = 0;   // tokens that stay for sure, tied ones: first those of the share
+#pragma unroll 4
+  for (int p = wb + lane; p < we; p += 32) {
+    const uint32_t u = rank(p);
+    before += u > prefix;
+    tied += u == prefix;
+  }
+  before = __reduce_add_sync(0xffffffffu, before);
+  tied = __reduce_add_sync(0xffffffffu, tied);
+  if (lane == 0) sh.warp_counts[0][warp] = before, sh.warp_counts[1][warp] = tied;
+  __syncthreads();
+  // Then those of the warps before, and, by the first two threads, of the part.
+  before = tied = 0;
+  int part = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    const int s0 = sh.warp_counts[0][w], s1 = sh.warp_counts[1][w];
+    if (w < warp) before += s0, tied += s1;
+    part += threadIdx.x == 0 ? s0 : s1;
+  }
+  if (threadIdx.x < 3) sh.counts[threadIdx.x] = threadIdx.x < 2 ? part : INT_MAX;
+  cluster.sync();
+  {
+    // And those of the CTAs before.
+    int s0 = 0, s1 = 0;
+    if (lane < c) {
+      const int* other = cluster.map_shared_rank(sh.counts, lane);
+      s0 = other[0], s1 = other[1];
+    }
+    before += __reduce_add_sync(0xffffffffu, s0);
+    tied += __reduce_add_sync(0xffffffffu, s1);
+  }
+  int moved = INT_MAX;   // the first place whose row moves
+  const unsigned below = (1u << lane) - 1u;
+#pragma unroll 4
+  for (int p0 = wb; p0 < we; p0 += 32) {
+    const int p = p0 + lane;
+    const uint32_t u = p < we ? rank(p) : 0u;
+    const bool over = p < we && u > prefix, equal = p < we && u == prefix;
+    const unsigned twos = __ballot_sync(0xffffffffu, over), ones = __ballot_sync(0xffffffffu, equal);
+    const int t = tied + __popc(ones & below);
+    const int j = before + __popc(twos & below) + min(t, left);
+    if (over || (equal && t < left)) {
+      kept[j] = p;
+      if (j != p) moved = min(moved, j);
+    }
+    before += __popc(twos);
+    tied += __popc(ones);
+  }
+  moved = __reduce_min_sync(0xffffffffu, moved);
+  if (lane == 0 && moved != INT_MAX) atomicMin(&sh.counts[2], moved);
+  cluster.sync();   // kept[] is complete, and seen by the cluster; the ranks are not needed
+}
+
 template <class Row>
-__global__ void __launch_bounds__(Ring<Row>::kAll, 2) evict_kernel(const __grid_constant__ EvictArgs a) {
+__global__ void __launch_bounds__(Ring<Row>::kAll, Row::kCtas) evict_kernel(const __grid_constant__ EvictArgs a) {
   using R = Ring<Row>;
-  constexpr int kPer = R::kPer, kSteps = R::kSteps;
+  constexpr int kThreads = R::kThreads, kPer = R::kPer, kSteps = R::kSteps;
   extern __shared__ __align__(16) uint8_t smem[];   // the part's ranks, then the ring
-  __shared__ int hist[256];
-  __shared__ int merged[256];
-  __shared__ int counts[3];   // this part's tokens above the threshold, at it; first place that moves
-  __shared__ int warp_counts[2][kWarps];
-  __shared__ uint32_t pick[2];   // threshold's bits so far, how many at or above it are wanted
+  __shared__ Shared shared;
   const int kvh = blockIdx.y, i = blockIdx.z;
   const int C = gridDim.x, c = blockIdx.x;   // cluster = grid.x
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const bool mover = threadIdx.x < kThreads;
   cg::cluster_group cluster = cg::this_cluster();
   pdl_wait();
@@ -163,131 +288,28 @@ __global__ void __launch_bounds__(Ring<Row>::kAll, 2) evict_kernel(const __grid_
 
   // ------------------------------------------------------------ selection
   // Candidates [lo, hi), of which `want` stay; this CTA's part [b, e) of all positions.
+  // The ranks of the part are held in shared memory (ones that stay in any case as
+  // kStays), or, where they do not fit it, made from the sums each time.
   const int lo = a.first, hi = seq - a.recent, want = a.budget - a.first - a.recent;
   const int per = (seq + C - 1) / C;
   const int b = min(seq, c * per), e = min(seq, b + per);
   uint32_t* keys = reinterpret_cast<uint32_t*>(smem);
-  const bool held = per <= R::kKeys;   // (else they are read again)
-  if (held) {
-#pragma unroll 4
-    for (int p = b + threadIdx.x; p < e; p += R::kAll) keys[p - b] = rank_of(scores[p]);
-  }
-  auto rank_at = [&](int p) { return held ? keys[p - b] : rank_of(scores[p]); };
-  uint32_t prefix = 0;
-  int left = want;   // of those that share the prefix
-  if (want > 0) {
-#pragma unroll 1
-    for (int shift = 24; shift >= 0; shift -= 8) {
-      if (mover) hist[threadIdx.x] = 0;
-      __syncthreads();
-#pragma unroll 4
-      for (int p = max(b, lo) + threadIdx.x; p < min(e, hi); p += R::kAll) {
-        const uint32_t u = rank_at(p);
-        if (shift == 24 || (u >> (shift + 8)) == (prefix >> (shift + 8)))
-          atomicAdd(&hist[(u >> shift) & 255], 1);
-      }
-      cluster.sync();
-      if (mover) {
-        int n = 0;
-#pragma unroll 8
-        for (int k = 0; k < C; ++k) n += cluster.map_shared_rank(hist, k)[threadIdx.x];
-        merged[threadIdx.x] = n;
-      }
-      cluster.sync();   // (the parts are read before they are cleared)
-      // The highest digit at which the counts from above reach `left`.
-      if (warp == 0) {
-        int mine = 0;   // digits 255 - 8 lane ... 248 - 8 lane
-#pragma unroll
-        for (int k = 0; k < 8; ++k) mine += merged[255 - 8 * lane - k];
-        int x = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int y = __shfl_up_sync(0xffffffffu, x, o);
-          if (lane >= o) x += y;
-        }
-        if (x >= left && x - mine < left) {
-          int above = x - mine;
-#pragma unroll 1
-          for (int k = 0; k < 8; ++k) {
-            const int digit = 255 - 8 * lane - k, n = merged[digit];
-            if (above + n >= left) {
-              pick[0] = prefix | (static_cast<uint32_t>(digit) << shift);
-              pick[1] = left - above;
-              break;
-            }
-            above += n;
-          }
-        }
-      }
-      __syncthreads();
-      prefix = pick[0];
-      left = static_cast<int>(pick[1]);
-    }
-  } else {
-    __syncthreads();   // (the ranks are there)
-  }
-  // What stays: first, recent, ranks above the threshold, and the first `left` at it.
-  auto level = [&](int p) {   // 2: stays, 1: at the threshold, 0: goes
-    if (p < lo || p >= hi) return 2;
-    if (want == 0) return 0;
-    const uint32_t u = rank_at(p);
-    return u > prefix ? 2 : u == prefix ? 1 : 0;
+  auto made = [&](int p) {
+    const uint32_t u = rank_of(scores[p]);
+    return p < lo || p >= hi ? kStays : u;
   };
-  // A warp's share of the part, in whole 32s.
-  const int share = ((e - b + kWarps - 1) / kWarps + 31) / 32 * 32;
-  const int wb = mover ? min(e, b + warp * share) : e, we = min(e, wb + share);
-  int sure = 0, at = 0;
-#pragma unroll 4
-  for (int p = wb + lane; p < we; p += 32) {
-    const int l = level(p);
-    sure += l == 2;
-    at += l == 1;
-  }
-  sure = __reduce_add_sync(0xffffffffu, sure);
-  at = __reduce_add_sync(0xffffffffu, at);
-  if (mover && lane == 0) warp_counts[0][warp] = sure, warp_counts[1][warp] = at;
-  __syncthreads();
-  if (threadIdx.x < 2) {
-    int n = 0;
-    for (int w = 0; w < kWarps; ++w) n += warp_counts[threadIdx.x][w];
-    counts[threadIdx.x] = n;
-  } else if (threadIdx.x == 2) {
-    counts[2] = INT_MAX;
-  }
-  cluster.sync();
-  int before = 0, tied = 0;   // sure and tied tokens before this warp's
+  if (per <= R::kKeys) {
 #pragma unroll 8
-  for (int k = 0; k < c; ++k) {
-    const int* other = cluster.map_shared_rank(counts, k);
-    before += other[0];
-    tied += other[1];
+    for (int p = b + threadIdx.x; p < e; p += R::kAll) keys[p - b] = made(p);
+    select<Row>(a, cluster, [=](int p) { return keys[p - b]; }, b, e, want, kept, shared);
+  } else {
+    select<Row>(a, cluster, made, b, e, want, kept, shared);
   }
-  for (int w = 0; w < min(warp, kWarps); ++w) before += warp_counts[0][w], tied += warp_counts[1][w];
-  int moved = INT_MAX;   // the first place whose row moves
-#pragma unroll 2
-  for (int p0 = wb; p0 < we; p0 += 32) {
-    const int p = p0 + lane;
-    const int l = p < we ? level(p) : 0;
-    const unsigned below = (1u << lane) - 1u;
-    const unsigned twos = __ballot_sync(0xffffffffu, l == 2), ones = __ballot_sync(0xffffffffu, l == 1);
-    const int t = tied + __popc(ones & below);
-    const int j = before + __popc(twos & below) + min(t, left);
-    if (l == 2 || (l == 1 && t < left)) {
-      kept[j] = p;
-      if (j != p) moved = min(moved, j);
-    }
-    before += __popc(twos);
-    tied += __popc(ones);
-  }
-  moved = __reduce_min_sync(0xffffffffu, moved);
-  if (lane == 0 && moved != INT_MAX) atomicMin(&counts[2], moved);
-  cluster.sync();   // kept[] is complete, and seen by the cluster; the ranks are not needed
 
   // ------------------------------------------------------------ rows
-  int from = INT_MAX;
-#pragma unroll 8
-  for (int k = 0; k < C; ++k) from = min(from, cluster.map_shared_rank(counts, k)[2]);
-  from = min(from, a.budget);
+  const int lane = threadIdx.x & 31;
+  const int first = lane < C ? cluster.map_shared_rank(shared.counts, lane)[2] : INT_MAX;
+  const int from = min(a.budget, __reduce_min_sync(0xffffffffu, first));
   // Step s, row q of this CTA: place from + (s C + c) kRows + q.  The warps behind the
   // movers make the lists, a thread for each row: a step's position, then its blocks,
   // then its addresses, each a turn of the loop after the one before, so that none is
@@ -298,33 +320,33 @@ __global__ void __launch_bounds__(Ring<Row>::kAll, 2) evict_kernel(const __grid_
   constexpr int kPass = kThreads / Row::kVecs;   // rows that the threads cover at once
   const int steps = (a.budget - from + C * R::kRows - 1) / (C * R::kRows);
   const int q0 = static_cast<int>(threadIdx.x) - kThreads;
-  auto place = [&](int s) { return from + (s * C + c) * R::kRows + q0; };
+  auto place = [&](int s, int q) { return from + (s * C + c) * R::kRows + q; };
+  // Row q of the list of step s: position p and blocks sb, db for its place j.
+  auto put = [&](int s, int q, int j, int p, int sb, int db) {
+    Move m{-1, -1, p, 0, 0};
+    if (p >= 0) {
+      if (sb >= 0 && sb < a.num_blocks && db >= 0 && db < a.num_blocks) {
+        const int so = mod_bs(p, a.bs, a.bs_log2), dof = mod_bs(j, a.bs, a.bs_log2);
+        m.from = Row::row(a, sb, so, kvh);
+        m.to = Row::row(a, db, dof, kvh);
+        m.from_tail = static_cast<int16_t>(Row::tail(so));
+        m.to_tail = static_cast<int16_t>(Row::tail(dof));
+      } else {
+        record_error(a.err, PA_DEVERR_BLOCK_ID);
+      }
+    }
+    moves[s % (kSteps + 1) * R::kRows + q] = m;
+  };
+  auto position = [&](int s, int j) { return s < steps && j < a.budget ? kept[j] : -1; };
+  auto block_of = [&](int p) { return p >= 0 ? table[div_bs(p, a.bs, a.bs_log2)] : -1; };
   int p1 = -1;                      // of the step after the next to be listed
   int p2 = -1, sb = -1, db = -1;    // of the next
   auto list = [&](int s) {          // the list of step s, blocks of s + 1, positions of s + 2
-    if (s >= 0) {
-      Move m{-1, -1, p2, 0, 0};
-      if (p2 >= 0) {
-        const int j = place(s);
-        if (sb >= 0 && sb < a.num_blocks && db >= 0 && db < a.num_blocks) {
-          const int so = mod_bs(p2, a.bs, a.bs_log2), dof = mod_bs(j, a.bs, a.bs_log2);
-          m.from = Row::row(a, sb, so, kvh);
-          m.to = Row::row(a, db, dof, kvh);
-          m.from_tail = static_cast<int16_t>(Row::tail(so));
-          m.to_tail = static_cast<int16_t>(Row::tail(dof));
-        } else {
-          record_error(a.err, PA_DEVERR_BLOCK_ID);
-        }
-      }
-      moves[s % (kSteps + 1) * R::kRows + q0] = m;
-    }
+    put(s, q0, place(s, q0), p2, sb, db);
     p2 = p1;
-    if (p2 >= 0) {
-      sb = table[div_bs(p2, a.bs, a.bs_log2)];
-      db = table[div_bs(place(s + 1), a.bs, a.bs_log2)];
-    }
-    const int j = place(s + 2);
-    p1 = s + 2 < steps && j < a.budget ? kept[j] : -1;
+    sb = block_of(p2);
+    db = block_of(p2 >= 0 ? place(s + 1, q0) : -1);
+    p1 = position(s + 2, place(s + 2, q0));
   };
   const int64_t mine = Row::vec(a, v);
   auto fetch = [&](int s) {
@@ -343,9 +365,18 @@ __global__ void __launch_bounds__(Ring<Row>::kAll, 2) evict_kernel(const __grid_
                                  a.cache + src + m[q].from_tail + v * Row::kTile);
     }
   };
-  if (!mover) {
+  // The first lists are made by all threads.
 #pragma unroll 1
-    for (int s = -2; s < kSteps; ++s) list(s);
+  for (int x = threadIdx.x; x < kSteps * R::kRows; x += R::kAll) {
+    const int s = x / R::kRows, q = x % R::kRows, j = place(s, q);
+    const int p = position(s, j);
+    put(s, q, j, p, block_of(p), block_of(p >= 0 ? j : -1));
+  }
+  if (!mover) {
+    p2 = position(kSteps, place(kSteps, q0));
+    p1 = position(kSteps + 1, place(kSteps + 1, q0));
+    sb = block_of(p2);
+    db = block_of(p2 >= 0 ? place(kSteps, q0) : -1);
   }
   __syncthreads();
   if (mover) {
@@ -504,49 +535,60 @@ __global__ void __launch_bounds__(kBlockThreads) evict_blocks_kernel(
     *a.new_free_start = room ? static_cast<int>(start - total) : start;
 }
 
-// Whether clusters of 16 are there to be had (they are not portable).
+// CTAs for each (request, kv head): as many as let all clusters run at once with kSpread
+// CTAs on an SM (a cluster's CTAs share one of the GPU's groups of SMs, which are not
+// alike: what fits is asked once for each device), and none with fewer than kLeastRows of
+// the budget; kSpread where the clusters are more than that.  One stream of 131072 tokens
+// in a 4-bit pool, 8 heads: 12 CTAs 58 us, 8: 70, 16 (7 clusters fit): 68.  128 heads of
+// 4096 tokens: 1 CTA 39 us, 2: 40, 4: 54, in bf16 1: 80, 2: 69, 4: 90; 512 heads: 111,
+// 125, 175 and 283, 245, 241.
+constexpr int kLeastRows = 128;
 template <class Row>
-bool wide_clusters() {
+int cluster_size(long long units, int budget) {
   static std::mutex mu;
-  static int known[64] = {};   // 1: yes, 2: no
+  static bool known[64] = {};
+  static int fit[64][kMaxCtas + 1] = {};
   int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 1;
   std::lock_guard<std::mutex> lock(mu);
-  if (known[dev] == 0) {
-    known[dev] = 2;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(kMaxCtas);
-    cfg.blockDim = dim3(Ring<Row>::kAll);
-    cfg.dynamicSmemBytes = Ring<Row>::kBytes;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = kMaxCtas;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    int n = 0;
-    if (cudaFuncSetAttribute(evict_kernel<Row>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) ==
-            cudaSuccess &&
-        cudaOccupancyMaxActiveClusters(&n, evict_kernel<Row>, &cfg) == cudaSuccess) {
-      if (n >= 4) known[dev] = 1;
-    } else {
-      cudaGetLastError();   // (a refused size is no error of the call)
+  if (!known[dev]) {
+    known[dev] = true;
+    // Shared memory that kSpread CTAs of an SM have at most.
+    constexpr int kShare = 224 * 1024 / Row::kSpread - 8 * 1024;
+    static_assert(kShare >= Ring<Row>::kBytes);
+    bool ok = cudaFuncSetAttribute(evict_kernel<Row>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                   kShare) == cudaSuccess;
+    const bool wide = ok && cudaFuncSetAttribute(evict_kernel<Row>,
+                                                 cudaFuncAttributeNonPortableClusterSizeAllowed,
+                                                 1) == cudaSuccess;
+    for (int C = 1; ok && C <= (wide ? kMaxCtas : 8); ++C) {
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3(C);
+      cfg.blockDim = dim3(Ring<Row>::kAll);
+      cfg.dynamicSmemBytes = kShare;
+      cudaLaunchAttribute attr[1];
+      attr[0].id = cudaLaunchAttributeClusterDimension;
+      attr[0].val.clusterDim.x = C;
+      attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+      cfg.attrs = attr;
+      cfg.numAttrs = 1;
+      ok = cudaOccupancyMaxActiveClusters(&fit[dev][C], evict_kernel<Row>, &cfg) == cudaSuccess;
+      if (!ok) fit[dev][C] = 0;
     }
+    if (!ok || !wide) cudaGetLastError();   // (a refused size is no error of the call)
   }
-  return known[dev] == 1;
+  const int most = std::max(1, std::min(kMaxCtas, budget / kLeastRows));
+  for (int C = most; C > 1; --C)
+    if (fit[dev][C] >= units) return C;
+  return fit[dev][1] >= units ? 1 : std::min(most, Row::kSpread);
 }
 
 template <class Row>
-cudaError_t launch_rows(const EvictArgs& a, int N, int sm_count, cudaStream_t stream) {
+cudaError_t launch_rows(const EvictArgs& a, int N, cudaStream_t stream) {
   static DeviceFlags smem_set;
   cudaError_t e = set_smem_once(evict_kernel<Row>, Ring<Row>::kBytes, smem_set);
   if (e != cudaSuccess) return e;
-  // CTAs per (request, kv head): a power of two, as many as leave eight CTAs for each SM
-  // (four rounds of two), but none with less than a step of rows.
-  const long long units = static_cast<long long>(N) * a.Hkv;
-  const int most = wide_clusters<Row>() ? kMaxCtas : 8;
-  int C = 1;
-  while (C < most && 2 * C * units <= 8LL * sm_count && 2LL * C * Ring<Row>::kRows <= a.budget) C *= 2;
+  const int C = cluster_size<Row>(static_cast<long long>(N) * a.Hkv, a.budget);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(C, a.Hkv, N);
   cfg.blockDim = dim3(Ring<Row>::kAll);
@@ -587,14 +629,14 @@ cudaError_t launch_evict(const EvictLaunch& n, cudaStream_t stream) {
   a.d = n.d;
   cudaError_t e;
   if (n.four)
-    e = n.d == 128 ? launch_rows<Four<128>>(a, n.N, n.sm_count, stream)
-                   : launch_rows<Four<64>>(a, n.N, n.sm_count, stream);
+    e = n.d == 128 ? launch_rows<Four<128>>(a, n.N, stream)
+                   : launch_rows<Four<64>>(a, n.N, stream);
   else if (n.row_bytes == 256)
-    e = launch_rows<Plain<256>>(a, n.N, n.sm_count, stream);
+    e = launch_rows<Plain<256>>(a, n.N, stream);
   else if (n.row_bytes == 128)
-    e = launch_rows<Plain<128>>(a, n.N, n.sm_count, stream);
+    e = launch_rows<Plain<128>>(a, n.N, stream);
   else
-    e = launch_rows<Plain<64>>(a, n.N, n.sm_count, stream);
+    e = launch_rows<Plain<64>>(a, n.N, stream);
   if (e != cudaSuccess) return e;
   BlocksArgs f{};
   f.block_table = n.block_table;
