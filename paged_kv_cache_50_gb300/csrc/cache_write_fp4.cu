@@ -7,8 +7,8 @@
 // largest code, so that a block's largest element keeps the most digits.
 //
 // One thread turns 16 elements of a key, and the value's, into 8 bytes of codes and one
-// scale each.  A batch of 18432
-// tokens of 8 heads of 128 (97 MB) takes 18 us (with one block of 16 for each thread: 29); a decode step's is bound by its launch.
+// scale each.  A batch of 18432 tokens of 8 heads of 128 (97 MB) takes 18 us (with one
+// block of 16 for each thread: 29); a decode step's is bound by its launch.
 #include "fp4.cuh"
 #include "pa_launch.h"
 
