@@ -138,8 +138,8 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
       tc::mbar_init(BAR(kVFull + b), 1);
       tc::mbar_init(BAR(kVEmpty + b), 1);
       tc::mbar_init(BAR(kSFull + b), 1);
-      tc::mbar_init(BAR(kPLo + b), 2 * C::kBM);
-      tc::mbar_init(BAR(kPHi + b), 2 * C::kBM);
+      tc::mbar_init(BAR(kPLo + b), 8);   // (warps)
+      tc::mbar_init(BAR(kPHi + b), 8);
       tc::mbar_init(BAR(kODone + b), 1);
       tc::mbar_init(BAR(kUnitFull + b), 1);
       tc::mbar_init(BAR(kUnitEmpty + b), kUnitReaders);
@@ -204,7 +204,7 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
       float m_used = -CUDART_INF_F, l = 0.f, lr = 0.f;
       bool alive = true;
       for (int j = 0; j < ntiles; ++j, ++g) {
-        if (__any_sync(0xffffffffu, *abort_flag != 0) || !wait_warp(BAR(kSFull + x), g & 1)) {
+        if (!wait_warp(BAR(kSFull + x), g & 1)) {
           alive = false;
           break;
         }
@@ -225,37 +225,64 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
             m1 = fmaxf(m1, __uint_as_float(r[1][c]));
           }
         }
+        // weights(c): exp2(s * scale_log2 - m) in the place of s, of 32 columns.
+        auto weights = [&](int c, float m) {
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            float x0, x1;
+            ffma2(x0, x1, __uint_as_float(r[c][e]), __uint_as_float(r[c][e + 1]), a.scale_log2, -m);
+            r[c][e] = __float_as_uint(ex2(x0));
+            r[c][e + 1] = __float_as_uint(ex2(x1));
+          }
+        };
+        auto pack = [&](int c) {
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            uint32_t pk[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              pk[e] = pack_bf16(__uint_as_float(r[c][16 * q + 2 * e]),
+                                __uint_as_float(r[c][16 * q + 2 * e + 1]));
+            tmem_st8(ts + c * 16 + q * 8, pk);
+          }
+        };
         // The row's maximum over both halves.
         float mx = fmaxf(m0, m1) * a.scale_log2;
-        {
-          float* mine = maxima + ((g & 1) * 4 + x * 2) * 128 + t;
-          mine[half * 128] = mx;
-          __syncwarp();
-          if (lane == 0) tc::mbar_arrive(BAR(pair));
-          if (!wait_warp(BAR(pair), met & 1)) {
-            alive = false;
-            break;
-          }
-          ++met;
-          mx = fmaxf(mx, mine[(half ^ 1) * 128]);
+        float* mine = maxima + ((g & 1) * 4 + x * 2) * 128 + t;
+        mine[half * 128] = mx;
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(BAR(pair));
+        float mu = m_used == -CUDART_INF_F ? 0.f : m_used;
+        if (!wait_warp(BAR(pair), met & 1)) {
+          alive = false;
+          break;
         }
-        const float m_new = fmaxf(m_used, mx);
-        const bool need = m_new > m_used + 8.f;
-        const float alpha = need ? ex2(m_used - m_new) : 1.f;
-        if (need) m_used = m_new;
-        const float mu = m_used == -CUDART_INF_F ? 0.f : m_used;
-        // S_x(j) has landed, hence PV_x(j-1) too: O_x may be rescaled now.
-        if (__any_sync(0xffffffffu, need) && j > 0) {
+        ++met;
+        mx = fmaxf(mx, mine[(half ^ 1) * 128]);
+        const bool need = mx > m_used + 8.f;
+        float alpha = 1.f;
+        if (__any_sync(0xffffffffu, need)) {
+          if (need) {
+            alpha = ex2(m_used - mx);
+            mu = m_used = mx;
+          }
+          // S_x(j) has landed, hence PV_x(j-1) too: O_x may be rescaled now.
+          if (j > 0) {
 #pragma unroll 1
-          for (int c = 0; c < D / 64; ++c) {
-            uint32_t o[32];
-            tc::tmem_ld32(to + c * 32, o);
-            tc::tmem_wait_ld();
+            for (int c = 0; c < D / 64; ++c) {
+#pragma unroll 1
+              for (int q = 0; q < 2; ++q) {
+                uint32_t o[16];
+                tmem_ld16(to + c * 32 + q * 16, o);
+                tc::tmem_wait_ld();
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-            tc::tmem_st32(to + c * 32, o);
+                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                tc::tmem_st16(to + c * 32 + q * 16, o);
+              }
+            }
           }
         }
+        weights(0, mu);
         // V rows behind the unit's last one may hold anything (0 * NaN is NaN):
         // cleared once V has landed, half a row per thread, before P is published.
         if (j * C::kBN + t >= end) {
@@ -269,28 +296,26 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
                          : "memory");
           tc::fence_proxy_async_smem();   // before this thread's P arrival
         }
-        // P = exp2(s * scale_log2 - m_used) as bf16 pairs over this half's first 32
-        // columns.
-        float l8[2] = {0.f, 0.f}, r8[2] = {0.f, 0.f};
+        // P as bf16 pairs over this half's first 32 columns.
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          uint32_t pk[16];
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            float x0, x1;
-            ffma2(x0, x1, __uint_as_float(r[c][2 * e]), __uint_as_float(r[c][2 * e + 1]),
-                  a.scale_log2, -mu);
-            const float p0 = ex2(x0);
-            const float p1 = ex2(x1);
-            fadd2(l8[0], l8[1], p0, p1);
-            pk[e] = pack_bf16(p0, p1);
-            add_bf16x2_f32(r8[0], r8[1], pk[e]);
-          }
-          tc::tmem_st16(ts + c * 16, pk);
+          pack(c);
+          if (c == 0) weights(1, mu);
           tc::tmem_wait_st();
           tc::tc_fence_before();
-          tc::mbar_arrive(BAR((c == 0 ? kPLo : kPHi) + x));
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(BAR((c == 0 ? kPLo : kPHi) + x));
         }
+        // The sums, while the MMAs run.
+        float l8[2] = {0.f, 0.f}, r8[2] = {0.f, 0.f};
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            const float p0 = __uint_as_float(r[c][e]), p1 = __uint_as_float(r[c][e + 1]);
+            fadd2(l8[0], l8[1], p0, p1);
+            add_bf16x2_f32(r8[0], r8[1], pack_bf16(p0, p1));
+          }
         l = l * alpha + (l8[0] + l8[1]);
         lr = lr * alpha + (r8[0] + r8[1]);
       }
@@ -400,7 +425,6 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
           if (!ok) break;
           tc::mma_commit(BAR(kKEmpty + (g & 1)));
           for (int j = 0; ok && j < ntiles; ++j, ++g) {
-            if (*abort_flag) { ok = false; break; }
             const bool more = j + 1 < ntiles;
             if (!wait(kVFull + (g & 1), (g >> 1) & 1)) { ok = false; break; }
             if (more && !wait(kKFull + ((g + 1) & 1), ((g + 1) >> 1) & 1)) { ok = false; break; }
