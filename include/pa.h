@@ -556,7 +556,9 @@ pa_status pa_decode_window_fp8(const void* q, const void* kv_cache, const int32_
  * key, value: [num_tokens, Hkv, d] bf16 with key_stride and value_stride elements
  * from token to token (dense heads; multiples of 8, at least Hkv * d): views of a
  * packed projection need no copy.  16-byte aligned.  Slots as for
- * pa_reshape_and_cache.  Supported: head_size in {64, 128}.  Scales finite and > 0.
+ * pa_reshape_and_cache; a slot that two tokens of a call share may get the codes of one
+ * and the scales of the other.  Supported: head_size in {64, 128}.  Scales finite and
+ * > 0.
  */
 pa_status pa_reshape_and_cache_fp4(const void* key, const void* value, int64_t key_stride,
                                    int64_t value_stride, void* kv_cache,

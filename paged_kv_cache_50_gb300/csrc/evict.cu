@@ -21,11 +21,12 @@
 //     rings, one barrier of the cluster for each, and no other order is needed.  A thread
 //     reads what it has copied itself.  Rows that stay where they are (all before the
 //     first one that goes) are not touched.
-// A second, small kernel writes the new lengths and pushes the blocks.
+// A second, small kernel writes the new lengths and pushes the blocks, beside the first
+// where SMs are free.
 //
 // Bound by HBM in the long run (each moved row is read and written once): 64 requests in
-// bf16 move 667 MB in 150 us.  One long stream has no more than 96 CTAs (8 clusters of 12)
-// and is bound by their chains of barriers: 58 us, of them 9 for the ranks' loads, 11 for
+// bf16 move 667 MB in 154 us.  One long stream has no more than 96 CTAs (8 clusters of 12)
+// and is bound by their chains of barriers: 52 us, of them 4 for the ranks' loads, 11 for
 // the four histograms, 8 for the list and the first rows, 21 for the rows.
 #include <cooperative_groups.h>
 #include <math_constants.h>
@@ -265,8 +266,11 @@ __global__ void __launch_bounds__(Ring<Row>::kAll, Row::kCtas) evict_kernel(cons
   const bool mover = threadIdx.x < kThreads;
   cg::cluster_group cluster = cg::this_cluster();
   pdl_wait();
-  pdl_trigger();
-  const int seq = max(0, a.seq_lens[i]);
+  // The kernel behind may write the lengths in place: it is let in when this CTA has its
+  // own (the branch needs the loaded value).
+  const int length = a.seq_lens[i];
+  if (length != INT_MIN) pdl_trigger();
+  const int seq = max(0, length);
   const int64_t unit = static_cast<int64_t>(i) * a.Hkv + kvh;
   const float* scores = a.scores + unit * a.score_tokens;
   float* fresh = a.new_scores + unit * a.score_tokens;
@@ -299,7 +303,7 @@ __global__ void __launch_bounds__(Ring<Row>::kAll, Row::kCtas) evict_kernel(cons
     return p < lo || p >= hi ? kStays : u;
   };
   if (per <= R::kKeys) {
-#pragma unroll 8
+#pragma unroll 16
     for (int p = b + threadIdx.x; p < e; p += R::kAll) keys[p - b] = made(p);
     select<Row>(a, cluster, [=](int p) { return keys[p - b]; }, b, e, want, kept, shared);
   } else {
@@ -460,8 +464,8 @@ __global__ void __launch_bounds__(kBlockThreads) evict_blocks_kernel(
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if (threadIdx.x < 2) totals[threadIdx.x] = 0;
   __syncthreads();
-  pdl_wait();
-  pdl_trigger();
+  // No wait here: this kernel starts when every CTA of the first has read its length and
+  // needs nothing else of it (what was before has ended when those run).
   auto ceil_bs = [&](int x) { return x > 0 ? div_bs(x - 1, a.bs, a.bs_log2) + 1 : 0; };
   auto lens = [&](int i, int& seq, int& keep) {
     seq = max(0, a.seq_lens[i]);
@@ -533,6 +537,9 @@ __global__ void __launch_bounds__(kBlockThreads) evict_blocks_kernel(
   }
   if (blockIdx.x == 0 && threadIdx.x == 0 && a.new_free_start != nullptr)
     *a.new_free_start = room ? static_cast<int>(start - total) : start;
+  // It ends when the first kernel has: what follows in the stream waits for both.
+  pdl_trigger();
+  pdl_wait();
 }
 
 // CTAs for each (request, kv head): as many as let all clusters run at once with kSpread
