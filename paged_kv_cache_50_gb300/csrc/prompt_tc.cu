@@ -172,32 +172,28 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
     tc::reg_alloc<C::kRegSoftmax>();
     const int x = (warp - 4) >> 3, half = ((warp - 4) >> 2) & 1;
     const int t = threadIdx.x & 127;         // row within the tile = TMEM lane
-    const int t_tok = t / a.grp, hh = t - t_tok * a.grp;
-    const bool row_used = t_tok < a.row_tokens;
+    const int t_tok = t / a.grp < a.row_tokens ? t / a.grp : 1 << 28;   // its query row, if any
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
     // This half's columns of S (and P over them) and of O.
     const uint32_t ts = tmem + lane_base + C::col_s(x) + 64 * half;
     const uint32_t to = tmem + lane_base + C::col_o(x) + (D / 2) * half;
     const int pair = kPair + x * 4 + (warp & 3);
-    float* maxima = reinterpret_cast<float*>(smem + C::kOffMax);
-    float2* sums = reinterpret_cast<float2*>(smem + C::kOffSum);
+    const uint32_t maxima = sbase + C::kOffMax + (x * 256 + t) * 4;   // [tile & 1][x][half][t]
+    const uint32_t sums = sbase + C::kOffSum + (x * 256 + t) * 8;     // [x][half][t]
     auto wait_warp = [&](uint32_t b, uint32_t parity) -> bool {
       const bool w = __all_sync(0xffffffffu, tc::mbar_wait(b, parity));
       if (!w) fail();
       return w;
     };
-    uint32_t g = 0, full = 0, met = 0;   // tiles, units with tiles, exchanges so far
+    uint32_t g = 0, full = 0;   // tiles, units with tiles so far (exchanges: their sum)
     for (int u = 0;; ++u) {
       if (__any_sync(0xffffffffu, *abort_flag != 0)) break;
       if (!wait_warp(BAR(kUnitFull + (u & 1)), (u >> 1) & 1)) break;
       volatile Unit* un = unit_slot(u);
-      const int live = un->live, ntiles = un->tiles, end = un->end;
-      const int qi = (un->tile * 2 + x) * a.row_tokens + t_tok;   // row of the prompt
-      const bool valid = row_used && qi < un->rows;
-      const int lim = valid ? qi + 1 : 0;
-      const int64_t qrow = static_cast<int64_t>(un->q0 + qi) * a.Hq + un->kvh * a.grp + hh;
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(BAR(kUnitEmpty + (u & 1)));
+      const int live = un->live, ntiles = un->tiles;
+      const int clear = un->end - t;   // V's row t is cleared in tiles at or behind it
+      const int lim = t_tok < un->rows - (un->tile * 2 + x) * a.row_tokens
+                          ? (un->tile * 2 + x) * a.row_tokens + t_tok + 1 : 0;
       if (!live) break;
       // l: this half's sum of weights (for the LSE); lr: the same weights rounded to
       // bf16, as PV multiplies them (the output's divisor).
@@ -248,17 +244,18 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
         };
         // The row's maximum over both halves.
         float mx = fmaxf(m0, m1) * a.scale_log2;
-        float* mine = maxima + ((g & 1) * 4 + x * 2) * 128 + t;
-        mine[half * 128] = mx;
+        const uint32_t mine = maxima + (g & 1) * 2048;
+        asm volatile("st.shared.f32 [%0], %1;" ::"r"(mine + half * 512), "f"(mx) : "memory");
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(BAR(pair));
         float mu = m_used == -CUDART_INF_F ? 0.f : m_used;
-        if (!wait_warp(BAR(pair), met & 1)) {
+        if (!wait_warp(BAR(pair), (g + full) & 1)) {
           alive = false;
           break;
         }
-        ++met;
-        mx = fmaxf(mx, mine[(half ^ 1) * 128]);
+        float others;
+        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(others) : "r"(mine + (half ^ 1) * 512) : "memory");
+        mx = fmaxf(mx, others);
         const bool need = mx > m_used + 8.f;
         float alpha = 1.f;
         if (__any_sync(0xffffffffu, need)) {
@@ -285,7 +282,7 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
         weights(0, mu);
         // V rows behind the unit's last one may hold anything (0 * NaN is NaN):
         // cleared once V has landed, half a row per thread, before P is published.
-        if (j * C::kBN + t >= end) {
+        if (j * C::kBN >= clear) {
           if (!tc::mbar_wait(BAR(kVFull + (g & 1)), (g >> 1) & 1)) fail();
           const uint32_t vbase = sbase + C::kOffV + (g & 1) * C::kTileBytes;
 #pragma unroll 1
@@ -321,19 +318,25 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
       }
       if (alive && ntiles > 0) {
         // Both halves' sums.
-        sums[(x * 2 + half) * 128 + t] = make_float2(l, lr);
+        asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(sums + half * 1024), "f"(l), "f"(lr)
+                     : "memory");
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(BAR(pair));
-        alive = wait_warp(BAR(pair), met & 1);
-        ++met;
-        const float2 other = sums[(x * 2 + (half ^ 1)) * 128 + t];
-        l += other.x;
-        lr += other.y;
+        alive = wait_warp(BAR(pair), (g + full) & 1);
+        float ol, olr;
+        asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];"
+                     : "=f"(ol), "=f"(olr)
+                     : "r"(sums + (half ^ 1) * 1024)
+                     : "memory");
+        l += ol;
+        lr += olr;
         if (alive) alive = wait_warp(BAR(kODone + x), full & 1);
         ++full;
       }
       if (alive && ntiles > 0) {   // warp-uniform
         tc::tc_fence_after();
+        const bool valid = lim > 0;
+        const int64_t qrow = static_cast<int64_t>(un->q0 + lim - 1) * a.Hq + un->kvh * a.grp + t % a.grp;
         const float inv = lr == 0.f ? 0.f : 1.f / lr;
         // 32-byte stores write whole sectors where `out` is 32-byte aligned.
         const bool a32 = (reinterpret_cast<uintptr_t>(a.out) & 31u) == 0;
@@ -367,6 +370,8 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
       // The output's TMEM reads come before this warp's next P arrival, which the
       // next unit's first PV waits for.
       tc::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(BAR(kUnitEmpty + (u & 1)));   // (it has been read)
       if (!alive) break;
     }
   } else {
