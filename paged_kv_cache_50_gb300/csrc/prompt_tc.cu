@@ -49,13 +49,13 @@ struct PromptCfg {
   static constexpr int kOffK = 2 * kQBytes;
   static constexpr int kOffV = kOffK + 2 * kTileBytes;
   static constexpr int kOffBar = kOffV + 2 * kTileBytes;
-  static constexpr int kOffMax = kOffBar + 512;      // [tile & 1][x][half][128] floats
+  static constexpr int kOffMax = kOffBar + 1024;     // [tile & 1][x][half][128] floats
   static constexpr int kOffSum = kOffMax + 4096;     // [x][half][128] float2
   static constexpr int kSmemBytes = kOffSum + 4096 + 1024;   // + alignment slack
   static constexpr uint32_t kTmemCols = 512;
   static constexpr int kThreads = 640;
   static constexpr uint32_t kRegSoftmax = 104;
-  static constexpr uint32_t kRegOther = 56;
+  static constexpr uint32_t kRegOther = 64;
   __host__ __device__ static constexpr uint32_t col_s(int x) { return 128u * x; }
   __host__ __device__ static constexpr uint32_t col_o(int x) { return 256u + 128u * x; }
 };
@@ -171,15 +171,19 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
     // ------------------------------------------------------ softmax, output
     tc::reg_alloc<C::kRegSoftmax>();
     const int x = (warp - 4) >> 3, half = ((warp - 4) >> 2) & 1;
-    const int t = threadIdx.x & 127;         // row within the tile = TMEM lane
-    const int t_tok = t / a.grp < a.row_tokens ? t / a.grp : 1 << 28;   // its query row, if any
-    const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    // Registers are short while a tile's S is held, and what is spilled comes back from L2:
+    // row() of the tile (= TMEM lane) is read anew where a unit begins and ends.
+    auto row = []() -> int {
+      uint32_t t;
+      asm volatile("mov.u32 %0, %%tid.x;" : "=r"(t));
+      return static_cast<int>(t & 127u);
+    };
     // This half's columns of S (and P over them) and of O.
-    const uint32_t ts = tmem + lane_base + C::col_s(x) + 64 * half;
-    const uint32_t to = tmem + lane_base + C::col_o(x) + (D / 2) * half;
+    const uint32_t ts = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + C::col_s(x) + 64 * half;
+    const uint32_t to = ts + C::col_o(0) - C::col_s(0) - (64 - D / 2) * half;
     const int pair = kPair + x * 4 + (warp & 3);
-    const uint32_t maxima = sbase + C::kOffMax + (x * 256 + t) * 4;   // [tile & 1][x][half][t]
-    const uint32_t sums = sbase + C::kOffSum + (x * 256 + t) * 8;     // [x][half][t]
+    // This row and half in [tile & 1][x][half][128]; the other half's is 512 bytes apart.
+    const uint32_t maxima = sbase + C::kOffMax + (x * 256 + half * 128 + (threadIdx.x & 127)) * 4;
     auto wait_warp = [&](uint32_t b, uint32_t parity) -> bool {
       const bool w = __all_sync(0xffffffffu, tc::mbar_wait(b, parity));
       if (!w) fail();
@@ -190,16 +194,17 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
       if (__any_sync(0xffffffffu, *abort_flag != 0)) break;
       if (!wait_warp(BAR(kUnitFull + (u & 1)), (u >> 1) & 1)) break;
       volatile Unit* un = unit_slot(u);
-      const int live = un->live, ntiles = un->tiles;
-      const int clear = un->end - t;   // V's row t is cleared in tiles at or behind it
-      const int lim = t_tok < un->rows - (un->tile * 2 + x) * a.row_tokens
-                          ? (un->tile * 2 + x) * a.row_tokens + t_tok + 1 : 0;
-      if (!live) break;
+      if (!un->live) break;
+      int seen = -64 * half;   // of a tile's columns of this half
+      {
+        const int t_tok = row() / a.grp, q = (un->tile * 2 + x) * a.row_tokens + t_tok;
+        seen += t_tok < a.row_tokens && q < un->rows ? q + 1 : 0;
+      }
       // l: this half's sum of weights (for the LSE); lr: the same weights rounded to
       // bf16, as PV multiplies them (the output's divisor).
       float m_used = -CUDART_INF_F, l = 0.f, lr = 0.f;
       bool alive = true;
-      for (int j = 0; j < ntiles; ++j, ++g) {
+      for (int left = un->tiles; left > 0; --left, ++g) {
         if (!wait_warp(BAR(kSFull + x), g & 1)) {
           alive = false;
           break;
@@ -210,7 +215,6 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
         tmem_ld32_max(ts, r[0], m0);
         tmem_ld32_max(ts + 32, r[1], m1);
         tc::tmem_wait_ld();
-        const int seen = lim - j * C::kBN - 64 * half;   // of these columns
         if (__any_sync(0xffffffffu, seen < 64)) {
           m0 = m1 = -CUDART_INF_F;
 #pragma unroll
@@ -221,6 +225,7 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
             m1 = fmaxf(m1, __uint_as_float(r[1][c]));
           }
         }
+        seen -= C::kBN;
         // weights(c): exp2(s * scale_log2 - m) in the place of s, of 32 columns.
         auto weights = [&](int c, float m) {
 #pragma unroll
@@ -245,7 +250,7 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
         // The row's maximum over both halves.
         float mx = fmaxf(m0, m1) * a.scale_log2;
         const uint32_t mine = maxima + (g & 1) * 2048;
-        asm volatile("st.shared.f32 [%0], %1;" ::"r"(mine + half * 512), "f"(mx) : "memory");
+        asm volatile("st.shared.f32 [%0], %1;" ::"r"(mine), "f"(mx) : "memory");
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(BAR(pair));
         float mu = m_used == -CUDART_INF_F ? 0.f : m_used;
@@ -254,7 +259,7 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
           break;
         }
         float others;
-        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(others) : "r"(mine + (half ^ 1) * 512) : "memory");
+        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(others) : "r"(mine ^ 512u) : "memory");
         mx = fmaxf(mx, others);
         const bool need = mx > m_used + 8.f;
         float alpha = 1.f;
@@ -264,7 +269,7 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
             mu = m_used = mx;
           }
           // S_x(j) has landed, hence PV_x(j-1) too: O_x may be rescaled now.
-          if (j > 0) {
+          if (left < un->tiles) {
 #pragma unroll 1
             for (int c = 0; c < D / 64; ++c) {
 #pragma unroll 1
@@ -282,7 +287,7 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
         weights(0, mu);
         // V rows behind the unit's last one may hold anything (0 * NaN is NaN):
         // cleared once V has landed, half a row per thread, before P is published.
-        if (j * C::kBN >= clear) {
+        if (const int t = left > 1 ? 0 : row(); left == 1 && (un->tiles - 1) * C::kBN + t >= un->end) {
           if (!tc::mbar_wait(BAR(kVFull + (g & 1)), (g >> 1) & 1)) fail();
           const uint32_t vbase = sbase + C::kOffV + (g & 1) * C::kTileBytes;
 #pragma unroll 1
@@ -316,9 +321,11 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
         l = l * alpha + (l8[0] + l8[1]);
         lr = lr * alpha + (r8[0] + r8[1]);
       }
-      if (alive && ntiles > 0) {
+      const bool some = un->tiles > 0;
+      if (alive && some) {
         // Both halves' sums.
-        asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(sums + half * 1024), "f"(l), "f"(lr)
+        const uint32_t sums = sbase + C::kOffSum + (x * 256 + half * 128 + row()) * 8;
+        asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(sums), "f"(l), "f"(lr)
                      : "memory");
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(BAR(pair));
@@ -326,17 +333,19 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
         float ol, olr;
         asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];"
                      : "=f"(ol), "=f"(olr)
-                     : "r"(sums + (half ^ 1) * 1024)
+                     : "r"(sums + 1024 - 2048 * half)
                      : "memory");
         l += ol;
         lr += olr;
         if (alive) alive = wait_warp(BAR(kODone + x), full & 1);
         ++full;
       }
-      if (alive && ntiles > 0) {   // warp-uniform
+      if (alive && some) {   // warp-uniform
         tc::tc_fence_after();
-        const bool valid = lim > 0;
-        const int64_t qrow = static_cast<int64_t>(un->q0 + lim - 1) * a.Hq + un->kvh * a.grp + t % a.grp;
+        const int t = row(), t_tok = t / a.grp, q = (un->tile * 2 + x) * a.row_tokens + t_tok;
+        const bool valid = t_tok < a.row_tokens && q < un->rows;
+        const int64_t qrow =
+            static_cast<int64_t>(un->q0 + q) * a.Hq + un->kvh * a.grp + (t - t_tok * a.grp);
         const float inv = lr == 0.f ? 0.f : 1.f / lr;
         // 32-byte stores write whole sectors where `out` is 32-byte aligned.
         const bool a32 = (reinterpret_cast<uintptr_t>(a.out) & 31u) == 0;
