@@ -51,7 +51,8 @@ struct PromptCfg {
   static constexpr int kOffBar = kOffV + 2 * kTileBytes;
   static constexpr int kOffMax = kOffBar + 1024;     // [tile & 1][x][half][128] floats
   static constexpr int kOffSum = kOffMax + 4096;     // [x][half][128] float2
-  static constexpr int kSmemBytes = kOffSum + 4096 + 1024;   // + alignment slack
+  static constexpr int kOffRows = kOffSum + 4096;    // [128] query row within the tile, head
+  static constexpr int kSmemBytes = kOffRows + 1024 + 1024;   // + alignment slack
   static constexpr uint32_t kTmemCols = 512;
   static constexpr int kThreads = 640;
   static constexpr uint32_t kRegSoftmax = 104;
@@ -150,6 +151,13 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
     *abort_flag = 0;
     tc::fence_barrier_init();
   }
+  // Which query row of the tile (past every prompt's where none) and head of the group a
+  // TMEM lane is.
+  if (threadIdx.x < C::kBM) {
+    const int tok = static_cast<int>(threadIdx.x) / a.grp;
+    reinterpret_cast<int2*>(smem + C::kOffRows)[threadIdx.x] =
+        make_int2(tok < a.row_tokens ? tok : 1 << 30, static_cast<int>(threadIdx.x) - tok * a.grp);
+  }
   if (warp == 0) tc::tmem_alloc(bars + kOffTmem, C::kTmemCols);
   if (warp == 1 && lane == 0) {
     tc::tma_prefetch_desc(&q_map);
@@ -178,6 +186,13 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
       asm volatile("mov.u32 %0, %%tid.x;" : "=r"(t));
       return static_cast<int>(t & 127u);
     };
+    auto row_is = [&](int t) {
+      int2 v;
+      asm volatile("ld.shared.v2.s32 {%0, %1}, [%2];"
+                   : "=r"(v.x), "=r"(v.y)
+                   : "r"(sbase + C::kOffRows + t * 8));
+      return v;
+    };
     // This half's columns of S (and P over them) and of O.
     const uint32_t ts = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + C::col_s(x) + 64 * half;
     const uint32_t to = ts + C::col_o(0) - C::col_s(0) - (64 - D / 2) * half;
@@ -197,8 +212,8 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
       if (!un->live) break;
       int seen = -64 * half;   // of a tile's columns of this half
       {
-        const int t_tok = row() / a.grp, q = (un->tile * 2 + x) * a.row_tokens + t_tok;
-        seen += t_tok < a.row_tokens && q < un->rows ? q + 1 : 0;
+        const int tok = row_is(row()).x, q = (un->tile * 2 + x) * a.row_tokens;
+        seen += tok < un->rows - q ? q + tok + 1 : 0;
       }
       // l: this half's sum of weights (for the LSE); lr: the same weights rounded to
       // bf16, as PV multiplies them (the output's divisor).
@@ -342,11 +357,12 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
       }
       if (alive && some) {   // warp-uniform
         tc::tc_fence_after();
-        const int t = row(), t_tok = t / a.grp, q = (un->tile * 2 + x) * a.row_tokens + t_tok;
-        const bool valid = t_tok < a.row_tokens && q < un->rows;
-        const int64_t qrow =
-            static_cast<int64_t>(un->q0 + q) * a.Hq + un->kvh * a.grp + (t - t_tok * a.grp);
-        const float inv = lr == 0.f ? 0.f : 1.f / lr;
+        const int2 is = row_is(row());
+        const int q = (un->tile * 2 + x) * a.row_tokens;
+        const bool valid = is.x < un->rows - q;
+        const int64_t qrow = static_cast<int64_t>(un->q0 + q + is.x) * a.Hq + un->kvh * a.grp + is.y;
+        // (A row with a visible token has a weight of 1.)
+        const float inv = lr == 0.f ? 0.f : __fdividef(1.f, lr);
         // 32-byte stores write whole sectors where `out` is 32-byte aligned.
         const bool a32 = (reinterpret_cast<uintptr_t>(a.out) & 31u) == 0;
         uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + qrow * D + half * (D / 2));
@@ -374,7 +390,7 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
           }
         }
         if (valid && half == 0 && a.lse != nullptr)
-          a.lse[qrow] = l == 0.f ? -CUDART_INF_F : (m_used + log2f(l)) * kLn2;
+          a.lse[qrow] = l == 0.f ? -CUDART_INF_F : (m_used + __log2f(l)) * kLn2;
       }
       // The output's TMEM reads come before this warp's next P arrival, which the
       // next unit's first PV waits for.
