@@ -16,9 +16,15 @@
 //    while the other Q tile's MMAs run; one thread per row needs about twice that.
 //    The halves exchange their maxima through shared memory (a barrier of two warps)
 //    and else work apart: each writes its P over its own S columns and rescales and
-//    stores its half of O.
+//    stores its half of O.  The weights' sums are formed once P is published, while the
+//    MMAs run (between S and P: 820 us for a prompt of 8192 tokens, so 775).
 //  * Units go longest first: a unit's work grows with its place in the prompt.
 //    With up to 64 prompts the order runs over all of them, else within each.
+//
+// Bound by the chain S -> softmax -> PV of a Q tile, ~3000 cycles for a tile pair, in which
+// 16 warps issue ~30000 instructions; and by units' ends (6 tiles each for 16 prompts of up
+// to 2048 tokens).  One prompt of 8192 tokens, 64 heads of 128: 742 us, 1.48 PFLOP/s; the 16
+// prompts, 32 heads: 202 us, 1.06.
 //
 // Warp roles (640 threads): warp 0 MMA issue; warp 1 K; warp 2 units and queries; warp
 // 3 V; warps 4-7, 8-11 halves 0, 1 of Q tile 0; warps 12-15, 16-19 of Q tile 1.  Every
@@ -363,29 +369,43 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
         const int64_t qrow = static_cast<int64_t>(un->q0 + q + is.x) * a.Hq + un->kvh * a.grp + is.y;
         // (A row with a visible token has a weight of 1.)
         const float inv = lr == 0.f ? 0.f : __fdividef(1.f, lr);
+        // Two lanes store 64 bytes of a row, first of the even lane's, then of the odd one's:
+        // they exchange half of what they have.  (Each its own row, 32 bytes in each of 32
+        // lines for a store, kept the load and store unit busy: 16 prompts 211 us, so 202.)
         // 32-byte stores write whole sectors where `out` is 32-byte aligned.
         const bool a32 = (reinterpret_cast<uintptr_t>(a.out) & 31u) == 0;
-        uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + qrow * D + half * (D / 2));
+        const bool odd = lane & 1;
+        auto mine = valid ? reinterpret_cast<unsigned long long>(a.out + qrow * D + half * (D / 2)) : 0ull;
+        auto other = __shfl_xor_sync(0xffffffffu, mine, 1);
+        if (odd) {
+          const auto m = mine;
+          mine = other;
+          other = m;
+        }
 #pragma unroll 1
         for (int c = 0; c < D / 64; ++c) {
-          uint32_t o[32];
+          uint32_t o[32], w[2][8];
           tc::tmem_ld32(to + c * 32, o);
           tc::tmem_wait_ld();
-          if (valid) {
 #pragma unroll
-            for (int v = 0; v < 2; ++v) {
-              uint32_t w[8];
+          for (int e = 0; e < 8; ++e) {
+            const uint32_t lo = pack_bf16(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
+            const uint32_t hi = pack_bf16(__uint_as_float(o[16 + 2 * e]) * inv,
+                                          __uint_as_float(o[16 + 2 * e + 1]) * inv);
+            const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? lo : hi, 1);
+            w[0][e] = odd ? got : lo;
+            w[1][e] = odd ? hi : got;
+          }
 #pragma unroll
-              for (int e = 0; e < 8; ++e)
-                w[e] = pack_bf16(__uint_as_float(o[v * 16 + 2 * e]) * inv,
-                                 __uint_as_float(o[v * 16 + 2 * e + 1]) * inv);
-              uint32_t* p = dst + c * 16 + v * 8;
-              if (a32) {
-                st_global_v8(p, w);
-              } else {
-                reinterpret_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-                reinterpret_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
-              }
+          for (int v = 0; v < 2; ++v) {
+            uint32_t* p = reinterpret_cast<uint32_t*>(v ? other : mine);
+            if (p == nullptr) continue;
+            p += c * 16 + odd * 8;
+            if (a32) {
+              st_global_v8(p, w[v]);
+            } else {
+              reinterpret_cast<uint4*>(p)[0] = make_uint4(w[v][0], w[v][1], w[v][2], w[v][3]);
+              reinterpret_cast<uint4*>(p)[1] = make_uint4(w[v][4], w[v][5], w[v][6], w[v][7]);
             }
           }
         }
