@@ -15,12 +15,12 @@
 //     warps and CTAs before it, it writes the positions to kept[], by ballots.
 //  3. Rows move in steps: a CTA copies its rows of a step into a ring in shared memory
 //     (cp.async), several steps ahead, and from there to their places, by lists of
-//     addresses that warps of their own make.  A kept row's
-//     source never lies before its place, and the places of a step hold sources of this
-//     step and of earlier ones only: so a step is written when all CTAs have it in their
-//     rings, one barrier of the cluster for each, and no other order is needed.  A thread
-//     reads what it has copied itself.  Rows that stay where they are (all before the
-//     first one that goes) are not touched.
+//     addresses that warps of their own make.  A kept row's source never lies before its
+//     place, and the places of a step hold sources of this step and of earlier ones only:
+//     so a step is written when all CTAs have it in their rings, one barrier of the
+//     cluster for each, and no other order is needed.  A thread reads what it has copied
+//     itself.  Rows that stay where they are (all before the first one that goes) are not
+//     touched.
 // A second, small kernel writes the new lengths and pushes the blocks, beside the first
 // where SMs are free.
 //
@@ -256,7 +256,8 @@ __device__ __forceinline__ void select(const EvictArgs& a, cg::cluster_group& cl
 }
 
 template <class Row>
-__global__ void __launch_bounds__(Ring<Row>::kAll, Row::kCtas) evict_kernel(const __grid_constant__ EvictArgs a) {
+__global__ void __launch_bounds__(Ring<Row>::kAll, Row::kCtas)
+evict_kernel(const __grid_constant__ EvictArgs a) {
   using R = Ring<Row>;
   constexpr int kThreads = R::kThreads, kPer = R::kPer, kSteps = R::kSteps;
   extern __shared__ __align__(16) uint8_t smem[];   // the part's ranks, then the ring

@@ -22,7 +22,7 @@
 //    With up to 64 prompts the order runs over all of them, else within each.
 //
 // Bound by the chain S -> softmax -> PV of a Q tile, ~3000 cycles for a tile pair, in which
-// 16 warps issue ~30000 instructions; and by units' ends (6 tiles each for 16 prompts of up
+// 16 warps issue ~8000 instructions; and by units' ends (6 tiles each for 16 prompts of up
 // to 2048 tokens).  One prompt of 8192 tokens, 64 heads of 128: 742 us, 1.48 PFLOP/s; the 16
 // prompts, 32 heads: 202 us, 1.06.
 //
@@ -200,7 +200,8 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
       return v;
     };
     // This half's columns of S (and P over them) and of O.
-    const uint32_t ts = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + C::col_s(x) + 64 * half;
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t ts = tmem + lanes + C::col_s(x) + 64 * half;
     const uint32_t to = ts + C::col_o(0) - C::col_s(0) - (64 - D / 2) * half;
     const int pair = kPair + x * 4 + (warp & 3);
     // This row and half in [tile & 1][x][half][128]; the other half's is 512 bytes apart.
@@ -375,7 +376,8 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
         // 32-byte stores write whole sectors where `out` is 32-byte aligned.
         const bool a32 = (reinterpret_cast<uintptr_t>(a.out) & 31u) == 0;
         const bool odd = lane & 1;
-        auto mine = valid ? reinterpret_cast<unsigned long long>(a.out + qrow * D + half * (D / 2)) : 0ull;
+        auto mine = reinterpret_cast<unsigned long long>(a.out + qrow * D + half * (D / 2));
+        if (!valid) mine = 0;
         auto other = __shfl_xor_sync(0xffffffffu, mine, 1);
         if (odd) {
           const auto m = mine;
@@ -389,7 +391,8 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constan
           tc::tmem_wait_ld();
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            const uint32_t lo = pack_bf16(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
+            const uint32_t lo = pack_bf16(__uint_as_float(o[2 * e]) * inv,
+                                          __uint_as_float(o[2 * e + 1]) * inv);
             const uint32_t hi = pack_bf16(__uint_as_float(o[16 + 2 * e]) * inv,
                                           __uint_as_float(o[16 + 2 * e + 1]) * inv);
             const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? lo : hi, 1);

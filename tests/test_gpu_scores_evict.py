@@ -1,6 +1,9 @@
 """Sums of attention weights against fp64, and eviction by them exactly."""
 
 import math
+import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -208,6 +211,53 @@ def test_evict_long(pa, kind):
     Store(20, kind, [9001], 1, 64, 16).check(pa, 4000, 500, 4)
     Store(21, kind, [6000, 5001, 100], 2, 128, 32).check(pa, 2500, 30, 0, True)
     Store(22, kind, list(range(150, 400)), 3, 64, 16).check(pa, 200, 16, 1, True)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("seqs,hkv,budget", [([9000], 8, 2100), ([6000, 5500], 8, 1700),
+                                             ([3000] * 4, 8, 1100), ([2600], 2, 2100),
+                                             ([700] * 19, 8, 300), ([300] * 70, 8, 140)])
+def test_evict_cluster_sizes(pa, kind, seqs, hkv, budget):
+    """As many CTAs for a head as fit beside the others', odd numbers of them among these."""
+    Store(50, kind, seqs, hkv, 64, 16).check(pa, budget, budget // 9, 3, len(seqs) % 2 == 1)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_evict_far_beyond_the_budget(pa, kind):
+    """More tokens than a CTA holds the ranks of, one CTA and several for a head."""
+    Store(51, kind, [40000, 21000, 30], 1, 64, 16).check(pa, 100, 10, 4)
+    Store(52, kind, [33000], 2, 128, 32).check(pa, 300, 0, 0, True)
+    Store(53, kind, [33000], 1, 64, 16, values=[1.0, 2.0, -1.0]).check(pa, 90, 30, 0)
+
+
+def test_evict_first_call_captured():
+    """A process whose first eviction is captured: the launch's sizes are found then."""
+    code = """
+import torch, paged_kv_cache_50_gb300 as pa
+t = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+g = torch.Generator("cuda").manual_seed(0)
+pool = torch.randn((24, 2, 16, 8, 64), generator=g, device="cuda").bfloat16()
+table, seq = torch.arange(24, dtype=torch.int32, device="cuda")[None], t([380])
+sums = torch.rand((1, 8, 384), generator=g, device="cuda")
+sums[:, :, 380:] = 0
+pools = [pool.clone(), pool.clone()]
+new = [dict(new_lens=t([0]), new_scores=torch.zeros_like(sums),
+            kept=torch.zeros((1, 8, 200), dtype=torch.int32, device="cuda")) for _ in pools]
+run = lambda k: pa.pa_evict(pools[k], table, seq, sums, 200, num_recent=9, num_first=2, **new[k])
+assert pa.pa_get_device_error() == 0
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    run(0)
+graph.replay()
+run(1)
+torch.cuda.synchronize()
+assert new[0]["new_lens"].tolist() == [200] and torch.equal(pools[0], pools[1])
+assert all(torch.equal(new[0][k], new[1][k]) for k in new[0])
+assert not torch.equal(pools[0], pool) and pa.pa_get_device_error() == 0
+"""
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300,
+                       cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert r.returncode == 0, r.stderr[-2000:]
 
 
 @pytest.mark.parametrize("values", [[1.0], [0.0, -0.0], [1.0, 2.0], [-1.0, 0.0, 1e-45, -1e-45],
