@@ -636,7 +636,8 @@ pa_status pa_decode_scores_fp4(const void* q, const void* kv_cache, const int32_
  * free_start (or free_start > num_free) none is pushed, new_free_start = free_start:
  * PA_DEVERR_LENGTH.
  * new_lens may be seq_lens, new_scores may be scores, new_free_start may be
- * free_start (in place); outputs overlap nothing otherwise (PA_ERR_INVALID).
+ * free_start (in place); outputs overlap nothing otherwise, and nothing the pool
+ * (PA_ERR_INVALID).
  * A request's blocks must be its own: a block that two requests (or two columns)
  * share would be moved in twice.
  * Refused on the device: a request longer than score_tokens or its table row

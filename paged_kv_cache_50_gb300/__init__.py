@@ -11,7 +11,11 @@ Function names follow the C ABI: ``pa_reshape_and_cache``, ``pa_varlen_fwd``,
 ``pa_num_kv_splits``, ``pa_decode_workspace_bytes``, ``pa_decode_splitkv``,
 ``pa_lse_merge``, ``pa_mla_decode``, ``pa_get_device_error``; the serving step
 around attention is ``pa_plan_step``, ``pa_qk_norm_rope_cache`` (and ``_fp8``),
-``pa_varlen_fwd_sinks`` and ``pa_decode_window`` (and ``_fp8``).
+``pa_varlen_fwd_sinks`` and ``pa_decode_window`` (and ``_fp8``).  Longer contexts from
+the same cache memory: ``fp4_pool``, ``pa_reshape_and_cache_fp4`` and ``pa_decode_fp4`` (a
+cache of 4-bit codes), ``pa_decode_scores`` (and ``_fp4``) and ``pa_evict`` (and ``_fp4``:
+what attention weighted least goes), and ``pa_prompt_fwd`` (whole prompts, whose keys and
+values need not be in a pool).
 """
 
 from __future__ import annotations

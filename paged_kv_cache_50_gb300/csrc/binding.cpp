@@ -1,4 +1,5 @@
-// The argument checks of the serving-step calls, compiled.
+// The argument checks of the serving-step calls, and of those over 4-bit pools, weights'
+// sums, evictions and whole prompts, compiled.
 //
 // A step's small calls (a plan of 64 requests, the norms of 64 tokens) run for 2
 // to 3 us on the GPU, and reading type, device, layout and address of a dozen

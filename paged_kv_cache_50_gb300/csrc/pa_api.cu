@@ -883,6 +883,11 @@ static pa_status evict(void* kv_cache, const pa_shape* shape, bool four, int ele
                           {kept, units4 * budget},
                           {free_blocks, static_cast<size_t>(num_free) * 4},
                           {new_free_start, one}};
+  const size_t row = four ? shape->head_size / 16 * 9 : shape->head_size * element_bytes;
+  const Range pool{kv_cache, static_cast<size_t>(shape->num_blocks) * shape->num_kv_heads *
+                                 shape->block_size * 2 * row};
+  for (const Range& r : ranges)
+    if (overlap(pool, r)) return PA_ERR_INVALID;
   for (int out = 4; out < 9; ++out)
     for (int k = 0; k < out; ++k) {
       const bool same = (out == 4 && k == 1) || (out == 5 && k == 2) || (out == 8 && k == 3);
@@ -914,8 +919,6 @@ static pa_status evict(void* kv_cache, const pa_shape* shape, bool four, int ele
   n.four = four;
   n.row_bytes = shape->head_size * element_bytes;
   n.err = device_error_ptr();
-  n.sm_count = pa_device_sm_count();
-  if (n.sm_count <= 0) return PA_ERR_CUDA;
   return from_cuda(pa::launch_evict(n, static_cast<cudaStream_t>(stream)));
 }
 

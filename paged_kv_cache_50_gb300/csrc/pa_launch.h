@@ -222,7 +222,6 @@ struct EvictLaunch {
   bool four;              // 4-bit pool; else rows of row_bytes in the standard layout
   int row_bytes;
   int* err;
-  int sm_count;
 };
 cudaError_t launch_evict(const EvictLaunch& n, cudaStream_t stream);
 

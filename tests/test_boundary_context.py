@@ -137,6 +137,13 @@ def test_evict_refusals(pa):
         assert call(four, _shape(pa, head_size=96)) == pa.PA_ERR_UNSUPPORTED
         assert call(four, _shape(pa, block_size=24)) == pa.PA_ERR_INVALID
         assert call(four, _shape(pa, num_seqs=0), table=NULL, cache=NULL) == pa.PA_OK
+        far = 1 << 20   # nothing may lie in the pool
+        for name in apart:
+            for at in (far, far + 64, far - size[name] + 4):
+                assert call(four, cache=far, **{name: at}) == pa.PA_ERR_INVALID, (name, at)
+        s = _shape(pa)
+        pool = s.num_blocks * s.num_kv_heads * s.block_size * 2 * s.head_size * 9 // 16
+        assert not four or call(four, cache=far, kept=far + pool - 4) == pa.PA_ERR_INVALID
     assert call(False, el=4) == call(False, el=0) == pa.PA_ERR_INVALID
 
 
