@@ -11,7 +11,7 @@
 // formed by one thread in the order of the heads: no atomics, the same result every
 // time.
 //
-// CTA 0 of a (request, kv head) merges the outputs, the others take 2048 tokens
+// The first CTAs of a (request, kv head) merge the outputs, the others take 2048 tokens
 // each.  Every CTA finds the group's log-sum-exps itself from the splits' (at most a
 // few hundred floats, in L2), with the logits of its tokens on their way meanwhile.
 //
@@ -29,6 +29,8 @@ namespace {
 constexpr int kScoreThreads = 256;
 constexpr int kScoreTokens = 2048;   // of a CTA
 constexpr int kMaxGroup = 16;
+constexpr int kFewStates = 16;
+constexpr int kFewUnits = 64;
 
 struct ScoreArgs {
   const float* ws;
@@ -44,6 +46,7 @@ struct ScoreArgs {
   float* lse;
   int* err;
   int S, Hq, Hkv, grp, max_seq_len;
+  int merging;        // CTAs of a (request, kv head) that merge, before those that add
   int64_t logit_tokens, score_tokens;
 };
 
@@ -60,6 +63,7 @@ __global__ void __launch_bounds__(kScoreThreads) decode_scores_kernel(
     const __grid_constant__ ScoreArgs a) {
   // Per row: the states' maximum, their sum, and the log-sum-exp.
   __shared__ __align__(16) float row_m[kMaxGroup], row_l[kMaxGroup], row_x[kMaxGroup];
+  __shared__ float factor[kScoreThreads], partial[kScoreThreads];
   pdl_wait();
   pdl_trigger();
   const int kvh = blockIdx.y, i = blockIdx.z, grp = a.grp;
@@ -69,8 +73,9 @@ __global__ void __launch_bounds__(kScoreThreads) decode_scores_kernel(
   if (cut) seq = min(seq, a.positions);   // (what lies past them has no logits)
   // Tokens past max_seq_len have no logits.
   const int end = min(seq, a.max_seq_len);
-  const int first = (static_cast<int>(blockIdx.x) - 1) * kScoreTokens;
-  if (blockIdx.x > 0 && first >= end) return;
+  const bool merges = static_cast<int>(blockIdx.x) < a.merging;
+  const int first = (static_cast<int>(blockIdx.x) - a.merging) * kScoreTokens;
+  if (!merges && first >= end) return;
   if (blockIdx.x == 0 && threadIdx.x == 0 && end < seq) record_error(a.err, PA_DEVERR_LENGTH);
   const int64_t unit = static_cast<int64_t>(i) * a.Hkv + kvh;
   const int64_t row0 = static_cast<int64_t>(i) * a.Hq + kvh * grp;
@@ -88,7 +93,7 @@ __global__ void __launch_bounds__(kScoreThreads) decode_scores_kernel(
                : a.ws + ((row0 + r) * a.S + s) * (D + 1);
   };
   const bool done = cut && states == 1;   // ... and these
-  if (done && blockIdx.x == 0) return;
+  if (done && merges) return;
   // The logits of a thread's tokens (their first VW heads) and their sums, on the way
   // while the log-sum-exps are formed.
   constexpr int kEach = kScoreTokens / kScoreThreads;
@@ -108,7 +113,7 @@ __global__ void __launch_bounds__(kScoreThreads) decode_scores_kernel(
       }
     }
   };
-  if (blockIdx.x > 0) {
+  if (!merges) {
     load(0);
 #pragma unroll
     for (int k = 0; k < kEach; ++k)
@@ -140,20 +145,51 @@ __global__ void __launch_bounds__(kScoreThreads) decode_scores_kernel(
     }
   }
   __syncthreads();
-  if (blockIdx.x == 0) {
-    for (int idx = threadIdx.x; idx < grp * D; idx += kScoreThreads) {
-      const int r = idx / D, e = idx % D;
-      const float m = row_m[r];
-      float acc = 0.f;
-#pragma unroll 4
-      for (int s = 0; s < states; ++s) {
-        const float* p = state(r, s);
-        const float f = cut ? (p[D] == m ? 1.f : fast_exp2(p[D] - m))
-                            : p[D] == -CUDART_INF_F ? 0.f : expf(p[D] - m);
-        acc += f * p[e];
-      }
+  if (merges) {
+    auto factor_of = [&](float x, float m) {
+      return cut ? (x == m ? 1.f : fast_exp2(x - m)) : x == -CUDART_INF_F ? 0.f : expf(x - m);
+    };
+    auto give = [&](int r, int e, float acc) {
       a.out[(row0 + r) * D + e] =
           __float2bfloat16_rn(row_l[r] == 0.f ? 0.f : acc / row_l[r] * a.out_scale);
+    };
+    const int m0 = static_cast<int>(blockIdx.x);
+    if (states <= kFewStates) {
+      const int rows = m0 < grp ? (grp - m0 + a.merging - 1) / a.merging : 0;
+      for (int idx = threadIdx.x; idx < rows * D; idx += kScoreThreads) {
+        const int r = m0 + idx / D * a.merging, e = idx % D;
+        float acc = 0.f;
+#pragma unroll 4
+        for (int s = 0; s < states; ++s) {
+          const float* p = state(r, s);
+          acc += factor_of(p[D], row_m[r]) * p[e];
+        }
+        give(r, e, acc);
+      }
+      return;
+    }
+    // Many states: their factors once, and the states dealt over the threads of an element.
+    constexpr int kParts = kScoreThreads / D;
+    const int e = threadIdx.x % D, part = threadIdx.x / D;
+    for (int r = m0; r < grp; r += a.merging) {
+      float acc = 0.f;
+      for (int s0 = 0; s0 < states; s0 += kScoreThreads) {
+        const int n = min(kScoreThreads, states - s0);
+        if (static_cast<int>(threadIdx.x) < n)
+          factor[threadIdx.x] = factor_of(state(r, s0 + threadIdx.x)[D], row_m[r]);
+        __syncthreads();
+#pragma unroll 8
+        for (int s = part; s < n; s += kParts) acc += factor[s] * state(r, s0 + s)[e];
+        __syncthreads();
+      }
+      partial[threadIdx.x] = acc;
+      __syncthreads();
+      if (part == 0) {
+#pragma unroll
+        for (int k = 1; k < kParts; ++k) acc += partial[threadIdx.x + k * D];
+        give(r, e, acc);
+      }
+      __syncthreads();
     }
     return;
   }
@@ -177,7 +213,7 @@ template <int D, int VW>
 cudaError_t launch_t(const ScoreArgs& a, int N, cudaStream_t stream) {
   const long long chunks = (static_cast<long long>(a.max_seq_len) + kScoreTokens - 1) / kScoreTokens;
   return launch_pdl(decode_scores_kernel<D, VW>,
-                    dim3(static_cast<unsigned>(chunks + 1), a.Hkv, N), dim3(kScoreThreads), 0, stream,
+                    dim3(static_cast<unsigned>(chunks + a.merging), a.Hkv, N), dim3(kScoreThreads), 0, stream,
                     a);
 }
 
@@ -204,6 +240,11 @@ cudaError_t launch_decode_scores(const ScoresLaunch& n, cudaStream_t stream) {
   a.max_seq_len = n.max_seq_len;
   a.logit_tokens = n.logit_tokens;
   a.score_tokens = n.score_tokens;
+  // Few (request, kv head) pairs are cut into many parts each: a CTA for each row then.
+  // (2 requests of 10210 tokens, one kv head of 16: 33 us with one for all, now 21, over a
+  // 4-bit pool 103, now 36; 4 requests with 8 kv heads of 4: 37 and 36; but 16 such of 4096
+  // tokens 38 and 40.)
+  a.merging = static_cast<long long>(n.N) * n.Hkv < kFewUnits ? a.grp : 1;
   const bool four = a.grp % 4 == 0;
   if (n.d == 128) return four ? launch_t<128, 4>(a, n.N, stream) : launch_t<128, 1>(a, n.N, stream);
   return four ? launch_t<64, 4>(a, n.N, stream) : launch_t<64, 1>(a, n.N, stream);
