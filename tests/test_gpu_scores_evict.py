@@ -67,6 +67,19 @@ def test_sums(pa, kind, shape):
         assert pa.pa_get_device_error() == 0
 
 
+@pytest.mark.parametrize("kind", [Cache, Plain], ids=["fp4", "bf16"])
+def test_sums_of_one_long_stream(pa, kind):
+    """One kv head cut into as many parts as there may be, merged row by row."""
+    for n, (seqs, hq, d, bs) in enumerate((([20011], 16, 128, 16), ([9000, 40], 5, 64, 32))):
+        c = kind(60 + n, seqs, hq, 1, d, bs)
+        got_s = torch.zeros((len(seqs), 1, c.longest), device="cuda")
+        refs, pool = c.check(sums(pa, c, got_s), f"{seqs}")
+        want, tol = ctx.weight_sums(c.q, pool, c.table, c.seqs, c.scale, refs,
+                                    torch.zeros_like(got_s))
+        assert ((got_s.double() - want).abs() <= tol).all(), seqs
+        assert pa.pa_get_device_error() == 0
+
+
 def test_sums_of_shared_blocks_and_short_max(pa):
     """Two requests over the same blocks keep sums of their own; tokens past
     max_seq_len are attended to, get none and are flagged."""
